@@ -83,7 +83,8 @@ typedef enum {
   PA_ERR_WORKSPACE = 6, /* ws_bytes < pa_workspace_bytes(dims)                 */
   PA_ERR_ARCH = 7,      /* current device is not compute capability 10.3       */
   PA_ERR_CUDA = 8,      /* a CUDA runtime / driver call or launch failed       */
-  PA_ERR_DTYPE = 9,     /* io_dtype is not a pa_io_dtype                       */
+  PA_ERR_DTYPE = 9,     /* io_dtype is not a pa_io_dtype, or a format not a
+                           pa_ckpt_format                                     */
   PA_ERR_HOST_MEMORY = 10 /* a host-side call could not allocate its scratch    */
 } pa_status;
 
@@ -405,6 +406,120 @@ size_t pa_lce_bwd_workspace_bytes(int32_t N, int32_t V, int32_t D);
 pa_status pa_lce_bwd(int32_t N, int32_t V, int32_t D, const void* hidden, const void* head, const int32_t* targets,
                      const float* lse, const float* g, void* dhidden, void* dhead, void* ws, size_t ws_bytes,
                      pa_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the most likely
+ * alternatives (beside the fused cross-entropy: a policy's loss takes the log
+ * probability of each token that was sampled and an entropy bonus, not a mean
+ * NLL). With z = H W^T / temperature, never stored, per token i
+ *   lse[i]     = ln sum_v exp(z[i, v])
+ *   logp[i]    = z[i, targets[i]] - lse[i]
+ *   entropy[i] = -sum_v p ln p,  p = exp(z[i, v] - lse[i])
+ *   top_ids[i, k], top_logp[i, k]  the `top` largest logits' vocabulary rows and
+ *                log probabilities, largest first, the lower row first among equals
+ *   hidden  : (N, D) bf16, row-major      head : (V, D) bf16, row-major
+ *   targets : (N) int32; outside [0, V) the token is not scored: its logp is 0
+ *             (its other outputs are written all the same)
+ *   logp, lse, entropy : (N) fp32;  top_ids (N, top) int32, top_logp (N, top) fp32
+ * N, V in [1, 2^30]; D a multiple of 64 in [64, 16384]; top in [0, 32] and <= V
+ * (0: no alternatives, their pointers are not used); temperature > 0. Any N is
+ * one pass over the head: a single token costs the reading of it.
+ * Alternatives are ranked by the unscaled logits as the tensor cores' fp32
+ * sums give them. Logits of -inf or NaN are no alternatives: a token with fewer
+ * others than `top` has id -1 and log probability -inf in the places left. A
+ * NaN or +inf logit makes the token's lse, logp and entropy NaN.
+ * Device pointers, caller-owned, 16-byte aligned; ws >=
+ * pa_logp_workspace_bytes(N, V, D, top), its first 4 bytes the status word.
+ * Asynchronous on `stream`; results do not depend on timing.
+ * Errors: PA_ERR_SHAPE, PA_ERR_NULL, PA_ERR_ALIGN, PA_ERR_WORKSPACE,
+ * PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+size_t pa_logp_workspace_bytes(int32_t N, int32_t V, int32_t D, int32_t top);
+pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_t top, const void* hidden,
+                      const void* head, const int32_t* targets, float* logp, float* lse, float* entropy,
+                      int32_t* top_ids, float* top_logp, void* ws, size_t ws_bytes, pa_stream_t stream);
+
+/*
+ * Its backward: for L = sum_i g_logp[i] * logp[i] + g_entropy[i] * entropy[i]
+ *   dz[i, v]   = (g_logp[i] ([v == targets[i]] - p) - g_entropy[i] p (ln p + entropy[i])) / temperature
+ *   dhidden[i] = sum_v dz[i, v] head[v]      (N, D) bf16, overwritten
+ *   dhead[v]   = sum_i dz[i, v] hidden[i]    (V, D) bf16, overwritten; NULL when
+ *                the head does not train
+ * lse and entropy are the forward's at the same temperature; g_entropy may be
+ * NULL (all 0), entropy then too. A target outside [0, V) leaves only the
+ * entropy's part. The vocabulary is taken in chunks as in pa_lce_bwd (the
+ * logits are formed again, dz of a chunk is held in bf16), in a fixed order.
+ * ws >= pa_logp_bwd_workspace_bytes(N, V, D). Arguments, execution and errors
+ * otherwise as pa_logp_fwd.
+ */
+size_t pa_logp_bwd_workspace_bytes(int32_t N, int32_t V, int32_t D);
+pa_status pa_logp_bwd(int32_t N, int32_t V, int32_t D, float temperature, const void* hidden, const void* head,
+                      const int32_t* targets, const float* lse, const float* entropy, const float* g_logp,
+                      const float* g_entropy, void* dhidden, void* dhead, void* ws, size_t ws_bytes,
+                      pa_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits: what the backward needs of the forward,
+ * kept at half the size of bf16 in between. The last dimension of a tensor is
+ * cut into blocks of `block` elements (32, 64 or 128; a row's last block may
+ * be short). Per block
+ *   scale = max |x| / top          fp32; top = 127 (PA_CKPT_INT8) or 448 (PA_CKPT_E4M3)
+ *   code  = x / scale              rounded once, to nearest even: an int8 in
+ *                                  [-127, 127], or a float8 of 4 exponent and 3 mantissa bits
+ * and loading gives code * scale, rounded to the tensor's type. A block of
+ * zeros has scale 0. A block that holds an infinity or a NaN has scale NaN and
+ * codes 0: it comes back as NaN throughout.
+ *   x      : (B, H, N, C), element (b, h, n, c) at b*s_b + h*s_h + n*s_n + c, bf16 or fp32
+ *            (io_dtype); the source of a save, the destination of a load.
+ *            C is a multiple of 8. Strides of dimensions larger than one are
+ *            >= C and multiples of 16 bytes; rows of a destination do not overlap.
+ *   codes  : (B, H, N, C) bytes, contiguous
+ *   scales : (B, H, N, ceil(C / block)) fp32, contiguous
+ * One launch for up to PA_CKPT_MAX_TENSORS tensors of one type (q, k, v and
+ * out of a layer, say). No workspace. Pointers 16-byte aligned; at most
+ * 2^31 - 4096 groups of eight elements per tensor, short blocks counted whole.
+ * Errors: PA_ERR_NULL, PA_ERR_SHAPE (also count and block), PA_ERR_DTYPE
+ * (io_dtype, format), PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+#define PA_CKPT_MAX_TENSORS 8
+typedef enum { PA_CKPT_INT8 = 0, PA_CKPT_E4M3 = 1 } pa_ckpt_format;
+typedef struct {
+  void* x;
+  void* codes;
+  float* scales;
+  int32_t B, H, N, C;
+  int64_t s_b, s_h, s_n;
+} pa_ckpt_tensor;
+pa_status pa_ckpt_save(int32_t count, const pa_ckpt_tensor* tensors, int32_t io_dtype, int32_t format, int32_t block,
+                       pa_stream_t stream);
+pa_status pa_ckpt_load(int32_t count, const pa_ckpt_tensor* tensors, int32_t io_dtype, int32_t format, int32_t block,
+                       pa_stream_t stream);
+
+/*
+ * Attention backward from 8-bit checkpoints: pa_bwd with q, k, v and out given
+ * as pa_ckpt_save left them (C = D, the four in one format and block). With ^
+ * for what a load gives, q^, k^ and v^ in bf16 and out^ unrounded:
+ *   P = exp(scale <q^, k^> - lse) over visible pairs, lse the forward's
+ *   delta_i = <dout_i, out^_i>,  and the gradients from those as in pa_bwd.
+ * One launch brings q^, k^ and v^ into the workspace and forms delta from
+ * out's codes; out^ is never stored.
+ *   q, out : codes (B, Hq, N, D), scales (B, Hq, N, ceil(D / block));  k, v with Hkv
+ *   dout, dq, dk, dv : bf16, contiguous, or with `strides` as in pa_bwd_strided
+ *            (dout and dq the q_* strides, dk and dv the k_* ones); NULL = contiguous
+ *   lse    : (B, Hq, N) fp32;  seg (B, N) int32, or NULL for plain causal; any N
+ * ws >= pa_bwd_ckpt_workspace_bytes(dims) (0 if dims are invalid).
+ * Errors: as pa_bwd_strided, and PA_ERR_SHAPE (block, or more than 2^31 - 4096
+ * groups of eight elements in q), PA_ERR_DTYPE (format).
+ */
+typedef struct {
+  const void* codes;
+  const float* scales;
+} pa_ckpt;
+size_t pa_bwd_ckpt_workspace_bytes(const pa_dims* dims);
+pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t format, int32_t block,
+                      const pa_ckpt* q, const pa_ckpt* k, const pa_ckpt* v, const pa_ckpt* out, const void* dout,
+                      const float* lse, const int32_t* seg, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                      pa_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* pa_status_string(pa_status s);

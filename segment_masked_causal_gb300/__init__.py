@@ -29,11 +29,15 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_HEAD_DIM", 3: "PA_ERR_G
                 5: "PA_ERR_ALIGN", 6: "PA_ERR_WORKSPACE", 7: "PA_ERR_ARCH", 8: "PA_ERR_CUDA", 9: "PA_ERR_DTYPE",
                 10: "PA_ERR_HOST_MEMORY"}
 PA_IO_BF16, PA_IO_F32 = 0, 1
+PA_CKPT_INT8, PA_CKPT_E4M3 = 0, 1
+PA_CKPT_MAX_TENSORS = 8
 EXPORTS = ["pa_workspace_bytes", "pa_fwd", "pa_bwd", "pa_fwd_causal", "pa_bwd_causal", "pa_build_tile_table",
            "pa_fwd_tiles", "pa_bwd_delta", "pa_bwd_dq", "pa_bwd_dkv", "pa_bwd_noalloc", "pa_device_status",
            "pa_selftest_wait_timeout", "pa_selftest_exp2_fma", "pa_pack_first_fit", "pa_workspace_bytes_strided", "pa_fwd_strided",
            "pa_bwd_strided", "pa_lce_workspace_bytes", "pa_lce_fwd", "pa_lce_bwd_workspace_bytes", "pa_lce_bwd",
-           "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_status_string"]
+           "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_logp_workspace_bytes", "pa_logp_fwd",
+           "pa_logp_bwd_workspace_bytes", "pa_logp_bwd", "pa_ckpt_save", "pa_ckpt_load", "pa_bwd_ckpt_workspace_bytes",
+           "pa_bwd_ckpt", "pa_status_string"]
 
 
 class LibraryMissing(RuntimeError):
@@ -54,6 +58,16 @@ class pa_dims(ctypes.Structure):
 class pa_strides(ctypes.Structure):
     _fields_ = [("q_b", ctypes.c_int64), ("q_h", ctypes.c_int64), ("q_n", ctypes.c_int64),
                 ("k_b", ctypes.c_int64), ("k_h", ctypes.c_int64), ("k_n", ctypes.c_int64)]
+
+
+class pa_ckpt_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("s_b", ctypes.c_int64), ("s_h", ctypes.c_int64), ("s_n", ctypes.c_int64)]
+
+
+class pa_ckpt(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -112,6 +126,24 @@ def lib():
             L.pa_lce_bwd_workspace_bytes.restype = S
             L.pa_lce_bwd.argtypes = [I32, I32, I32, P, P, P, P, P, P, P, P, S, P]
             L.pa_lce_bwd.restype = ctypes.c_int
+            F = ctypes.c_float
+            L.pa_logp_workspace_bytes.argtypes = [I32, I32, I32, I32]
+            L.pa_logp_workspace_bytes.restype = S
+            L.pa_logp_fwd.argtypes = [I32, I32, I32, F, I32, P, P, P, P, P, P, P, P, P, S, P]
+            L.pa_logp_fwd.restype = ctypes.c_int
+            L.pa_logp_bwd_workspace_bytes.argtypes = [I32, I32, I32]
+            L.pa_logp_bwd_workspace_bytes.restype = S
+            L.pa_logp_bwd.argtypes = [I32, I32, I32, F, P, P, P, P, P, P, P, P, P, P, S, P]
+            L.pa_logp_bwd.restype = ctypes.c_int
+            CT, CK = ctypes.POINTER(pa_ckpt_tensor), ctypes.POINTER(pa_ckpt)
+            L.pa_ckpt_save.argtypes = [I32, CT, I32, I32, I32, P]
+            L.pa_ckpt_save.restype = ctypes.c_int
+            L.pa_ckpt_load.argtypes = [I32, CT, I32, I32, I32, P]
+            L.pa_ckpt_load.restype = ctypes.c_int
+            L.pa_bwd_ckpt_workspace_bytes.argtypes = [D]
+            L.pa_bwd_ckpt_workspace_bytes.restype = S
+            L.pa_bwd_ckpt.argtypes = [D, ST, I32, I32, CK, CK, CK, CK, P, P, P, P, P, P, P, S, P]
+            L.pa_bwd_ckpt.restype = ctypes.c_int
             L.pa_pack_first_fit.argtypes = [P, P, I32, P, I32, I32, I32, U64, U64, P, P, P, P, P, P, P]
             L.pa_pack_first_fit.restype = ctypes.c_int
             L.pa_status_string.argtypes = [ctypes.c_int]
@@ -524,6 +556,284 @@ def linear_cross_entropy_backward(hidden, head, targets, lse, g, train_head=True
         ws = torch.empty(n, dtype=torch.uint8, device=hidden.device)
     pa_lce_bwd(hidden, head, targets, lse, g, dh, dw, ws)
     return dh, dw
+
+
+# ------------------------------------------------- token log probabilities
+def _on_current_device(*ts):
+    """The tensors share one CUDA device and it is the current one (whose
+    stream the call takes)."""
+    import torch
+    at = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != at):
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at}), got one on {t.device}")
+
+
+def _logp_dims(hidden, head, targets):
+    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1]:
+        raise ValueError("hidden must be (N, D) and head (V, D)")
+    if tuple(targets.shape) != (hidden.shape[0],):
+        raise ValueError("targets must be (N,)")
+    return hidden.shape[0], head.shape[0], hidden.shape[1]
+
+
+def _want(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def pa_logp_workspace_bytes(N, V, D, top=0) -> int:
+    return int(lib().pa_logp_workspace_bytes(int(N), int(V), int(D), int(top)))
+
+
+def pa_logp_fwd(hidden, head, targets, logp, lse, entropy, top_ids, top_logp, ws, temperature=1.0, top=0, stream=None):
+    """logp, lse and entropy (N,) fp32 and, with top > 0, top_ids (N, top)
+    int32 and top_logp (N, top) fp32, all outputs (see include/pa.h)."""
+    import torch
+    N, V, D = _logp_dims(hidden, head, targets)
+    f, bf, i32 = torch.float32, torch.bfloat16, torch.int32
+    for t, n in ((logp, "logp"), (lse, "lse"), (entropy, "entropy")):
+        _want(t, (N,), n)
+    for t, n in ((top_ids, "top_ids"), (top_logp, "top_logp")):
+        _want(t, (N, top), n)
+    _on_current_device(hidden, head, targets, logp, lse, entropy, top_ids, top_logp, ws)
+    _check(lib().pa_logp_fwd(N, V, D, float(temperature), int(top), _ptr(hidden, bf, "hidden"), _ptr(head, bf, "head"),
+                             _ptr(targets, i32, "targets"), _ptr(logp, f, "logp"), _ptr(lse, f, "lse"),
+                             _ptr(entropy, f, "entropy"), _ptr(top_ids, i32, "top_ids"),
+                             _ptr(top_logp, f, "top_logp"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def token_logprobs_forward(hidden, head, targets, temperature=1.0, top=0, ws=None):
+    """Log probabilities of `targets` under softmax(hidden head^T / temperature)
+    with the entropy and the `top` most likely alternatives, without the
+    logits. hidden (N, D) and head (V, D) bf16; targets (N,) int32, outside
+    [0, V) = not scored (logp 0). Returns (logp, lse, entropy, top_ids,
+    top_logp), the last two None when top is 0."""
+    import torch
+    N, V, D = _logp_dims(hidden, head, targets)
+    dev, f = hidden.device, torch.float32
+    if ws is None:
+        n = pa_logp_workspace_bytes(N, V, D, top)
+        if n == 0:
+            raise PAError(4, "invalid token log probability dims")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    logp, lse, entropy = (torch.empty(N, dtype=f, device=dev) for _ in range(3))
+    ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
+    alt = torch.empty((N, top), dtype=f, device=dev) if top else None
+    pa_logp_fwd(hidden, head, targets, logp, lse, entropy, ids, alt, ws, temperature, top)
+    return logp, lse, entropy, ids, alt
+
+
+def pa_logp_bwd_workspace_bytes(N, V, D) -> int:
+    return int(lib().pa_logp_bwd_workspace_bytes(int(N), int(V), int(D)))
+
+
+def pa_logp_bwd(hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden, dhead, ws, temperature=1.0, stream=None):
+    """dhidden (N, D) and dhead (V, D) bf16 are outputs (dhead None when the
+    head does not train); g_logp and g_entropy (N,) fp32 = dL/dlogp and
+    dL/dentropy per token, g_entropy None for no entropy term."""
+    import torch
+    N, V, D = _logp_dims(hidden, head, targets)
+    f, bf = torch.float32, torch.bfloat16
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy")):
+        _want(t, (N,), n)
+    _want(dhidden, (N, D), "dhidden")
+    _want(dhead, (V, D), "dhead")
+    _on_current_device(hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden, dhead, ws)
+    _check(lib().pa_logp_bwd(N, V, D, float(temperature), _ptr(hidden, bf, "hidden"), _ptr(head, bf, "head"),
+                             _ptr(targets, torch.int32, "targets"), _ptr(lse, f, "lse"), _ptr(entropy, f, "entropy"),
+                             _ptr(g_logp, f, "g_logp"), _ptr(g_entropy, f, "g_entropy"), _ptr(dhidden, bf, "dhidden"),
+                             _ptr(dhead, bf, "dhead"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def token_logprobs_backward(hidden, head, targets, lse, entropy, g_logp, g_entropy=None, temperature=1.0,
+                            train_head=True, ws=None):
+    """Gradients of sum(g_logp * logp + g_entropy * entropy) into hidden and
+    head: (dhidden, dhead), dhead None when the head does not train. hidden
+    may be a Checkpoint (of a (N, D) tensor): its values are brought back for
+    the call."""
+    import torch
+    if isinstance(hidden, Checkpoint):
+        hidden = checkpoint_load([hidden])[0]
+    N, V, D = _logp_dims(hidden, head, targets)
+    if ws is None:
+        n = pa_logp_bwd_workspace_bytes(N, V, D)
+        if n == 0:
+            raise PAError(4, "invalid token log probability dims")
+        ws = torch.empty(n, dtype=torch.uint8, device=hidden.device)
+    dh = torch.empty_like(hidden)
+    dw = torch.empty_like(head) if train_head else None
+    pa_logp_bwd(hidden, head, targets, lse, entropy, g_logp, g_entropy, dh, dw, ws, temperature)
+    return dh, dw
+
+
+# ------------------------------------------------------- 8-bit checkpoints
+class Checkpoint:
+    """A tensor kept in 8 bits: codes (int8 or float8_e4m3fn, the tensor's
+    shape, contiguous) and fp32 scales, one per block of the last dim; dtype
+    is what loading gives back."""
+    __slots__ = ("codes", "scales", "block", "dtype")
+
+    def __init__(self, codes, scales, block=64, dtype=None):
+        import torch
+        self.codes, self.scales, self.block = codes, scales, int(block)
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        _ckpt_format(codes.dtype)
+        if self.block not in (32, 64, 128):
+            raise ValueError(f"block must be 32, 64 or 128, got {block}")
+        want = tuple(codes.shape[:-1]) + (-(-codes.shape[-1] // self.block),)
+        if tuple(scales.shape) != want:
+            raise ValueError(f"scales must be {want}, got {tuple(scales.shape)}")
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _ckpt_format(dtype):
+    import torch
+    if dtype == torch.int8:
+        return PA_CKPT_INT8
+    if dtype == torch.float8_e4m3fn:
+        return PA_CKPT_E4M3
+    raise ValueError(f"codes must be int8 or float8_e4m3fn, got {dtype}")
+
+
+def _ckpt_tensor(x, c):
+    """The C description of tensor x (1 to 4 dims, last contiguous) and checkpoint c."""
+    if not 1 <= x.dim() <= 4 or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
+    pad = 4 - x.dim()
+    B, H, N, C = (1,) * pad + tuple(x.shape)
+    sb, sh, sn = ((0,) * pad + tuple(x.stride()))[:3]
+    _want(c.codes, x.shape, "codes")
+    return pa_ckpt_tensor(x.data_ptr(), _ptr(c.codes, None, "codes"), _ptr(c.scales, _torch().float32, "scales"), B, H, N,
+                          C, sb, sh, sn)
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _ckpt_call(fn, xs, cs, stream):
+    """pa_ckpt_save or pa_ckpt_load of matching lists, PA_CKPT_MAX_TENSORS a launch."""
+    if not xs:
+        return
+    first = cs[0]
+    _, io = _io_dtype(xs[0])
+    fmt = _ckpt_format(first.codes.dtype)
+    for x, c in zip(xs, cs):
+        if x.dtype != xs[0].dtype or c.codes.dtype != first.codes.dtype or c.block != first.block:
+            raise ValueError("the tensors of one call share their type, format and block")
+        _on_current_device(x, c.codes, c.scales)
+    st = _stream(stream)
+    for i in range(0, len(xs), PA_CKPT_MAX_TENSORS):
+        part = [_ckpt_tensor(x, c) for x, c in zip(xs[i:i + PA_CKPT_MAX_TENSORS], cs[i:i + PA_CKPT_MAX_TENSORS])]
+        _check(fn(len(part), (pa_ckpt_tensor * len(part))(*part), io, fmt, first.block, st))
+
+
+def pa_ckpt_save(tensors, checkpoints, stream=None):
+    """Fill the checkpoints' codes and scales (see include/pa.h)."""
+    _ckpt_call(lib().pa_ckpt_save, tensors, checkpoints, stream)
+
+
+def pa_ckpt_load(tensors, checkpoints, stream=None):
+    """Fill the tensors from the checkpoints (see include/pa.h)."""
+    _ckpt_call(lib().pa_ckpt_load, tensors, checkpoints, stream)
+
+
+def checkpoint_save(tensors, format="int8", block=64):
+    """Keep activations in 8 bits: a list of Checkpoints of the given tensors
+    (bf16 or fp32, all alike; 1 to 4 dims, the last contiguous and a multiple
+    of 8). format "int8" or "e4m3"; one scale per `block` elements of the
+    last dim (32, 64 or 128). One launch for up to eight tensors."""
+    import torch
+    kinds = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+    if format not in kinds:
+        raise ValueError(f"format must be one of {sorted(kinds)}, got {format!r}")
+    tensors = list(tensors)
+    kept = [Checkpoint(torch.empty(x.shape, dtype=kinds[format], device=x.device),
+                       torch.empty(x.shape[:-1] + (-(-x.shape[-1] // block),), dtype=torch.float32, device=x.device),
+                       block, x.dtype) for x in tensors]
+    pa_ckpt_save(tensors, kept)
+    return kept
+
+
+def checkpoint_load(checkpoints, out=None):
+    """The checkpoints' values as contiguous tensors of their dtypes, or into
+    the tensors `out` (any strides with the last dim contiguous)."""
+    import torch
+    checkpoints = list(checkpoints)
+    if out is None:
+        out = [torch.empty(c.codes.shape, dtype=c.dtype, device=c.codes.device) for c in checkpoints]
+    out = list(out)
+    if len(out) != len(checkpoints):
+        raise ValueError("out must have one tensor per checkpoint")
+    pa_ckpt_load(out, checkpoints)
+    return out
+
+
+def pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D) -> int:
+    d = make_dims(B, Hq, Hkv, N, D)
+    return int(lib().pa_bwd_ckpt_workspace_bytes(ctypes.byref(d)))
+
+
+def pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale=0.0, stream=None):
+    """pa_bwd from Checkpoints of q, k, v and out (one format and block).
+    dout and dq share their strides, dk and dv theirs; seg None = plain
+    causal."""
+    import torch
+    bf, f = torch.bfloat16, torch.float32
+    if q.codes.dim() != 4 or k.codes.dim() != 4:
+        raise ValueError("q and k must be checkpoints of (B, H, N, D) tensors")
+    B, Hq, N, D = q.shape
+    Hkv = k.shape[1]
+    fmt = _ckpt_format(q.codes.dtype)
+    for c, H, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (out, Hq, "out")):
+        _want(c.codes, (B, H, N, D), n)
+        if c.codes.dtype != q.codes.dtype or c.block != q.block or c.dtype != bf:
+            raise ValueError("q, k, v and out must be bf16 checkpoints in one format and block")
+        _on_current_device(c.codes, c.scales)
+    for t, H, n in ((dout, Hq, "dout"), (dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")):
+        _want(t, (B, H, N, D), n)
+    _want(lse, (B, Hq, N), "lse")
+    _want(seg, (B, N), "seg")
+    _on_current_device(dout, lse, seg, dq, dk, dv, ws)
+    d = make_dims(B, Hq, Hkv, N, D, scale)
+    plain = _all_contiguous(dout, dq, dk, dv)
+    st = None if plain else ctypes.byref(_strides_of(dout, dk))
+    c = [ctypes.byref(pa_ckpt(_ptr(x.codes, None, n), _ptr(x.scales, f, n))) for x, n in
+         ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
+    _check(lib().pa_bwd_ckpt(ctypes.byref(d), st, fmt, q.block, *c, _ptr_rows(dout, bf, "dout"), _ptr(lse, f, "lse"),
+                             _ptr(seg, torch.int32, "seg"), _ptr_rows(dq, bf, "dq", dout), _ptr_rows(dk, bf, "dk"),
+                             _ptr_rows(dv, bf, "dv", dk), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def backward_from_checkpoint(q, k, v, out, dout, lse, seg=None, scale=0.0, ws=None):
+    """The attention backward from 8-bit Checkpoints of q, k, v and out:
+    (dq, dk, dv) in bf16. They take dout's memory order: contiguous, or
+    (B, N, H, D) memory for a dout that is a view of such."""
+    import torch
+    B, Hq, N, D = q.shape
+    Hkv = k.shape[1]
+    if ws is None:
+        n = pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D)
+        if n == 0:
+            raise PAError(4, "invalid dims")
+        ws = torch.empty(n, dtype=torch.uint8, device=dout.device)
+    if dout.is_contiguous():
+        dq = torch.empty_like(dout)
+        dk, dv = (torch.empty((B, Hkv, N, D), dtype=dout.dtype, device=dout.device) for _ in range(2))
+    else:
+        dq = torch.empty_strided(dout.shape, dout.stride(), dtype=dout.dtype, device=dout.device)
+        dk, dv = (torch.empty((B, N, Hkv, D), dtype=dout.dtype, device=dout.device).transpose(1, 2) for _ in range(2))
+    pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale)
+    return dq, dk, dv
 
 
 def pa_status_string(code: int) -> str:

@@ -598,6 +598,202 @@ pa_status pa_lce_bwd(int32_t N, int32_t V, int32_t D, const void* hidden, const 
              : PA_ERR_CUDA;
 }
 
+// ------------------------------------------------------ token log probabilities
+// Indexes and tile counts are 32-bit; T and 1 / T finite.
+static bool logp_dims_ok(int32_t N, int32_t V, int32_t D) {
+  return lce_dims_ok(N, V, D) && N <= (1 << 30) && V <= (1 << 30);
+}
+static bool temperature_ok(float t) { return std::isfinite(t) && t > 0.f && std::isfinite(1.4426950408889634f / t); }
+
+size_t pa_logp_workspace_bytes(int32_t N, int32_t V, int32_t D, int32_t top) {
+  if (!logp_dims_ok(N, V, D) || top < 0 || top > pa::kLogpMaxTop || top > V) return 0;
+  return pa::logp_fwd_layout(N, V, top).bytes;
+}
+
+pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_t top, const void* hidden,
+                      const void* head, const int32_t* targets, float* logp, float* lse, float* entropy,
+                      int32_t* top_ids, float* top_logp, void* ws, size_t ws_bytes, pa_stream_t stream) {
+  if (!logp_dims_ok(N, V, D) || top < 0 || top > pa::kLogpMaxTop || top > V || !temperature_ok(temperature))
+    return PA_ERR_SHAPE;
+  for (const void* x : {hidden, head, (const void*)targets, (const void*)logp, (const void*)lse, (const void*)entropy,
+                        (const void*)ws})
+    if (!x) return PA_ERR_NULL;
+  if (top > 0 && (!top_ids || !top_logp)) return PA_ERR_NULL;
+  for (const void* x : {hidden, head, (const void*)targets, (const void*)logp, (const void*)lse, (const void*)entropy,
+                        (const void*)(top > 0 ? top_ids : nullptr), (const void*)(top > 0 ? top_logp : nullptr),
+                        (const void*)ws})
+    if (!aligned16(x)) return PA_ERR_ALIGN;
+  if (ws_bytes < pa_logp_workspace_bytes(N, V, D, top)) return PA_ERR_WORKSPACE;
+  pa_status why = device_ok();
+  if (why != PA_OK) return why;
+  const cudaStream_t st = cu(stream);
+  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return PA_ERR_CUDA;
+  return pa::launch_logp_fwd(N, V, D, temperature, top, hidden, head, targets, logp, lse, entropy, top_ids, top_logp,
+                             ws, st) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+size_t pa_logp_bwd_workspace_bytes(int32_t N, int32_t V, int32_t D) {
+  if (!logp_dims_ok(N, V, D)) return 0;
+  return pa::logp_bwd_layout(N, V, D).bytes;
+}
+
+pa_status pa_logp_bwd(int32_t N, int32_t V, int32_t D, float temperature, const void* hidden, const void* head,
+                      const int32_t* targets, const float* lse, const float* entropy, const float* g_logp,
+                      const float* g_entropy, void* dhidden, void* dhead, void* ws, size_t ws_bytes,
+                      pa_stream_t stream) {
+  if (!logp_dims_ok(N, V, D) || !temperature_ok(temperature)) return PA_ERR_SHAPE;
+  for (const void* x : {hidden, head, (const void*)targets, (const void*)lse, (const void*)g_logp,
+                        (const void*)dhidden, (const void*)ws})
+    if (!x) return PA_ERR_NULL;
+  if (g_entropy && !entropy) return PA_ERR_NULL;
+  for (const void* x : {hidden, head, (const void*)targets, (const void*)lse, (const void*)entropy,
+                        (const void*)g_logp, (const void*)g_entropy, (const void*)dhidden, (const void*)dhead,
+                        (const void*)ws})
+    if (!aligned16(x)) return PA_ERR_ALIGN;
+  if (ws_bytes < pa_logp_bwd_workspace_bytes(N, V, D)) return PA_ERR_WORKSPACE;
+  pa_status why = device_ok();
+  if (why != PA_OK) return why;
+  const cudaStream_t st = cu(stream);
+  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return PA_ERR_CUDA;
+  return pa::launch_logp_bwd(N, V, D, temperature, hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden,
+                             dhead, ws, st) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// ------------------------------------------------------ 8-bit checkpoints
+static bool ckpt_block_ok(int32_t block) { return block == 32 || block == 64 || block == 128; }
+static bool ckpt_format_ok(int32_t f) { return f == PA_CKPT_INT8 || f == PA_CKPT_E4M3; }
+// vectors of eight elements are counted in 31 bits, less a thread block's worth
+constexpr int64_t kCkptMaxVecs = 0x7FFFF000;
+
+static pa_status ckpt_checks(int32_t count, const pa_ckpt_tensor* t, int32_t io_dtype, int32_t format, int32_t block,
+                             pa::CkptTensor* out) {
+  if (!t) return PA_ERR_NULL;
+  if (count < 1 || count > PA_CKPT_MAX_TENSORS || !ckpt_block_ok(block)) return PA_ERR_SHAPE;
+  pa_status why = io_ok(io_dtype);
+  if (why != PA_OK) return why;
+  if (!ckpt_format_ok(format)) return PA_ERR_DTYPE;
+  for (int i = 0; i < count; ++i) {
+    const pa_ckpt_tensor& x = t[i];
+    if (x.B <= 0 || x.H <= 0 || x.N <= 0 || x.C <= 0 || x.C % 8 != 0) return PA_ERR_SHAPE;
+    // in steps, so that no product overflows 64 bits
+    const int64_t nb = ((int64_t)x.C + block - 1) / block, bh = (int64_t)x.B * x.H;
+    if (bh > kCkptMaxVecs || bh * x.N > kCkptMaxVecs || bh * x.N * (nb * (block / 8)) > kCkptMaxVecs) return PA_ERR_SHAPE;
+    const int32_t n[3] = {x.B, x.H, x.N};
+    const int64_t s[3] = {x.s_b, x.s_h, x.s_n};
+    for (int k = 0; k < 3; ++k)  // the stride of a dimension of one is never used
+      if (n[k] > 1 && s[k] < x.C) return PA_ERR_SHAPE;
+    for (int k = 0; k < 3; ++k)
+      if (n[k] > 1 && s[k] % (io_dtype == PA_IO_F32 ? 4 : 8) != 0) return PA_ERR_ALIGN;
+    for (const void* p : {(const void*)x.x, (const void*)x.codes, (const void*)x.scales})
+      if (!p) return PA_ERR_NULL;
+    for (const void* p : {(const void*)x.x, (const void*)x.codes, (const void*)x.scales})
+      if (!aligned16(p)) return PA_ERR_ALIGN;
+    out[i] = pa::CkptTensor{x.x, x.codes, x.scales, x.B, x.H, x.N, x.C, x.s_b, x.s_h, x.s_n};
+  }
+  return device_ok();
+}
+
+pa_status pa_ckpt_save(int32_t count, const pa_ckpt_tensor* tensors, int32_t io_dtype, int32_t format, int32_t block,
+                       pa_stream_t stream) {
+  pa::CkptTensor x[PA_CKPT_MAX_TENSORS];
+  const pa_status why = ckpt_checks(count, tensors, io_dtype, format, block, x);
+  if (why != PA_OK) return why;
+  return pa::launch_ckpt_save(x, count, io_dtype == PA_IO_F32, format, block, cu(stream)) == cudaSuccess ? PA_OK
+                                                                                                       : PA_ERR_CUDA;
+}
+
+pa_status pa_ckpt_load(int32_t count, const pa_ckpt_tensor* tensors, int32_t io_dtype, int32_t format, int32_t block,
+                       pa_stream_t stream) {
+  pa::CkptTensor x[PA_CKPT_MAX_TENSORS];
+  const pa_status why = ckpt_checks(count, tensors, io_dtype, format, block, x);
+  if (why != PA_OK) return why;
+  return pa::launch_ckpt_load(x, count, io_dtype == PA_IO_F32, format, block, cu(stream)) == cudaSuccess ? PA_OK
+                                                                                                       : PA_ERR_CUDA;
+}
+
+// The kernels' part of the workspace for whole tiles, then q, k and v in bf16.
+struct CkptBwdLayout {
+  size_t q, k, v, bytes;
+};
+static CkptBwdLayout ckpt_bwd_layout(const pa_dims* d) {
+  pa_dims dp = *d;
+  dp.N = padded_n(d);
+  CkptBwdLayout L;
+  L.q = round_up(ws_layout(&dp).base);
+  L.k = L.q + round_up((size_t)d->B * d->Hq * d->N * d->D * 2);
+  L.v = L.k + round_up((size_t)d->B * d->Hkv * d->N * d->D * 2);
+  L.bytes = L.v + round_up((size_t)d->B * d->Hkv * d->N * d->D * 2);
+  return L;
+}
+static bool ckpt_bwd_dims_ok(const pa_dims* d, pa_status* why) {
+  if (!dims_ok(d, why)) return false;
+  if ((int64_t)d->B * d->Hq * d->N * (d->D / 8) > kCkptMaxVecs) {
+    *why = PA_ERR_SHAPE;
+    return false;
+  }
+  return true;
+}
+
+size_t pa_bwd_ckpt_workspace_bytes(const pa_dims* dims) {
+  pa_status why;
+  return ckpt_bwd_dims_ok(dims, &why) ? ckpt_bwd_layout(dims).bytes : 0;
+}
+
+pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t format, int32_t block,
+                      const pa_ckpt* q, const pa_ckpt* k, const pa_ckpt* v, const pa_ckpt* out, const void* dout,
+                      const float* lse, const int32_t* seg, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                      pa_stream_t stream) {
+  pa_status s = PA_OK;
+  if (!ckpt_bwd_dims_ok(dims, &s)) return s;
+  if (!ckpt_block_ok(block)) return PA_ERR_SHAPE;
+  if (!ckpt_format_ok(format)) return PA_ERR_DTYPE;
+  if (strides && (s = strides_ok(dims, strides, false)) != PA_OK) return s;
+  if (!q || !k || !v || !out) return PA_ERR_NULL;
+  pa_dims dp = *dims;
+  dp.N = padded_n(dims);
+  const CkptBwdLayout L = ckpt_bwd_layout(dims);
+  if (!ws) return PA_ERR_NULL;
+  if (!aligned16(ws)) return PA_ERR_ALIGN;
+  if (ws_bytes < L.bytes) return PA_ERR_WORKSPACE;
+  s = check_call(&dp, ws, ws_bytes,
+                 {q->codes, q->scales, k->codes, k->scales, v->codes, v->scales, out->codes, out->scales, dout, lse,
+                  dq, dk, dv},
+                 seg);
+  if (s != PA_OK) return s;
+  const cudaStream_t st = cu(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int32_t* ids = seg;
+  if (seg && !tiled(dims)) {
+    int32_t* pseg = reinterpret_cast<int32_t*>(w + ws_layout(&dp).pseg);
+    if (pa::launch_stage_words_in(pseg, seg, (uint64_t)dims->B, dims->N, dp.N, true, st) != cudaSuccess)
+      return PA_ERR_CUDA;
+    ids = pseg;
+  }
+  pa::AttnParams p = make_params(&dp, ids, ws, dims->N);
+  p.lse_in = lse;
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  const pa::RowStrides rs = rows_of(dims, strides);
+  const pa::RowStrides in = pa::contiguous_rows(dims->Hq, dims->Hkv, dims->N, dims->D);
+  const auto kept = [&](const pa_ckpt* c, size_t at, int H) {
+    return pa::CkptTensor{w + at,    const_cast<void*>(c->codes), const_cast<float*>(c->scales), dims->B, H, dims->N,
+                          dims->D, (int64_t)H * dims->N * dims->D, (int64_t)dims->N * dims->D, dims->D};
+  };
+  const pa::CkptTensor qkv[3] = {kept(q, L.q, dims->Hq), kept(k, L.k, dims->Hkv), kept(v, L.v, dims->Hkv)};
+  if (pa::launch_tile_table(p, const_cast<int4*>(p.tiles), st) != cudaSuccess ||
+      pa::launch_bwd_ckpt_prologue(p, dims->D, rs, qkv, out->codes, out->scales, format, block, st) != cudaSuccess ||
+      pa::launch_bwd_dq(p, dims->D, rs, w + L.q, w + L.k, w + L.v, dout, st, &in) != cudaSuccess ||
+      pa::launch_bwd_dkv(p, dims->D, rs, w + L.q, w + L.k, w + L.v, dout, st, &in) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}
+
 pa_status pa_selftest_wait_timeout(void* ws, size_t ws_bytes, pa_stream_t stream) {
   if (!ws) return PA_ERR_NULL;
   if (!aligned16(ws)) return PA_ERR_ALIGN;

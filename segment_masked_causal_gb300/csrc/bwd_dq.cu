@@ -358,22 +358,22 @@ __global__ void __launch_bounds__(352, 1)
 
 template <int D, int DM = D>
 cudaError_t launch_dq_d(const AttnParams& p, int Dio, const RowStrides& rs, const void* q, const void* k, const void* v,
-                        const void* dout, cudaStream_t st) {
+                        const void* dout, cudaStream_t st, const RowStrides& in) {
   using L = DqLayout<D>;
   CUtensorMap tq, tdo, tk, tv, tdq;
   // contiguous tensors: 2-D maps over their rows (cheaper for TMA than the
   // 4-D form, which strided tensors need)
   AttnParams pp = p;
-  pp.tma4 = (p.Nr == p.N && is_contiguous(rs, p.Hq, p.Hkv, p.N, Dio)) ? 0 : 1;
-  const auto qmap = [&](CUtensorMap* m, const void* t) {
-    return pp.tma4 ? tmap_bf16_bhnd_sw128(m, t, Dio, p.Nr, p.Hq, p.B, rs.q_n, rs.q_h, rs.q_b)
+  pp.tma4 = (p.Nr == p.N && is_contiguous(rs, p.Hq, p.Hkv, p.N, Dio) && is_contiguous(in, p.Hq, p.Hkv, p.N, Dio)) ? 0 : 1;
+  const auto qmap = [&](CUtensorMap* m, const void* t, const RowStrides& x) {
+    return pp.tma4 ? tmap_bf16_bhnd_sw128(m, t, Dio, p.Nr, p.Hq, p.B, x.q_n, x.q_h, x.q_b)
                    : tmap_bf16_2d_sw128(m, t, Dio, (uint64_t)p.B * p.Hq * p.N, 128);
   };
-  const auto kmap = [&](CUtensorMap* m, const void* t) {
-    return pp.tma4 ? tmap_bf16_bhnd_sw128(m, t, Dio, p.Nr, p.Hkv, p.B, rs.k_n, rs.k_h, rs.k_b)
+  const auto kmap = [&](CUtensorMap* m, const void* t, const RowStrides& x) {
+    return pp.tma4 ? tmap_bf16_bhnd_sw128(m, t, Dio, p.Nr, p.Hkv, p.B, x.k_n, x.k_h, x.k_b)
                    : tmap_bf16_2d_sw128(m, t, Dio, (uint64_t)p.B * p.Hkv * p.N, 128);
   };
-  if (!qmap(&tq, q) || !qmap(&tdo, dout) || !kmap(&tk, k) || !kmap(&tv, v) || !qmap(&tdq, p.dq))
+  if (!qmap(&tq, q, in) || !qmap(&tdo, dout, rs) || !kmap(&tk, k, in) || !kmap(&tv, v, in) || !qmap(&tdq, p.dq, rs))
     return cudaErrorInvalidValue;
   // the tensor maps' form is fixed at compile time: the contiguous case runs
   // exactly the 2-D code
@@ -388,14 +388,14 @@ cudaError_t launch_dq_d(const AttnParams& p, int Dio, const RowStrides& rs, cons
 }  // namespace
 
 cudaError_t launch_bwd_dq(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                          const void* v, const void* dout, cudaStream_t st) {
+                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in) {
   // head dim 96 runs the 128-wide tile layout: its tensor maps are 96
   // elements wide, so TMA fills columns 96..127 of every loaded tile with
   // zeros and drops them from every store; the MMAs contract over 96 (six
   // K-steps) and produce 96 columns (N = 96), so no work is spent on them.
-  if (D == 64) return launch_dq_d<64>(p, 64, rs, q, k, v, dout, st);
-  if (D == 96) return launch_dq_d<128, 96>(p, 96, rs, q, k, v, dout, st);
-  return launch_dq_d<128>(p, 128, rs, q, k, v, dout, st);
+  if (D == 64) return launch_dq_d<64>(p, 64, rs, q, k, v, dout, st, in ? *in : rs);
+  if (D == 96) return launch_dq_d<128, 96>(p, 96, rs, q, k, v, dout, st, in ? *in : rs);
+  return launch_dq_d<128>(p, 128, rs, q, k, v, dout, st, in ? *in : rs);
 }
 
 }  // namespace pa

@@ -1,5 +1,6 @@
 // kernels.h -- host-side launchers of the packed-attention kernels (internal).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/pa.h"
@@ -37,10 +38,11 @@ cudaError_t launch_wait_timeout_selftest(uint32_t* status, cudaStream_t st);
 cudaError_t launch_exp2_fma_selftest(const float* x, float* y, int64_t n, cudaStream_t st);
 cudaError_t launch_fwd(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k, const void* v,
                        cudaStream_t st);
+// in: the strides of q, k and v where they are not those of dout and the gradients.
 cudaError_t launch_bwd_dq(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                          const void* v, const void* dout, cudaStream_t st);
+                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr);
 cudaError_t launch_bwd_dkv(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                           const void* v, const void* dout, cudaStream_t st);
+                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr);
 // Single-pass backward: dK, dV and the fp32 dQ accumulator p.dq_acc (zeroed
 // beforehand), then p.dq = the accumulator rounded to bf16.
 cudaError_t launch_bwd_fused(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
@@ -87,5 +89,65 @@ cudaError_t launch_lce_bwd(int N, int V, int D, const void* hidden, const void* 
 cudaError_t launch_lce_fwd(int N, int V, int D, const void* hidden, const void* head, const int32_t* targets,
                            float* nll, float* lse, float* target_logit, float* part, uint32_t* status,
                            cudaStream_t st);
+
+// C (M x N, N contiguous, a multiple of 64) from A (M x K, K contiguous, boxes
+// of 128 rows x 64) and B (K x N, N contiguous, boxes of 64 rows x 64) on the
+// tensor cores. splits > 1 cuts the contraction into that many runs, each
+// with an accumulator of its own (acc + run * M * N): kAccInit or kAccAdd
+// only, joined by launch_sum_splits.
+enum GemmMode : int { kStoreBf16 = 0, kAccInit = 1, kAccAdd = 2, kAccFinal = 3 };
+struct GemmCall {
+  int M, N, K;
+  int mode;          // GemmMode
+  int splits;        // <= 1: one run
+  __nv_bfloat16* c;  // bf16 result (kStoreBf16: the product; kAccFinal: accumulator + product)
+  float* acc;        // fp32 accumulator (kAccInit: set; kAccAdd: add; kAccFinal: read)
+  uint32_t* status;
+};
+cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st);
+// The number of runs that makes an M x N x K product shortest on `slots` SMs;
+// no run is empty.
+int gemm_splits(int M, int N, int K, int slots);
+cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st);
+
+// Token log probabilities. The vocabulary is cut into runs of whole units of
+// 32 rows, one CTA column each.
+constexpr int kLogpUnit = 32;
+constexpr int kLogpMaxSplits = 160;
+constexpr int kLogpMaxTop = 32;
+int logp_max_splits(int N, int V);
+LceSplit logp_split(int N, int V, int slots);
+struct LogpFwdLayout {
+  size_t part, cand_z, cand_v, bytes;  // after the 256-byte status region
+};
+LogpFwdLayout logp_fwd_layout(int N, int V, int top);
+cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, const void* hidden, const void* head,
+                            const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
+                            float* top_logp, void* ws, cudaStream_t st);
+struct LogpBwdLayout {
+  int vc, chunks, ld_dzt, splits;
+  size_t acc, dz, dzt, bytes;
+};
+LogpBwdLayout logp_bwd_layout(int N, int V, int D);
+cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* hidden, const void* head,
+                            const int32_t* targets, const float* lse, const float* entropy, const float* g_logp,
+                            const float* g_entropy, void* dhidden, void* dhead, void* ws, cudaStream_t st);
+
+// Activations in 8 bits (ckpt.cu): x (B, H, N, C) with element strides s_b,
+// s_h, s_n against contiguous codes (B, H, N, C) and scales (B, H, N, ceil(C / block)).
+struct CkptTensor {
+  const void* x;  // save: source; load: destination
+  void* codes;
+  float* scales;
+  int B, H, N, C;
+  int64_t s_b, s_h, s_n;
+};
+cudaError_t launch_ckpt_save(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st);
+cudaError_t launch_ckpt_load(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st);
+// Start of the attention backward from 8-bit tensors: q, k and v to bf16, and
+// delta and lse2 of p with the output taken from its codes.
+cudaError_t launch_bwd_ckpt_prologue(const AttnParams& p, int D, const RowStrides& rs, const CkptTensor (&qkv)[3],
+                                     const void* out_codes, const float* out_scales, int format, int block,
+                                     cudaStream_t st);
 
 }  // namespace pa

@@ -393,14 +393,14 @@ constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + kGemmSta
 #endif
 constexpr int kGemmGroup = PA_LCE_GEMM_GROUP;
 
-enum GemmMode : int { kStoreBf16 = 0, kAccInit = 1, kAccAdd = 2, kAccFinal = 3 };
-
 struct GemmParams {
   int M, N, K;         // N a multiple of 64
   int mode;            // GemmMode
   int m_tiles;         // row blocks of 128
   int n_tiles;         // N tiles of kGemmN per row block
-  int tiles;           // M tiles x N tiles
+  int per_split;       // M tiles x N tiles
+  int tiles;           // per_split x the runs that K is cut into
+  int kb_per;          // K blocks of 64 per run
   __nv_bfloat16* c;    // bf16 result (kStoreBf16: the product; kAccFinal: accumulator + product)
   int ldc;
   float* acc;          // fp32 accumulator (kAccInit: set; kAccAdd: add; kAccFinal: read)
@@ -426,11 +426,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t sRing = smem_u32(ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (p.K + 63) / 64;
+  // K blocks kb0 .. kb1 - 1 of tile t: its run of the contraction
+  const auto tile_run = [&](int t) -> int2 {
+    const int k0 = t / p.per_split * p.kb_per;
+    return make_int2(k0, min(k0 + p.kb_per, KB));
+  };
   // this CTA's tiles: t = blockIdx.x + j * gridDim.x for j < nt (>= 1: the
   // grid is never larger than the tile count)
   const int nt = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   // first row and column of tile t: group gi holds row blocks g0 .. g0 + gs - 1
   const auto tile_origin = [&](int t) -> int2 {
+    t %= p.per_split;
     const int gi = t / (kGemmGroup * p.n_tiles), r = t - gi * kGemmGroup * p.n_tiles;
     const int g0 = gi * kGemmGroup, gs = min(kGemmGroup, p.m_tiles - g0);
     return make_int2((g0 + r % gs) * 128, (r / gs) * kGemmN);
@@ -468,7 +474,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int j = 0; ok && j < nt; ++j) {
         const int2 o = tile_origin((int)blockIdx.x + j * (int)gridDim.x);
         const int m0 = o.x, n0 = o.y;
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int2 run = tile_run((int)blockIdx.x + j * (int)gridDim.x);
+        for (int kb = run.x; kb < run.y; ++kb, ++it) {
           const int st = it % kGemmStages;
           if (!g.wait(&m.empty[st], ((it / kGemmStages) & 1) ^ 1, 45)) { ok = false; break; }
           uint8_t* sa = ring + st * kGemmStage;
@@ -493,7 +500,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // accumulator buf is free once the epilogue has read tile j - 2 from it
       if (j >= 2 && !g.wait_warp(&m.acc_empty[buf], ((j - 2) >> 1) & 1, 48)) { ok = false; break; }
       tc_fence_after();
-      for (int kb = 0; kb < KB; ++kb, ++it) {
+      const int2 run = tile_run((int)blockIdx.x + j * (int)gridDim.x);
+      for (int kb = run.x; kb < run.y; ++kb, ++it) {
         const int st = it % kGemmStages;
         if (!g.wait_warp(&m.full[st], (it / kGemmStages) & 1, 46)) { ok = false; break; }
         tc_fence_after();
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int kk = 0; kk < 4; ++kk)
           if (leader)
             umma_bf16(tmem + buf * kGemmN, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), idC,
-                      (kb > 0 || kk > 0) ? 1u : 0u);
+                      (kb > run.x || kk > 0) ? 1u : 0u);
         if (leader) umma_commit(&m.empty[st]);
         __syncwarp();
       }
@@ -528,6 +536,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int2 o = tile_origin((int)blockIdx.x + j * (int)gridDim.x);
       const int m0 = o.x, n0 = o.y;
       const int row = m0 + quarter * 32 + lane;
+      // each run of K has an accumulator of its own
+      float* acc = p.acc + (size_t)(((int)blockIdx.x + j * (int)gridDim.x) / p.per_split) * p.M * p.ldacc;
 #pragma unroll 1
       for (int c0 = 0; c0 < kGemmN; c0 += 32) {
         uint32_t a[32];
@@ -535,7 +545,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int col = n0 + c0;
         if (row >= p.M || col >= p.N) continue;  // N is a multiple of 64: 32 columns are all in or all out
         if (p.mode == kAccInit || p.mode == kAccAdd || p.mode == kAccFinal) {
-          float4* ac = reinterpret_cast<float4*>(p.acc + (size_t)row * p.ldacc + col);
+          float4* ac = reinterpret_cast<float4*>(acc + (size_t)row * p.ldacc + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float4 v = make_float4(__uint_as_float(a[4 * q]), __uint_as_float(a[4 * q + 1]),
@@ -579,19 +589,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmParams& gp, cudaStream_t st) {
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(lce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-    if (e != cudaSuccess) return e;
-    attr = true;
+// Sum of the runs' accumulators, in run order, rounded to bf16: 4 elements a thread.
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float4* __restrict__ acc, int splits, size_t n4,
+                                                         uint2* __restrict__ out) {
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += (size_t)gridDim.x * blockDim.x) {
+    float4 v = acc[i];
+    for (int s = 1; s < splits; ++s) {
+      const float4 o = acc[s * n4 + i];
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    out[i] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
-  GemmParams q = gp;
-  const long long mt = (gp.M + 127) / 128, ntl = (gp.N + kGemmN - 1) / kGemmN;
-  if (mt * ntl > (1ll << 30)) return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(lce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+  if (e != cudaSuccess) return e;
+  const long long mt = (gc.M + 127) / 128, ntl = (gc.N + kGemmN - 1) / kGemmN;
+  const int KB = (gc.K + 63) / 64, splits = gc.splits > 1 ? gc.splits : 1;
+  if (mt * ntl * splits > (1ll << 30)) return cudaErrorInvalidValue;
+  GemmParams q{};
+  q.M = gc.M;
+  q.N = gc.N;
+  q.K = gc.K;
+  q.mode = gc.mode;
   q.m_tiles = (int)mt;
   q.n_tiles = (int)ntl;
-  q.tiles = (int)(mt * ntl);
+  q.per_split = (int)(mt * ntl);
+  q.tiles = q.per_split * splits;
+  q.kb_per = (KB + splits - 1) / splits;
+  q.c = gc.c;
+  q.ldc = gc.N;
+  q.acc = gc.acc;
+  q.ldacc = gc.N;
+  q.status = gc.status;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -601,7 +637,34 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   return cudaGetLastError();
 }
 
-}  // namespace
+// Time of a run in K blocks (four 128 x 256 x 16 products, about 0.27 us an
+// SM): waves x (blocks per run + 8 for the pipeline's fill and the tile's
+// epilogue), and, with more than one run, writing and reading the
+// accumulators at 6.5 TB/s.
+int gemm_splits(int M, int N, int K, int slots) {
+  const long long tiles = (long long)((M + 127) / 128) * ((N + kGemmN - 1) / kGemmN);
+  const int KB = (K + 63) / 64;
+  int best = 1;
+  double best_cost = -1;
+  for (int s = 1; s <= 64 && s <= KB; ++s) {
+    const int per = (KB + s - 1) / s;
+    if ((KB + per - 1) / per != s) continue;  // the last run would be empty
+    const long long waves = (tiles * s + slots - 1) / slots;
+    const double cost = (double)waves * (per + 8) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 / 0.27 : 0.0);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st) {
+  const size_t n4 = n / 4, blocks = (n4 + 255) / 256;
+  sum_splits_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(reinterpret_cast<const float4*>(acc), splits,
+                                                                              n4, reinterpret_cast<uint2*>(out));
+  return cudaGetLastError();
+}
 
 // The vocabulary split of the (token tile x split) grid: the one that makes
 // waves x (tiles per CTA + 1) smallest for `slots` resident CTAs, i.e. the
@@ -729,13 +792,12 @@ cudaError_t launch_lce_bwd(int N, int V, int D, const void* hidden, const void* 
     if (dhead) {
       CUtensorMap tA;
       if (!tmap_bf16_2d_sw128_pitch(&tA, dzt, N, kc, L.ld_dzt, 128)) return cudaErrorInvalidValue;
-      GemmParams gp{};
+      GemmCall gp{};
       gp.M = kc;
       gp.N = D;
       gp.K = N;
       gp.mode = kStoreBf16;
       gp.c = static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D;
-      gp.ldc = D;
       gp.status = status;
       if ((e = launch_gemm(tA, tHb, gp, st)) != cudaSuccess) return e;
     }
@@ -744,15 +806,13 @@ cudaError_t launch_lce_bwd(int N, int V, int D, const void* hidden, const void* 
     if (!tmap_bf16_2d_sw128_pitch(&tA, dz, kc, N, L.vc, 128) ||
         !tmap_bf16_2d_sw128(&tB, static_cast<const __nv_bfloat16*>(head) + (size_t)cv0 * D, D, kc, 64))
       return cudaErrorInvalidValue;
-    GemmParams gp{};
+    GemmCall gp{};
     gp.M = N;
     gp.N = D;
     gp.K = kc;
     gp.mode = L.chunks == 1 ? kStoreBf16 : c == 0 ? kAccInit : c == L.chunks - 1 ? kAccFinal : kAccAdd;
     gp.c = static_cast<__nv_bfloat16*>(dhidden);
-    gp.ldc = D;
     gp.acc = acc;
-    gp.ldacc = D;
     gp.status = status;
     if ((e = launch_gemm(tA, tB, gp, st)) != cudaSuccess) return e;
   }

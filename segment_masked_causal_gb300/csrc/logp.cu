@@ -1,0 +1,744 @@
+// logp.cu -- log probabilities of given tokens with entropy and the most
+// likely alternatives, and the gradient of the first two, straight from the
+// hidden states and the head: z = H W^T / T without storing the (N, V) logits.
+//
+//   lse_i  = ln sum_v exp(z_iv)          logp_i = z_i,t(i) - lse_i
+//   H_i    = lse_i - sum_v p_iv z_iv     p = exp(z - lse)
+//   dz_iv  = (g_i ([v = t(i)] - p_iv) - e_i p_iv (ln p_iv + H_i)) / T
+//
+// for L = sum_i g_i logp_i + e_i H_i. The backward forms the logits again
+// (as the fused cross-entropy beside it does, mlx-train-perf 0.5.1 README,
+// "The fused cross-entropy loss"), writes dz of a vocabulary chunk in bf16
+// and multiplies it out with the GEMM of lce.cu.
+//
+// Forward: one pass over the vocabulary. With m the running maximum of the
+// scaled logits in base 2 (t = z log2 e - m), a row keeps S = sum 2^t and
+// A = sum 2^t t, so that lse = ln 2 (m + log2 S) and H = ln 2 (log2 S - A / S):
+// A is a sum of terms that are all <= 0 and vanish at both ends, so nothing
+// cancels in it. A larger maximum m' = m + d turns (S, A) into
+// (S 2^-d, (A - d S) 2^-d).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/pa.h"
+#include "kernels.h"
+#include "sm103.cuh"
+#include "tmap.h"
+
+namespace pa {
+namespace {
+
+constexpr int kStages = 4;                 // 4 x 48 KB: one CTA per SM
+constexpr int kTok = 128;                  // tokens per CTA: the MMA's rows
+constexpr int kUnit = kLogpUnit;           // vocabulary rows of one unit: what splits are counted in
+constexpr int kTileUnits = 8;              // units per logit tile: 256 columns
+constexpr uint32_t kSliceH = kTok * 128;   // 128 x 64 bf16, 16 KB
+constexpr uint32_t kSliceU = kUnit * 128;  // 32 x 64 bf16, 4 KB
+constexpr uint32_t kStage = kSliceH + kTileUnits * kSliceU;
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 512;  // two 256-column fp32 accumulators
+constexpr uint32_t kSmem = 1024 /* misc */ + 1024 /* alignment */ + kStages * kStage;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Misc {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t fin;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct FwdParams {
+  int N, V, D, top;
+  int units_per_split, splits;
+  float sl2;  // log2(e) / temperature
+  const int32_t* targets;
+  float4* part;    // (splits, N) {m, S, A, the target's raw logit}
+  float* cand_z;   // (N, splits, top) raw logits, largest first
+  int32_t* cand_v; // (N, splits, top) their vocabulary rows, -1 for none
+  uint32_t* status;
+};
+
+struct BwdParams {
+  int N, V, D;
+  int vt_base, vt_end;  // the chunk's vocabulary tiles of 256 rows
+  float sl2, inv_t;
+  const int32_t* targets;
+  const float* lse;
+  const float* entropy;    // read where g_entropy is given
+  const float* g_logp;
+  const float* g_entropy;  // may be null
+  __nv_bfloat16* dz;       // (N, ld_dz)
+  int ld_dz;
+  __nv_bfloat16* dzt;      // (vc, ld_dzt), or null (frozen head)
+  int ld_dzt;
+  uint32_t* status;
+};
+
+// One logit tile: 128 tokens from tile row tm, `units` x 32 vocabulary rows
+// from unit u.
+struct Tile {
+  int tm, u, units;
+};
+
+// Token tiles per group of the backward's order, token tile fastest: a
+// group's H stays in L2 while it walks the chunk's vocabulary tiles (the
+// cross-entropy backward measured 22.2 ms without groups, 21.0 with 32).
+constexpr int kGroup = 32;
+
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+  float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+#pragma unroll
+  for (int e = 2; e < 30; e += 4) {
+    a = fmax3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    b = fmax3(b, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+  }
+  return fmax3(a, b, fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+}
+
+// One 32-bit column of this thread's TMEM lane.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r)
+      : "r"(taddr)
+      : "memory");
+  return r;
+}
+
+__device__ __forceinline__ void setup(Misc& m) {
+  if (threadIdx.x == 0) {
+    m.abort_flag = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&m.full[s], 1);
+      mbar_init(&m.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&m.acc_full[b], 1);
+      mbar_init(&m.acc_empty[b], 128);
+    }
+    mbar_init(&m.fin, 1);
+    fence_mbar_init();
+  }
+  if ((threadIdx.x >> 5) == 1) {
+    tmem_alloc(&m.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+__device__ __forceinline__ void teardown(uint32_t tmem) {
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Warp 0, lane 0: 64-wide K slices of H and W through the ring. A whole tile
+// of W is one 256-row box, a shorter one its units one by one (eight-row
+// swizzle atoms, so the boxes' layouts join).
+template <class TileOf>
+__device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* ring, const CUtensorMap* tmH,
+                                           const CUtensorMap* tmW, const CUtensorMap* tmWu, int nt, int KS,
+                                           TileOf tile_of) {
+  prefetch_tmap(tmH);
+  prefetch_tmap(tmW);
+  prefetch_tmap(tmWu);
+  int it = 0;
+  bool ok = true;
+  for (int j = 0; ok && j < nt; ++j) {
+    const Tile t = tile_of(j);
+    for (int kc = 0; kc < KS; ++kc, ++it) {
+      const int st = it % kStages;
+      if (!g.wait(&m.empty[st], ((it / kStages) & 1) ^ 1, 50)) { ok = false; break; }
+      uint8_t* sh = ring + st * kStage;
+      mbar_expect_tx(&m.full[st], kSliceH + t.units * kSliceU);
+      tma_load_2d(sh, tmH, &m.full[st], kc * 64, t.tm * kTok);
+      if (t.units == kTileUnits) {
+        tma_load_2d(sh + kSliceH, tmW, &m.full[st], kc * 64, t.u * kUnit);
+      } else {
+        for (int x = 0; x < t.units; ++x)
+          tma_load_2d(sh + kSliceH + x * kSliceU, tmWu, &m.full[st], kc * 64, (t.u + x) * kUnit);
+      }
+    }
+  }
+  // no copy may still be landing when the CTA exits
+  for (int i = (it > kStages ? it - kStages : 0); i < it; ++i) g.drain(&m.full[i % kStages], (i / kStages) & 1);
+}
+
+// Warp 1: the tile's products into accumulator j mod 2. The whole warp runs
+// the loop and the waits; lane 0 issues.
+template <class TileOf>
+__device__ __forceinline__ void multiply_tiles(Misc& m, const Guard& g, uint32_t sRing, uint32_t tmem, int nt, int KS,
+                                               TileOf tile_of) {
+  const bool leader = (threadIdx.x & 31) == 0;
+  bool ok = true;
+  int it = 0;
+  for (int j = 0; ok && j < nt; ++j) {
+    const int buf = j & 1;
+    const uint32_t id = idesc_bf16_f32(128, tile_of(j).units * kUnit, false, false);
+    if (j >= 2 && !g.wait_warp(&m.acc_empty[buf], ((j - 2) >> 1) & 1, 51)) { ok = false; break; }
+    tc_fence_after();
+    for (int kc = 0; kc < KS; ++kc, ++it) {
+      const int st = it % kStages;
+      if (!g.wait_warp(&m.full[st], (it / kStages) & 1, 52)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t hd = sdesc_sw128(sRing + st * kStage, 16, 1024);
+      const uint64_t wd = sdesc_sw128(sRing + st * kStage + kSliceH, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (leader)
+          umma_bf16(tmem + buf * 256, sdesc_add(hd, kk * 32), sdesc_add(wd, kk * 32), id, (kc > 0 || kk > 0) ? 1u : 0u);
+      if (leader) umma_commit(&m.empty[st]);
+      __syncwarp();
+    }
+    if (ok && leader) umma_commit(&m.acc_full[buf]);
+    __syncwarp();
+  }
+  if (leader) {
+    umma_commit(&m.fin);  // every MMA issued has completed once this arrives
+    g.drain(&m.fin, 0);
+  }
+  __syncwarp();
+}
+
+// Put (v, id) into a list that runs from the largest down, behind every entry
+// that is not smaller: with ids coming in increasing order, equal values keep
+// the lower id first. v = -inf leaves the list as it is.
+template <int KM>
+__device__ __forceinline__ void insert(float (&z)[KM], int (&id)[KM], float v, int vid) {
+#pragma unroll
+  for (int p = KM - 1; p > 0; --p) {
+    id[p] = v > z[p - 1] ? id[p - 1] : (v > z[p] ? vid : id[p]);
+    z[p] = fmaxf(z[p], fminf(z[p - 1], v));
+  }
+  id[0] = v > z[0] ? vid : id[0];
+  z[0] = fmaxf(z[0], v);
+}
+
+// Forward. CTA (token tile blockIdx.x, split blockIdx.y) walks its split's
+// units in tiles of eight; the epilogue warps hold one token per thread. The
+// alternatives are kept in registers, KM slots of which the first KM - top are
+// filled with +inf, so that the smallest kept value is always in the last
+// slot: a 32-column chunk whose maximum does not beat it is done with one
+// comparison. Where some lane's does, the warp walks the columns that any
+// lane wants (one ballot) and reads each again from TMEM, because a register
+// array cannot be indexed at run time.
+template <int KM>
+__global__ void __launch_bounds__(kThreads, 1)
+    logp_fwd_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmWu, const FwdParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Misc& m = *reinterpret_cast<Misc*>(smem_raw);
+  uint8_t* ring =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int U = (p.V + kUnit - 1) / kUnit;
+  const int u0 = (int)blockIdx.y * p.units_per_split, u1 = min(u0 + p.units_per_split, U);
+  const int nt = (u1 - u0 + kTileUnits - 1) / kTileUnits;  // >= 1 by construction of the grid
+  const int KS = p.D / 64;
+  const Guard g{&m.abort_flag, p.status};
+  const auto tile_of = [&](int j) {
+    const int u = u0 + j * kTileUnits;
+    return Tile{(int)blockIdx.x, u, min(kTileUnits, u1 - u)};
+  };
+  setup(m);
+  const uint32_t tmem = m.tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, tile_of);
+    __syncwarp();
+  } else if (warp == 1) {
+    multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    const int row0 = (int)blockIdx.x * kTok + quarter * 32, token = row0 + lane;
+    const bool live = token < p.N, any = row0 < p.N;
+    const int t = live ? p.targets[token] : -1;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    constexpr int KL = KM > 0 ? KM : 1;
+    float tz[KL];
+    int ti[KL];
+#pragma unroll
+    for (int k = 0; k < KL; ++k) {
+      tz[k] = k < KM - p.top ? INFINITY : -INFINITY;
+      ti[k] = -1;
+    }
+    float m_run = -INFINITY, s_run = 0.f, a_run = 0.f, tgt = 0.f;
+    const uint64_t sl2 = f2(p.sl2, p.sl2);
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      const int buf = j & 1;
+      ok = __all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 53));
+      if (!ok) break;
+      tc_fence_after();
+      const Tile tl = tile_of(j);
+      if (any) {
+#pragma unroll 1
+        for (int c = 0; c < tl.units; ++c) {
+          uint32_t a[32];
+          const uint32_t col = tmem + lane_base + buf * 256 + c * 32;
+          tmem_ld32(col, a);
+          const int vc = (tl.u + c) * kUnit;
+          if (vc + 32 > p.V) {  // rows past the vocabulary
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (vc + i >= p.V) a[i] = __float_as_uint(-INFINITY);
+          }
+          const float cmax = max32(a);
+          // a row with nothing but -inf so far: the shift is 0, and S and A stay 0
+          const float m_new = fmaxf(m_run, cmax * p.sl2);
+          const float shift = m_new > -INFINITY ? m_new : 0.f;
+          const uint64_t off = f2(-shift, -shift);
+          uint64_t s2 = 0ull, a2 = 0ull;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 x = f2_split(fma2(f2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), sl2, off));
+            const uint64_t e = f2(ex2(x.x), ex2(x.y));
+            s2 = add2(s2, e);
+            // 2^t t -> 0 as t -> -inf: a finite factor keeps 0 * inf out (2^-30000 is 0)
+            a2 = fma2(e, f2(fmaxf(x.x, -30000.f), fmaxf(x.y, -30000.f)), a2);
+          }
+          const float2 ss = f2_split(s2), aa = f2_split(a2);
+          const float d = m_run > -INFINITY ? m_run - shift : 0.f, sc = ex2(d);
+          a_run = fmaf(fmaf(d, s_run, a_run), sc, aa.x + aa.y);
+          s_run = fmaf(s_run, sc, ss.x + ss.y);
+          m_run = m_new;
+          if (t >= vc && t < vc + 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (t == vc + i) tgt = __uint_as_float(a[i]);
+          }
+          if (KM > 0) {
+            const float least = tz[KL - 1];
+            if (__any_sync(~0u, live && cmax > least)) {
+              uint32_t want = 0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (live && __uint_as_float(a[i]) > least) want |= 1u << i;
+              for (uint32_t u = __reduce_or_sync(~0u, want); u; u &= u - 1) {
+                const int i = __ffs(u) - 1;
+                const float z = __uint_as_float(tmem_ld1(col + i));
+                insert<KL>(tz, ti, (want >> i) & 1u ? z : -INFINITY, vc + i);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&m.acc_empty[buf]);
+    }
+    if (ok && live) {
+      p.part[(size_t)blockIdx.y * p.N + token] = make_float4(m_run, s_run, a_run, tgt);
+      if (KM > 0) {
+        const size_t o = ((size_t)token * p.splits + blockIdx.y) * p.top;
+#pragma unroll
+        for (int k = 0; k < KL; ++k) {
+          const int at = k - (KM - p.top);
+          if (at >= 0) {
+            p.cand_z[o + at] = tz[k];
+            p.cand_v[o + at] = ti[k];
+          }
+        }
+      }
+    }
+  }
+  teardown(tmem);
+}
+
+// Bits of a float in an unsigned order, both zeros alike; > 0 for every number.
+__device__ __forceinline__ uint32_t ordered(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One warp per token: the splits' (m, S, A) in a fixed tree, then `top` rounds
+// that each take the largest head of the splits' lists (lowest id first among
+// equals), with the lists in shared memory. Each lane owns the splits
+// lane, lane + 32, ....
+constexpr int kListsPerLane = (kLogpMaxSplits + 31) / 32;
+__global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, float* __restrict__ logp,
+                                                         float* __restrict__ lse, float* __restrict__ entropy,
+                                                         int32_t* __restrict__ top_ids, float* __restrict__ top_logp) {
+  extern __shared__ float2 lists[];  // per warp: splits x top {logit, id}
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int token = blockIdx.x * warps + (threadIdx.x >> 5);
+  if (token >= p.N) return;
+  const int n = p.splits * p.top;
+  float2* mine = lists + (size_t)(threadIdx.x >> 5) * n;
+  for (int i = lane; i < n; i += 32)
+    mine[i] = make_float2(p.cand_z[(size_t)token * n + i], __int_as_float(p.cand_v[(size_t)token * n + i]));
+  float4 q[kListsPerLane];
+  float M = -INFINITY;
+#pragma unroll
+  for (int l = 0; l < kListsPerLane; ++l) {
+    const int s = lane + 32 * l;
+    q[l] = s < p.splits ? p.part[(size_t)s * p.N + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    M = fmaxf(M, q[l].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+  float S = 0.f, A = 0.f;
+#pragma unroll
+  for (int l = 0; l < kListsPerLane; ++l) {
+    const float d = q[l].x > -INFINITY ? q[l].x - M : 0.f, sc = exp2f(d);
+    S = fmaf(q[l].y, sc, S);
+    A = fmaf(fmaf(d, q[l].y, q[l].z), sc, A);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    S += __shfl_xor_sync(~0u, S, o);
+    A += __shfl_xor_sync(~0u, A, o);
+  }
+  // From the logit and not from lse: a likely token's log probability is a
+  // small difference, and M's own rounding is in S as well, so it cancels here.
+  const float l2 = log2f(S), ls = kLn2 * (M + l2);
+  const auto log_p = [&](float z) { return kLn2 * (fmaf(z, p.sl2, -M) - l2); };
+  if (lane == 0) {
+    const int t = p.targets[token];
+    float lp = 0.f;
+    if (t >= 0 && t < p.V)
+      lp = log_p(p.part[(size_t)(t / kUnit / p.units_per_split) * p.N + token].w);
+    const float h = kLn2 * (l2 - A / S);
+    logp[token] = lp;
+    lse[token] = ls;
+    entropy[token] = h < 0.f ? 0.f : h;  // rounding below the least entropy there is; NaN stays
+  }
+  if (p.top == 0) return;
+  __syncwarp();
+  int pos[kListsPerLane] = {};
+  uint32_t key[kListsPerLane];
+  const auto head = [&](int l) {  // 0: the list is at its end
+    const int s = lane + 32 * l;
+    if (s >= p.splits || pos[l] >= p.top) return 0u;
+    const float2 x = mine[s * p.top + pos[l]];
+    return __float_as_int(x.y) < 0 ? 0u : ordered(x.x);
+  };
+#pragma unroll
+  for (int l = 0; l < kListsPerLane; ++l) key[l] = head(l);
+  for (int k = 0; k < p.top; ++k) {
+    uint32_t best = 0;
+    int bl = 0;
+#pragma unroll
+    for (int l = 0; l < kListsPerLane; ++l)
+      if (key[l] > best) {  // the lower split of a lane's equal heads holds the lower ids
+        best = key[l];
+        bl = l;
+      }
+    float2 x = make_float2(-INFINITY, __int_as_float(-1));
+#pragma unroll
+    for (int l = 0; l < kListsPerLane; ++l)
+      if (l == bl && best > 0) x = mine[(lane + 32 * l) * p.top + pos[l]];
+    const uint32_t most = __reduce_max_sync(~0u, best);
+    const uint32_t id = best == most && best > 0 ? (uint32_t)__float_as_int(x.y) : 0xFFFFFFFFu;
+    const uint32_t low = __reduce_min_sync(~0u, id);
+    if (most == 0) {  // fewer logits above -inf than asked for
+      if (lane == 0) {
+        top_ids[(size_t)token * p.top + k] = -1;
+        top_logp[(size_t)token * p.top + k] = -INFINITY;
+      }
+      continue;
+    }
+    if (id == low) {  // one lane: ids differ
+      top_ids[(size_t)token * p.top + k] = (int32_t)low;
+      top_logp[(size_t)token * p.top + k] = log_p(x.x);
+#pragma unroll
+      for (int l = 0; l < kListsPerLane; ++l)
+        if (l == bl) {
+          ++pos[l];
+          key[l] = head(l);
+        }
+    }
+    __syncwarp();
+  }
+}
+
+// Backward, one chunk of the vocabulary: one CTA per SM over the chunk's
+// (token tile, vocabulary tile) pairs. Each recomputed logit becomes
+//   dz = p (cA + cB log2 p) + [v = t] g / T,
+//   cA = -(g + e H) / T,  cB = -e ln 2 / T,
+// exactly 0 in rows without a gradient and in columns past V. dz is rounded
+// to bf16, the operand type of the two products that follow (at most
+// 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
+__global__ void __launch_bounds__(kThreads, 1)
+    logp_dz_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+                   const BwdParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Misc& m = *reinterpret_cast<Misc*>(smem_raw);
+  uint8_t* ring =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TM = (p.N + kTok - 1) / kTok, VT = p.vt_end - p.vt_base;
+  const int nt = (TM * VT - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int KS = p.D / 64;
+  const Guard g{&m.abort_flag, p.status};
+  const auto tile_of = [&](int j) {
+    const int q = (int)blockIdx.x + j * (int)gridDim.x;
+    const int gi = q / (kGroup * VT), r = q - gi * kGroup * VT;
+    const int g0 = gi * kGroup, gs = min(kGroup, TM - g0);
+    return Tile{g0 + r % gs, (p.vt_base + r / gs) * kTileUnits, kTileUnits};
+  };
+  setup(m);
+  const uint32_t tmem = m.tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmW, nt, KS, tile_of);
+    __syncwarp();
+  } else if (warp == 1) {
+    multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    for (int j = 0; j < nt; ++j) {
+      const int buf = j & 1;
+      const Tile tl = tile_of(j);
+      const int token = tl.tm * kTok + quarter * 32 + lane;
+      const bool live = token < p.N;
+      const int t = live ? p.targets[token] : -1;
+      const float gl = live && t >= 0 && t < p.V ? p.g_logp[token] : 0.f;
+      const float ge = live && p.g_entropy ? p.g_entropy[token] : 0.f;
+      const bool use = gl != 0.f || ge != 0.f;
+      const float cA = -p.inv_t * (ge != 0.f ? fmaf(ge, p.entropy[token], gl) : gl), cB = -p.inv_t * ge * kLn2;
+      const float one = p.inv_t * gl, l2 = use ? p.lse[token] * kLog2e : 0.f;
+      if (!__all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 54))) break;
+      tc_fence_after();
+      const int v0 = tl.u * kUnit, c0v = v0 - p.vt_base * 256;  // column of v0 in the chunk
+#pragma unroll 1
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        uint32_t a[32];
+        tmem_ld32(tmem + lane_base + buf * 256 + c0, a);
+        const int vc = v0 + c0;
+        float d[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float x = fmaf(__uint_as_float(a[i]), p.sl2, -l2);
+          d[i] = ex2(x) * fmaf(cB, fmaxf(x, -30000.f), cA);
+        }
+        if (t >= vc && t < vc + 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (t == vc + i) d[i] += one;
+        }
+        if (!use || vc + 32 > p.V) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!use || vc + i >= p.V) d[i] = 0.f;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+        if (live) {
+          __nv_bfloat16* row = p.dz + (size_t)token * p.ld_dz + c0v + c0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (vc + 8 * u < p.V)
+              *reinterpret_cast<uint4*>(row + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+          if (p.dzt) {
+            __nv_bfloat16* colp = p.dzt + (size_t)(c0v + c0) * p.ld_dzt + token;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (vc + i < p.V)
+                colp[(size_t)i * p.ld_dzt] =
+                    __ushort_as_bfloat16((unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu));
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&m.acc_empty[buf]);
+    }
+  }
+  teardown(tmem);
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      sms <= 0)
+    sms = 152;
+  return sms;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// Most splits of the vocabulary: each at least one unit, and no more CTAs in
+// all than about sixteen a SM.
+int logp_max_splits(int N, int V) {
+  const int TM = (N + kTok - 1) / kTok, U = (V + kUnit - 1) / kUnit;
+  int s = 2432 / TM;
+  if (s > kLogpMaxSplits) s = kLogpMaxSplits;
+  if (s > U) s = U;
+  return s < 1 ? 1 : s;
+}
+
+// The split that makes waves x (units per CTA + 8) smallest: a CTA's pipeline
+// fill and last epilogue take about as long as one tile of eight units.
+LceSplit logp_split(int N, int V, int slots) {
+  const int TM = (N + kTok - 1) / kTok, U = (V + kUnit - 1) / kUnit;
+  LceSplit best{1, U};
+  long long best_cost = -1;
+  for (int s = 1, most = logp_max_splits(N, V); s <= most; ++s) {
+    const int per = (U + s - 1) / s, used = (U + per - 1) / per;
+    const long long waves = ((long long)TM * used + slots - 1) / slots, cost = waves * (per + kTileUnits);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = LceSplit{used, per};
+    }
+  }
+  return best;
+}
+
+LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
+  const size_t rows = (size_t)logp_max_splits(N, V) * N;
+  LogpFwdLayout L;
+  L.part = 256;
+  L.cand_z = L.part + up256(rows * sizeof(float4));
+  L.cand_v = L.cand_z + up256(rows * top * 4);
+  L.bytes = L.cand_v + up256(rows * top * 4);
+  return L;
+}
+
+cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, const void* hidden, const void* head,
+                            const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
+                            float* top_logp, void* ws, cudaStream_t st) {
+  const LceSplit sp = logp_split(N, V, sm_count());
+  const LogpFwdLayout L = logp_fwd_layout(N, V, top);
+  CUtensorMap tH, tW, tWu;
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) ||
+      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit))
+    return cudaErrorInvalidValue;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  FwdParams p{};
+  p.N = N;
+  p.V = V;
+  p.D = D;
+  p.top = top;
+  p.units_per_split = sp.per;
+  p.splits = sp.splits;
+  p.sl2 = kLog2e / temperature;
+  p.targets = targets;
+  p.part = reinterpret_cast<float4*>(w + L.part);
+  p.cand_z = reinterpret_cast<float*>(w + L.cand_z);
+  p.cand_v = reinterpret_cast<int32_t*>(w + L.cand_v);
+  p.status = reinterpret_cast<uint32_t*>(w);
+  const auto kfn = top == 0 ? logp_fwd_kernel<0> : top <= 8 ? logp_fwd_kernel<8> : logp_fwd_kernel<kLogpMaxTop>;
+  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kfn<<<dim3((N + kTok - 1) / kTok, sp.splits), kThreads, kSmem, st>>>(tH, tW, tWu, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // as many tokens a block as 40 KB of lists hold, 8 at most
+  const size_t lists = (size_t)sp.splits * top * sizeof(float2);
+  int warps = 8;
+  while (warps > 1 && warps * lists > 40960) --warps;
+  logp_merge_kernel<<<(N + warps - 1) / warps, 32 * warps, warps * lists, st>>>(p, logp, lse, entropy, top_ids,
+                                                                                top_logp);
+  return cudaGetLastError();
+}
+
+LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
+  LogpBwdLayout L;
+  // dz and dz^T of one chunk: at most 128 MiB each (L2 holds about one of
+  // them), in whole vocabulary tiles
+  const long long vmax = (long long)(V + 255) / 256 * 256;
+  long long vc = (1ll << 26) / N / 256 * 256;
+  if (vc > vmax) vc = vmax;
+  if (vc < 256) vc = 256;
+  L.vc = (int)vc;
+  L.chunks = (V + L.vc - 1) / L.vc;
+  L.ld_dzt = (N + 63) / 64 * 64;
+  L.splits = gemm_splits(N, D, L.vc < V ? L.vc : V, 152);
+  L.acc = 256;
+  L.dz = L.acc + (L.chunks > 1 || L.splits > 1 ? up256((size_t)L.splits * N * D * 4) : 0);
+  L.dzt = L.dz + up256((size_t)N * L.vc * 2);
+  L.bytes = L.dzt + up256((size_t)L.vc * L.ld_dzt * 2);
+  return L;
+}
+
+cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* hidden, const void* head,
+                            const int32_t* targets, const float* lse, const float* entropy, const float* g_logp,
+                            const float* g_entropy, void* dhidden, void* dhead, void* ws, cudaStream_t st) {
+  const LogpBwdLayout L = logp_bwd_layout(N, V, D);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint32_t* status = reinterpret_cast<uint32_t*>(w);
+  __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(w + L.dz);
+  __nv_bfloat16* dzt = reinterpret_cast<__nv_bfloat16*>(w + L.dzt);
+  float* acc = reinterpret_cast<float*>(w + L.acc);
+  CUtensorMap tH, tW, tHb;
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) ||
+      !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(logp_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count(), TM = (N + kTok - 1) / kTok;
+  for (int c = 0; c < L.chunks; ++c) {
+    const int cv0 = c * L.vc, kc = V - cv0 < L.vc ? V - cv0 : L.vc;  // the chunk's vocabulary rows
+    BwdParams p{};
+    p.N = N;
+    p.V = V;
+    p.D = D;
+    p.vt_base = cv0 / 256;
+    p.vt_end = (cv0 + kc + 255) / 256;
+    p.sl2 = kLog2e / temperature;
+    p.inv_t = 1.f / temperature;
+    p.targets = targets;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.g_logp = g_logp;
+    p.g_entropy = g_entropy;
+    p.dz = dz;
+    p.ld_dz = L.vc;
+    p.dzt = dhead ? dzt : nullptr;
+    p.ld_dzt = L.ld_dzt;
+    p.status = status;
+    const long long pairs = (long long)TM * (p.vt_end - p.vt_base);
+    logp_dz_kernel<<<pairs < sms ? (int)pairs : sms, kThreads, kSmem, st>>>(tH, tW, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // dW rows of the chunk = dz^T H (the tokens are the contraction)
+    if (dhead) {
+      CUtensorMap tA;
+      if (!tmap_bf16_2d_sw128_pitch(&tA, dzt, N, kc, L.ld_dzt, 128)) return cudaErrorInvalidValue;
+      GemmCall gc{};
+      gc.M = kc;
+      gc.N = D;
+      gc.K = N;
+      gc.mode = kStoreBf16;
+      gc.c = static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D;
+      gc.status = status;
+      if ((e = launch_gemm(tA, tHb, gc, st)) != cudaSuccess) return e;
+    }
+    // dH += dz W[chunk] (the chunk's vocabulary rows are the contraction),
+    // the contraction cut into L.splits runs with an accumulator each
+    CUtensorMap tA, tB;
+    if (!tmap_bf16_2d_sw128_pitch(&tA, dz, kc, N, L.vc, 128) ||
+        !tmap_bf16_2d_sw128(&tB, static_cast<const __nv_bfloat16*>(head) + (size_t)cv0 * D, D, kc, 64))
+      return cudaErrorInvalidValue;
+    GemmCall gc{};
+    gc.M = N;
+    gc.N = D;
+    gc.K = kc;
+    gc.splits = L.splits;
+    if (L.splits > 1)
+      gc.mode = c == 0 ? kAccInit : kAccAdd;
+    else
+      gc.mode = L.chunks == 1 ? kStoreBf16 : c == 0 ? kAccInit : c == L.chunks - 1 ? kAccFinal : kAccAdd;
+    gc.c = static_cast<__nv_bfloat16*>(dhidden);
+    gc.acc = acc;
+    gc.status = status;
+    if ((e = launch_gemm(tA, tB, gc, st)) != cudaSuccess) return e;
+  }
+  if (L.splits > 1) return launch_sum_splits(acc, L.splits, (size_t)N * D, static_cast<__nv_bfloat16*>(dhidden), st);
+  return cudaSuccess;
+}
+
+}  // namespace pa

@@ -1,0 +1,358 @@
+"""Token log probabilities on the GPU against the fp64 oracle.
+
+Hidden states and head lie on grids (multiples of 1/8 and of a power of two),
+so that every logit is exact in fp32 whatever the order of its sum: the
+alternatives' order, ties included, has to be the oracle's, and the
+tolerances below count only what the epilogue does.
+
+With Z = max |z| (after the temperature) in nats:
+  t = z log2 e - m    the factor log2(e)/T is off by 2^-24, the fused product
+                      rounds once: |dt| <= 2^-24 (1.45 Z) + 2^-24 (2 * 1.45 Z)
+  2^t                 2^-22 from the exponential, so each term is within
+                      r = ln 2 * |dt| + 2^-22 of itself
+  S                   a split's sum runs over at most V / 32 chunk sums, each
+                      of 16 pairwise-packed terms: 2^-24 (V / 32 + 32) more
+so lse is within r + 2^-24 (V / 32 + 32) plus a few roundings of itself, logp
+adds one of the logit's, and the entropy, whose sum takes |t| <= L = H + ln V
++ 1 in the mean, within (2 + L) times that."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import segment_masked_causal_gb300 as pa
+import synth
+from oracle import logprobs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from segment_masked_causal_gb300 import build
+    build.build()
+
+
+def grid(seed, stream, shape, most, step):
+    """Uniform integers in [-most, most] times step, fp64."""
+    u = synth.uint64s(seed, stream, int(np.prod(shape)))
+    return ((u % np.uint64(2 * most + 1)).astype(np.float64) - most).reshape(shape) * step
+
+
+def inputs(N, V, D, seed):
+    H = grid(seed, 60, (N, D), 15, 1 / 8)  # std 1.1
+    W = grid(seed, 61, (V, D), 15, 2.0 ** -round(math.log2(4 * math.sqrt(D))))  # logits of std 2 to 4
+    t = (synth.uint64s(seed, 62, N) % np.uint64(V)).astype(np.int32)
+    if N > 3:
+        t[1], t[3] = -1, V  # not scored
+    return H, W, t
+
+
+def dev_bf16(x, dev):
+    b = torch.from_numpy(np.ascontiguousarray(x)).to(torch.bfloat16)
+    assert (b.double().numpy() == x).all() or not np.isfinite(x).all()
+    return b.to(dev)
+
+
+def run(H, W, t, dev, T=1.0, top=0):
+    h, w, tt = dev_bf16(H, dev), dev_bf16(W, dev), torch.from_numpy(t).to(dev)
+    ws = torch.empty(pa.pa_logp_workspace_bytes(h.shape[0], w.shape[0], h.shape[1], top), dtype=torch.uint8, device=dev)
+    got = pa.token_logprobs_forward(h, w, tt, temperature=T, top=top, ws=ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    return [None if g is None else g.cpu().numpy() for g in got]
+
+
+def check(got, want, V, Z):
+    logp, lse, ent, ids, alt = (None if g is None else g.astype(np.float64) for g in got)
+    e_logp, e_lse, e_ent, e_ids, e_alt = want
+    u = 2.0 ** -24
+    r = 3 * 1.45 * Z * u + 4 * u + u * (V / 32 + 32)
+    bar = r + 4 * u * (np.abs(e_lse) + Z)
+    for g, e, n in ((logp, e_logp, "logp"), (lse, e_lse, "lse")):
+        err = np.abs(g - e)
+        print(f"{n}: max err {err.max():.2e} of {bar.min():.2e}")
+        assert (err <= bar).all(), n
+    L = e_ent + math.log(V) + 1
+    err = np.abs(ent - e_ent)
+    print(f"entropy: max err {err.max():.2e}, relative to its bar {(err / (bar * (2 + L))).max():.2e}")
+    assert (err <= bar * (2 + L)).all() and (ent >= 0).all()
+    if ids is not None:
+        assert (ids == e_ids).all()
+        assert (np.abs(alt - e_alt) <= bar[:, None]).all()
+
+
+CASES = [
+    # one token and few; every row an alternative; a vocabulary of one and of
+    # part of a unit; ragged everything over many splits; several token tiles;
+    # the 32-slot and the 8-slot lists; the ring wraps
+    (1, 33, 64, 1, 1.0), (1, 1000, 128, 5, 1.0), (3, 32, 64, 32, 1.0), (5, 8, 64, 8, 0.5), (2, 1, 64, 1, 1.0),
+    (128, 31, 64, 3, 1.0), (130, 1003, 192, 8, 0.7), (300, 5000, 256, 20, 1.3), (257, 2049, 64, 0, 1.0),
+    (33, 20011, 1024, 9, 1.0), (1, 40000, 512, 32, 1.0), (1000, 700, 640, 2, 2.0),
+]
+
+
+@pytest.mark.parametrize("N,V,D,top,T", CASES)
+def test_forward_matches_oracle(N, V, D, top, T, cuda_dev):
+    H, W, t = inputs(N, V, D, 7 * N + V)
+    got = run(H, W, t, cuda_dev, T, top)
+    want = logprobs.forward(H, W, t, T, top)
+    if top == 0:
+        assert got[3] is None and got[4] is None
+    check(got, want, V, np.abs(H @ W.T).max() / T)
+
+
+def test_ties_and_uniform_logits(cuda_dev):
+    """Zero states make every logit equal: the lowest rows win, the entropy is
+    ln V. Rows of the head that repeat tie exactly."""
+    N, V, D = 40, 3001, 64
+    H, W, t = inputs(N, V, D, 5)
+    H[:7] = 0
+    W[2000:] = W[:1001]
+    for top in (6, 32):
+        got = run(H, W, t, cuda_dev, 1.0, top)
+        assert (got[3][:7] == np.arange(top)).all()
+        check(got, logprobs.forward(H, W, t, 1.0, top), V, np.abs(H @ W.T).max())
+
+
+def test_a_sure_token(cuda_dev):
+    """One logit far above the rest: logp is the little that the others add,
+    the entropy is tiny and not negative."""
+    N, V, D = 3, 500, 64
+    H, W = np.zeros((N, D)), np.zeros((V, D))
+    H[0, 0], H[1, 0], H[2, 0] = 8, 16, 120
+    W[77, 0] = 1
+    got = run(H, W, np.array([77, 77, 77], np.int32), cuda_dev, 1.0, 2)
+    want = logprobs.forward(H, W, [77] * 3, 1.0, 2)
+    check(got, want, V, 120)
+    assert (got[3] == [[77, 0]] * 3).all()
+    # with 500 exp(-120) beside it S is 1 within half a step of fp32: log2 S and t
+    # are off by 2^-23 together
+    assert abs(got[2][2]) <= 2.0 ** -22 and abs(got[0][2]) <= 2.0 ** -22
+
+
+def test_infinities_and_nan_stay_in_their_rows(cuda_dev):
+    N, V, D = 6, 300, 64
+    H, W, t = inputs(N, V, D, 9)
+    H[:, 0] = 1
+    clean = run(H, W, t, cuda_dev, 1.0, 4)
+    H2 = H.copy()
+    H2[2, 5] = np.nan
+    got = run(H2, W, t, cuda_dev, 1.0, 4)
+    others = [0, 1, 3, 4, 5]
+    for g, c in zip(got, clean):
+        assert (g[others] == c[others]).all()
+    assert np.isnan(got[1][2]) and np.isnan(got[2][2]) and (got[3][2] == -1).all() and (got[4][2] == -np.inf).all()
+    # logits of -inf: no alternatives, nothing to the sums; a scored one has logp -inf
+    W2 = np.zeros_like(W)
+    W2[:, 1] = W[:, 1]
+    W2[10:, 0] = -np.inf
+    H3 = np.zeros_like(H)
+    H3[:, :2] = np.abs(H[:, :2]) + 1 / 8
+    H3[:, 2:] = 0
+    # columns of zeros times -inf rows would be NaN: only column 0 is infinite there
+    t3 = np.array([0, 1, 9, 10, 299, -1], np.int32)
+    got = run(H3, W2, t3, cuda_dev, 1.0, 16)
+    want = logprobs.forward(H3, W2[:10], np.where(t3 < 10, t3, -1), 1.0, 10)
+    assert (got[3][:, :10] == want[3]).all() and (got[3][:, 10:] == -1).all() and (got[4][:, 10:] == -np.inf).all()
+    assert np.abs(got[1] - want[1]).max() < 1e-5 and np.abs(got[2] - want[2]).max() < 1e-5
+    assert (got[0][[3, 4]] == -np.inf).all() and got[0][5] == 0
+
+
+def test_the_same_bits_again_and_in_a_graph(cuda_dev):
+    """Two calls, a call on another stream, and a captured call replayed on
+    new inputs give the same bits; two graphs keep workspaces of their own."""
+    N, V, D, top = 70, 4000, 256, 8
+    sets = [[dev_bf16(x, cuda_dev) for x in inputs(N, V, D, s)[:2]] + [torch.from_numpy(inputs(N, V, D, s)[2]).to(cuda_dev)]
+            for s in (1, 2)]
+    want = [pa.token_logprobs_forward(*s, top=top) for s in sets]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        again = pa.token_logprobs_forward(*sets[0], top=top)
+    side.synchronize()
+    for a, b in zip(again, want[0]):
+        assert torch.equal(a, b)
+    static = [x.clone() for x in sets[0]]
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = pa.token_logprobs_forward(*static, top=top)
+        graphs.append((g, out))
+    for s, w in ((1, want[1]), (0, want[0])):
+        for x, y in zip(static, sets[s]):
+            x.copy_(y)
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            for a, b in zip(out, w):
+                assert torch.equal(a, b)
+
+
+def test_one_token_is_a_row_of_many(cuda_dev):
+    """A token scored alone gives what it gives in a batch, within the bars."""
+    N, V, D = 200, 9001, 128
+    H, W, t = inputs(N, V, D, 12)
+    want = logprobs.forward(H, W, t, 1.0, 5)
+    for i in (0, 1, 199):
+        check(run(H[i:i + 1], W, t[i:i + 1], cuda_dev, 1.0, 5), [x[i:i + 1] for x in want], V, np.abs(H @ W.T).max())
+
+
+# ------------------------------------------------------------------ backward
+# bf16 keeps 8 significant bits: in [1, 2) its step is 2^-7, so a rounding is off
+# by at most half of that, 2^-8 of the value. dz is rounded to bf16 and the
+# gradient to bf16 again; the fp32 sums between are far more exact. So an
+# element of the gradient is within 2^-8 sum |dz||w| + 2^-8 |gradient| of the
+# exact one. Over a tensor the roundings have random signs and are spread
+# evenly over the half steps (1 / sqrt(3) of the largest, and 1 / 1.4 for the
+# mean place in [1, 2)): 1.6e-3 of the norm for each of the two, 2.3e-3
+# together, so 2^-8 = 3.9e-3 is the bar for the norm.
+BWD = [
+    (1, 33, 64, True, True, 1.0), (2, 1, 64, True, True, 1.0), (5, 1000, 128, True, True, 0.7),
+    (130, 1003, 192, True, True, 1.3), (300, 5000, 256, True, False, 1.0), (300, 5000, 256, False, True, 1.0),
+    (96, 32003, 128, True, True, 1.0), (4500, 17000, 64, True, True, 1.0), (257, 130, 1088, True, True, 2.0),
+]
+
+
+def bwd(H, W, t, g, e, dev, T, head):
+    h, w, tt = dev_bf16(H, dev), dev_bf16(W, dev), torch.from_numpy(t).to(dev)
+    _, lse, ent, _, _ = pa.token_logprobs_forward(h, w, tt, temperature=T)
+    f = lambda x: None if x is None else torch.from_numpy(x.astype(np.float32)).to(dev)
+    ws = torch.empty(pa.pa_logp_bwd_workspace_bytes(h.shape[0], w.shape[0], h.shape[1]), dtype=torch.uint8, device=dev)
+    got = pa.token_logprobs_backward(h, w, tt, lse, ent, f(g), f(e), temperature=T, train_head=head, ws=ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    return [None if x is None else x.float().cpu().numpy().astype(np.float64) for x in got]
+
+
+def upstream(N, t, V, seed, entropy):
+    g = synth.normals(seed, 63, N).astype(np.float32).astype(np.float64)
+    e = 0.5 * synth.normals(seed, 64, N).astype(np.float32).astype(np.float64) if entropy else None
+    return g, None if e is None else e.astype(np.float32).astype(np.float64)
+
+
+def check_grads(got, H, W, t, g, e, T):
+    N, V = H.shape[0], W.shape[0]
+    z = H @ W.T / T
+    lp = z - z.max(1, keepdims=True)
+    lp -= np.log(np.exp(lp).sum(1, keepdims=True))
+    p = np.exp(lp)
+    gs = np.where((t >= 0) & (t < V), g, 0)
+    dz = -gs[:, None] * p
+    ok = gs != 0
+    dz[np.arange(N)[ok], t[ok]] += gs[ok]
+    # what dz is made of before its terms cancel bounds its own error (2e-5 of it)
+    size = np.abs(gs)[:, None] * p
+    size[np.arange(N)[ok], t[ok]] += np.abs(gs[ok])
+    if e is not None:
+        ent = -(p * lp).sum(1, keepdims=True)
+        dz -= e[:, None] * p * (lp + ent)
+        size += np.abs(e)[:, None] * p * (np.abs(lp) + ent)
+    dz, size = dz / T, size / T
+    for x, a, b, s, n in ((got[0], dz, W, size, "dH"), (got[1], dz.T, H, size.T, "dW")):
+        if x is None:
+            continue
+        exact = a @ b
+        norm = np.linalg.norm(exact)
+        rel = np.linalg.norm(x - exact) / norm if norm else np.abs(x).max()
+        bound = 2.0 ** -8 * (np.abs(a) @ np.abs(b)) + 2e-5 * (s @ np.abs(b)) + 2.0 ** -8 * np.abs(exact)
+        worst = (np.abs(x - exact) / np.maximum(bound, 1e-30)).max()
+        print(f"{n}: relL2 {rel:.2e}, worst element {worst:.2f} of its bound")
+        assert worst <= 1.01, n
+        if x.size > 1000:
+            assert rel <= 2.0 ** -8, n
+
+
+@pytest.mark.parametrize("N,V,D,head,entropy,T", BWD)
+def test_backward_matches_the_formula(N, V, D, head, entropy, T, cuda_dev):
+    H, W, t = inputs(N, V, D, 3 * N + V)
+    g, e = upstream(N, t, V, N, entropy)
+    if N > 6:
+        g[5], t[6] = 0, -1
+        if e is not None:
+            e[5] = e[6] = 0
+    got = bwd(H, W, t, g, e, cuda_dev, T, head)
+    assert (got[1] is None) == (not head)
+    check_grads(got, H, W, t, g, e, T)
+    if N > 6:
+        assert (got[0][5] == 0).all() and (got[0][6] == 0).all()  # no gradient, exactly
+
+
+def test_backward_matches_the_oracle_and_differences(cuda_dev):
+    """Against the oracle's gradient, and the change of the loss along it:
+    for a step s along the direction of the gradient itself the loss changes by
+    s |dH|^2 up to third order (1e-3 of it at this step)."""
+    N, V, D, T = 9, 64, 64, 0.8
+    H, W, t = inputs(N, V, D, 31)
+    g, e = upstream(N, t, V, 31, True)
+    dh, dw = bwd(H, W, t, g, e, cuda_dev, T, True)
+    eh, ew = logprobs.backward(H, W, t, g, e, T)
+    assert np.linalg.norm(dh - eh) <= 2.0 ** -8 * np.linalg.norm(eh)
+    assert np.linalg.norm(dw - ew) <= 2.0 ** -8 * np.linalg.norm(ew)
+
+    def loss(H, W):
+        logp, _, ent, _, _ = logprobs.forward(H, W, t, T)
+        return (g * logp + e * ent).sum()
+    for d, f in ((dh, lambda s: loss(H + s * dh, W)), (dw, lambda s: loss(H, W + s * dw))):
+        s = 1e-3 / np.linalg.norm(d)
+        slope = (f(s) - f(-s)) / (2 * s)
+        assert abs(slope / (d * d).sum() - 1) < 2.0 ** -7 + 1e-3
+
+
+def test_backward_frozen_head_bits_and_graph(cuda_dev):
+    """Without the head's gradient dhidden has the same bits; so does a second
+    call and a captured one replayed beside an eager one."""
+    N, V, D = 200, 9000, 128
+    H, W, t = inputs(N, V, D, 15)
+    h, w, tt = dev_bf16(H, cuda_dev), dev_bf16(W, cuda_dev), torch.from_numpy(t).to(cuda_dev)
+    _, lse, ent, _, _ = pa.token_logprobs_forward(h, w, tt)
+    g, e = (torch.from_numpy(x.astype(np.float32)).to(cuda_dev) for x in upstream(N, t, V, 4, True))
+    dh, dw = pa.token_logprobs_backward(h, w, tt, lse, ent, g, e)
+    dh2, none = pa.token_logprobs_backward(h, w, tt, lse, ent, g, e, train_head=False)
+    assert none is None and torch.equal(dh, dh2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gh, gw = pa.token_logprobs_backward(h, w, tt, lse, ent, g, e)
+    for _ in range(2):
+        gh.zero_()
+        gw.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(gh, dh) and torch.equal(gw, dw)
+
+
+def test_the_mean_nll_is_the_cross_entropys(cuda_dev):
+    """At temperature 1 logp is minus the cross-entropy's NLL, and its gradient
+    the cross-entropy's with the sign turned."""
+    N, V, D = 150, 2000, 128
+    H, W, t = inputs(N, V, D, 21)
+    h, w, tt = dev_bf16(H, cuda_dev), dev_bf16(W, cuda_dev), torch.from_numpy(t).to(cuda_dev)
+    nll, lse_x, _ = pa.linear_cross_entropy_forward(h, w, tt)
+    logp, lse, ent, _, _ = pa.token_logprobs_forward(h, w, tt)
+    assert (logp + nll).abs().max() < 2e-5 and (lse - lse_x).abs().max() < 2e-5
+    g = torch.full((N,), 1.0 / N, device=cuda_dev)
+    a = pa.linear_cross_entropy_backward(h, w, tt, lse_x, g)
+    b = pa.token_logprobs_backward(h, w, tt, lse, ent, -g)
+    for x, y in zip(a, b):
+        # each is within 2^-8 of the exact gradient
+        assert (x.float() - y.float()).norm() <= 2.0 ** -7 * x.float().norm()
+
+
+def test_refused_shapes_and_devices(cuda_dev):
+    h, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=cuda_dev), torch.zeros(9, 64, dtype=torch.bfloat16, device=cuda_dev)
+    t = torch.zeros(4, dtype=torch.int32, device=cuda_dev)
+    with pytest.raises(ValueError):
+        pa.token_logprobs_forward(h.float(), w, t)
+    with pytest.raises(ValueError):
+        pa.token_logprobs_forward(h, w, t.long())
+    with pytest.raises(ValueError):
+        pa.token_logprobs_forward(h, w.cpu(), t)
+    with pytest.raises(ValueError):
+        pa.token_logprobs_forward(h.t().contiguous().t(), w, t)
+    with pytest.raises(pa.PAError):
+        pa.token_logprobs_forward(h, w, t, temperature=0.0)
+    with pytest.raises(pa.PAError):
+        pa.token_logprobs_forward(h, w, t, ws=torch.empty(64, dtype=torch.uint8, device=cuda_dev))
