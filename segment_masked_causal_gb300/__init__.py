@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +78,8 @@ _lock = threading.Lock()
 def lib():
     """The loaded libpa.so (ctypes), with argument types declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -135,10 +138,10 @@ def lib():
             L.pa_logp_bwd_workspace_bytes.restype = S
             L.pa_logp_bwd.argtypes = [I32, I32, I32, F, P, P, P, P, P, P, P, P, P, P, S, P]
             L.pa_logp_bwd.restype = ctypes.c_int
-            CT, CK = ctypes.POINTER(pa_ckpt_tensor), ctypes.POINTER(pa_ckpt)
-            L.pa_ckpt_save.argtypes = [I32, CT, I32, I32, I32, P]
+            CK = ctypes.POINTER(pa_ckpt)
+            L.pa_ckpt_save.argtypes = [I32, P, I32, I32, I32, P]  # an array of pa_ckpt_tensor, or its bytes
             L.pa_ckpt_save.restype = ctypes.c_int
-            L.pa_ckpt_load.argtypes = [I32, CT, I32, I32, I32, P]
+            L.pa_ckpt_load.argtypes = [I32, P, I32, I32, I32, P]
             L.pa_ckpt_load.restype = ctypes.c_int
             L.pa_bwd_ckpt_workspace_bytes.argtypes = [D]
             L.pa_bwd_ckpt_workspace_bytes.restype = S
@@ -177,7 +180,9 @@ def _ptr(t, dtype=None, name=""):
 def _stream(stream):
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the same stream without building a Stream object (3 us of a launch-bound call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -565,7 +570,7 @@ def _on_current_device(*ts):
     import torch
     at = torch.cuda.current_device()
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != at):
+        if t is not None and t.get_device() != at:  # -1 for a CPU tensor
             raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at}), got one on {t.device}")
 
 
@@ -703,38 +708,39 @@ def _ckpt_format(dtype):
     raise ValueError(f"codes must be int8 or float8_e4m3fn, got {dtype}")
 
 
-def _ckpt_tensor(x, c):
-    """The C description of tensor x (1 to 4 dims, last contiguous) and checkpoint c."""
-    if not 1 <= x.dim() <= 4 or (x.shape[-1] > 1 and x.stride(-1) != 1):
-        raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
-    pad = 4 - x.dim()
-    B, H, N, C = (1,) * pad + tuple(x.shape)
-    sb, sh, sn = ((0,) * pad + tuple(x.stride()))[:3]
-    _want(c.codes, x.shape, "codes")
-    return pa_ckpt_tensor(x.data_ptr(), _ptr(c.codes, None, "codes"), _ptr(c.scales, _torch().float32, "scales"), B, H, N,
-                          C, sb, sh, sn)
-
-
-def _torch():
-    import torch
-    return torch
+_CKPT_FIELDS = "PPPiiiiqqq"  # pa_ckpt_tensor
 
 
 def _ckpt_call(fn, xs, cs, stream):
-    """pa_ckpt_save or pa_ckpt_load of matching lists, PA_CKPT_MAX_TENSORS a launch."""
+    """pa_ckpt_save or pa_ckpt_load of matching lists, PA_CKPT_MAX_TENSORS a
+    launch. Each tensor has 1 to 4 dims, the last contiguous."""
+    import torch
+    if len(xs) != len(cs):
+        raise ValueError("one checkpoint per tensor")
     if not xs:
         return
-    first = cs[0]
-    _, io = _io_dtype(xs[0])
-    fmt = _ckpt_format(first.codes.dtype)
+    dtype, kind, block = xs[0].dtype, cs[0].codes.dtype, cs[0].block
+    io, fmt, f32, at = _io_dtype(xs[0])[1], _ckpt_format(kind), torch.float32, torch.cuda.current_device()
+    fields = []
     for x, c in zip(xs, cs):
-        if x.dtype != xs[0].dtype or c.codes.dtype != first.codes.dtype or c.block != first.block:
+        codes, scales = c.codes, c.scales
+        shape, stride = x.shape, x.stride()
+        n = len(shape)
+        if x.dtype != dtype or codes.dtype != kind or c.block != block:
             raise ValueError("the tensors of one call share their type, format and block")
-        _on_current_device(x, c.codes, c.scales)
+        if not 1 <= n <= 4 or (stride[-1] != 1 and shape[-1] > 1):
+            raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
+        if codes.shape != shape:
+            raise ValueError(f"codes must be {tuple(shape)}, got {tuple(codes.shape)}")
+        if not (x.get_device() == codes.get_device() == scales.get_device() == at):
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+        if not codes.is_contiguous() or not scales.is_contiguous() or scales.dtype != f32:
+            raise ValueError("codes and scales must be contiguous, scales float32")
+        fields += (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *(1,) * (4 - n), *shape, *(0,) * (4 - n), *stride[:-1])
     st = _stream(stream)
     for i in range(0, len(xs), PA_CKPT_MAX_TENSORS):
-        part = [_ckpt_tensor(x, c) for x, c in zip(xs[i:i + PA_CKPT_MAX_TENSORS], cs[i:i + PA_CKPT_MAX_TENSORS])]
-        _check(fn(len(part), (pa_ckpt_tensor * len(part))(*part), io, fmt, first.block, st))
+        n = min(PA_CKPT_MAX_TENSORS, len(xs) - i)
+        _check(fn(n, struct.pack(_CKPT_FIELDS * n, *fields[10 * i:10 * (i + n)]), io, fmt, block, st))
 
 
 def pa_ckpt_save(tensors, checkpoints, stream=None):
@@ -753,13 +759,19 @@ def checkpoint_save(tensors, format="int8", block=64):
     of 8). format "int8" or "e4m3"; one scale per `block` elements of the
     last dim (32, 64 or 128). One launch for up to eight tensors."""
     import torch
-    kinds = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
-    if format not in kinds:
-        raise ValueError(f"format must be one of {sorted(kinds)}, got {format!r}")
-    tensors = list(tensors)
-    kept = [Checkpoint(torch.empty(x.shape, dtype=kinds[format], device=x.device),
-                       torch.empty(x.shape[:-1] + (-(-x.shape[-1] // block),), dtype=torch.float32, device=x.device),
-                       block, x.dtype) for x in tensors]
+    if format not in ("int8", "e4m3"):
+        raise ValueError(f"format must be int8 or e4m3, got {format!r}")
+    if block not in (32, 64, 128):
+        raise ValueError(f"block must be 32, 64 or 128, got {block}")
+    tensors, kept = list(tensors), []
+    kind, f32, empty = torch.int8 if format == "int8" else torch.float8_e4m3fn, torch.float32, torch.empty
+    for x in tensors:
+        shape, dev, c = x.shape, x.device, object.__new__(Checkpoint)
+        if not shape:
+            raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
+        c.codes, c.block, c.dtype = empty(shape, dtype=kind, device=dev), block, x.dtype
+        c.scales = empty((*shape[:-1], -(-shape[-1] // block)), dtype=f32, device=dev)
+        kept.append(c)
     pa_ckpt_save(tensors, kept)
     return kept
 
@@ -768,12 +780,8 @@ def checkpoint_load(checkpoints, out=None):
     """The checkpoints' values as contiguous tensors of their dtypes, or into
     the tensors `out` (any strides with the last dim contiguous)."""
     import torch
-    checkpoints = list(checkpoints)
-    if out is None:
-        out = [torch.empty(c.codes.shape, dtype=c.dtype, device=c.codes.device) for c in checkpoints]
-    out = list(out)
-    if len(out) != len(checkpoints):
-        raise ValueError("out must have one tensor per checkpoint")
+    checkpoints, empty = list(checkpoints), torch.empty
+    out = [empty(c.codes.shape, dtype=c.dtype, device=c.codes.device) for c in checkpoints] if out is None else list(out)
     pa_ckpt_load(out, checkpoints)
     return out
 

@@ -627,7 +627,6 @@ pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_
   pa_status why = device_ok();
   if (why != PA_OK) return why;
   const cudaStream_t st = cu(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return PA_ERR_CUDA;
   return pa::launch_logp_fwd(N, V, D, temperature, top, hidden, head, targets, logp, lse, entropy, top_ids, top_logp,
                              ws, st) == cudaSuccess
              ? PA_OK

@@ -9,9 +9,14 @@
 // and codes 0, so that all of it comes back as NaN instead of hiding the fault.
 //
 // All of it is bound by memory: 3 bytes an element in bf16 either way, 1/G of
-// a float for the scale. A thread takes vectors of 8 elements (16-byte loads
-// of bf16, 8-byte stores of codes), four of them at a time so that enough
-// loads are in flight, and a block's G / 8 lanes share its maximum by shuffles.
+// a float for the scale. A thread takes vectors of 16 elements (a 32-byte load
+// of bf16, a 16-byte store of codes) where every row is a whole number of
+// blocks without gaps and the tensor starts on 32 bytes, else of 8, with
+// several loads in flight, and a block's lanes share its maximum by shuffles.
+// What a block needs once (its scale, the reciprocal) is computed by every lane
+// that holds a part of it, so longer vectors also mean fewer instructions: saving
+// 8192 x 4096 bf16 as int8 took 25.6 us with vectors of 8 and 18.4 us with vectors
+// of 16 (5.6 TB/s), loading it 19.5 and 13.3 us.
 //
 // The rounding is exact without a division per element: q = x * (1 / s) is
 // within 2^-23 of x / s relatively, so only a quotient that lies that close
@@ -24,11 +29,16 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm103.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kCkptThreads = 256, kCkptUnroll = 4;
+constexpr int kCkptThreads = 256;
+// Vectors in flight per thread, in a save and in a load.
+template <int VEC>
+constexpr int kUnroll = VEC == 16 ? 2 : 4;
+constexpr int kLoadUnroll = 4;
 
 // n / d for n < 2^31 as a product (Granlund and Montgomery, "Division by
 // invariant integers using multiplication", 1994): q = (mulhi(m, n) + n) >> s.
@@ -47,7 +57,7 @@ struct Tensor {
   void* codes;
   float* scales;
   uint32_t blocks0;     // thread blocks of the tensors before this one
-  uint32_t vecs;        // vectors in all (save: short blocks filled up to G / 8 vectors)
+  uint32_t vecs;        // vectors in all (save: short blocks filled up to G elements)
   uint32_t rows;
   int C;                // elements per row
   int nb;               // blocks of G per row
@@ -66,65 +76,109 @@ __device__ __forceinline__ size_t row_offset(const Tensor& t, uint32_t row) {
   return (size_t)b * t.sb + (size_t)h * t.sh + (size_t)n * t.sn;
 }
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// Eight elements as they lie in memory, their largest magnitude as the bits
-// of an fp32 value (NaN and infinity order above every number), and as fp32.
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 w;
-  __device__ __forceinline__ void load(const void* p, size_t e) {
-    w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + e));
-  }
-  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ uint32_t top() const {
-    constexpr uint32_t k = 0x7FFF7FFFu;
-    const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
-    return max(m << 16, m & 0xFFFF0000u);
-  }
-  __device__ __forceinline__ void floats(float (&f)[8]) const {
-    f[0] = bf_lo(w.x), f[1] = bf_hi(w.x), f[2] = bf_lo(w.y), f[3] = bf_hi(w.y);
-    f[4] = bf_lo(w.z), f[5] = bf_hi(w.z), f[6] = bf_lo(w.w), f[7] = bf_hi(w.w);
-  }
+// Where vector i of a tensor lies: its elements, its codes and its block's
+// scale (2^shift vectors a block). FLAT: rows without gaps or short blocks, so
+// that vector i is simply the elements from VEC i on.
+struct Place {
+  size_t x, code, scale;
+  bool on;
 };
-template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p, size_t e) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-    a = __ldg(s);
-    b = __ldg(s + 1);
+template <int VEC, bool FLAT, bool SAVE>
+__device__ __forceinline__ Place place_of(const Tensor& t, uint32_t i, int shift) {
+  Place p;
+  if (FLAT) {
+    p.on = i < t.vecs;
+    p.x = p.code = (size_t)i * VEC;
+    p.scale = i >> shift;
+  } else {
+    const uint32_t row = quot(i, t.row_vecs), at = i - row * t.row_vecs.d;
+    p.on = i < t.vecs && (!SAVE || (int)at * VEC < t.C);  // a save counts short blocks as whole
+    p.x = row_offset(t, row) + at * VEC;
+    p.code = (size_t)row * t.C + at * VEC;
+    p.scale = (size_t)row * t.nb + (at >> shift);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ uint32_t top() const {
-    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t m = 0;
+  return p;
+}
+
+// 32 bytes of one lane in one access (aligned to them).
+__device__ __forceinline__ void ld_32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// VEC elements as they lie in memory, their largest magnitude as the bits of an
+// fp32 value (NaN and infinity order above every number), and as fp32.
+template <typename T, int VEC>
+struct Vec {
+  static constexpr int W = VEC * sizeof(T) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const void* base, size_t e) {
+    const T* p = static_cast<const T*>(base) + e;
+    if (VEC == 16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < W; i += 8) ld_32(reinterpret_cast<const uint32_t*>(p) + i, w + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* base, size_t e) const {
+    T* p = static_cast<T*>(base) + e;
+    if (VEC == 16) {
+#pragma unroll
+      for (int i = 0; i < W; i += 8) st_32(reinterpret_cast<uint32_t*>(p) + i, w + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+    if (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      return max(m << 16, m & 0xFFFF0000u);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
     return m;
   }
-  __device__ __forceinline__ void floats(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  // elements 8 part .. 8 part + 7
+  __device__ __forceinline__ void floats(int part, float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (sizeof(T) == 2) {
+        const uint32_t x = w[4 * part + i / 2];
+        f[i] = __uint_as_float(i & 1 ? x & 0xFFFF0000u : x << 16);
+      } else {
+        f[i] = __uint_as_float(w[(8 * part + i) % W]);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(int part, const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (sizeof(T) == 2) {
+        if (i & 1) w[4 * part + i / 2] = pack_bf16x2(f[i - 1], f[i]);
+      } else {
+        w[(8 * part + i) % W] = __float_as_uint(f[i]);
+      }
+    }
   }
 };
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, size_t e, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p + e) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, size_t e, const float (&f)[8]) {
-  float4* d = reinterpret_cast<float4*>(p + e);
-  d[0] = make_float4(f[0], f[1], f[2], f[3]);
-  d[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
 
 // ------------------------------------------------------------------- formats
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
@@ -148,21 +202,25 @@ struct Format;
 template <>
 struct Format<PA_CKPT_INT8> {
   static constexpr float kTop = 127.f;
-  // Codes of x[0..7], with r within 2^-23 of 1 / s and |x| r <= 127.5 or so.
+  // Codes of x[0..7], with r = 1 / s rounded: x r is within 2^-24 of x / s,
+  // relatively, and at most 127 (1 + 2^-23).
   static __device__ __forceinline__ uint2 encode(const float (&x)[8], float s, float r) {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the nearest integer
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the nearest integer
+    const uint64_t r2 = f2(r, r), magic2 = f2(kMagic, kMagic), minus1 = f2(-1.f, -1.f);
     uint32_t u[8];
-    bool near = false;
+    float far = 0.f;  // the largest distance of an x r from its code
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = fminf(fmaxf(x[i] * r, -127.f), 127.f), y = q + kMagic;
-      u[i] = __float_as_uint(y);
-      near |= fabsf(q - (y - kMagic)) > 0.4999f;  // q is off by 1.6e-5 at most
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t x2 = f2(x[i], x[i + 1]), y = fma2(x2, r2, magic2);
+      const float2 d = f2_split(fma2(x2, r2, fma2(y, minus1, magic2))), yy = f2_split(y);
+      u[i] = __float_as_uint(yy.x);
+      u[i + 1] = __float_as_uint(yy.y);
+      far = fmax3(far, fabsf(d.x), fabsf(d.y));
     }
-    if (near) {
+    if (far > 0.4999f) {  // x r is off by 127 * 2^-24 at most, and the distance by a rounding
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(x[i] * r, -127.f), 127.f), k = (q + kMagic) - kMagic, d = q - k;
+        const float k = fmaf(x[i], r, kMagic) - kMagic, d = fmaf(x[i], r, -k);
         if (fabsf(d) > 0.4999f) {
           const float up = d > 0.f ? 1.f : -1.f, side = up * fmaf(-(k + 0.5f * up), s, x[i]);
           const bool odd = __float_as_uint(k + kMagic) & 1u;
@@ -222,94 +280,125 @@ struct Format<PA_CKPT_E4M3> {
   }
 };
 
-__device__ __forceinline__ const Tensor& tensor_of(const Tensors& a, uint32_t block, uint32_t* first) {
+__device__ __forceinline__ const Tensor& tensor_of(const Tensors& a, uint32_t block, uint32_t per_block, uint32_t* first) {
   int i = 0;
   while (i + 1 < a.count && block >= a.t[i + 1].blocks0) ++i;
-  *first = (block - a.t[i].blocks0) * (kCkptThreads * kCkptUnroll);
+  *first = (block - a.t[i].blocks0) * per_block;
   return a.t[i];
 }
 
-// LG = G / 8 lanes hold one block.
-template <typename T, int FMT, int LG>
+// max / top, rounded correctly: a first quotient from the rounded reciprocal of
+// top, its remainder exactly, and one correction (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000", 1990). Below 2^-100 the
+// remainder could be lost, and the division is left to the compiler.
+template <int FMT>
+__device__ __forceinline__ float scale_of(float m) {
+  constexpr float kTop = Format<FMT>::kTop, kInv = 1.f / kTop;
+  if (m < 0x1p-100f) return __fdiv_rn(m, kTop);
+  const float q = m * kInv;
+  return fmaf(fmaf(-q, kTop, m), kInv, q);
+}
+
+// LG lanes hold one block of LG * VEC elements.
+template <typename T, int FMT, int VEC, int LG>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_save_kernel(const __grid_constant__ Tensors a) {
   using F = Format<FMT>;
+  constexpr int U = kUnroll<VEC>, kShift = LG == 2 ? 1 : LG == 4 ? 2 : LG == 8 ? 3 : 4;
   uint32_t first;
-  const Tensor& t = tensor_of(a, blockIdx.x, &first);
-  Vec8<T> v[kCkptUnroll];
-  uint32_t row[kCkptUnroll], at[kCkptUnroll];
-  bool on[kCkptUnroll];
+  const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * U, &first);
+  Vec<T, VEC> v[U];
+  Place at[U];
 #pragma unroll
-  for (int u = 0; u < kCkptUnroll; ++u) {
-    const uint32_t i = first + u * kCkptThreads + threadIdx.x;
-    row[u] = quot(i, t.row_vecs);
-    at[u] = i - row[u] * t.row_vecs.d;  // vector within the row, short blocks filled up
-    on[u] = i < t.vecs && (int)at[u] * 8 < t.C;
-    if (on[u])
-      v[u].load(t.x, row_offset(t, row[u]) + at[u] * 8);
+  for (int u = 0; u < U; ++u) {
+    at[u] = place_of<VEC, VEC == 16, true>(t, first + u * kCkptThreads + threadIdx.x, kShift);
+    if (at[u].on)
+      v[u].load(t.x, at[u].x);
     else
       v[u].zero();
   }
 #pragma unroll
-  for (int u = 0; u < kCkptUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     uint32_t m = v[u].top();
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-    if (!on[u]) continue;
+    if (!at[u].on) continue;
     const bool finite = m < 0x7F800000u;
-    float s = finite ? __fdiv_rn(__uint_as_float(m), F::kTop) : __uint_as_float(0x7FC00000u);
-    if (threadIdx.x % LG == 0) t.scales[(size_t)row[u] * t.nb + at[u] / LG] = s;
-    uint2 c = make_uint2(0u, 0u);
-    if (finite && s > 0.f) {
-      float f[8];
-      v[u].floats(f);
-      if (s < 0x1p-100f) {  // 1 / s could overflow: both by 2^100, which changes no bits of either
-        s *= 0x1p100f;
+    float s = finite ? scale_of<FMT>(__uint_as_float(m)) : __uint_as_float(0x7FC00000u);
+    if (threadIdx.x % LG == 0) t.scales[at[u].scale] = s;
+    uint2 c[VEC / 8];
+    const bool small = s < 0x1p-100f;
+    if (small) s *= 0x1p100f;  // 1 / s could overflow: both by 2^100, which changes no bits of either
+    const float r = __frcp_rn(s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= 0x1p100f;
+    for (int h = 0; h < VEC / 8; ++h) {
+      float f[8];
+      v[u].floats(h, f);
+      if (small) {
+        // a scale below the normal range has been rounded to few bits: quotients
+        // past the largest code are cut there
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i] * 0x1p100f, -F::kTop * s), F::kTop * s);
       }
-      c = F::encode(f, s, __frcp_rn(s));
+      c[h] = finite && s > 0.f ? F::encode(f, s, r) : make_uint2(0u, 0u);
     }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.codes) + (size_t)row[u] * t.C + at[u] * 8) = c;
+    uint8_t* out = static_cast<uint8_t*>(t.codes) + at[u].code;
+    if (VEC == 16)
+      *reinterpret_cast<uint4*>(out) = make_uint4(c[0].x, c[0].y, c[VEC / 8 - 1].x, c[VEC / 8 - 1].y);
+    else
+      *reinterpret_cast<uint2*>(out) = c[0];
   }
 }
 
-// Vectors first .. of one tensor: codes and scales to T. shift = log2(G / 8).
-template <typename T, int FMT>
+// Vectors first .. of one tensor: codes and scales to T. shift = log2 of the
+// vectors in a block.
+template <typename T, int FMT, int VEC>
 __device__ __forceinline__ void load_vectors(const Tensor& t, uint32_t first, int shift) {
   using F = Format<FMT>;
-  uint2 c[kCkptUnroll];
-  float s[kCkptUnroll];
-  uint32_t row[kCkptUnroll], at[kCkptUnroll];
-  bool on[kCkptUnroll];
+  constexpr int U = kLoadUnroll;
+  uint2 c[U][VEC / 8];
+  float s[U];
+  Place at[U];
 #pragma unroll
-  for (int u = 0; u < kCkptUnroll; ++u) {
-    const uint32_t i = first + u * kCkptThreads + threadIdx.x;
-    on[u] = i < t.vecs;
-    row[u] = quot(i, t.row_vecs);
-    at[u] = i - row[u] * t.row_vecs.d;
-    c[u] = make_uint2(0u, 0u);
+  for (int u = 0; u < U; ++u) {
+    at[u] = place_of<VEC, VEC == 16, false>(t, first + u * kCkptThreads + threadIdx.x, shift);
     s[u] = 0.f;
-    if (on[u]) {
-      c[u] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.codes) + (size_t)row[u] * t.C + at[u] * 8));
-      s[u] = __ldg(t.scales + (size_t)row[u] * t.nb + (at[u] >> shift));
+#pragma unroll
+    for (int h = 0; h < VEC / 8; ++h) c[u][h] = make_uint2(0u, 0u);
+    if (!at[u].on) continue;
+    const uint8_t* from = static_cast<const uint8_t*>(t.codes) + at[u].code;
+    if (VEC == 16) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(from));
+      c[u][0] = make_uint2(w.x, w.y);
+      c[u][VEC / 8 - 1] = make_uint2(w.z, w.w);
+    } else {
+      c[u][0] = __ldg(reinterpret_cast<const uint2*>(from));
     }
+    s[u] = __ldg(t.scales + at[u].scale);
   }
 #pragma unroll
-  for (int u = 0; u < kCkptUnroll; ++u) {
-    if (!on[u]) continue;
-    float f[8];
-    F::decode(c[u], f);
+  for (int u = 0; u < U; ++u) {
+    if (!at[u].on) continue;
+    Vec<T, VEC> v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= s[u];
-    store8(static_cast<T*>(const_cast<void*>(t.x)), row_offset(t, row[u]) + at[u] * 8, f);
+    for (int h = 0; h < VEC / 8; ++h) {
+      float f[8];
+      F::decode(c[u][h], f);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 y = f2_split(mul2(f2(f[i], f[i + 1]), f2(s[u], s[u])));
+        f[i] = y.x;
+        f[i + 1] = y.y;
+      }
+      v.set(h, f);
+    }
+    v.store(const_cast<void*>(t.x), at[u].x);
   }
 }
-
-template <typename T, int FMT>
+template <typename T, int FMT, int VEC>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_load_kernel(const __grid_constant__ Tensors a, int shift) {
   uint32_t first;
-  const Tensor& t = tensor_of(a, blockIdx.x, &first);
-  load_vectors<T, FMT>(t, first, shift);
+  const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * kLoadUnroll, &first);
+  load_vectors<T, FMT, VEC>(t, first, shift);
 }
 
 // Start of the attention backward from 8-bit tensors, in one launch: the
@@ -325,22 +414,22 @@ struct DeltaArgs {
   float* lse2;
   uint32_t rows;  // B * H * N, N padded to whole tiles
   FastDiv N, H;
-  int Nr, nb;
+  int Nr, nb, shift;   // shift: log2 of a block's groups of eight
   int64_t sb, sh, sn;  // of dout
 };
 constexpr int row_lanes(int D) { return D == 128 ? 16 : D == 64 ? 8 : 4; }  // divides D / 8 and a warp
 
-template <int D, int FMT>
+template <int D, int FMT, int VEC>
 __global__ void __launch_bounds__(kCkptThreads)
     bwd_ckpt_prologue_kernel(const __grid_constant__ Tensors a, uint32_t load_blocks, const DeltaArgs p, int shift) {
   if (blockIdx.x < load_blocks) {
     uint32_t first;
-    const Tensor& t = tensor_of(a, blockIdx.x, &first);
-    load_vectors<__nv_bfloat16, FMT>(t, first, shift);
+    const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * kLoadUnroll, &first);
+    load_vectors<__nv_bfloat16, FMT, VEC>(t, first, shift);
     return;
   }
   using F = Format<FMT>;
-  constexpr int VEC = D / 8, LPR = row_lanes(D), RPB = kCkptThreads / LPR;
+  constexpr int NV = D / 8, LPR = row_lanes(D), RPB = kCkptThreads / LPR;
   const uint32_t row = (blockIdx.x - load_blocks) * RPB + threadIdx.x / LPR;
   const int sub = threadIdx.x % LPR;
   const bool in = row < p.rows;
@@ -353,14 +442,14 @@ __global__ void __launch_bounds__(kCkptThreads)
   float acc = 0.f;
   if (live) {
 #pragma unroll
-    for (int v = sub; v < VEC; v += LPR) {
+    for (int v = sub; v < NV; v += LPR) {
       const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.codes + r * D) + v);
-      const float s = __ldg(p.scales + r * p.nb + (v >> shift));
-      Vec8<__nv_bfloat16> g;
+      const float s = __ldg(p.scales + r * p.nb + (v >> p.shift));
+      Vec<__nv_bfloat16, 8> g;
       g.load(dout, v * 8);
       float o[8], d[8];
       F::decode(c, o);
-      g.floats(d);
+      g.floats(0, d);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(o[i], d[i], sum);
@@ -375,8 +464,21 @@ __global__ void __launch_bounds__(kCkptThreads)
   }
 }
 
-// The tensors' descriptions; vectors per row counted with whole blocks for a save.
-uint32_t describe(const CkptTensor* x, int count, int G, bool save, Tensors* a) {
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// Whether all the tensors can be taken in vectors of 16 without looking at rows.
+bool all_flat(const CkptTensor* x, int count, int G) {
+  for (int i = 0; i < count; ++i) {
+    const bool contiguous = (x[i].N == 1 || x[i].s_n == x[i].C) && (x[i].H == 1 || x[i].s_h == (int64_t)x[i].N * x[i].C) &&
+                            (x[i].B == 1 || x[i].s_b == (int64_t)x[i].H * x[i].N * x[i].C);
+    if (!contiguous || x[i].C % G != 0 || !aligned32(x[i].x)) return false;
+  }
+  return true;
+}
+
+// The tensors' descriptions in vectors of VEC elements and thread blocks of
+// `per_block` vectors; a save counts short blocks as whole.
+uint32_t describe(const CkptTensor* x, int count, int G, int VEC, uint32_t per_block, bool save, Tensors* a) {
   uint32_t blocks = 0;
   a->count = count;
   for (int i = 0; i < count; ++i) {
@@ -387,7 +489,7 @@ uint32_t describe(const CkptTensor* x, int count, int G, bool save, Tensors* a) 
     t.blocks0 = blocks;
     t.C = x[i].C;
     t.nb = (x[i].C + G - 1) / G;
-    const uint32_t rv = save ? (uint32_t)t.nb * (G / 8) : (uint32_t)x[i].C / 8;
+    const uint32_t rv = save ? (uint32_t)t.nb * (G / VEC) : (uint32_t)x[i].C / VEC;
     t.rows = (uint32_t)((int64_t)x[i].B * x[i].H * x[i].N);
     t.vecs = t.rows * rv;
     t.row_vecs = fast_div(rv);
@@ -398,66 +500,74 @@ uint32_t describe(const CkptTensor* x, int count, int G, bool save, Tensors* a) 
     t.sn = x[i].s_n;
     t.contiguous = (x[i].N == 1 || t.sn == t.C) && (x[i].H == 1 || t.sh == (int64_t)x[i].N * t.C) &&
                    (x[i].B == 1 || t.sb == (int64_t)x[i].H * x[i].N * t.C);
-    blocks += (uint32_t)(((uint64_t)t.vecs + kCkptThreads * kCkptUnroll - 1) / (kCkptThreads * kCkptUnroll));
+    blocks += (uint32_t)(((uint64_t)t.vecs + per_block - 1) / per_block);
   }
   return blocks;
 }
-int lane_shift(int G) { return G == 32 ? 2 : G == 64 ? 3 : 4; }
+int log2_of(int n) { return n == 2 ? 1 : n == 4 ? 2 : n == 8 ? 3 : 4; }
 
-template <typename T, int FMT>
-void save_launch(const Tensors& a, uint32_t blocks, int G, cudaStream_t st) {
+template <typename T, int FMT, int VEC>
+void save_launch(const CkptTensor* x, int count, int G, cudaStream_t st) {
+  Tensors a{};
+  const uint32_t blocks = describe(x, count, G, VEC, kCkptThreads * kUnroll<VEC>, true, &a);
   if (G == 32)
-    ckpt_save_kernel<T, FMT, 4><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 32 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
   else if (G == 64)
-    ckpt_save_kernel<T, FMT, 8><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 64 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
   else
-    ckpt_save_kernel<T, FMT, 16><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 128 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
+}
+template <typename T>
+void save_any(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
+  if (all_flat(x, count, G))
+    format == PA_CKPT_INT8 ? save_launch<T, PA_CKPT_INT8, 16>(x, count, G, st) : save_launch<T, PA_CKPT_E4M3, 16>(x, count, G, st);
+  else
+    format == PA_CKPT_INT8 ? save_launch<T, PA_CKPT_INT8, 8>(x, count, G, st) : save_launch<T, PA_CKPT_E4M3, 8>(x, count, G, st);
 }
 
-template <int D>
-void prologue_launch(int format, const Tensors& a, uint32_t load_blocks, const DeltaArgs& d, int shift, cudaStream_t st) {
+template <typename T, int VEC>
+void load_launch(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
+  Tensors a{};
+  const uint32_t blocks = describe(x, count, G, VEC, kCkptThreads * kLoadUnroll, false, &a);
+  const int shift = log2_of(G / VEC);
+  if (format == PA_CKPT_INT8)
+    ckpt_load_kernel<T, PA_CKPT_INT8, VEC><<<blocks, kCkptThreads, 0, st>>>(a, shift);
+  else
+    ckpt_load_kernel<T, PA_CKPT_E4M3, VEC><<<blocks, kCkptThreads, 0, st>>>(a, shift);
+}
+template <typename T>
+void load_any(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
+  all_flat(x, count, G) ? load_launch<T, 16>(x, count, format, G, st) : load_launch<T, 8>(x, count, format, G, st);
+}
+
+template <int D, int VEC>
+void prologue_launch(const CkptTensor* qkv, int format, int G, const DeltaArgs& d, cudaStream_t st) {
+  Tensors a{};
+  const uint32_t load_blocks = describe(qkv, 3, G, VEC, kCkptThreads * kLoadUnroll, false, &a);
   constexpr int RPB = kCkptThreads / row_lanes(D);
   const uint32_t blocks = load_blocks + (d.rows + RPB - 1) / RPB;
+  const int shift = log2_of(G / VEC);
   if (format == PA_CKPT_INT8)
-    bwd_ckpt_prologue_kernel<D, PA_CKPT_INT8><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
+    bwd_ckpt_prologue_kernel<D, PA_CKPT_INT8, VEC><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
   else
-    bwd_ckpt_prologue_kernel<D, PA_CKPT_E4M3><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
+    bwd_ckpt_prologue_kernel<D, PA_CKPT_E4M3, VEC><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st) {
-  Tensors a{};
-  const uint32_t blocks = describe(x, count, block, true, &a);
-  if (f32)
-    format == PA_CKPT_INT8 ? save_launch<float, PA_CKPT_INT8>(a, blocks, block, st)
-                           : save_launch<float, PA_CKPT_E4M3>(a, blocks, block, st);
-  else
-    format == PA_CKPT_INT8 ? save_launch<__nv_bfloat16, PA_CKPT_INT8>(a, blocks, block, st)
-                           : save_launch<__nv_bfloat16, PA_CKPT_E4M3>(a, blocks, block, st);
+  f32 ? save_any<float>(x, count, format, block, st) : save_any<__nv_bfloat16>(x, count, format, block, st);
   return cudaGetLastError();
 }
 
 cudaError_t launch_ckpt_load(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st) {
-  Tensors a{};
-  const uint32_t blocks = describe(x, count, block, false, &a);
-  const int shift = lane_shift(block);
-  if (f32 && format == PA_CKPT_INT8)
-    ckpt_load_kernel<float, PA_CKPT_INT8><<<blocks, kCkptThreads, 0, st>>>(a, shift);
-  else if (f32)
-    ckpt_load_kernel<float, PA_CKPT_E4M3><<<blocks, kCkptThreads, 0, st>>>(a, shift);
-  else if (format == PA_CKPT_INT8)
-    ckpt_load_kernel<__nv_bfloat16, PA_CKPT_INT8><<<blocks, kCkptThreads, 0, st>>>(a, shift);
-  else
-    ckpt_load_kernel<__nv_bfloat16, PA_CKPT_E4M3><<<blocks, kCkptThreads, 0, st>>>(a, shift);
+  f32 ? load_any<float>(x, count, format, block, st) : load_any<__nv_bfloat16>(x, count, format, block, st);
   return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_ckpt_prologue(const AttnParams& p, int D, const RowStrides& rs, const CkptTensor (&qkv)[3],
                                      const void* out_codes, const float* out_scales, int format, int block,
                                      cudaStream_t st) {
-  Tensors a{};
-  const uint32_t load_blocks = describe(qkv, 3, block, false, &a);
   DeltaArgs d{};
   d.codes = static_cast<const uint8_t*>(out_codes);
   d.scales = out_scales;
@@ -470,16 +580,17 @@ cudaError_t launch_bwd_ckpt_prologue(const AttnParams& p, int D, const RowStride
   d.H = fast_div(p.Hq);
   d.Nr = p.Nr;
   d.nb = (D + block - 1) / block;
+  d.shift = log2_of(block / 8);
   d.sb = rs.q_b;
   d.sh = rs.q_h;
   d.sn = rs.q_n;
-  const int shift = lane_shift(block);
+  const bool flat = all_flat(qkv, 3, block);
   if (D == 64)
-    prologue_launch<64>(format, a, load_blocks, d, shift, st);
+    flat ? prologue_launch<64, 16>(qkv, format, block, d, st) : prologue_launch<64, 8>(qkv, format, block, d, st);
   else if (D == 96)
-    prologue_launch<96>(format, a, load_blocks, d, shift, st);
+    flat ? prologue_launch<96, 16>(qkv, format, block, d, st) : prologue_launch<96, 8>(qkv, format, block, d, st);
   else
-    prologue_launch<128>(format, a, load_blocks, d, shift, st);
+    flat ? prologue_launch<128, 16>(qkv, format, block, d, st) : prologue_launch<128, 8>(qkv, format, block, d, st);
   return cudaGetLastError();
 }
 

@@ -118,7 +118,7 @@ constexpr int kLogpMaxTop = 32;
 int logp_max_splits(int N, int V);
 LceSplit logp_split(int N, int V, int slots);
 struct LogpFwdLayout {
-  size_t part, cand_z, cand_v, bytes;  // after the 256-byte status region
+  size_t part, cand, bytes;  // after the 256-byte status region
 };
 LogpFwdLayout logp_fwd_layout(int N, int V, int top);
 cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, const void* hidden, const void* head,

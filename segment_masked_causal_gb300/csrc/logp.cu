@@ -55,11 +55,11 @@ struct Misc {
 struct FwdParams {
   int N, V, D, top;
   int units_per_split, splits;
+  int reps;   // 1, 2 or 4: how often the token tile's rows are repeated (see logp_fwd_kernel)
   float sl2;  // log2(e) / temperature
   const int32_t* targets;
   float4* part;    // (splits, N) {m, S, A, the target's raw logit}
-  float* cand_z;   // (N, splits, top) raw logits, largest first
-  int32_t* cand_v; // (N, splits, top) their vocabulary rows, -1 for none
+  float2* cand;    // (N, splits, top) {raw logit, vocabulary row or -1}, largest first
   uint32_t* status;
 };
 
@@ -144,12 +144,13 @@ __device__ __forceinline__ void teardown(uint32_t tmem) {
   }
 }
 
-// Warp 0, lane 0: 64-wide K slices of H and W through the ring. A whole tile
-// of W is one 256-row box, a shorter one its units one by one (eight-row
-// swizzle atoms, so the boxes' layouts join).
+// Warp 0, lane 0: 64-wide K slices of H and W through the ring. The tile's
+// tokens are one box of 128 / reps rows loaded `reps` times, one below the
+// other. A whole tile of W is one 256-row box, a shorter one its units one by
+// one (eight-row swizzle atoms, so the boxes' layouts join).
 template <class TileOf>
 __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* ring, const CUtensorMap* tmH,
-                                           const CUtensorMap* tmW, const CUtensorMap* tmWu, int nt, int KS,
+                                           const CUtensorMap* tmW, const CUtensorMap* tmWu, int nt, int KS, int reps,
                                            TileOf tile_of) {
   prefetch_tmap(tmH);
   prefetch_tmap(tmW);
@@ -163,7 +164,8 @@ __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* rin
       if (!g.wait(&m.empty[st], ((it / kStages) & 1) ^ 1, 50)) { ok = false; break; }
       uint8_t* sh = ring + st * kStage;
       mbar_expect_tx(&m.full[st], kSliceH + t.units * kSliceU);
-      tma_load_2d(sh, tmH, &m.full[st], kc * 64, t.tm * kTok);
+      for (int r = 0; r < reps; ++r)
+        tma_load_2d(sh + r * (kSliceH / reps), tmH, &m.full[st], kc * 64, t.tm * (kTok / reps));
       if (t.units == kTileUnits) {
         tma_load_2d(sh + kSliceH, tmW, &m.full[st], kc * 64, t.u * kUnit);
       } else {
@@ -226,6 +228,62 @@ __device__ __forceinline__ void insert(float (&z)[KM], int (&id)[KM], float v, i
   z[0] = fmaxf(z[0], v);
 }
 
+// What the epilogue warps leave for each other where they share tokens.
+struct Joint {
+  float4 sums[4][32];              // [quarter][lane] {m, S, A, the target's raw logit}
+  float2 top[4][kLogpMaxTop][32];  // [quarter][slot][lane] {raw logit, vocabulary row}
+};
+static_assert(sizeof(Joint) <= kStages * kStage, "fits the ring");
+
+// (m, S, A) of two disjoint sets of columns as that of both.
+__device__ __forceinline__ void join(float4& x, const float4& y) {
+  const float m = fmaxf(x.x, y.x);
+  const float dx = x.x > -INFINITY ? x.x - m : 0.f, dy = y.x > -INFINITY ? y.x - m : 0.f;
+  const float sx = ex2(dx), sy = ex2(dy);
+  x.z = fmaf(fmaf(dx, x.y, x.z), sx, fmaf(dy, y.y, y.z) * sy);
+  x.y = fmaf(x.y, sx, y.y * sy);
+  x.x = m;
+  x.w += y.w;  // 0 where the target lies in other columns
+}
+
+// The split's results of one token whose columns the warps quarter,
+// quarter + groups, ... have taken: the sums joined, the lists merged (among
+// equal logits the lower row first).
+template <int KL>
+__device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, int quarter, int lane, int groups,
+                                            int token, bool lists) {
+  float4 x = j.sums[quarter][lane];
+  for (int r = 1; r < p.reps; ++r) join(x, j.sums[quarter + r * groups][lane]);
+  p.part[(size_t)blockIdx.y * p.N + token] = x;
+  if (!lists) return;
+  const int first = KL - p.top;  // slots before it hold no candidates
+  float2 head[4];
+  int pos[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    pos[r] = first;
+    head[r] = r < p.reps ? j.top[quarter + r * groups][first][lane] : make_float2(-INFINITY, __int_as_float(-1));
+  }
+  float2* out = p.cand + ((size_t)token * p.splits + blockIdx.y) * p.top;
+  for (int k = 0; k < p.top; ++k) {
+    int best = 0;
+    float2 b = head[0];
+#pragma unroll
+    for (int r = 1; r < 4; ++r)
+      if (head[r].x > b.x || (head[r].x == b.x && (unsigned)__float_as_int(head[r].y) < (unsigned)__float_as_int(b.y))) {
+        b = head[r];
+        best = r;
+      }
+    out[k] = b;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r == best && ++pos[r] < KL)
+        head[r] = j.top[quarter + r * groups][pos[r]][lane];
+      else if (r == best)
+        head[r] = make_float2(-INFINITY, __int_as_float(-1));
+  }
+}
+
 // Forward. CTA (token tile blockIdx.x, split blockIdx.y) walks its split's
 // units in tiles of eight; the epilogue warps hold one token per thread. The
 // alternatives are kept in registers, KM slots of which the first KM - top are
@@ -234,6 +292,13 @@ __device__ __forceinline__ void insert(float (&z)[KM], int (&id)[KM], float v, i
 // comparison. Where some lane's does, the warp walks the columns that any
 // lane wants (one ballot) and reads each again from TMEM, because a register
 // array cannot be indexed at run time.
+//
+// A TMEM lane is read by one warp of the four alone, so with few tokens most
+// epilogue warps would have none. For N <= 64 (32) the tile holds the tokens'
+// rows twice (four times) instead of rows past N: the product costs the same,
+// and each warp takes every second (fourth) 32-column chunk of the tokens,
+// whose results the CTA joins through shared memory at the end. 17 tokens with
+// 20 alternatives at V 151,936, D 4096 took 217 us without and 206 us with it.
 template <int KM>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_fwd_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
@@ -252,17 +317,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u = u0 + j * kTileUnits;
     return Tile{(int)blockIdx.x, u, min(kTileUnits, u1 - u)};
   };
+  // The status word starts at 0: no wait can give up within 2 s of the launch.
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;
   setup(m);
+  // the merge may take its place on the SMs; it waits for this kernel's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, tile_of);
+    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, p.reps, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
   } else if (warp >= 4) {
     const int quarter = warp & 3;
-    const int row0 = (int)blockIdx.x * kTok + quarter * 32, token = row0 + lane;
+    const int groups = 4 / p.reps, share = quarter / groups;  // this warp's share of the columns
+    const int row0 = (int)blockIdx.x * (kTok / p.reps) + (quarter % groups) * 32, token = row0 + lane;
     const bool live = token < p.N, any = row0 < p.N;
     const int t = live ? p.targets[token] : -1;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -285,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile tl = tile_of(j);
       if (any) {
 #pragma unroll 1
-        for (int c = 0; c < tl.units; ++c) {
+        for (int c = share; c < tl.units; c += p.reps) {
           uint32_t a[32];
           const uint32_t col = tmem + lane_base + buf * 256 + c * 32;
           tmem_ld32(col, a);
@@ -338,17 +408,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&m.acc_empty[buf]);
     }
-    if (ok && live) {
+    if (p.reps > 1) {
+      // every product has completed and every copy been read: the ring is free
+      Joint* joint = reinterpret_cast<Joint*>(ring);
+      joint->sums[quarter][lane] = make_float4(m_run, s_run, a_run, tgt);
+      if (KM > 0) {
+#pragma unroll
+        for (int k = 0; k < KL; ++k) joint->top[quarter][k][lane] = make_float2(tz[k], __int_as_float(ti[k]));
+      }
+      named_bar_sync(1, 128);  // warps 4..7, whether their waits ended well or not
+      if (ok && live && share == 0) write_joint<KL>(p, *joint, quarter, lane, groups, token, KM > 0);
+    } else if (ok && live) {
       p.part[(size_t)blockIdx.y * p.N + token] = make_float4(m_run, s_run, a_run, tgt);
       if (KM > 0) {
         const size_t o = ((size_t)token * p.splits + blockIdx.y) * p.top;
 #pragma unroll
         for (int k = 0; k < KL; ++k) {
           const int at = k - (KM - p.top);
-          if (at >= 0) {
-            p.cand_z[o + at] = tz[k];
-            p.cand_v[o + at] = ti[k];
-          }
+          if (at >= 0) p.cand[o + at] = make_float2(tz[k], __int_as_float(ti[k]));
         }
       }
     }
@@ -362,30 +439,44 @@ __device__ __forceinline__ uint32_t ordered(float z) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One warp per token: the splits' (m, S, A) in a fixed tree, then `top` rounds
-// that each take the largest head of the splits' lists (lowest id first among
-// equals), with the lists in shared memory. Each lane owns the splits
-// lane, lane + 32, ....
+// The splits' results of a token: their (m, S, A) in a fixed tree, then `top`
+// rounds that each take the largest head of the splits' lists (lowest row first
+// among equals) from shared memory. One warp per token and eight tokens a
+// block, or, where tokens are few, a block per token (WPT = 8): reading the
+// lists is what takes the time, 3,000 entries for 20 alternatives of 149
+// splits, and eight warps have eight times the loads in flight. Each lane of
+// the token's first warp owns the splits lane, lane + 32, ....
 constexpr int kListsPerLane = (kLogpMaxSplits + 31) / 32;
+template <int WPT>
 __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, float* __restrict__ logp,
                                                          float* __restrict__ lse, float* __restrict__ entropy,
                                                          int32_t* __restrict__ top_ids, float* __restrict__ top_logp) {
-  extern __shared__ float2 lists[];  // per warp: splits x top {logit, id}
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int token = blockIdx.x * warps + (threadIdx.x >> 5);
-  if (token >= p.N) return;
+  extern __shared__ float2 lists[];  // per token: splits x top {logit, row}
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, tokens = (blockDim.x >> 5) / WPT, slot = (threadIdx.x >> 5) / WPT;
+  const int token = blockIdx.x * tokens + slot;
   const int n = p.splits * p.top;
-  float2* mine = lists + (size_t)(threadIdx.x >> 5) * n;
-  for (int i = lane; i < n; i += 32)
-    mine[i] = make_float2(p.cand_z[(size_t)token * n + i], __int_as_float(p.cand_v[(size_t)token * n + i]));
+  float2* mine = lists + (size_t)slot * n;
+  const bool first = (threadIdx.x >> 5) % WPT == 0;
   float4 q[kListsPerLane];
-  float M = -INFINITY;
 #pragma unroll
   for (int l = 0; l < kListsPerLane; ++l) {
     const int s = lane + 32 * l;
-    q[l] = s < p.splits ? p.part[(size_t)s * p.N + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    M = fmaxf(M, q[l].x);
+    q[l] = first && token < p.N && s < p.splits ? p.part[(size_t)s * p.N + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
   }
+  if (token < p.N) {
+    const float2* from = p.cand + (size_t)token * n;
+#pragma unroll 4
+    for (int i = threadIdx.x % (32 * WPT); i < n; i += 32 * WPT) mine[i] = from[i];
+  }
+  if (WPT > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+  if (token >= p.N || !first) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int l = 0; l < kListsPerLane; ++l) M = fmaxf(M, q[l].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
   float S = 0.f, A = 0.f;
@@ -407,15 +498,13 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
   if (lane == 0) {
     const int t = p.targets[token];
     float lp = 0.f;
-    if (t >= 0 && t < p.V)
-      lp = log_p(p.part[(size_t)(t / kUnit / p.units_per_split) * p.N + token].w);
+    if (t >= 0 && t < p.V) lp = log_p(p.part[(size_t)(t / kUnit / p.units_per_split) * p.N + token].w);
     const float h = kLn2 * (l2 - A / S);
     logp[token] = lp;
     lse[token] = ls;
     entropy[token] = h < 0.f ? 0.f : h;  // rounding below the least entropy there is; NaN stays
   }
   if (p.top == 0) return;
-  __syncwarp();
   int pos[kListsPerLane] = {};
   uint32_t key[kListsPerLane];
   const auto head = [&](int l) {  // 0: the list is at its end
@@ -428,20 +517,15 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
   for (int l = 0; l < kListsPerLane; ++l) key[l] = head(l);
   for (int k = 0; k < p.top; ++k) {
     uint32_t best = 0;
-    int bl = 0;
+    int at = 0, bl = 0;
 #pragma unroll
     for (int l = 0; l < kListsPerLane; ++l)
-      if (key[l] > best) {  // the lower split of a lane's equal heads holds the lower ids
+      if (key[l] > best) {  // the lower split of a lane's equal heads holds the lower rows
         best = key[l];
         bl = l;
+        at = (lane + 32 * l) * p.top + pos[l];
       }
-    float2 x = make_float2(-INFINITY, __int_as_float(-1));
-#pragma unroll
-    for (int l = 0; l < kListsPerLane; ++l)
-      if (l == bl && best > 0) x = mine[(lane + 32 * l) * p.top + pos[l]];
     const uint32_t most = __reduce_max_sync(~0u, best);
-    const uint32_t id = best == most && best > 0 ? (uint32_t)__float_as_int(x.y) : 0xFFFFFFFFu;
-    const uint32_t low = __reduce_min_sync(~0u, id);
     if (most == 0) {  // fewer logits above -inf than asked for
       if (lane == 0) {
         top_ids[(size_t)token * p.top + k] = -1;
@@ -449,7 +533,9 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
       }
       continue;
     }
-    if (id == low) {  // one lane: ids differ
+    const float2 x = best == most ? mine[at] : make_float2(0.f, __int_as_float(-1));
+    const uint32_t low = __reduce_min_sync(~0u, (uint32_t)__float_as_int(x.y));
+    if ((uint32_t)__float_as_int(x.y) == low) {  // one lane: rows differ
       top_ids[(size_t)token * p.top + k] = (int32_t)low;
       top_logp[(size_t)token * p.top + k] = log_p(x.x);
 #pragma unroll
@@ -492,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmW, nt, KS, tile_of);
+    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmW, nt, KS, 1, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
@@ -603,9 +689,8 @@ LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
   const size_t rows = (size_t)logp_max_splits(N, V) * N;
   LogpFwdLayout L;
   L.part = 256;
-  L.cand_z = L.part + up256(rows * sizeof(float4));
-  L.cand_v = L.cand_z + up256(rows * top * 4);
-  L.bytes = L.cand_v + up256(rows * top * 4);
+  L.cand = L.part + up256(rows * sizeof(float4));
+  L.bytes = L.cand + up256(rows * top * sizeof(float2));
   return L;
 }
 
@@ -615,11 +700,13 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   const LceSplit sp = logp_split(N, V, sm_count());
   const LogpFwdLayout L = logp_fwd_layout(N, V, top);
   CUtensorMap tH, tW, tWu;
-  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) ||
-      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit))
+  const int reps = N <= 32 ? 4 : N <= 64 ? 2 : 1;
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok / reps) ||
+      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) || !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit))
     return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(ws);
   FwdParams p{};
+  p.reps = reps;
   p.N = N;
   p.V = V;
   p.D = D;
@@ -629,21 +716,32 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   p.sl2 = kLog2e / temperature;
   p.targets = targets;
   p.part = reinterpret_cast<float4*>(w + L.part);
-  p.cand_z = reinterpret_cast<float*>(w + L.cand_z);
-  p.cand_v = reinterpret_cast<int32_t*>(w + L.cand_v);
+  p.cand = reinterpret_cast<float2*>(w + L.cand);
   p.status = reinterpret_cast<uint32_t*>(w);
   const auto kfn = top == 0 ? logp_fwd_kernel<0> : top <= 8 ? logp_fwd_kernel<8> : logp_fwd_kernel<kLogpMaxTop>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   kfn<<<dim3((N + kTok - 1) / kTok, sp.splits), kThreads, kSmem, st>>>(tH, tW, tWu, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // a block per token while that fills less than two rounds of the SMs; else
   // as many tokens a block as 40 KB of lists hold, 8 at most
   const size_t lists = (size_t)sp.splits * top * sizeof(float2);
+  const bool few = top > 0 && N <= 304;
   int warps = 8;
-  while (warps > 1 && warps * lists > 40960) --warps;
-  logp_merge_kernel<<<(N + warps - 1) / warps, 32 * warps, warps * lists, st>>>(p, logp, lse, entropy, top_ids,
-                                                                                top_logp);
-  return cudaGetLastError();
+  if (!few)
+    while (warps > 1 && warps * lists > 40960) --warps;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(few ? N : (N + warps - 1) / warps);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = few ? lists : warps * lists;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few ? logp_merge_kernel<8> : logp_merge_kernel<1>, p, logp, lse, entropy, top_ids,
+                            top_logp);
 }
 
 LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
