@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // a kernel launched programmatically behind this one may start on the SMs that this one leaves idle
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {

@@ -354,11 +354,13 @@ __global__ void __launch_bounds__(352, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::TMEM_COLS);
   }
+  // launched beside the kernel ahead of it, this one ends no earlier (else there is nothing to wait for)
+  if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, int DM = D>
 cudaError_t launch_dq_d(const AttnParams& p, int Dio, const RowStrides& rs, const void* q, const void* k, const void* v,
-                        const void* dout, cudaStream_t st, const RowStrides& in) {
+                        const void* dout, cudaStream_t st, const RowStrides& in, bool beside) {
   using L = DqLayout<D>;
   CUtensorMap tq, tdo, tk, tv, tdq;
   // contiguous tensors: 2-D maps over their rows (cheaper for TMA than the
@@ -381,6 +383,17 @@ cudaError_t launch_dq_d(const AttnParams& p, int Dio, const RowStrides& rs, cons
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(p.T * p.Hq * p.B);
+  if (beside) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(352);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = programmatic_launch();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kfn, tq, tdo, tk, tv, tdq, pp);
+  }
   kfn<<<grid, 352, L::SMEM, st>>>(tq, tdo, tk, tv, tdq, pp);
   return cudaGetLastError();
 }
@@ -388,14 +401,14 @@ cudaError_t launch_dq_d(const AttnParams& p, int Dio, const RowStrides& rs, cons
 }  // namespace
 
 cudaError_t launch_bwd_dq(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in) {
+                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in, bool beside) {
   // head dim 96 runs the 128-wide tile layout: its tensor maps are 96
   // elements wide, so TMA fills columns 96..127 of every loaded tile with
   // zeros and drops them from every store; the MMAs contract over 96 (six
   // K-steps) and produce 96 columns (N = 96), so no work is spent on them.
-  if (D == 64) return launch_dq_d<64>(p, 64, rs, q, k, v, dout, st, in ? *in : rs);
-  if (D == 96) return launch_dq_d<128, 96>(p, 96, rs, q, k, v, dout, st, in ? *in : rs);
-  return launch_dq_d<128>(p, 128, rs, q, k, v, dout, st, in ? *in : rs);
+  if (D == 64) return launch_dq_d<64>(p, 64, rs, q, k, v, dout, st, in ? *in : rs, beside);
+  if (D == 96) return launch_dq_d<128, 96>(p, 96, rs, q, k, v, dout, st, in ? *in : rs, beside);
+  return launch_dq_d<128>(p, 128, rs, q, k, v, dout, st, in ? *in : rs, beside);
 }
 
 }  // namespace pa

@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_load_kernel(const __grid_co
 // Start of the attention backward from 8-bit tensors, in one launch: the
 // first thread blocks bring q, k and v back as bf16 (the operand type of the
 // products), the rest form delta = rowsum(dO * O) with O straight from its
-// codes, O itself never being stored, and lse * log2(e).
+// codes, O itself never being stored, and lse * log2(e). Bound by memory; the
+// packed 8k row (Hq 32, Hkv 8, D 128; 251 MB) took @@.
 struct DeltaArgs {
   const uint8_t* codes;  // (B, H, Nr, D)
   const float* scales;
@@ -414,12 +415,17 @@ struct DeltaArgs {
   float* lse2;
   uint32_t rows;  // B * H * N, N padded to whole tiles
   FastDiv N, H;
-  int Nr, nb, shift;   // shift: log2 of a block's groups of eight
+  int Nr, nb, shift;   // shift: log2 of a block's groups of 16
   int64_t sb, sh, sn;  // of dout
 };
-constexpr int row_lanes(int D) { return D == 128 ? 16 : D == 64 ? 8 : 4; }  // divides D / 8 and a warp
+// A row's groups of 16 elements on a power of two of lanes, and rows in flight
+// per thread (six to four groups a thread).
+constexpr int row_lanes(int D) { return D == 128 ? 8 : D == 64 ? 4 : 2; }
+constexpr int row_unroll(int D) { return D == 96 ? 2 : 4; }
+constexpr int block_rows(int D) { return kCkptThreads / row_lanes(D) * row_unroll(D); }
 
-template <int D, int FMT, int VEC>
+// VEC: of the load. WIDE: dout's rows start on 32 bytes.
+template <int D, int FMT, int VEC, bool WIDE>
 __global__ void __launch_bounds__(kCkptThreads)
     bwd_ckpt_prologue_kernel(const __grid_constant__ Tensors a, uint32_t load_blocks, const DeltaArgs p, int shift) {
   if (blockIdx.x < load_blocks) {
@@ -429,39 +435,67 @@ __global__ void __launch_bounds__(kCkptThreads)
     return;
   }
   using F = Format<FMT>;
-  constexpr int NV = D / 8, LPR = row_lanes(D), RPB = kCkptThreads / LPR;
-  const uint32_t row = (blockIdx.x - load_blocks) * RPB + threadIdx.x / LPR;
+  constexpr int LPR = row_lanes(D), NL = D / 16 / LPR, R = row_unroll(D);
+  const uint32_t row0 = (blockIdx.x - load_blocks) * block_rows(D) + threadIdx.x / LPR;
   const int sub = threadIdx.x % LPR;
-  const bool in = row < p.rows;
-  const uint32_t bh = quot(in ? row : 0u, p.N), n = (in ? row : 0u) - bh * p.N.d;
-  const uint32_t b = quot(bh, p.H), h = bh - b * p.H.d;
-  // rows past the caller's N get P = 0 (lse = +inf) and delta = 0, so they add nothing
-  const bool live = in && n < (uint32_t)p.Nr;
-  const size_t r = (size_t)bh * p.Nr + n;
-  const __nv_bfloat16* dout = p.dout + (size_t)b * p.sb + (size_t)h * p.sh + (size_t)n * p.sn;
-  float acc = 0.f;
-  if (live) {
+  uint4 c[R][NL];
+  float s[R][NL];
+  Vec<__nv_bfloat16, 16> g[R][NL];
+  bool live[R];
 #pragma unroll
-    for (int v = sub; v < NV; v += LPR) {
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.codes + r * D) + v);
-      const float s = __ldg(p.scales + r * p.nb + (v >> p.shift));
-      Vec<__nv_bfloat16, 8> g;
-      g.load(dout, v * 8);
-      float o[8], d[8];
-      F::decode(c, o);
-      g.floats(0, d);
-      float sum = 0.f;
+  for (int u = 0; u < R; ++u) {
+    const uint32_t row = row0 + u * (kCkptThreads / LPR);
+    const uint32_t bh = quot(row, p.N), n = row - bh * p.N.d, b = quot(bh, p.H), h = bh - b * p.H.d;
+    // rows past the caller's N get P = 0 (lse = +inf) and delta = 0, so they add nothing
+    live[u] = row < p.rows && n < (uint32_t)p.Nr;
+    const size_t r = (size_t)bh * p.Nr + n;
+    const __nv_bfloat16* dout = p.dout + (size_t)b * p.sb + (size_t)h * p.sh + (size_t)n * p.sn;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(o[i], d[i], sum);
-      acc = fmaf(s, sum, acc);
+    for (int k = 0; k < NL; ++k) {
+      const int v = sub + k * LPR;
+      if (live[u]) {
+        c[u][k] = __ldg(reinterpret_cast<const uint4*>(p.codes + r * D) + v);
+        s[u][k] = __ldg(p.scales + r * p.nb + (v >> p.shift));
+        if (WIDE) {
+          ld_32(dout + v * 16, g[u][k].w);
+        } else {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(dout + v * 16)), y = __ldg(reinterpret_cast<const uint4*>(dout + v * 16) + 1);
+          g[u][k].w[0] = x.x, g[u][k].w[1] = x.y, g[u][k].w[2] = x.z, g[u][k].w[3] = x.w;
+          g[u][k].w[4] = y.x, g[u][k].w[5] = y.y, g[u][k].w[6] = y.z, g[u][k].w[7] = y.w;
+        }
+      }
     }
   }
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
-  if (in && sub == 0) {
-    p.delta[row] = acc;
-    p.lse2[row] = live ? p.lse[r] * 1.4426950408889634f : INFINITY;
+  for (int u = 0; u < R; ++u) {
+    float acc = 0.f;
+    if (live[u]) {
+#pragma unroll
+      for (int k = 0; k < NL; ++k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float o[8], d[8];
+          F::decode(h ? make_uint2(c[u][k].z, c[u][k].w) : make_uint2(c[u][k].x, c[u][k].y), o);
+          g[u][k].floats(h, d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(o[i], d[i], sum);
+        }
+        acc = fmaf(s[u][k], sum, acc);
+      }
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
+    const uint32_t row = row0 + u * (kCkptThreads / LPR);
+    if (sub == 0 && row < p.rows) {
+      const uint32_t bh = quot(row, p.N), n = row - bh * p.N.d;
+      p.delta[row] = acc;
+      p.lse2[row] = live[u] ? p.lse[(size_t)bh * p.Nr + n] * 1.4426950408889634f : INFINITY;
+    }
   }
+  // This kernel runs beside the tile table's, on which nothing here depends;
+  // the one after it needs both, so the last block waits for the other's end.
+  if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -541,16 +575,21 @@ void load_any(const CkptTensor* x, int count, int format, int G, cudaStream_t st
 }
 
 template <int D, int VEC>
-void prologue_launch(const CkptTensor* qkv, int format, int G, const DeltaArgs& d, cudaStream_t st) {
+cudaError_t prologue_launch(const CkptTensor* qkv, int format, int G, const DeltaArgs& d, cudaStream_t st) {
   Tensors a{};
   const uint32_t load_blocks = describe(qkv, 3, G, VEC, kCkptThreads * kLoadUnroll, false, &a);
-  constexpr int RPB = kCkptThreads / row_lanes(D);
-  const uint32_t blocks = load_blocks + (d.rows + RPB - 1) / RPB;
-  const int shift = log2_of(G / VEC);
-  if (format == PA_CKPT_INT8)
-    bwd_ckpt_prologue_kernel<D, PA_CKPT_INT8, VEC><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
-  else
-    bwd_ckpt_prologue_kernel<D, PA_CKPT_E4M3, VEC><<<blocks, kCkptThreads, 0, st>>>(a, load_blocks, d, shift);
+  const bool wide = aligned32(d.dout) && d.sb % 16 == 0 && d.sh % 16 == 0 && d.sn % 16 == 0;
+  const bool i8 = format == PA_CKPT_INT8;
+  const auto kfn = wide ? (i8 ? bwd_ckpt_prologue_kernel<D, PA_CKPT_INT8, VEC, true> : bwd_ckpt_prologue_kernel<D, PA_CKPT_E4M3, VEC, true>)
+                        : (i8 ? bwd_ckpt_prologue_kernel<D, PA_CKPT_INT8, VEC, false> : bwd_ckpt_prologue_kernel<D, PA_CKPT_E4M3, VEC, false>);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(load_blocks + (d.rows + block_rows(D) - 1) / block_rows(D));
+  cfg.blockDim = dim3(kCkptThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = programmatic_launch();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, a, load_blocks, d, log2_of(G / VEC));
 }
 
 }  // namespace
@@ -580,18 +619,14 @@ cudaError_t launch_bwd_ckpt_prologue(const AttnParams& p, int D, const RowStride
   d.H = fast_div(p.Hq);
   d.Nr = p.Nr;
   d.nb = (D + block - 1) / block;
-  d.shift = log2_of(block / 8);
+  d.shift = log2_of(block / 16);
   d.sb = rs.q_b;
   d.sh = rs.q_h;
   d.sn = rs.q_n;
   const bool flat = all_flat(qkv, 3, block);
-  if (D == 64)
-    flat ? prologue_launch<64, 16>(qkv, format, block, d, st) : prologue_launch<64, 8>(qkv, format, block, d, st);
-  else if (D == 96)
-    flat ? prologue_launch<96, 16>(qkv, format, block, d, st) : prologue_launch<96, 8>(qkv, format, block, d, st);
-  else
-    flat ? prologue_launch<128, 16>(qkv, format, block, d, st) : prologue_launch<128, 8>(qkv, format, block, d, st);
-  return cudaGetLastError();
+  if (D == 64) return flat ? prologue_launch<64, 16>(qkv, format, block, d, st) : prologue_launch<64, 8>(qkv, format, block, d, st);
+  if (D == 96) return flat ? prologue_launch<96, 16>(qkv, format, block, d, st) : prologue_launch<96, 8>(qkv, format, block, d, st);
+  return flat ? prologue_launch<128, 16>(qkv, format, block, d, st) : prologue_launch<128, 8>(qkv, format, block, d, st);
 }
 
 }  // namespace pa

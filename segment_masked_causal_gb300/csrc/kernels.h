@@ -13,6 +13,18 @@ namespace pa {
 // the query itself fails). Cached per device.
 pa_status device_check();
 
+// Launch attribute with which a kernel may start before the one ahead of it on
+// the stream has ended, once every block of that one has started and said so
+// (griddepcontrol.launch_dependents). It runs griddepcontrol.wait before it
+// reads what that one writes, and somewhere before its end in any case, so that
+// what follows on the stream finds both finished.
+inline cudaLaunchAttribute programmatic_launch() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 // Element strides of the (B, H, N, D) tensors the kernels read and write in
 // place (D contiguous): q, out, dout and dq use the q_* strides, k, v, dk and
 // dv the k_* strides.
@@ -39,8 +51,11 @@ cudaError_t launch_exp2_fma_selftest(const float* x, float* y, int64_t n, cudaSt
 cudaError_t launch_fwd(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k, const void* v,
                        cudaStream_t st);
 // in: the strides of q, k and v where they are not those of dout and the gradients.
+// beside: launch dQ programmatically behind the kernel ahead of it (dK/dV),
+// of which it needs nothing.
 cudaError_t launch_bwd_dq(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr);
+                          const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr,
+                          bool beside = false);
 cudaError_t launch_bwd_dkv(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
                            const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr);
 // Single-pass backward: dK, dV and the fp32 dQ accumulator p.dq_acc (zeroed

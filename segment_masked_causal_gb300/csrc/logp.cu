@@ -735,9 +735,7 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = few ? lists : warps * lists;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr = programmatic_launch();
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, few ? logp_merge_kernel<8> : logp_merge_kernel<1>, p, logp, lse, entropy, top_ids,

@@ -171,6 +171,8 @@ __global__ void __launch_bounds__(1024) prologue_small_kernel(const int32_t* __r
   int2* range = sm2 + n;                           // {kv_lo, q_hi} per tile
   int* cnt = reinterpret_cast<int*>(sm2 + 2 * n);  // 2 (T + 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  // a kernel launched programmatically behind this one may run beside it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0 && status) *status = 0u;
   for (int e0 = 4 * warp; e0 < n; e0 += 4 * warps) {
     int4 v[4];
