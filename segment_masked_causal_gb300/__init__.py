@@ -18,6 +18,7 @@ not be a multiple of 128 except in the single-step calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -587,6 +588,7 @@ def _want(t, shape, name):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
+@functools.lru_cache(maxsize=256)  # a function of the numbers alone
 def pa_logp_workspace_bytes(N, V, D, top=0) -> int:
     return int(lib().pa_logp_workspace_bytes(int(N), int(V), int(D), int(top)))
 
@@ -629,6 +631,7 @@ def token_logprobs_forward(hidden, head, targets, temperature=1.0, top=0, ws=Non
     return logp, lse, entropy, ids, alt
 
 
+@functools.lru_cache(maxsize=256)  # a function of the numbers alone
 def pa_logp_bwd_workspace_bytes(N, V, D) -> int:
     return int(lib().pa_logp_bwd_workspace_bytes(int(N), int(V), int(D)))
 
@@ -708,7 +711,8 @@ def _ckpt_format(dtype):
     raise ValueError(f"codes must be int8 or float8_e4m3fn, got {dtype}")
 
 
-_CKPT_FIELDS = "PPPiiiiqqq"  # pa_ckpt_tensor
+_CKPT_FIELDS = struct.Struct("PPPiiiiqqq")  # pa_ckpt_tensor
+_ONES, _ZEROS = ((), (1,), (1, 1), (1, 1, 1)), ((), (0,), (0, 0), (0, 0, 0))
 
 
 def _ckpt_call(fn, xs, cs, stream):
@@ -721,26 +725,26 @@ def _ckpt_call(fn, xs, cs, stream):
         return
     dtype, kind, block = xs[0].dtype, cs[0].codes.dtype, cs[0].block
     io, fmt, f32, at = _io_dtype(xs[0])[1], _ckpt_format(kind), torch.float32, torch.cuda.current_device()
-    fields = []
+    pack, parts = _CKPT_FIELDS.pack, []
     for x, c in zip(xs, cs):
-        codes, scales = c.codes, c.scales
-        shape, stride = x.shape, x.stride()
-        n = len(shape)
+        codes, scales, shape, stride = c.codes, c.scales, x.shape, x.stride()
+        pad = 4 - len(shape)
         if x.dtype != dtype or codes.dtype != kind or c.block != block:
             raise ValueError("the tensors of one call share their type, format and block")
-        if not 1 <= n <= 4 or (stride[-1] != 1 and shape[-1] > 1):
+        if not 0 <= pad <= 3 or (stride[-1] != 1 and shape[-1] > 1):
             raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
         if codes.shape != shape:
             raise ValueError(f"codes must be {tuple(shape)}, got {tuple(codes.shape)}")
-        if not (x.get_device() == codes.get_device() == scales.get_device() == at):
+        if not x.get_device() == codes.get_device() == scales.get_device() == at:
             raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
-        if not codes.is_contiguous() or not scales.is_contiguous() or scales.dtype != f32:
+        if not (codes.is_contiguous() and scales.is_contiguous()) or scales.dtype != f32:
             raise ValueError("codes and scales must be contiguous, scales float32")
-        fields += (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *(1,) * (4 - n), *shape, *(0,) * (4 - n), *stride[:-1])
+        parts.append(pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *_ONES[pad], *shape, *_ZEROS[pad],
+                          *stride[:-1]))
     st = _stream(stream)
-    for i in range(0, len(xs), PA_CKPT_MAX_TENSORS):
-        n = min(PA_CKPT_MAX_TENSORS, len(xs) - i)
-        _check(fn(n, struct.pack(_CKPT_FIELDS * n, *fields[10 * i:10 * (i + n)]), io, fmt, block, st))
+    for i in range(0, len(parts), PA_CKPT_MAX_TENSORS):
+        some = parts[i:i + PA_CKPT_MAX_TENSORS]
+        _check(fn(len(some), b"".join(some), io, fmt, block, st))
 
 
 def pa_ckpt_save(tensors, checkpoints, stream=None):
@@ -786,6 +790,7 @@ def checkpoint_load(checkpoints, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=256)  # a function of the numbers alone
 def pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D) -> int:
     d = make_dims(B, Hq, Hkv, N, D)
     return int(lib().pa_bwd_ckpt_workspace_bytes(ctypes.byref(d)))
@@ -796,28 +801,30 @@ def pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale=0.0, stream=
     dout and dq share their strides, dk and dv theirs; seg None = plain
     causal."""
     import torch
-    bf, f = torch.bfloat16, torch.float32
+    bf, f, kind, block = torch.bfloat16, torch.float32, q.codes.dtype, q.block
     if q.codes.dim() != 4 or k.codes.dim() != 4:
         raise ValueError("q and k must be checkpoints of (B, H, N, D) tensors")
-    B, Hq, N, D = q.shape
-    Hkv = k.shape[1]
-    fmt = _ckpt_format(q.codes.dtype)
-    for c, H, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (out, Hq, "out")):
-        _want(c.codes, (B, H, N, D), n)
-        if c.codes.dtype != q.codes.dtype or c.block != q.block or c.dtype != bf:
+    qs, ks = q.codes.shape, k.codes.shape
+    B, Hq, N, D = qs
+    Hkv = ks[1]
+    kept = []
+    for c, want, n in ((q, qs, "q"), (k, (B, Hkv, N, D), "k"), (v, ks, "v"), (out, qs, "out")):
+        codes = c.codes
+        if codes.shape != want:
+            raise ValueError(f"{n} must be {tuple(want)}, got {tuple(codes.shape)}")
+        if codes.dtype != kind or c.block != block or c.dtype != bf:
             raise ValueError("q, k, v and out must be bf16 checkpoints in one format and block")
-        _on_current_device(c.codes, c.scales)
-    for t, H, n in ((dout, Hq, "dout"), (dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")):
-        _want(t, (B, H, N, D), n)
-    _want(lse, (B, Hq, N), "lse")
+        kept.append(pa_ckpt(_ptr(codes, kind, n), _ptr(c.scales, f, n)))
+    for t, want, n in ((dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"), (dv, ks, "dv"), (lse, (B, Hq, N), "lse")):
+        if t.shape != want:
+            raise ValueError(f"{n} must be {tuple(want)}, got {tuple(t.shape)}")
     _want(seg, (B, N), "seg")
-    _on_current_device(dout, lse, seg, dq, dk, dv, ws)
-    d = make_dims(B, Hq, Hkv, N, D, scale)
-    plain = _all_contiguous(dout, dq, dk, dv)
-    st = None if plain else ctypes.byref(_strides_of(dout, dk))
-    c = [ctypes.byref(pa_ckpt(_ptr(x.codes, None, n), _ptr(x.scales, f, n))) for x, n in
-         ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
-    _check(lib().pa_bwd_ckpt(ctypes.byref(d), st, fmt, q.block, *c, _ptr_rows(dout, bf, "dout"), _ptr(lse, f, "lse"),
+    _on_current_device(q.codes, q.scales, k.codes, k.scales, v.codes, v.scales, out.codes, out.scales, dout, lse, seg, dq,
+                       dk, dv, ws)
+    st = None if _all_contiguous(dout, dq, dk, dv) else _strides_of(dout, dk)
+    ref = ctypes.byref
+    _check(lib().pa_bwd_ckpt(ref(make_dims(B, Hq, Hkv, N, D, scale)), st and ref(st), _ckpt_format(kind), block, ref(kept[0]),
+                             ref(kept[1]), ref(kept[2]), ref(kept[3]), _ptr_rows(dout, bf, "dout"), _ptr(lse, f, "lse"),
                              _ptr(seg, torch.int32, "seg"), _ptr_rows(dq, bf, "dq", dout), _ptr_rows(dk, bf, "dk"),
                              _ptr_rows(dv, bf, "dv", dk), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
 
@@ -827,19 +834,21 @@ def backward_from_checkpoint(q, k, v, out, dout, lse, seg=None, scale=0.0, ws=No
     (dq, dk, dv) in bf16. They take dout's memory order: contiguous, or
     (B, N, H, D) memory for a dout that is a view of such."""
     import torch
-    B, Hq, N, D = q.shape
-    Hkv = k.shape[1]
+    if q.codes.dim() != 4 or k.codes.dim() != 4:
+        raise ValueError("q and k must be checkpoints of (B, H, N, D) tensors")
+    B, Hq, N, D = q.codes.shape
+    Hkv = k.codes.shape[1]
     if ws is None:
         n = pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D)
         if n == 0:
             raise PAError(4, "invalid dims")
         ws = torch.empty(n, dtype=torch.uint8, device=dout.device)
     if dout.is_contiguous():
-        dq = torch.empty_like(dout)
-        dk, dv = (torch.empty((B, Hkv, N, D), dtype=dout.dtype, device=dout.device) for _ in range(2))
+        dq, shape, stride = torch.empty_like(dout), (B, Hkv, N, D), (Hkv * N * D, N * D, D, 1)
     else:
         dq = torch.empty_strided(dout.shape, dout.stride(), dtype=dout.dtype, device=dout.device)
-        dk, dv = (torch.empty((B, N, Hkv, D), dtype=dout.dtype, device=dout.device).transpose(1, 2) for _ in range(2))
+        shape, stride = (B, Hkv, N, D), (N * Hkv * D, D, Hkv * D, 1)
+    dk, dv = (torch.empty_strided(shape, stride, dtype=dout.dtype, device=dout.device) for _ in range(2))
     pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale)
     return dq, dk, dv
 

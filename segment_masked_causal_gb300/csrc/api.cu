@@ -655,7 +655,6 @@ pa_status pa_logp_bwd(int32_t N, int32_t V, int32_t D, float temperature, const 
   pa_status why = device_ok();
   if (why != PA_OK) return why;
   const cudaStream_t st = cu(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return PA_ERR_CUDA;
   return pa::launch_logp_bwd(N, V, D, temperature, hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden,
                              dhead, ws, st) == cudaSuccess
              ? PA_OK

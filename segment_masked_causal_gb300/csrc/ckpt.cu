@@ -419,14 +419,14 @@ struct DeltaArgs {
   int64_t sb, sh, sn;  // of dout
 };
 // A row's groups of 16 elements on a power of two of lanes, and rows in flight
-// per thread (six to four groups a thread).
+// per thread.
 constexpr int row_lanes(int D) { return D == 128 ? 8 : D == 64 ? 4 : 2; }
-constexpr int row_unroll(int D) { return D == 96 ? 2 : 4; }
+constexpr int row_unroll(int D) { return D == 96 ? 1 : 2; }
 constexpr int block_rows(int D) { return kCkptThreads / row_lanes(D) * row_unroll(D); }
 
 // VEC: of the load. WIDE: dout's rows start on 32 bytes.
 template <int D, int FMT, int VEC, bool WIDE>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kCkptThreads, 5)
     bwd_ckpt_prologue_kernel(const __grid_constant__ Tensors a, uint32_t load_blocks, const DeltaArgs p, int shift) {
   if (blockIdx.x < load_blocks) {
     uint32_t first;

@@ -111,6 +111,11 @@ cudaError_t launch_lce_fwd(int N, int V, int D, const void* hidden, const void* 
 // with an accumulator of its own (acc + run * M * N): kAccInit or kAccAdd
 // only, joined by launch_sum_splits.
 enum GemmMode : int { kStoreBf16 = 0, kAccInit = 1, kAccAdd = 2, kAccFinal = 3 };
+// kInOrder: an ordinary launch. kAfter: a programmatic one that waits for the
+// kernel ahead before it reads or writes memory (and before it lets a kernel
+// behind it start). kBeside: a programmatic one that needs nothing of the kernel
+// ahead, only of those before it, so the kernel ahead is kInOrder or kAfter.
+enum GemmOrder : int { kInOrder = 0, kAfter = 1, kBeside = 2 };
 struct GemmCall {
   int M, N, K;
   int mode;          // GemmMode
@@ -118,6 +123,7 @@ struct GemmCall {
   __nv_bfloat16* c;  // bf16 result (kStoreBf16: the product; kAccFinal: accumulator + product)
   float* acc;        // fp32 accumulator (kAccInit: set; kAccAdd: add; kAccFinal: read)
   uint32_t* status;
+  int order;         // GemmOrder
 };
 cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st);
 // The number of runs that makes an M x N x K product shortest on `slots` SMs;

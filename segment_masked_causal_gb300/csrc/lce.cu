@@ -372,14 +372,20 @@ __global__ void __launch_bounds__(256) lce_merge_kernel(const LceParams p, int s
 // tiles, so a tile's epilogue runs beside the next tile's products. The
 // epilogue (one thread per output row) stores bf16, or starts / adds to /
 // finishes an fp32 accumulator in global memory; each output tile belongs to
-// one CTA, so no two threads touch the same element.
+// one CTA, so no two threads touch the same element. What is only written
+// (bf16, or an accumulator's start) goes through 32 KB of shared memory and
+// TMA stores: rows written piecewise by their threads cost 32 separate sectors
+// an instruction, which bounds a product of few K (the head's gradient of 96
+// tokens, 131 MB of it, took 49 us that way and @@ us through TMA).
 constexpr int kGemmStages = 4;
 constexpr int kGemmN = 256;                               // output columns per tile
 constexpr uint32_t kGemmA = 128 * 128;                    // 128 rows x 64 K, 16 KB
 constexpr uint32_t kGemmBHalf = 64 * 128;                 // 64 K rows x 64 N columns, 8 KB
 constexpr uint32_t kGemmStage = kGemmA + 4 * kGemmBHalf;  // 48 KB
 constexpr int kGemmThreads = 192;
-constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + kGemmStages * kGemmStage;
+constexpr uint32_t kGemmOut = 2 * 128 * 128;              // two boxes of 128 rows x 128 bytes on their way out
+constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + kGemmStages * kGemmStage + kGemmOut;
+static_assert(kGemmSmem <= 232448, "shared memory");
 
 // Row blocks per group of the tile order. Measured on the N = 8192,
 // V = 151,936, D = 4096 backward (38 launches a call), in one run: 20.95,
@@ -406,6 +412,7 @@ struct GemmParams {
   float* acc;          // fp32 accumulator (kAccInit: set; kAccAdd: add; kAccFinal: read)
   int ldacc;
   uint32_t* status;
+  int order;           // GemmOrder
 };
 
 struct GemmMisc {
@@ -416,9 +423,33 @@ struct GemmMisc {
   int abort_flag;
 };
 
+// One thread's row of a box of 128 rows x 128 bytes, 128-byte swizzled: 64
+// columns as bf16, or 32 as fp32.
+__device__ __forceinline__ void store_box(uint32_t taddr, uint32_t out, int r, bool f32) {
+  const uint32_t row = out + r * 128;
+  const int x = r & 7;
+  if (f32) {
+    uint32_t a[32];
+    tmem_ld32(taddr, a);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) st_shared_v4(row + ((q ^ x) << 4), a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+    return;
+  }
+  uint32_t a[2][32];
+  tmem_ld32x2(taddr, taddr + 32, a[0], a[1]);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t* e = &a[q >> 2][8 * (q & 3)];
+    st_shared_v4(row + ((q ^ x) << 4), pack_bf16x2(__uint_as_float(e[0]), __uint_as_float(e[1])),
+                 pack_bf16x2(__uint_as_float(e[2]), __uint_as_float(e[3])),
+                 pack_bf16x2(__uint_as_float(e[4]), __uint_as_float(e[5])),
+                 pack_bf16x2(__uint_as_float(e[6]), __uint_as_float(e[7])));
+  }
+}
+
 __global__ void __launch_bounds__(kGemmThreads, 1)
     lce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const GemmParams p) {
+                    const __grid_constant__ CUtensorMap tmC, const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   GemmMisc& m = *reinterpret_cast<GemmMisc*>(smem_raw);
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) &
@@ -463,6 +494,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // What is launched programmatically behind this kernel may take the SMs that
+  // it leaves, but no earlier than the kernel ahead has ended: a kBeside kernel
+  // counts on what that one has written.
+  if (p.order == kAfter) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
@@ -528,6 +564,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // warps 2..5: TMEM lane quarter warp % 4, one thread per output row
     const int quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const bool f32 = p.mode == kAccInit, through = f32 || p.mode == kStoreBf16;
+    uint8_t* out = ring + kGemmStages * kGemmStage;
+    const bool issuer = threadIdx.x == 64;
+    int box = 0;
+    if (through && issuer) prefetch_tmap(&tmC);
     for (int j = 0; j < nt; ++j) {
       const int buf = j & 1;
       const bool ok = __all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 47));
@@ -536,6 +577,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int2 o = tile_origin((int)blockIdx.x + j * (int)gridDim.x);
       const int m0 = o.x, n0 = o.y;
       const int row = m0 + quarter * 32 + lane;
+      if (through) {
+        // a box of 128 rows x 128 bytes at a time, through two buffers in turn
+        const int run = ((int)blockIdx.x + j * (int)gridDim.x) / p.per_split, step = f32 ? 32 : 64;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kGemmN && n0 + c0 < p.N; c0 += step, box ^= 1) {
+          if (issuer) bulk_wait_read1();  // the buffer's last copy has left it
+          named_bar_sync(1, 128);
+          store_box(tmem + lane_base + buf * kGemmN + c0, smem_u32(out) + box * 16384, quarter * 32 + lane, f32);
+          fence_async_smem();
+          named_bar_sync(1, 128);
+          if (issuer) {
+            tma_store_3d(&tmC, out + box * 16384, n0 + c0, m0, run);
+            bulk_commit();
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&m.acc_empty[buf]);
+        continue;
+      }
       // each run of K has an accumulator of its own
       float* acc = p.acc + (size_t)(((int)blockIdx.x + j * (int)gridDim.x) / p.per_split) * p.M * p.ldacc;
 #pragma unroll 1
@@ -544,19 +604,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_ld32(tmem + lane_base + buf * kGemmN + c0, a);
         const int col = n0 + c0;
         if (row >= p.M || col >= p.N) continue;  // N is a multiple of 64: 32 columns are all in or all out
-        if (p.mode == kAccInit || p.mode == kAccAdd || p.mode == kAccFinal) {
+        {
           float4* ac = reinterpret_cast<float4*>(acc + (size_t)row * p.ldacc + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float4 v = make_float4(__uint_as_float(a[4 * q]), __uint_as_float(a[4 * q + 1]),
                                    __uint_as_float(a[4 * q + 2]), __uint_as_float(a[4 * q + 3]));
-            if (p.mode != kAccInit) {
-              const float4 o = ac[q];
-              v.x += o.x;
-              v.y += o.y;
-              v.z += o.z;
-              v.w += o.w;
-            }
+            const float4 o = ac[q];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
             if (p.mode == kAccFinal) {
               a[4 * q] = __float_as_uint(v.x);
               a[4 * q + 1] = __float_as_uint(v.y);
@@ -567,7 +625,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
           }
         }
-        if (p.mode == kStoreBf16 || p.mode == kAccFinal) {
+        if (p.mode == kAccFinal) {
           uint4* cr = reinterpret_cast<uint4*>(p.c + (size_t)row * p.ldc + col);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -580,6 +638,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_before();
       mbar_arrive(&m.acc_empty[buf]);
     }
+    if (through && issuer) bulk_wait_all();  // the last stores have completed before the CTA exits
   }
   tc_fence_before();
   __syncthreads();
@@ -587,11 +646,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kGemmN);
   }
+  // beside the kernel ahead of it, this one ends no earlier
+  if (p.order == kBeside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Sum of the runs' accumulators, in run order, rounded to bf16: 4 elements a thread.
 __global__ void __launch_bounds__(256) sum_splits_kernel(const float4* __restrict__ acc, int splits, size_t n4,
                                                          uint2* __restrict__ out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += (size_t)gridDim.x * blockDim.x) {
     float4 v = acc[i];
     for (int s = 1; s < splits; ++s) {
@@ -628,13 +690,27 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   q.acc = gc.acc;
   q.ldacc = gc.N;
   q.status = gc.status;
+  q.order = gc.order;
+  CUtensorMap tC;
+  if (gc.mode == kAccInit) {
+    if (!tmap_3d_sw128(&tC, gc.acc, true, gc.N, gc.M, splits)) return cudaErrorInvalidValue;
+  } else if (!tmap_3d_sw128(&tC, gc.mode == kAccAdd ? static_cast<void*>(gc.acc) : gc.c, gc.mode == kAccAdd, gc.N, gc.M, 1)) {
+    return cudaErrorInvalidValue;  // (only read by the modes that store through it)
+  }
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = q.tiles < sms ? q.tiles : sms;
   if (grid < 1) return cudaSuccess;
-  lce_gemm_kernel<<<grid, kGemmThreads, kGemmSmem, st>>>(tA, tB, q);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = programmatic_launch();
+  cfg.attrs = &attr;
+  cfg.numAttrs = gc.order == kInOrder ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, lce_gemm_kernel, tA, tB, tC, q);
 }
 
 // Time of a run in K blocks (four 128 x 256 x 16 products, about 0.27 us an
@@ -661,9 +737,15 @@ int gemm_splits(int M, int N, int K, int slots) {
 
 cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st) {
   const size_t n4 = n / 4, blocks = (n4 + 255) / 256;
-  sum_splits_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(reinterpret_cast<const float4*>(acc), splits,
-                                                                              n4, reinterpret_cast<uint2*>(out));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(blocks < 4096 ? blocks : 4096));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = programmatic_launch();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_splits_kernel, reinterpret_cast<const float4*>(acc), splits, n4,
+                            reinterpret_cast<uint2*>(out));
 }
 
 // The vocabulary split of the (token tile x split) grid: the one that makes

@@ -65,7 +65,9 @@ struct FwdParams {
 
 struct BwdParams {
   int N, V, D;
-  int vt_base, vt_end;  // the chunk's vocabulary tiles of 256 rows
+  int v_base, v_end;   // the chunk's vocabulary rows
+  int tile_units;      // units of 32 rows per logit tile
+  int first;           // 1: this launch starts the call (clears the status word)
   float sl2, inv_t;
   const int32_t* targets;
   const float* lse;
@@ -550,7 +552,9 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 }
 
 // Backward, one chunk of the vocabulary: one CTA per SM over the chunk's
-// (token tile, vocabulary tile) pairs. Each recomputed logit becomes
+// (token tile, vocabulary tile) pairs; the vocabulary tiles have eight units,
+// or fewer where that makes the longest CTA shorter (few tokens). Each
+// recomputed logit becomes
 //   dz = p (cA + cB log2 p) + [v = t] g / T,
 //   cA = -(g + e H) / T,  cB = -e ln 2 / T,
 // exactly 0 in rows without a gradient and in columns past V. dz is rounded
@@ -558,13 +562,14 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 // 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
 __global__ void __launch_bounds__(kThreads, 1)
     logp_dz_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
-                   const BwdParams p) {
+                   const __grid_constant__ CUtensorMap tmWu, const BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Misc& m = *reinterpret_cast<Misc*>(smem_raw);
   uint8_t* ring =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int TM = (p.N + kTok - 1) / kTok, VT = p.vt_end - p.vt_base;
+  const int TM = (p.N + kTok - 1) / kTok, units = (p.v_end - p.v_base + kUnit - 1) / kUnit;
+  const int VT = (units + p.tile_units - 1) / p.tile_units;
   const int nt = (TM * VT - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   const int KS = p.D / 64;
   const Guard g{&m.abort_flag, p.status};
@@ -572,13 +577,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = (int)blockIdx.x + j * (int)gridDim.x;
     const int gi = q / (kGroup * VT), r = q - gi * kGroup * VT;
     const int g0 = gi * kGroup, gs = min(kGroup, TM - g0);
-    return Tile{g0 + r % gs, (p.vt_base + r / gs) * kTileUnits, kTileUnits};
+    const int u = r / gs * p.tile_units;
+    return Tile{g0 + r % gs, p.v_base / kUnit + u, min(p.tile_units, units - u)};
   };
+  if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait can give up within 2 s
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   setup(m);
+  if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");  // the last chunk's products have read dz
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmW, nt, KS, 1, tile_of);
+    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, 1, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
@@ -598,9 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float one = p.inv_t * gl, l2 = use ? p.lse[token] * kLog2e : 0.f;
       if (!__all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 54))) break;
       tc_fence_after();
-      const int v0 = tl.u * kUnit, c0v = v0 - p.vt_base * 256;  // column of v0 in the chunk
+      const int v0 = tl.u * kUnit, c0v = v0 - p.v_base;  // column of v0 in the chunk
 #pragma unroll 1
-      for (int c0 = 0; c0 < 256; c0 += 32) {
+      for (int c0 = 0; c0 < tl.units * kUnit; c0 += 32) {
         uint32_t a[32];
         tmem_ld32(tmem + lane_base + buf * 256 + c0, a);
         const int vc = v0 + c0;
@@ -742,6 +751,22 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
                             top_logp);
 }
 
+// Units per vocabulary tile of the dz kernel: waves x (units + 1), the one for
+// a tile's fixed cost, is what the longest CTA takes.
+static int dz_tile_units(int TM, int rows, int slots) {
+  const int units = (rows + kUnit - 1) / kUnit;
+  int best = kTileUnits;
+  long long best_cost = -1;
+  for (int u = kTileUnits; u >= 4; --u) {
+    const long long pairs = (long long)TM * ((units + u - 1) / u), cost = (pairs + slots - 1) / slots * (u + 1);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = u;
+    }
+  }
+  return best;
+}
+
 LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   LogpBwdLayout L;
   // dz and dz^T of one chunk: at most 128 MiB each (L2 holds about one of
@@ -770,21 +795,26 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(w + L.dz);
   __nv_bfloat16* dzt = reinterpret_cast<__nv_bfloat16*>(w + L.dzt);
   float* acc = reinterpret_cast<float*>(w + L.acc);
-  CUtensorMap tH, tW, tHb;
+  CUtensorMap tH, tW, tWu, tHb;
   if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) ||
-      !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
+      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(logp_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count(), TM = (N + kTok - 1) / kTok;
+  cudaLaunchAttribute attr = programmatic_launch();
+  // Each kernel but the first is launched programmatically behind the one
+  // ahead: dz after the products of the chunk before, dW after dz, dH beside dW.
   for (int c = 0; c < L.chunks; ++c) {
     const int cv0 = c * L.vc, kc = V - cv0 < L.vc ? V - cv0 : L.vc;  // the chunk's vocabulary rows
     BwdParams p{};
     p.N = N;
     p.V = V;
     p.D = D;
-    p.vt_base = cv0 / 256;
-    p.vt_end = (cv0 + kc + 255) / 256;
+    p.v_base = cv0;
+    p.v_end = cv0 + kc;
+    p.tile_units = dz_tile_units(TM, kc, sms);
+    p.first = c == 0;
     p.sl2 = kLog2e / temperature;
     p.inv_t = 1.f / temperature;
     p.targets = targets;
@@ -797,9 +827,16 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     p.dzt = dhead ? dzt : nullptr;
     p.ld_dzt = L.ld_dzt;
     p.status = status;
-    const long long pairs = (long long)TM * (p.vt_end - p.vt_base);
-    logp_dz_kernel<<<pairs < sms ? (int)pairs : sms, kThreads, kSmem, st>>>(tH, tW, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int units = (kc + kUnit - 1) / kUnit;
+    const long long pairs = (long long)TM * ((units + p.tile_units - 1) / p.tile_units);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(pairs < sms ? (int)pairs : sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = c == 0 ? 0 : 1;
+    if ((e = cudaLaunchKernelEx(&cfg, logp_dz_kernel, tH, tW, tWu, p)) != cudaSuccess) return e;
     // dW rows of the chunk = dz^T H (the tokens are the contraction)
     if (dhead) {
       CUtensorMap tA;
@@ -811,6 +848,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
       gc.mode = kStoreBf16;
       gc.c = static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D;
       gc.status = status;
+      gc.order = kAfter;
       if ((e = launch_gemm(tA, tHb, gc, st)) != cudaSuccess) return e;
     }
     // dH += dz W[chunk] (the chunk's vocabulary rows are the contraction),
@@ -831,6 +869,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     gc.c = static_cast<__nv_bfloat16*>(dhidden);
     gc.acc = acc;
     gc.status = status;
+    gc.order = dhead ? kBeside : kAfter;
     if ((e = launch_gemm(tA, tB, gc, st)) != cudaSuccess) return e;
   }
   if (L.splits > 1) return launch_sum_splits(acc, L.splits, (size_t)N * D, static_cast<__nv_bfloat16*>(dhidden), st);

@@ -188,6 +188,15 @@ __device__ __forceinline__ void tma_store_rows(const CUtensorMap* m, const void*
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until every committed bulk-async group of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Wait until the shared memory of all but this thread's last committed bulk-async group has been read.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// 3-D tile store (tmap_3d_sw128), in a bulk-async group of the issuing thread.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int32_t c, int32_t row, int32_t plane) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c), "r"(row), "r"(plane)
+               : "memory");
+}
 // Named barrier over `count` threads (a multiple of 32), id 1..15.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");

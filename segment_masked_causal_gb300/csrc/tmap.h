@@ -77,4 +77,21 @@ inline bool tmap_bf16_bhnd_sw128(CUtensorMap* m, const void* base, uint64_t D, u
   return r == CUDA_SUCCESS;
 }
 
+// `planes` planes of `rows` rows x `inner` contiguous bf16 or fp32 elements
+// (16-byte multiples), in boxes of 128 rows x 128 bytes of one plane with the
+// 128-byte swizzle; what lies past `inner` or `rows` is dropped from stores.
+inline bool tmap_3d_sw128(CUtensorMap* m, void* base, bool f32, uint64_t inner, uint64_t rows, uint64_t planes) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {inner, rows, planes};
+  cuuint64_t strides[2] = {inner * size, inner * size * rows};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / size), 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace pa
