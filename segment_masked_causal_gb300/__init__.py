@@ -576,11 +576,24 @@ def _on_current_device(*ts):
 
 
 def _logp_dims(hidden, head, targets):
-    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1]:
+    hs, ws = hidden.shape, head.shape
+    if len(hs) != 2 or len(ws) != 2 or hs[1] != ws[1]:
         raise ValueError("hidden must be (N, D) and head (V, D)")
-    if tuple(targets.shape) != (hidden.shape[0],):
+    if targets.shape != hs[:1]:
         raise ValueError("targets must be (N,)")
-    return hidden.shape[0], head.shape[0], hidden.shape[1]
+    return hs[0], ws[0], hs[1]
+
+
+def _logp_inputs(hidden, head, targets):
+    """The three inputs' types, layout and device."""
+    import torch
+    if hidden.dtype != torch.bfloat16 or head.dtype != torch.bfloat16 or targets.dtype != torch.int32:
+        raise ValueError(f"hidden and head must be bfloat16 and targets int32, got {hidden.dtype}, {head.dtype} and {targets.dtype}")
+    at = torch.cuda.current_device()
+    if not hidden.get_device() == head.get_device() == targets.get_device() == at:
+        raise ValueError(f"hidden, head and targets must be on the current CUDA device (cuda:{at})")
+    if not (hidden.is_contiguous() and head.is_contiguous() and targets.is_contiguous()):
+        raise ValueError("hidden, head and targets must be contiguous")
 
 
 def _want(t, shape, name):
@@ -598,16 +611,17 @@ def pa_logp_fwd(hidden, head, targets, logp, lse, entropy, top_ids, top_logp, ws
     int32 and top_logp (N, top) fp32, all outputs (see include/pa.h)."""
     import torch
     N, V, D = _logp_dims(hidden, head, targets)
-    f, bf, i32 = torch.float32, torch.bfloat16, torch.int32
+    f, i32 = torch.float32, torch.int32
     for t, n in ((logp, "logp"), (lse, "lse"), (entropy, "entropy")):
         _want(t, (N,), n)
     for t, n in ((top_ids, "top_ids"), (top_logp, "top_logp")):
         _want(t, (N, top), n)
-    _on_current_device(hidden, head, targets, logp, lse, entropy, top_ids, top_logp, ws)
-    _check(lib().pa_logp_fwd(N, V, D, float(temperature), int(top), _ptr(hidden, bf, "hidden"), _ptr(head, bf, "head"),
-                             _ptr(targets, i32, "targets"), _ptr(logp, f, "logp"), _ptr(lse, f, "lse"),
-                             _ptr(entropy, f, "entropy"), _ptr(top_ids, i32, "top_ids"),
-                             _ptr(top_logp, f, "top_logp"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    _logp_inputs(hidden, head, targets)
+    _on_current_device(logp, lse, entropy, top_ids, top_logp, ws)
+    _check(lib().pa_logp_fwd(N, V, D, float(temperature), int(top), hidden.data_ptr(), head.data_ptr(), targets.data_ptr(),
+                             _ptr(logp, f, "logp"), _ptr(lse, f, "lse"), _ptr(entropy, f, "entropy"),
+                             _ptr(top_ids, i32, "top_ids"), _ptr(top_logp, f, "top_logp"), _ptr(ws, torch.uint8, "ws"),
+                             ws.numel(), _stream(stream)))
 
 
 def token_logprobs_forward(hidden, head, targets, temperature=1.0, top=0, ws=None):
@@ -618,16 +632,19 @@ def token_logprobs_forward(hidden, head, targets, temperature=1.0, top=0, ws=Non
     top_logp), the last two None when top is 0."""
     import torch
     N, V, D = _logp_dims(hidden, head, targets)
-    dev, f = hidden.device, torch.float32
+    dev, f, empty = hidden.device, torch.float32, torch.empty
     if ws is None:
         n = pa_logp_workspace_bytes(N, V, D, top)
         if n == 0:
             raise PAError(4, "invalid token log probability dims")
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    logp, lse, entropy = (torch.empty(N, dtype=f, device=dev) for _ in range(3))
-    ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
-    alt = torch.empty((N, top), dtype=f, device=dev) if top else None
-    pa_logp_fwd(hidden, head, targets, logp, lse, entropy, ids, alt, ws, temperature, top)
+        ws = empty(n, dtype=torch.uint8, device=dev)
+    logp, lse, entropy = empty(N, dtype=f, device=dev), empty(N, dtype=f, device=dev), empty(N, dtype=f, device=dev)
+    ids, alt = (empty((N, top), dtype=torch.int32, device=dev), empty((N, top), dtype=f, device=dev)) if top else (None, None)
+    _logp_inputs(hidden, head, targets)
+    _on_current_device(ws)
+    _check(lib().pa_logp_fwd(N, V, D, float(temperature), top, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(),
+                             logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), ids.data_ptr() if top else None,
+                             alt.data_ptr() if top else None, _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(None)))
     return logp, lse, entropy, ids, alt
 
 
@@ -647,9 +664,10 @@ def pa_logp_bwd(hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden,
         _want(t, (N,), n)
     _want(dhidden, (N, D), "dhidden")
     _want(dhead, (V, D), "dhead")
-    _on_current_device(hidden, head, targets, lse, entropy, g_logp, g_entropy, dhidden, dhead, ws)
-    _check(lib().pa_logp_bwd(N, V, D, float(temperature), _ptr(hidden, bf, "hidden"), _ptr(head, bf, "head"),
-                             _ptr(targets, torch.int32, "targets"), _ptr(lse, f, "lse"), _ptr(entropy, f, "entropy"),
+    _logp_inputs(hidden, head, targets)
+    _on_current_device(lse, entropy, g_logp, g_entropy, dhidden, dhead, ws)
+    _check(lib().pa_logp_bwd(N, V, D, float(temperature), hidden.data_ptr(), head.data_ptr(), targets.data_ptr(),
+                             _ptr(lse, f, "lse"), _ptr(entropy, f, "entropy"),
                              _ptr(g_logp, f, "g_logp"), _ptr(g_entropy, f, "g_entropy"), _ptr(dhidden, bf, "dhidden"),
                              _ptr(dhead, bf, "dhead"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
 
@@ -663,9 +681,8 @@ def token_logprobs_backward(hidden, head, targets, lse, entropy, g_logp, g_entro
     import torch
     if isinstance(hidden, Checkpoint):
         hidden = checkpoint_load([hidden])[0]
-    N, V, D = _logp_dims(hidden, head, targets)
     if ws is None:
-        n = pa_logp_bwd_workspace_bytes(N, V, D)
+        n = pa_logp_bwd_workspace_bytes(*_logp_dims(hidden, head, targets))
         if n == 0:
             raise PAError(4, "invalid token log probability dims")
         ws = torch.empty(n, dtype=torch.uint8, device=hidden.device)
@@ -684,14 +701,14 @@ class Checkpoint:
 
     def __init__(self, codes, scales, block=64, dtype=None):
         import torch
-        self.codes, self.scales, self.block = codes, scales, int(block)
-        self.dtype = torch.bfloat16 if dtype is None else dtype
-        _ckpt_format(codes.dtype)
-        if self.block not in (32, 64, 128):
+        if block not in (32, 64, 128):
             raise ValueError(f"block must be 32, 64 or 128, got {block}")
-        want = tuple(codes.shape[:-1]) + (-(-codes.shape[-1] // self.block),)
-        if tuple(scales.shape) != want:
-            raise ValueError(f"scales must be {want}, got {tuple(scales.shape)}")
+        if codes.dtype != torch.int8:
+            _ckpt_format(codes.dtype)
+        shape, blocks = codes.shape, scales.shape
+        if len(shape) != len(blocks) or shape[:-1] != blocks[:-1] or blocks[-1] != -(-shape[-1] // block):
+            raise ValueError(f"scales must be {(*shape[:-1], -(-shape[-1] // block))}, got {tuple(blocks)}")
+        self.codes, self.scales, self.block, self.dtype = codes, scales, block, torch.bfloat16 if dtype is None else dtype
 
     @property
     def shape(self):
@@ -715,46 +732,55 @@ _CKPT_FIELDS = struct.Struct("PPPiiiiqqq")  # pa_ckpt_tensor
 _ONES, _ZEROS = ((), (1,), (1, 1), (1, 1, 1)), ((), (0,), (0, 0), (0, 0, 0))
 
 
-def _ckpt_call(fn, xs, cs, stream):
-    """pa_ckpt_save or pa_ckpt_load of matching lists, PA_CKPT_MAX_TENSORS a
-    launch. Each tensor has 1 to 4 dims, the last contiguous."""
-    import torch
-    if len(xs) != len(cs):
-        raise ValueError("one checkpoint per tensor")
-    if not xs:
-        return
-    dtype, kind, block = xs[0].dtype, cs[0].codes.dtype, cs[0].block
-    io, fmt, f32, at = _io_dtype(xs[0])[1], _ckpt_format(kind), torch.float32, torch.cuda.current_device()
-    pack, parts = _CKPT_FIELDS.pack, []
-    for x, c in zip(xs, cs):
-        codes, scales, shape, stride = c.codes, c.scales, x.shape, x.stride()
-        pad = 4 - len(shape)
-        if x.dtype != dtype or codes.dtype != kind or c.block != block:
-            raise ValueError("the tensors of one call share their type, format and block")
-        if not 0 <= pad <= 3 or (stride[-1] != 1 and shape[-1] > 1):
-            raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
-        if codes.shape != shape:
-            raise ValueError(f"codes must be {tuple(shape)}, got {tuple(codes.shape)}")
-        if not x.get_device() == codes.get_device() == scales.get_device() == at:
-            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
-        if not (codes.is_contiguous() and scales.is_contiguous()) or scales.dtype != f32:
-            raise ValueError("codes and scales must be contiguous, scales float32")
-        parts.append(pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *_ONES[pad], *shape, *_ZEROS[pad],
-                          *stride[:-1]))
+def _ckpt_of(x, codes, scales, at):
+    """The bytes of the C description of tensor x (1 to 4 dims, the last
+    contiguous) with codes and scales (contiguous) on device `at`."""
+    shape, stride = x.shape, x.stride()
+    pad = 4 - len(shape)
+    if not 0 <= pad <= 3 or (stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
+    if not x.get_device() == codes.get_device() == scales.get_device() == at:
+        raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+    return _CKPT_FIELDS.pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *_ONES[pad], *shape, *_ZEROS[pad],
+                             *stride[:-1])
+
+
+def _ckpt_call(fn, parts, io, fmt, block, stream):
     st = _stream(stream)
     for i in range(0, len(parts), PA_CKPT_MAX_TENSORS):
         some = parts[i:i + PA_CKPT_MAX_TENSORS]
         _check(fn(len(some), b"".join(some), io, fmt, block, st))
 
 
+def _ckpt_lists(fn, xs, cs, stream):
+    """pa_ckpt_save or pa_ckpt_load of matching lists, PA_CKPT_MAX_TENSORS a launch."""
+    import torch
+    if len(xs) != len(cs):
+        raise ValueError("one checkpoint per tensor")
+    if not xs:
+        return
+    dtype, kind, block, f32 = xs[0].dtype, cs[0].codes.dtype, cs[0].block, torch.float32
+    io, fmt, at, parts = _io_dtype(xs[0])[1], _ckpt_format(kind), torch.cuda.current_device(), []
+    for x, c in zip(xs, cs):
+        codes, scales = c.codes, c.scales
+        if x.dtype != dtype or codes.dtype != kind or c.block != block:
+            raise ValueError("the tensors of one call share their type, format and block")
+        if codes.shape != x.shape:
+            raise ValueError(f"codes must be {tuple(x.shape)}, got {tuple(codes.shape)}")
+        if not (codes.is_contiguous() and scales.is_contiguous()) or scales.dtype != f32:
+            raise ValueError("codes and scales must be contiguous, scales float32")
+        parts.append(_ckpt_of(x, codes, scales, at))
+    _ckpt_call(fn, parts, io, fmt, block, stream)
+
+
 def pa_ckpt_save(tensors, checkpoints, stream=None):
     """Fill the checkpoints' codes and scales (see include/pa.h)."""
-    _ckpt_call(lib().pa_ckpt_save, tensors, checkpoints, stream)
+    _ckpt_lists(lib().pa_ckpt_save, tensors, checkpoints, stream)
 
 
 def pa_ckpt_load(tensors, checkpoints, stream=None):
     """Fill the tensors from the checkpoints (see include/pa.h)."""
-    _ckpt_call(lib().pa_ckpt_load, tensors, checkpoints, stream)
+    _ckpt_lists(lib().pa_ckpt_load, tensors, checkpoints, stream)
 
 
 def checkpoint_save(tensors, format="int8", block=64):
@@ -767,16 +793,24 @@ def checkpoint_save(tensors, format="int8", block=64):
         raise ValueError(f"format must be int8 or e4m3, got {format!r}")
     if block not in (32, 64, 128):
         raise ValueError(f"block must be 32, 64 or 128, got {block}")
-    tensors, kept = list(tensors), []
-    kind, f32, empty = torch.int8 if format == "int8" else torch.float8_e4m3fn, torch.float32, torch.empty
+    tensors = list(tensors)
+    if not tensors:
+        return []
+    kept, parts, empty, f32, new = [], [], torch.empty, torch.float32, object.__new__
+    kind, fmt = (torch.int8, PA_CKPT_INT8) if format == "int8" else (torch.float8_e4m3fn, PA_CKPT_E4M3)
+    (dtype, io), at = _io_dtype(tensors[0]), torch.cuda.current_device()
     for x in tensors:
-        shape, dev, c = x.shape, x.device, object.__new__(Checkpoint)
+        if x.dtype != dtype:
+            raise ValueError("the tensors of one call share their type")
+        shape, dev, c = x.shape, x.device, new(Checkpoint)
         if not shape:
             raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
-        c.codes, c.block, c.dtype = empty(shape, dtype=kind, device=dev), block, x.dtype
-        c.scales = empty((*shape[:-1], -(-shape[-1] // block)), dtype=f32, device=dev)
+        c.codes = codes = empty(shape, dtype=kind, device=dev)
+        c.scales = scales = empty((*shape[:-1], -(-shape[-1] // block)), dtype=f32, device=dev)
+        c.block, c.dtype = block, dtype
         kept.append(c)
-    pa_ckpt_save(tensors, kept)
+        parts.append(_ckpt_of(x, codes, scales, at))
+    _ckpt_call(lib().pa_ckpt_save, parts, io, fmt, block, None)
     return kept
 
 
@@ -801,32 +835,38 @@ def pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale=0.0, stream=
     dout and dq share their strides, dk and dv theirs; seg None = plain
     causal."""
     import torch
-    bf, f, kind, block = torch.bfloat16, torch.float32, q.codes.dtype, q.block
-    if q.codes.dim() != 4 or k.codes.dim() != 4:
-        raise ValueError("q and k must be checkpoints of (B, H, N, D) tensors")
+    bf, f, kind, block, at = torch.bfloat16, torch.float32, q.codes.dtype, q.block, torch.cuda.current_device()
     qs, ks = q.codes.shape, k.codes.shape
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("q and k must be checkpoints of (B, H, N, D) tensors")
     B, Hq, N, D = qs
     Hkv = ks[1]
     kept = []
     for c, want, n in ((q, qs, "q"), (k, (B, Hkv, N, D), "k"), (v, ks, "v"), (out, qs, "out")):
-        codes = c.codes
+        codes, scales = c.codes, c.scales
         if codes.shape != want:
             raise ValueError(f"{n} must be {tuple(want)}, got {tuple(codes.shape)}")
-        if codes.dtype != kind or c.block != block or c.dtype != bf:
+        if codes.dtype != kind or c.block != block or c.dtype != bf or scales.dtype != f:
             raise ValueError("q, k, v and out must be bf16 checkpoints in one format and block")
-        kept.append(pa_ckpt(_ptr(codes, kind, n), _ptr(c.scales, f, n)))
-    for t, want, n in ((dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"), (dv, ks, "dv"), (lse, (B, Hq, N), "lse")):
-        if t.shape != want:
-            raise ValueError(f"{n} must be {tuple(want)}, got {tuple(t.shape)}")
-    _want(seg, (B, N), "seg")
-    _on_current_device(q.codes, q.scales, k.codes, k.scales, v.codes, v.scales, out.codes, out.scales, dout, lse, seg, dq,
-                       dk, dv, ws)
-    st = None if _all_contiguous(dout, dq, dk, dv) else _strides_of(dout, dk)
-    ref = ctypes.byref
-    _check(lib().pa_bwd_ckpt(ref(make_dims(B, Hq, Hkv, N, D, scale)), st and ref(st), _ckpt_format(kind), block, ref(kept[0]),
-                             ref(kept[1]), ref(kept[2]), ref(kept[3]), _ptr_rows(dout, bf, "dout"), _ptr(lse, f, "lse"),
-                             _ptr(seg, torch.int32, "seg"), _ptr_rows(dq, bf, "dq", dout), _ptr_rows(dk, bf, "dk"),
-                             _ptr_rows(dv, bf, "dv", dk), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        if not codes.get_device() == scales.get_device() == at or not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous and on the current CUDA device (cuda:{at})")
+        kept.append(ctypes.byref(pa_ckpt(codes.data_ptr(), scales.data_ptr())))
+    plain = True
+    for t, want, n in ((dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"), (dv, ks, "dv")):
+        if t.shape != want or t.dtype != bf or t.get_device() != at or t.stride(3) != 1:
+            raise ValueError(f"{n} must be {tuple(want)} {bf} with a contiguous last dim on the current CUDA device (cuda:{at})")
+        plain = plain and t.is_contiguous()
+    if lse.shape != (B, Hq, N) or (seg is not None and seg.shape != (B, N)):
+        raise ValueError(f"lse must be {(B, Hq, N)} and seg {(B, N)}")
+    _on_current_device(lse, seg, ws)
+    st = None
+    if not plain:
+        if dq.stride() != dout.stride() or dk.stride() != dv.stride():
+            raise ValueError("dq must have dout's strides and dv dk's")
+        st = ctypes.byref(_strides_of(dout, dk))
+    _check(lib().pa_bwd_ckpt(ctypes.byref(pa_dims(B, Hq, Hkv, N, D, scale)), st, _ckpt_format(kind), block, *kept,
+                             dout.data_ptr(), _ptr(lse, f, "lse"), _ptr(seg, torch.int32, "seg"), dq.data_ptr(),
+                             dk.data_ptr(), dv.data_ptr(), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
 
 
 def backward_from_checkpoint(q, k, v, out, dout, lse, seg=None, scale=0.0, ws=None):
