@@ -786,7 +786,7 @@ pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t fo
   const pa::CkptTensor qkv[3] = {kept(q, L.q, dims->Hq), kept(k, L.k, dims->Hkv), kept(v, L.v, dims->Hkv)};
   if (pa::launch_tile_table(p, const_cast<int4*>(p.tiles), st) != cudaSuccess ||
       pa::launch_bwd_ckpt_prologue(p, dims->D, rs, qkv, out->codes, out->scales, format, block, st) != cudaSuccess ||
-      pa::launch_bwd_dkv(p, dims->D, rs, w + L.q, w + L.k, w + L.v, dout, st, &in) != cudaSuccess ||
+      pa::launch_bwd_dkv(p, dims->D, rs, w + L.q, w + L.k, w + L.v, dout, st, &in, true) != cudaSuccess ||
       // dK/dV first: its blocks are fewer and longer, and dQ's fill the SMs that they leave
       pa::launch_bwd_dq(p, dims->D, rs, w + L.q, w + L.k, w + L.v, dout, st, &in, true) != cudaSuccess)
     return PA_ERR_CUDA;

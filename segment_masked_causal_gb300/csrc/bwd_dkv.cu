@@ -23,6 +23,12 @@
 // warps have read dP^T_i, and dP^T_{i+1} goes where P^T_i/dS^T_i were once
 // the gradient MMAs of step i have read them.
 //
+// With PF32 dS^T is formed from P^T as it was before its rounding, which then
+// stays in registers between the phases: one rounding to bf16 instead of two in
+// dK (an error of 2.3e-3 instead of 2.9e-3 of its norm). The backward from 8-bit
+// checkpoints runs that form (it costs the packed 8k row 1% of its time); the
+// others keep theirs and its bits.
+//
 // Two warps issue MMAs, each in its own order, so neither waits behind the
 // other's dependencies: one issues S^T_i and dP^T_i (looking ahead), the
 // other dV_i as soon as P^T_i is ready and dK_i once dS^T_i is. The
@@ -84,7 +90,7 @@ struct DkvLayout {
   static __device__ __forceinline__ uint32_t reg_dp(int i) { return (i & 1) ? TM_X : TM_Y; }
 };
 
-template <int D, int DM, bool T4>
+template <int D, int DM, bool T4, bool PF32>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -330,6 +336,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const int c0 = hsel * 32;        // first query column of this thread within the tile
         const int q0 = tq * kTile + c0;  // its token index
         // ---- phase A: P^T = exp2(S^T * scale*log2e - lse*log2e), bf16 over S^T
+        float pf[PF32 ? 32 : 1];
         {
           uint32_t sv[32];
           tmem_ld32(sreg, sv);
@@ -353,6 +360,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             float pz[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) pz[e] = ex2(fmaf(sz[e], sl2, -lz[e]));
+            if (PF32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pf[(e4 * 4 + e) & (PF32 ? 31 : 0)] = pz[e];
+            }
             pw[e4 * 2] = pack_bf16x2(pz[0], pz[1]);
             pw[e4 * 2 + 1] = pack_bf16x2(pz[2], pz[3]);
           }
@@ -367,11 +378,32 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         tc_fence_after();
         const float4* d4 = reinterpret_cast<const float4*>(&m.dl[ds][c0]);
-        uint32_t dpa[32], pb[16];
-        tmem_ld32_ld16(dreg, sreg, dpa, pb);
-        tc_fence_before();
-        mbar_arrive(&m.dp_free[i & 1]);
-        {
+        if (PF32) {
+          // half the columns at a time, beside the 32 values of P that stay in registers
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t dpa[16], dw[8];
+            tmem_ld16(dreg + 16 * h, dpa);
+            if (h == 1) {
+              tc_fence_before();
+              mbar_arrive(&m.dp_free[i & 1]);
+            }
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+              const float4 dv = d4[4 * h + e4];
+              const float* pp = &pf[(16 * h + 4 * e4) & (PF32 ? 31 : 0)];
+              dw[e4 * 2] = pack_bf16x2(pp[0] * (__uint_as_float(dpa[e4 * 4]) - dv.x),
+                                       pp[1] * (__uint_as_float(dpa[e4 * 4 + 1]) - dv.y));
+              dw[e4 * 2 + 1] = pack_bf16x2(pp[2] * (__uint_as_float(dpa[e4 * 4 + 2]) - dv.z),
+                                           pp[3] * (__uint_as_float(dpa[e4 * 4 + 3]) - dv.w));
+            }
+            tmem_st8_nowait(sreg + 16 + 8 * h, dw);
+          }
+        } else {
+          uint32_t dpa[32], pb[16];
+          tmem_ld32_ld16(dreg, sreg, dpa, pb);
+          tc_fence_before();
+          mbar_arrive(&m.dp_free[i & 1]);
           uint32_t dw[16];
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) {
@@ -447,7 +479,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
 template <int D, int DM = D>
 cudaError_t launch_dkv_d(const AttnParams& p, int Dio, const RowStrides& rs, const void* q, const void* k,
-                         const void* v, const void* dout, cudaStream_t st, const RowStrides& in) {
+                         const void* v, const void* dout, cudaStream_t st, const RowStrides& in, bool fp32_p) {
   using L = DkvLayout<D>;
   CUtensorMap tq, tdo, tk, tv, tdk, tdv;
   // contiguous tensors: 2-D maps over their rows (cheaper for TMA than the
@@ -467,7 +499,8 @@ cudaError_t launch_dkv_d(const AttnParams& p, int Dio, const RowStrides& rs, con
     return cudaErrorInvalidValue;
   // the tensor maps' form is fixed at compile time: the contiguous case runs
   // exactly the 2-D code
-  const auto kfn = pp.tma4 ? dkv_kernel<D, DM, true> : dkv_kernel<D, DM, false>;
+  const auto kfn = fp32_p ? (pp.tma4 ? dkv_kernel<D, DM, true, true> : dkv_kernel<D, DM, false, true>)
+                          : (pp.tma4 ? dkv_kernel<D, DM, true, false> : dkv_kernel<D, DM, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(p.T * p.Hkv * p.B);
@@ -478,14 +511,14 @@ cudaError_t launch_dkv_d(const AttnParams& p, int Dio, const RowStrides& rs, con
 }  // namespace
 
 cudaError_t launch_bwd_dkv(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in) {
+                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in, bool fp32_p) {
   // head dim 96 runs the 128-wide tile layout: its tensor maps are 96
   // elements wide, so TMA fills columns 96..127 of every loaded tile with
   // zeros and drops them from every store; the MMAs contract over 96 (six
   // K-steps) and produce 96 columns (N = 96), so no work is spent on them.
-  if (D == 64) return launch_dkv_d<64>(p, 64, rs, q, k, v, dout, st, in ? *in : rs);
-  if (D == 96) return launch_dkv_d<128, 96>(p, 96, rs, q, k, v, dout, st, in ? *in : rs);
-  return launch_dkv_d<128>(p, 128, rs, q, k, v, dout, st, in ? *in : rs);
+  if (D == 64) return launch_dkv_d<64>(p, 64, rs, q, k, v, dout, st, in ? *in : rs, fp32_p);
+  if (D == 96) return launch_dkv_d<128, 96>(p, 96, rs, q, k, v, dout, st, in ? *in : rs, fp32_p);
+  return launch_dkv_d<128>(p, 128, rs, q, k, v, dout, st, in ? *in : rs, fp32_p);
 }
 
 }  // namespace pa

@@ -51,13 +51,15 @@ cudaError_t launch_exp2_fma_selftest(const float* x, float* y, int64_t n, cudaSt
 cudaError_t launch_fwd(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k, const void* v,
                        cudaStream_t st);
 // in: the strides of q, k and v where they are not those of dout and the gradients.
+// fp32_p: dS from P before its rounding to bf16 (see bwd_dkv.cu).
 // beside: launch dQ programmatically behind the kernel ahead of it (dK/dV),
 // of which it needs nothing.
 cudaError_t launch_bwd_dq(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr,
                           bool beside = false);
 cudaError_t launch_bwd_dkv(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
-                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr);
+                           const void* v, const void* dout, cudaStream_t st, const RowStrides* in = nullptr,
+                           bool fp32_p = false);
 // Single-pass backward: dK, dV and the fp32 dQ accumulator p.dq_acc (zeroed
 // beforehand), then p.dq = the accumulator rounded to bf16.
 cudaError_t launch_bwd_fused(const AttnParams& p, int D, const RowStrides& rs, const void* q, const void* k,
