@@ -25,6 +25,16 @@ inline cudaLaunchAttribute programmatic_launch() {
   return a;
 }
 
+// Launch attribute: clusters of two CTAs along x.
+inline cudaLaunchAttribute cluster_pair() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = 2;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
 // Element strides of the (B, H, N, D) tensors the kernels read and write in
 // place (D contiguous): q, out, dout and dq use the q_* strides, k, v, dk and
 // dv the k_* strides.
@@ -139,7 +149,11 @@ constexpr int kLogpUnit = 32;
 constexpr int kLogpMaxSplits = 160;
 constexpr int kLogpMaxTop = 32;
 int logp_max_splits(int N, int V);
-LceSplit logp_split(int N, int V, int slots);
+struct LogpPlan {
+  bool pair;  // two CTAs per product
+  int splits, per;
+};
+LogpPlan logp_plan(int N, int V, int sms);
 struct LogpFwdLayout {
   size_t part, cand, bytes;  // after the 256-byte status region
 };

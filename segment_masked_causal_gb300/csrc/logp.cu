@@ -31,21 +31,31 @@
 namespace pa {
 namespace {
 
-constexpr int kStages = 4;                 // 4 x 48 KB: one CTA per SM
-constexpr int kTok = 128;                  // tokens per CTA: the MMA's rows
+constexpr int kTok = 128;                  // tokens per CTA
 constexpr int kUnit = kLogpUnit;           // vocabulary rows of one unit: what splits are counted in
 constexpr int kTileUnits = 8;              // units per logit tile: 256 columns
 constexpr uint32_t kSliceH = kTok * 128;   // 128 x 64 bf16, 16 KB
-constexpr uint32_t kSliceU = kUnit * 128;  // 32 x 64 bf16, 4 KB
-constexpr uint32_t kStage = kSliceH + kTileUnits * kSliceU;
 constexpr int kThreads = 256;
 constexpr uint32_t kTmemCols = 512;  // two 256-column fp32 accumulators
-constexpr uint32_t kSmem = 1024 /* misc */ + 1024 /* alignment */ + kStages * kStage;
-static_assert(kSmem <= 232448, "shared memory");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The ring of K slices: one CTA per SM. PAIR: two CTAs form one product of 256
+// tokens x 256 vocabulary rows, each holding its own 128 tokens and half of the
+// vocabulary rows. A tile of 128 x 256 alone takes 48 KB a K slice into an SM
+// for 512 cycles of products, and an SM's port to the L2 moves 64 bytes a
+// cycle, 768 cycles: the tensor pipe is 60% busy. The pair takes 32 KB.
+template <bool PAIR>
+struct Ring {
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr uint32_t UNIT = (PAIR ? kUnit / 2 : kUnit) * 128;  // this CTA's rows of a unit
+  static constexpr uint32_t STAGE = kSliceH + kTileUnits * UNIT;
+  static constexpr uint32_t BYTES = STAGES * STAGE;
+};
+constexpr uint32_t kSmem = 1024 /* misc */ + 1024 /* alignment */ + Ring<false>::BYTES;
+static_assert(Ring<true>::BYTES == Ring<false>::BYTES && kSmem <= 232448, "shared memory");
+
 struct Misc {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[6], empty[6];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t fin;
   uint32_t tmem_base;
@@ -114,106 +124,158 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   return r;
 }
 
+// Barriers and TMEM. In a pair the full and acc_empty barriers of rank 0 serve
+// both CTAs; the others are each CTA's own.
+template <bool PAIR>
 __device__ __forceinline__ void setup(Misc& m) {
   if (threadIdx.x == 0) {
     m.abort_flag = 0;
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < Ring<PAIR>::STAGES; ++s) {
       mbar_init(&m.full[s], 1);
       mbar_init(&m.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&m.acc_full[b], 1);
-      mbar_init(&m.acc_empty[b], 128);
+      mbar_init(&m.acc_empty[b], PAIR ? 256 : 128);
     }
     mbar_init(&m.fin, 1);
     fence_mbar_init();
   }
   if ((threadIdx.x >> 5) == 1) {
-    tmem_alloc(&m.tmem_base, kTmemCols);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&m.tmem_base, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&m.tmem_base, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // both CTAs' barriers are ready
   tc_fence_after();
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void teardown(uint32_t tmem) {
   tc_fence_before();
   __syncthreads();
+  // neither CTA of a pair leaves while the other's products read its shared memory
+  if (PAIR) cluster_sync();
   if ((threadIdx.x >> 5) == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, kTmemCols);
+    else
+      tmem_dealloc(tmem, kTmemCols);
   }
 }
 
 // Warp 0, lane 0: 64-wide K slices of H and W through the ring. The tile's
 // tokens are one box of 128 / reps rows loaded `reps` times, one below the
-// other. A whole tile of W is one 256-row box, a shorter one its units one by
-// one (eight-row swizzle atoms, so the boxes' layouts join).
-template <class TileOf>
+// other. A whole tile of W is one box, a shorter one its units one by one
+// (eight-row swizzle atoms, so the boxes' layouts join). In a pair each CTA
+// loads its own tokens and its half of the tile's vocabulary rows, the first
+// half in rank 0, and rank 0's barrier counts the bytes of both.
+template <bool PAIR, class TileOf>
 __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* ring, const CUtensorMap* tmH,
                                            const CUtensorMap* tmW, const CUtensorMap* tmWu, int nt, int KS, int reps,
                                            TileOf tile_of) {
+  using R = Ring<PAIR>;
   prefetch_tmap(tmH);
   prefetch_tmap(tmW);
   prefetch_tmap(tmWu);
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
   int it = 0;
   bool ok = true;
   for (int j = 0; ok && j < nt; ++j) {
     const Tile t = tile_of(j);
+    const int w0 = t.u * kUnit + (PAIR ? (int)rank * t.units * (kUnit / 2) : 0);  // first vocabulary row here
     for (int kc = 0; kc < KS; ++kc, ++it) {
-      const int st = it % kStages;
-      if (!g.wait(&m.empty[st], ((it / kStages) & 1) ^ 1, 50)) { ok = false; break; }
-      uint8_t* sh = ring + st * kStage;
-      mbar_expect_tx(&m.full[st], kSliceH + t.units * kSliceU);
+      const int st = it % R::STAGES;
+      if (!g.wait(&m.empty[st], ((it / R::STAGES) & 1) ^ 1, 50)) { ok = false; break; }
+      uint8_t* sh = ring + st * R::STAGE;
+      if (PAIR) {
+        const uint32_t full = cluster_addr(&m.full[st], 0);
+        if (rank == 0) mbar_expect_tx(&m.full[st], 2 * (kSliceH + t.units * R::UNIT));
+        tma_load_2d_pair(sh, tmH, full, kc * 64, t.tm * kTok);
+        if (t.units == kTileUnits) {
+          tma_load_2d_pair(sh + kSliceH, tmW, full, kc * 64, w0);
+        } else {
+          for (int x = 0; x < t.units; ++x)
+            tma_load_2d_pair(sh + kSliceH + x * R::UNIT, tmWu, full, kc * 64, w0 + x * (kUnit / 2));
+        }
+        continue;
+      }
+      mbar_expect_tx(&m.full[st], kSliceH + t.units * R::UNIT);
       for (int r = 0; r < reps; ++r)
         tma_load_2d(sh + r * (kSliceH / reps), tmH, &m.full[st], kc * 64, t.tm * (kTok / reps));
       if (t.units == kTileUnits) {
-        tma_load_2d(sh + kSliceH, tmW, &m.full[st], kc * 64, t.u * kUnit);
+        tma_load_2d(sh + kSliceH, tmW, &m.full[st], kc * 64, w0);
       } else {
         for (int x = 0; x < t.units; ++x)
-          tma_load_2d(sh + kSliceH + x * kSliceU, tmWu, &m.full[st], kc * 64, (t.u + x) * kUnit);
+          tma_load_2d(sh + kSliceH + x * R::UNIT, tmWu, &m.full[st], kc * 64, w0 + x * kUnit);
       }
     }
   }
-  // no copy may still be landing when the CTA exits
-  for (int i = (it > kStages ? it - kStages : 0); i < it; ++i) g.drain(&m.full[i % kStages], (i / kStages) & 1);
+  // No copy may still be landing when the CTA exits, and in a pair no arrival
+  // of the other CTA's: there each stage's last release says both.
+  for (int i = (it > R::STAGES ? it - R::STAGES : 0); i < it; ++i)
+    g.drain(PAIR ? &m.empty[i % R::STAGES] : &m.full[i % R::STAGES], (i / R::STAGES) & 1);
 }
 
-// Warp 1: the tile's products into accumulator j mod 2. The whole warp runs
-// the loop and the waits; lane 0 issues.
-template <class TileOf>
+// Warp 1 (of rank 0 in a pair): the tile's products into accumulator j mod 2.
+// The whole warp runs the loop and the waits; lane 0 issues.
+template <bool PAIR, class TileOf>
 __device__ __forceinline__ void multiply_tiles(Misc& m, const Guard& g, uint32_t sRing, uint32_t tmem, int nt, int KS,
                                                TileOf tile_of) {
+  using R = Ring<PAIR>;
+  if (PAIR && cluster_rank() != 0) return;
   const bool leader = (threadIdx.x & 31) == 0;
   bool ok = true;
   int it = 0;
   for (int j = 0; ok && j < nt; ++j) {
     const int buf = j & 1;
-    const uint32_t id = idesc_bf16_f32(128, tile_of(j).units * kUnit, false, false);
+    const uint32_t id = idesc_bf16_f32(PAIR ? 256 : 128, tile_of(j).units * kUnit, false, false);
     if (j >= 2 && !g.wait_warp(&m.acc_empty[buf], ((j - 2) >> 1) & 1, 51)) { ok = false; break; }
+    if (PAIR) fence_cluster();  // half of the arrivals are the other CTA's
     tc_fence_after();
     for (int kc = 0; kc < KS; ++kc, ++it) {
-      const int st = it % kStages;
-      if (!g.wait_warp(&m.full[st], (it / kStages) & 1, 52)) { ok = false; break; }
+      const int st = it % R::STAGES;
+      if (!g.wait_warp(&m.full[st], (it / R::STAGES) & 1, 52)) { ok = false; break; }
       tc_fence_after();
-      const uint64_t hd = sdesc_sw128(sRing + st * kStage, 16, 1024);
-      const uint64_t wd = sdesc_sw128(sRing + st * kStage + kSliceH, 16, 1024);
+      const uint64_t hd = sdesc_sw128(sRing + st * R::STAGE, 16, 1024);
+      const uint64_t wd = sdesc_sw128(sRing + st * R::STAGE + kSliceH, 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (leader)
-          umma_bf16(tmem + buf * 256, sdesc_add(hd, kk * 32), sdesc_add(wd, kk * 32), id, (kc > 0 || kk > 0) ? 1u : 0u);
-      if (leader) umma_commit(&m.empty[st]);
+        if (leader) {
+          const uint32_t add = (kc > 0 || kk > 0) ? 1u : 0u;
+          if (PAIR)
+            umma_bf16_pair(tmem + buf * 256, sdesc_add(hd, kk * 32), sdesc_add(wd, kk * 32), id, add);
+          else
+            umma_bf16(tmem + buf * 256, sdesc_add(hd, kk * 32), sdesc_add(wd, kk * 32), id, add);
+        }
+      if (leader) PAIR ? umma_commit_pair(&m.empty[st]) : umma_commit(&m.empty[st]);
       __syncwarp();
     }
-    if (ok && leader) umma_commit(&m.acc_full[buf]);
+    if (ok && leader) PAIR ? umma_commit_pair(&m.acc_full[buf]) : umma_commit(&m.acc_full[buf]);
     __syncwarp();
   }
   if (leader) {
-    umma_commit(&m.fin);  // every MMA issued has completed once this arrives
+    PAIR ? umma_commit_pair_own(&m.fin) : umma_commit(&m.fin);  // every MMA issued has completed once this arrives
     g.drain(&m.fin, 0);
   }
   __syncwarp();
+}
+
+// An epilogue thread has read its share of accumulator `buf`.
+template <bool PAIR>
+__device__ __forceinline__ void release_acc(Misc& m, int buf) {
+  tc_fence_before();
+  if (PAIR)
+    mbar_arrive_cluster(cluster_addr(&m.acc_empty[buf], 0));
+  else
+    mbar_arrive(&m.acc_empty[buf]);
 }
 
 // Put (v, id) into a list that runs from the largest down, behind every entry
@@ -235,7 +297,7 @@ struct Joint {
   float4 sums[4][32];              // [quarter][lane] {m, S, A, the target's raw logit}
   float2 top[4][kLogpMaxTop][32];  // [quarter][slot][lane] {raw logit, vocabulary row}
 };
-static_assert(sizeof(Joint) <= kStages * kStage, "fits the ring");
+static_assert(sizeof(Joint) <= Ring<false>::BYTES, "fits the ring");
 
 // (m, S, A) of two disjoint sets of columns as that of both.
 __device__ __forceinline__ void join(float4& x, const float4& y) {
@@ -301,7 +363,7 @@ __device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, 
 // and each warp takes every second (fourth) 32-column chunk of the tokens,
 // whose results the CTA joins through shared memory at the end. 17 tokens with
 // 20 alternatives at V 151,936, D 4096 took 217 us without and 206 us with it.
-template <int KM>
+template <int KM, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_fwd_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmWu, const FwdParams p) {
@@ -321,16 +383,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // The status word starts at 0: no wait can give up within 2 s of the launch.
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;
-  setup(m);
+  setup<PAIR>(m);
   // the merge may take its place on the SMs; it waits for this kernel's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, p.reps, tile_of);
+    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, p.reps, tile_of);
     __syncwarp();
   } else if (warp == 1) {
-    multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
+    multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     const int groups = 4 / p.reps, share = quarter / groups;  // this warp's share of the columns
@@ -407,10 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(&m.acc_empty[buf]);
+      release_acc<PAIR>(m, buf);
     }
-    if (p.reps > 1) {
+    if (!PAIR && p.reps > 1) {
       // every product has completed and every copy been read: the ring is free
       Joint* joint = reinterpret_cast<Joint*>(ring);
       joint->sums[quarter][lane] = make_float4(m_run, s_run, a_run, tgt);
@@ -432,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  teardown(tmem);
+  teardown<PAIR>(tmem);
 }
 
 // Bits of a float in an unsigned order, both zeros alike; > 0 for every number.
@@ -560,6 +621,7 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 // exactly 0 in rows without a gradient and in columns past V. dz is rounded
 // to bf16, the operand type of the two products that follow (at most
 // 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_dz_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmWu, const BwdParams p) {
@@ -568,29 +630,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int TM = (p.N + kTok - 1) / kTok, units = (p.v_end - p.v_base + kUnit - 1) / kUnit;
+  // token tiles are counted in rows of 256 in a pair
+  constexpr int kPer = PAIR ? 2 : 1;
+  const int cta = (int)blockIdx.x / kPer, ctas = (int)gridDim.x / kPer, rank = PAIR ? (int)blockIdx.x % 2 : 0;
+  const int TM = (p.N + kPer * kTok - 1) / (kPer * kTok), units = (p.v_end - p.v_base + kUnit - 1) / kUnit;
   const int VT = (units + p.tile_units - 1) / p.tile_units;
-  const int nt = (TM * VT - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int nt = (TM * VT - cta + ctas - 1) / ctas;
   const int KS = p.D / 64;
   const Guard g{&m.abort_flag, p.status};
   const auto tile_of = [&](int j) {
-    const int q = (int)blockIdx.x + j * (int)gridDim.x;
-    const int gi = q / (kGroup * VT), r = q - gi * kGroup * VT;
-    const int g0 = gi * kGroup, gs = min(kGroup, TM - g0);
+    constexpr int kG = kGroup / kPer;
+    const int q = cta + j * ctas;
+    const int gi = q / (kG * VT), r = q - gi * kG * VT;
+    const int g0 = gi * kG, gs = min(kG, TM - g0);
     const int u = r / gs * p.tile_units;
-    return Tile{g0 + r % gs, p.v_base / kUnit + u, min(p.tile_units, units - u)};
+    return Tile{(g0 + r % gs) * kPer + rank, p.v_base / kUnit + u, min(p.tile_units, units - u)};
   };
   if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait can give up within 2 s
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  setup(m);
+  setup<PAIR>(m);
   if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");  // the last chunk's products have read dz
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, 1, tile_of);
+    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, 1, tile_of);
     __syncwarp();
   } else if (warp == 1) {
-    multiply_tiles(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
+    multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -648,11 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(&m.acc_empty[buf]);
+      release_acc<PAIR>(m, buf);
     }
   }
-  teardown(tmem);
+  teardown<PAIR>(tmem);
 }
 
 int sm_count() {
@@ -678,9 +743,10 @@ int logp_max_splits(int N, int V) {
 }
 
 // The split that makes waves x (units per CTA + 8) smallest: a CTA's pipeline
-// fill and last epilogue take about as long as one tile of eight units.
-LceSplit logp_split(int N, int V, int slots) {
-  const int TM = (N + kTok - 1) / kTok, U = (V + kUnit - 1) / kUnit;
+// fill and last epilogue take about as long as one tile of eight units. slots:
+// CTAs (or pairs of them) that run at once; rows: tokens of each.
+static LceSplit best_split(int N, int V, int slots, int rows, long long* cost_out) {
+  const int TM = (N + rows - 1) / rows, U = (V + kUnit - 1) / kUnit;
   LceSplit best{1, U};
   long long best_cost = -1;
   for (int s = 1, most = logp_max_splits(N, V); s <= most; ++s) {
@@ -691,7 +757,18 @@ LceSplit logp_split(int N, int V, int slots) {
       best = LceSplit{used, per};
     }
   }
+  *cost_out = best_cost;
   return best;
+}
+
+// Pairs of CTAs where that is faster: a unit takes them two thirds of the time
+// (see Ring), but tokens come in rows of 256, so 777 of them are 1,024 rows
+// instead of 896. Up to 128 tokens the head's bytes are what takes the time.
+LogpPlan logp_plan(int N, int V, int sms) {
+  long long single = 0, paired = 0;
+  const LceSplit a = best_split(N, V, sms, kTok, &single), b = best_split(N, V, sms / 2, 2 * kTok, &paired);
+  const bool pair = N > kTok && sms >= 2 && 2 * paired < 3 * single;
+  return pair ? LogpPlan{true, b.splits, b.per} : LogpPlan{false, a.splits, a.per};
 }
 
 LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
@@ -706,12 +783,13 @@ LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
 cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, const void* hidden, const void* head,
                             const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
                             float* top_logp, void* ws, cudaStream_t st) {
-  const LceSplit sp = logp_split(N, V, sm_count());
+  const LogpPlan sp = logp_plan(N, V, sm_count());
   const LogpFwdLayout L = logp_fwd_layout(N, V, top);
   CUtensorMap tH, tW, tWu;
   const int reps = N <= 32 ? 4 : N <= 64 ? 2 : 1;
   if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok / reps) ||
-      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) || !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit))
+      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / (sp.pair ? 2 : 1)) ||
+      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit / (sp.pair ? 2 : 1)))
     return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(ws);
   FwdParams p{};
@@ -727,11 +805,22 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   p.part = reinterpret_cast<float4*>(w + L.part);
   p.cand = reinterpret_cast<float2*>(w + L.cand);
   p.status = reinterpret_cast<uint32_t*>(w);
-  const auto kfn = top == 0 ? logp_fwd_kernel<0> : top <= 8 ? logp_fwd_kernel<8> : logp_fwd_kernel<kLogpMaxTop>;
+  const auto kfn = top == 0   ? (sp.pair ? logp_fwd_kernel<0, true> : logp_fwd_kernel<0, false>)
+                   : top <= 8 ? (sp.pair ? logp_fwd_kernel<8, true> : logp_fwd_kernel<8, false>)
+                              : (sp.pair ? logp_fwd_kernel<kLogpMaxTop, true> : logp_fwd_kernel<kLogpMaxTop, false>);
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  kfn<<<dim3((N + kTok - 1) / kTok, sp.splits), kThreads, kSmem, st>>>(tH, tW, tWu, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sp.pair ? (N + 2 * kTok - 1) / (2 * kTok) * 2 : (N + kTok - 1) / kTok, sp.splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = cluster_pair();
+    cfg.attrs = &attr;
+    cfg.numAttrs = sp.pair ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, tWu, p)) != cudaSuccess) return e;
+  }
   // a block per token while that fills less than two rounds of the SMs; else
   // as many tokens a block as 40 KB of lists hold, 8 at most
   const size_t lists = (size_t)sp.splits * top * sizeof(float2);
@@ -752,8 +841,8 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
 }
 
 // Units per vocabulary tile of the dz kernel: waves x (units + 1), the one for
-// a tile's fixed cost, is what the longest CTA takes.
-static int dz_tile_units(int TM, int rows, int slots) {
+// a tile's fixed cost, is what the longest CTA (or pair) takes.
+static int dz_tile_units(int TM, int rows, int slots, long long* cost_out) {
   const int units = (rows + kUnit - 1) / kUnit;
   int best = kTileUnits;
   long long best_cost = -1;
@@ -764,6 +853,7 @@ static int dz_tile_units(int TM, int rows, int slots) {
       best = u;
     }
   }
+  *cost_out = best_cost;
   return best;
 }
 
@@ -795,14 +885,22 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(w + L.dz);
   __nv_bfloat16* dzt = reinterpret_cast<__nv_bfloat16*>(w + L.dzt);
   float* acc = reinterpret_cast<float*>(w + L.acc);
+  const int sms = sm_count(), TM1 = (N + kTok - 1) / kTok, TM2 = (N + 2 * kTok - 1) / (2 * kTok);
+  const int first_rows = V < L.vc ? V : L.vc;
+  long long single = 0, paired = 0;
+  dz_tile_units(TM1, first_rows, sms, &single);
+  dz_tile_units(TM2, first_rows, sms / 2, &paired);
+  const bool pair = N > kTok && 2 * paired < 3 * single;  // as in logp_plan
+  const int TM = pair ? TM2 : TM1, slots = pair ? sms / 2 : sms;
   CUtensorMap tH, tW, tWu, tHb;
-  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit) ||
-      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) ||
+      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / (pair ? 2 : 1)) ||
+      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit / (pair ? 2 : 1)) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(logp_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kfn = pair ? logp_dz_kernel<true> : logp_dz_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count(), TM = (N + kTok - 1) / kTok;
-  cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchAttribute attrs[2] = {cluster_pair(), programmatic_launch()};
   // Each kernel but the first is launched programmatically behind the one
   // ahead: dz after the products of the chunk before, dW after dz, dH beside dW.
   for (int c = 0; c < L.chunks; ++c) {
@@ -813,7 +911,8 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     p.D = D;
     p.v_base = cv0;
     p.v_end = cv0 + kc;
-    p.tile_units = dz_tile_units(TM, kc, sms);
+    long long cost = 0;
+    p.tile_units = dz_tile_units(TM, kc, slots, &cost);
     p.first = c == 0;
     p.sl2 = kLog2e / temperature;
     p.inv_t = 1.f / temperature;
@@ -830,13 +929,13 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     const int units = (kc + kUnit - 1) / kUnit;
     const long long pairs = (long long)TM * ((units + p.tile_units - 1) / p.tile_units);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pairs < sms ? (int)pairs : sms);
+    cfg.gridDim = dim3((pairs < slots ? (int)pairs : slots) * (pair ? 2 : 1));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = c == 0 ? 0 : 1;
-    if ((e = cudaLaunchKernelEx(&cfg, logp_dz_kernel, tH, tW, tWu, p)) != cudaSuccess) return e;
+    cfg.attrs = pair ? attrs : attrs + 1;
+    cfg.numAttrs = (pair ? 1 : 0) + (c == 0 ? 0 : 1);
+    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, tWu, p)) != cudaSuccess) return e;
     // dW rows of the chunk = dz^T H (the tokens are the contraction)
     if (dhead) {
       CUtensorMap tA;
