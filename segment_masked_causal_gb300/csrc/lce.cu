@@ -376,16 +376,23 @@ __global__ void __launch_bounds__(256) lce_merge_kernel(const LceParams p, int s
 // (bf16, or an accumulator's start) goes through 32 KB of shared memory and
 // TMA stores: rows written piecewise by their threads cost 32 separate sectors
 // an instruction, which bounds a product of few K (the head's gradient of 96
-// tokens, 131 MB of it, took 49 us that way and @@ us through TMA).
-constexpr int kGemmStages = 4;
+// tokens, 131 MB of it, took 49 us that way and 31 us through TMA).
 constexpr int kGemmN = 256;                               // output columns per tile
 constexpr uint32_t kGemmA = 128 * 128;                    // 128 rows x 64 K, 16 KB
 constexpr uint32_t kGemmBHalf = 64 * 128;                 // 64 K rows x 64 N columns, 8 KB
-constexpr uint32_t kGemmStage = kGemmA + 4 * kGemmBHalf;  // 48 KB
 constexpr int kGemmThreads = 192;
-constexpr uint32_t kGemmOut = 2 * 128 * 128;              // two boxes of 128 rows x 128 bytes on their way out
-constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + kGemmStages * kGemmStage + kGemmOut;
-static_assert(kGemmSmem <= 232448, "shared memory");
+// PAIR: two CTAs of a cluster form one product of 256 x 256, each loading its
+// own 128 rows of A and half of B's columns: 32 KB a K block instead of 48.
+template <bool PAIR>
+struct GemmRing {
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr int BBOXES = PAIR ? 2 : 4;  // boxes of 64 columns of B in this CTA
+  static constexpr uint32_t STAGE = kGemmA + BBOXES * kGemmBHalf;
+  static constexpr uint32_t BYTES = STAGES * STAGE;
+};
+constexpr uint32_t kGemmOut = 2 * 128 * 128;  // two boxes of 128 rows x 128 bytes on their way out
+constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + GemmRing<false>::BYTES + kGemmOut;
+static_assert(GemmRing<true>::BYTES == GemmRing<false>::BYTES && kGemmSmem <= 232448, "shared memory");
 
 // Row blocks per group of the tile order. Measured on the N = 8192,
 // V = 151,936, D = 4096 backward (38 launches a call), in one run: 20.95,
@@ -402,7 +409,7 @@ constexpr int kGemmGroup = PA_LCE_GEMM_GROUP;
 struct GemmParams {
   int M, N, K;         // N a multiple of 64
   int mode;            // GemmMode
-  int m_tiles;         // row blocks of 128
+  int m_tiles;         // row blocks of 128, or of 256 in a pair
   int n_tiles;         // N tiles of kGemmN per row block
   int per_split;       // M tiles x N tiles
   int tiles;           // per_split x the runs that K is cut into
@@ -416,7 +423,7 @@ struct GemmParams {
 };
 
 struct GemmMisc {
-  uint64_t full[kGemmStages], empty[kGemmStages];
+  uint64_t full[6], empty[6];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t fin;
   uint32_t tmem_base;
@@ -447,6 +454,7 @@ __device__ __forceinline__ void store_box(uint32_t taddr, uint32_t out, int r, b
   }
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     lce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const GemmParams p) {
@@ -456,43 +464,52 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                              ~uintptr_t(1023));
   const uint32_t sRing = smem_u32(ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using R = GemmRing<PAIR>;
+  constexpr int kPer = PAIR ? 2 : 1, kRows = 128 * kPer, kGroup = kGemmGroup / kPer;
+  const int cta = (int)blockIdx.x / kPer, ctas = (int)gridDim.x / kPer, rank = PAIR ? (int)blockIdx.x % 2 : 0;
   const int KB = (p.K + 63) / 64;
   // K blocks kb0 .. kb1 - 1 of tile t: its run of the contraction
   const auto tile_run = [&](int t) -> int2 {
     const int k0 = t / p.per_split * p.kb_per;
     return make_int2(k0, min(k0 + p.kb_per, KB));
   };
-  // this CTA's tiles: t = blockIdx.x + j * gridDim.x for j < nt (>= 1: the
+  // this CTA's (or pair's) tiles: t = cta + j * ctas for j < nt (>= 1: the
   // grid is never larger than the tile count)
-  const int nt = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  // first row and column of tile t: group gi holds row blocks g0 .. g0 + gs - 1
+  const int nt = (p.tiles - cta + ctas - 1) / ctas;
+  // first row (of this CTA) and column of tile t: group gi holds row blocks g0 .. g0 + gs - 1
   const auto tile_origin = [&](int t) -> int2 {
     t %= p.per_split;
-    const int gi = t / (kGemmGroup * p.n_tiles), r = t - gi * kGemmGroup * p.n_tiles;
-    const int g0 = gi * kGemmGroup, gs = min(kGemmGroup, p.m_tiles - g0);
-    return make_int2((g0 + r % gs) * 128, (r / gs) * kGemmN);
+    const int gi = t / (kGroup * p.n_tiles), r = t - gi * kGroup * p.n_tiles;
+    const int g0 = gi * kGroup, gs = min(kGroup, p.m_tiles - g0);
+    return make_int2((g0 + r % gs) * kRows + rank * 128, (r / gs) * kGemmN);
   };
   const Guard g{&m.abort_flag, p.status};
 
   if (threadIdx.x == 0) {
     m.abort_flag = 0;
-    for (int s = 0; s < kGemmStages; ++s) {
+    for (int s = 0; s < R::STAGES; ++s) {
       mbar_init(&m.full[s], 1);
       mbar_init(&m.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&m.acc_full[b], 1);
-      mbar_init(&m.acc_empty[b], 128);
+      mbar_init(&m.acc_empty[b], 128 * kPer);
     }
     mbar_init(&m.fin, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&m.tmem_base, 2 * kGemmN);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&m.tmem_base, 2 * kGemmN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&m.tmem_base, 2 * kGemmN);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // both CTAs' barriers are ready
   tc_fence_after();
   // What is launched programmatically behind this kernel may take the SMs that
   // it leaves, but no earlier than the kernel ahead has ended: a kBeside kernel
@@ -508,55 +525,69 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int it = 0;
       bool ok = true;
       for (int j = 0; ok && j < nt; ++j) {
-        const int2 o = tile_origin((int)blockIdx.x + j * (int)gridDim.x);
+        const int2 o = tile_origin(cta + j * ctas);
         const int m0 = o.x, n0 = o.y;
-        const int2 run = tile_run((int)blockIdx.x + j * (int)gridDim.x);
+        const int2 run = tile_run(cta + j * ctas);
         for (int kb = run.x; kb < run.y; ++kb, ++it) {
-          const int st = it % kGemmStages;
-          if (!g.wait(&m.empty[st], ((it / kGemmStages) & 1) ^ 1, 45)) { ok = false; break; }
-          uint8_t* sa = ring + st * kGemmStage;
-          mbar_expect_tx(&m.full[st], kGemmStage);
+          const int st = it % R::STAGES;
+          if (!g.wait(&m.empty[st], ((it / R::STAGES) & 1) ^ 1, 45)) { ok = false; break; }
+          uint8_t* sa = ring + st * R::STAGE;
+          if (PAIR) {  // rank 0's barrier counts the bytes of both
+            const uint32_t full = cluster_addr(&m.full[st], 0);
+            if (rank == 0) mbar_expect_tx(&m.full[st], 2 * R::STAGE);
+            tma_load_2d_pair(sa, &tmA, full, kb * 64, m0);
+            for (int c = 0; c < R::BBOXES; ++c)
+              tma_load_2d_pair(sa + kGemmA + c * kGemmBHalf, &tmB, full, n0 + 64 * (rank * R::BBOXES + c), kb * 64);
+            continue;
+          }
+          mbar_expect_tx(&m.full[st], R::STAGE);
           tma_load_2d(sa, &tmA, &m.full[st], kb * 64, m0);
-          for (int c = 0; c < kGemmN / 64; ++c)
+          for (int c = 0; c < R::BBOXES; ++c)
             tma_load_2d(sa + kGemmA + c * kGemmBHalf, &tmB, &m.full[st], n0 + 64 * c, kb * 64);
         }
       }
-      // no copy may still be landing when the CTA exits
-      for (int i = (it > kGemmStages ? it - kGemmStages : 0); i < it; ++i)
-        g.drain(&m.full[i % kGemmStages], (i / kGemmStages) & 1);
+      // no copy may still be landing when the CTA exits (in a pair, no arrival of
+      // the other CTA's either: each stage's last release says both)
+      for (int i = (it > R::STAGES ? it - R::STAGES : 0); i < it; ++i)
+        g.drain(PAIR ? &m.empty[i % R::STAGES] : &m.full[i % R::STAGES], (i / R::STAGES) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
     const bool leader = lane == 0;
-    constexpr uint32_t idC = idesc_bf16_f32(128, kGemmN, false, true);
+    constexpr uint32_t idC = idesc_bf16_f32(kRows, kGemmN, false, true);
     bool ok = true;
     int it = 0;
-    for (int j = 0; ok && j < nt; ++j) {
+    for (int j = 0; ok && rank == 0 && j < nt; ++j) {  // rank 0 issues for both
       const int buf = j & 1;
       // accumulator buf is free once the epilogue has read tile j - 2 from it
       if (j >= 2 && !g.wait_warp(&m.acc_empty[buf], ((j - 2) >> 1) & 1, 48)) { ok = false; break; }
+      if (PAIR) fence_cluster();  // half of the arrivals are the other CTA's
       tc_fence_after();
-      const int2 run = tile_run((int)blockIdx.x + j * (int)gridDim.x);
+      const int2 run = tile_run(cta + j * ctas);
       for (int kb = run.x; kb < run.y; ++kb, ++it) {
-        const int st = it % kGemmStages;
-        if (!g.wait_warp(&m.full[st], (it / kGemmStages) & 1, 46)) { ok = false; break; }
+        const int st = it % R::STAGES;
+        if (!g.wait_warp(&m.full[st], (it / R::STAGES) & 1, 46)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sa = sRing + st * kGemmStage;
+        const uint32_t sa = sRing + st * R::STAGE;
         const uint64_t ad = sdesc_sw128(sa, 16, 1024);
         const uint64_t bd = sdesc_sw128(sa + kGemmA, kGemmBHalf, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          if (leader)
-            umma_bf16(tmem + buf * kGemmN, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), idC,
-                      (kb > run.x || kk > 0) ? 1u : 0u);
-        if (leader) umma_commit(&m.empty[st]);
+          if (leader) {
+            const uint32_t add = (kb > run.x || kk > 0) ? 1u : 0u;
+            if (PAIR)
+              umma_bf16_pair(tmem + buf * kGemmN, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), idC, add);
+            else
+              umma_bf16(tmem + buf * kGemmN, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), idC, add);
+          }
+        if (leader) PAIR ? umma_commit_pair(&m.empty[st]) : umma_commit(&m.empty[st]);
         __syncwarp();
       }
-      if (ok && leader) umma_commit(&m.acc_full[buf]);
+      if (ok && leader) PAIR ? umma_commit_pair(&m.acc_full[buf]) : umma_commit(&m.acc_full[buf]);
       __syncwarp();
     }
-    if (leader) {
-      umma_commit(&m.fin);  // every MMA issued has completed once this arrives
+    if (leader && rank == 0) {
+      PAIR ? umma_commit_pair_own(&m.fin) : umma_commit(&m.fin);  // every MMA issued has completed once this arrives
       g.drain(&m.fin, 0);
     }
     __syncwarp();
@@ -565,21 +596,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const bool f32 = p.mode == kAccInit, through = f32 || p.mode == kStoreBf16;
-    uint8_t* out = ring + kGemmStages * kGemmStage;
+    uint8_t* out = ring + R::STAGES * R::STAGE;
     const bool issuer = threadIdx.x == 64;
     int box = 0;
+    const auto release = [&](int buf) {
+      if (PAIR)
+        mbar_arrive_cluster(cluster_addr(&m.acc_empty[buf], 0));
+      else
+        mbar_arrive(&m.acc_empty[buf]);
+    };
     if (through && issuer) prefetch_tmap(&tmC);
     for (int j = 0; j < nt; ++j) {
       const int buf = j & 1;
       const bool ok = __all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 47));
       if (!ok) break;
       tc_fence_after();
-      const int2 o = tile_origin((int)blockIdx.x + j * (int)gridDim.x);
+      const int2 o = tile_origin(cta + j * ctas);
       const int m0 = o.x, n0 = o.y;
       const int row = m0 + quarter * 32 + lane;
       if (through) {
         // a box of 128 rows x 128 bytes at a time, through two buffers in turn
-        const int run = ((int)blockIdx.x + j * (int)gridDim.x) / p.per_split, step = f32 ? 32 : 64;
+        const int run = (cta + j * ctas) / p.per_split, step = f32 ? 32 : 64;
 #pragma unroll 1
         for (int c0 = 0; c0 < kGemmN && n0 + c0 < p.N; c0 += step, box ^= 1) {
           if (issuer) bulk_wait_read1();  // the buffer's last copy has left it
@@ -587,17 +624,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           store_box(tmem + lane_base + buf * kGemmN + c0, smem_u32(out) + box * 16384, quarter * 32 + lane, f32);
           fence_async_smem();
           named_bar_sync(1, 128);
-          if (issuer) {
+          if (issuer && m0 < p.M) {
             tma_store_3d(&tmC, out + box * 16384, n0 + c0, m0, run);
             bulk_commit();
           }
         }
         tc_fence_before();
-        mbar_arrive(&m.acc_empty[buf]);
+        release(buf);
         continue;
       }
       // each run of K has an accumulator of its own
-      float* acc = p.acc + (size_t)(((int)blockIdx.x + j * (int)gridDim.x) / p.per_split) * p.M * p.ldacc;
+      float* acc = p.acc + (size_t)((cta + j * ctas) / p.per_split) * p.M * p.ldacc;
 #pragma unroll 1
       for (int c0 = 0; c0 < kGemmN; c0 += 32) {
         uint32_t a[32];
@@ -636,15 +673,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&m.acc_empty[buf]);
+      release(buf);
     }
     if (through && issuer) bulk_wait_all();  // the last stores have completed before the CTA exits
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // neither CTA leaves while the other's products read its shared memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kGemmN);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 2 * kGemmN);
+    else
+      tmem_dealloc(tmem, 2 * kGemmN);
   }
   // beside the kernel ahead of it, this one ends no earlier
   if (p.order == kBeside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -669,11 +710,60 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float4* __restric
 
 }  // namespace
 
+// Fewest K blocks of a run for which pairs are taken: below, a tile is mostly
+// its epilogue, and the cluster's barriers cost more than the loads that a pair
+// saves. Both gradients over V 32,003, D 2048 in us, pairs always / never / from
+// 8 blocks on: 96 tokens 107 / 95 / 95, 256 tokens 128 / 120 / 117, 512 tokens
+// 185 / 192 / 185, 2,048 tokens 471 / 491 / 471.
+#ifndef PA_GEMM_PAIR_BLOCKS
+#define PA_GEMM_PAIR_BLOCKS 8
+#endif
+constexpr int kGemmPairBlocks = PA_GEMM_PAIR_BLOCKS;
+
+// Time of an M x N x K product cut into s runs of K, on `slots` SMs: waves x
+// (blocks per run + 8 for the pipeline's fill and the tile's epilogue), a
+// block on a pair two thirds of the time that it takes one CTA (see
+// GemmRing), in units of a third of that (0.09 us); and, with more than one
+// run, writing and reading the accumulators at 6.5 TB/s. < 0 where a run would
+// be empty.
+static double gemm_cost(int M, int N, int K, int slots, int s, bool pair) {
+  const int KB = (K + 63) / 64, per = (KB + s - 1) / s;
+  if ((KB + per - 1) / per != s || (pair && (M <= 128 || slots < 2 || per < kGemmPairBlocks))) return -1.0;
+  const long long rows = pair ? 256 : 128, at_once = pair ? slots / 2 : slots;
+  const long long tiles = ((M + rows - 1) / rows) * ((N + kGemmN - 1) / kGemmN);
+  const long long waves = (tiles * s + at_once - 1) / at_once;
+  return (double)waves * (per + 8) * (pair ? 2 : 3) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 / 0.09 : 0.0);
+}
+
+int gemm_splits(int M, int N, int K, int slots) {
+  int best = 1;
+  double best_cost = -1;
+  for (int s = 1; s <= 64 && s <= (K + 63) / 64; ++s)
+    for (const bool pair : {false, true}) {
+      const double cost = gemm_cost(M, N, K, slots, s, pair);
+      if (cost >= 0 && (best_cost < 0 || cost < best_cost)) {
+        best_cost = cost;
+        best = s;
+      }
+    }
+  return best;
+}
+
 cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(lce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+  const int KB = (gc.K + 63) / 64, planes = gc.splits > 1 ? gc.splits : 1, kb_per = (KB + planes - 1) / planes;
+  // A short K (a vocabulary's last chunk) may fill fewer runs: the others' tiles
+  // are left out, which leaves their accumulators as they are.
+  const int splits = (KB + kb_per - 1) / kb_per;
+  if (splits != planes && gc.mode != kAccAdd) return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const double one = gemm_cost(gc.M, gc.N, gc.K, sms, splits, false), two = gemm_cost(gc.M, gc.N, gc.K, sms, splits, true);
+  const bool pair = two >= 0 && two < one;
+  const auto kfn = pair ? lce_gemm_kernel<true> : lce_gemm_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   if (e != cudaSuccess) return e;
-  const long long mt = (gc.M + 127) / 128, ntl = (gc.N + kGemmN - 1) / kGemmN;
-  const int KB = (gc.K + 63) / 64, splits = gc.splits > 1 ? gc.splits : 1;
+  const long long rows = pair ? 256 : 128, mt = (gc.M + rows - 1) / rows, ntl = (gc.N + kGemmN - 1) / kGemmN;
   if (mt * ntl * splits > (1ll << 30)) return cudaErrorInvalidValue;
   GemmParams q{};
   q.M = gc.M;
@@ -684,7 +774,7 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   q.n_tiles = (int)ntl;
   q.per_split = (int)(mt * ntl);
   q.tiles = q.per_split * splits;
-  q.kb_per = (KB + splits - 1) / splits;
+  q.kb_per = kb_per;
   q.c = gc.c;
   q.ldc = gc.N;
   q.acc = gc.acc;
@@ -697,42 +787,17 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   } else if (!tmap_3d_sw128(&tC, gc.mode == kAccAdd ? static_cast<void*>(gc.acc) : gc.c, gc.mode == kAccAdd, gc.N, gc.M, 1)) {
     return cudaErrorInvalidValue;  // (only read by the modes that store through it)
   }
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int grid = q.tiles < sms ? q.tiles : sms;
+  const int at_once = pair ? sms / 2 : sms, grid = q.tiles < at_once ? q.tiles : at_once;
   if (grid < 1) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(grid * (pair ? 2 : 1));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr = programmatic_launch();
-  cfg.attrs = &attr;
-  cfg.numAttrs = gc.order == kInOrder ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, lce_gemm_kernel, tA, tB, tC, q);
-}
-
-// Time of a run in K blocks (four 128 x 256 x 16 products, about 0.27 us an
-// SM): waves x (blocks per run + 8 for the pipeline's fill and the tile's
-// epilogue), and, with more than one run, writing and reading the
-// accumulators at 6.5 TB/s.
-int gemm_splits(int M, int N, int K, int slots) {
-  const long long tiles = (long long)((M + 127) / 128) * ((N + kGemmN - 1) / kGemmN);
-  const int KB = (K + 63) / 64;
-  int best = 1;
-  double best_cost = -1;
-  for (int s = 1; s <= 64 && s <= KB; ++s) {
-    const int per = (KB + s - 1) / s;
-    if ((KB + per - 1) / per != s) continue;  // the last run would be empty
-    const long long waves = (tiles * s + slots - 1) / slots;
-    const double cost = (double)waves * (per + 8) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 / 0.27 : 0.0);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
+  cudaLaunchAttribute attrs[2] = {cluster_pair(), programmatic_launch()};
+  cfg.attrs = pair ? attrs : attrs + 1;
+  cfg.numAttrs = (pair ? 1 : 0) + (gc.order == kInOrder ? 0 : 1);
+  return cudaLaunchKernelEx(&cfg, kfn, tA, tB, tC, q);
 }
 
 cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st) {

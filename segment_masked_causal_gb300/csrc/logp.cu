@@ -52,7 +52,10 @@ struct Ring {
   static constexpr uint32_t BYTES = STAGES * STAGE;
 };
 constexpr uint32_t kSmem = 1024 /* misc */ + 1024 /* alignment */ + Ring<false>::BYTES;
-static_assert(Ring<true>::BYTES == Ring<false>::BYTES && kSmem <= 232448, "shared memory");
+// Behind the ring, with alternatives: 32 candidates of each epilogue thread.
+constexpr int kCands = 32;
+constexpr uint32_t kSmemTop = kSmem + kCands * 128 * sizeof(float2);
+static_assert(Ring<true>::BYTES == Ring<false>::BYTES && kSmemTop <= 232448, "shared memory");
 
 struct Misc {
   uint64_t full[6], empty[6];
@@ -102,26 +105,28 @@ struct Tile {
 // cross-entropy backward measured 22.2 ms without groups, 21.0 with 32).
 constexpr int kGroup = 32;
 
-__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
-  float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
-#pragma unroll
-  for (int e = 2; e < 30; e += 4) {
-    a = fmax3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-    b = fmax3(b, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-  }
-  return fmax3(a, b, fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+// The largest of the W values from x[W s] on; NaN is passed over.
+template <int W>
+__device__ __forceinline__ float max_of(const uint32_t (&x)[32], int s) {
+  const auto f = [&](int i) { return __uint_as_float(x[W * s + i]); };
+  if (W == 2) return fmaxf(f(0), f(1));
+  if (W == 4) return fmax3(f(0), f(1), fmaxf(f(2), f(3 % W)));
+  return fmaxf(fmax3(f(0), f(1), f(2 % W)), fmax3(fmax3(f(3 % W), f(4 % W), f(5 % W)), f(6 % W), f(7 % W)));
 }
 
-// One 32-bit column of this thread's TMEM lane.
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r)
-      : "r"(taddr)
-      : "memory");
-  return r;
+// Which of the eight values from a[8 s] on are above `least`, as bits.
+__device__ __forceinline__ uint32_t over8(const uint32_t (&a)[32], int s, float least) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m |= __uint_as_float(a[8 * s + i]) > least ? 1u << i : 0u;
+  return m;
+}
+
+// Two words to shared memory where `on` is not 0, without a branch.
+__device__ __forceinline__ void st_shared_if(uint32_t on, uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.shared.v2.b32 [%1], {%2, %3};\n\t}" ::"r"(on), "r"(addr),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 // Barriers and TMEM. In a pair the full and acc_empty barriers of rank 0 serve
@@ -348,21 +353,55 @@ __device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, 
   }
 }
 
+// The same for values alone.
+template <int KM>
+__device__ __forceinline__ void insert_value(float (&z)[KM], float v) {
+#pragma unroll
+  for (int p = KM - 1; p > 0; --p) z[p] = fmaxf(z[p], fminf(z[p - 1], v));
+  z[0] = fmaxf(z[0], v);
+}
+
+// The largest float below x (-inf stays).
+__device__ __forceinline__ float below(float x) {
+  const int b = __float_as_int(x);
+  return x == 0.f ? -1.4e-45f : __int_as_float(x > 0.f ? b - 1 : x > -INFINITY ? b + 1 : b);
+}
+
+// 32 columns of this thread's TMEM lane from vocabulary row vc on, those past V as -inf.
+__device__ __forceinline__ void load_chunk(uint32_t taddr, int vc, int V, uint32_t (&a)[32]) {
+  tmem_ld32(taddr, a);
+  if (vc + 32 > V) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (vc + i >= V) a[i] = __float_as_uint(-INFINITY);
+  }
+}
+
 // Forward. CTA (token tile blockIdx.x, split blockIdx.y) walks its split's
 // units in tiles of eight; the epilogue warps hold one token per thread. The
 // alternatives are kept in registers, KM slots of which the first KM - top are
 // filled with +inf, so that the smallest kept value is always in the last
-// slot: a 32-column chunk whose maximum does not beat it is done with one
-// comparison. Where some lane's does, the warp walks the columns that any
-// lane wants (one ballot) and reads each again from TMEM, because a register
-// array cannot be indexed at run time.
+// slot: a 32-column chunk (then each eight of it) in which no lane's maximum
+// beats it is done with one vote. Otherwise each lane notes its columns that do
+// in a buffer of 32, and
+// only when some lane's would overflow do all lanes put theirs into their
+// lists, side by side. A row gets a new alternative ever more rarely (in
+// column n with probability top / n), but one of a warp's 32 rows nearly
+// always does: inserting column by column, for the one or two lanes that want
+// it, took 777 tokens with 8 alternatives over V 50,257, D 1024 from 71 to
+// 144 us; with the buffers it is 103 us. Most of a list's insertions come from
+// the first columns, so the first tile is read twice: the top-th largest of
+// its groups' maxima (two, four or eight columns each) is a value that `top`
+// columns reach, and only columns that reach it are taken: 99 us (and 17 tokens
+// with 20 of them over V 151,936, D 4096 205 us instead of 211).
 //
 // A TMEM lane is read by one warp of the four alone, so with few tokens most
 // epilogue warps would have none. For N <= 64 (32) the tile holds the tokens'
 // rows twice (four times) instead of rows past N: the product costs the same,
 // and each warp takes every second (fourth) 32-column chunk of the tokens,
 // whose results the CTA joins through shared memory at the end. 17 tokens with
-// 20 alternatives at V 151,936, D 4096 took 217 us without and 206 us with it.
+// 20 alternatives at V 151,936, D 4096 took 217 us without and 206 us with it
+// (before the buffers).
 template <int KM, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_fwd_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
@@ -403,11 +442,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KL = KM > 0 ? KM : 1;
     float tz[KL];
     int ti[KL];
+    const auto clear_list = [&]() {
 #pragma unroll
-    for (int k = 0; k < KL; ++k) {
-      tz[k] = k < KM - p.top ? INFINITY : -INFINITY;
-      ti[k] = -1;
-    }
+      for (int k = 0; k < KL; ++k) {
+        tz[k] = k < KM - p.top ? INFINITY : -INFINITY;
+        ti[k] = -1;
+      }
+    };
+    clear_list();
+    float least = -INFINITY;  // no alternative is this small or smaller
+    float2* mine = reinterpret_cast<float2*>(ring + Ring<PAIR>::BYTES) + quarter * 32 + lane;  // entry e at 128 e
+    const uint32_t mine_at = smem_u32(mine);
+    uint32_t held = 0;
+    const auto insert_held = [&]() {  // in column order, so that equal values keep the lower row first
+      const uint32_t most = __reduce_max_sync(~0u, held);
+      float2 next = mine[0];
+      for (uint32_t e = 0; e < most; ++e) {
+        const float2 x = next;
+        next = mine[128 * min(e + 1, kCands - 1u)];
+        insert<KL>(tz, ti, e < held ? x.x : -INFINITY, __float_as_int(x.y));
+      }
+      held = 0;
+      least = fmaxf(least, tz[KL - 1]);
+    };
     float m_run = -INFINITY, s_run = 0.f, a_run = 0.f, tgt = 0.f;
     const uint64_t sl2 = f2(p.sl2, p.sl2);
     bool ok = true;
@@ -417,19 +474,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const Tile tl = tile_of(j);
+      if (KM > 0 && j == 0 && any) {
+#pragma unroll 1
+        for (int c = share; c < tl.units; c += p.reps) {
+          uint32_t a[32];
+          load_chunk(tmem + lane_base + buf * 256 + c * 32, (tl.u + c) * kUnit, p.V, a);
+          if (KM == 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) insert_value<KL>(tz, fmaxf(max_of<8>(a, q), -INFINITY));  // NaN as -inf
+          } else if (p.reps == 1) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) insert_value<KL>(tz, fmaxf(max_of<4>(a, q), -INFINITY));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) insert_value<KL>(tz, fmaxf(max_of<2>(a, q), -INFINITY));
+          }
+        }
+        least = below(tz[KL - 1]);
+        clear_list();
+      }
       if (any) {
 #pragma unroll 1
         for (int c = share; c < tl.units; c += p.reps) {
           uint32_t a[32];
           const uint32_t col = tmem + lane_base + buf * 256 + c * 32;
-          tmem_ld32(col, a);
           const int vc = (tl.u + c) * kUnit;
-          if (vc + 32 > p.V) {  // rows past the vocabulary
+          load_chunk(col, vc, p.V, a);
+          float m8[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (vc + i >= p.V) a[i] = __float_as_uint(-INFINITY);
-          }
-          const float cmax = max32(a);
+          for (int q = 0; q < 4; ++q) m8[q] = max_of<8>(a, q);
+          const float cmax = fmaxf(fmax3(m8[0], m8[1], m8[2]), m8[3]);
           // a row with nothing but -inf so far: the shift is 0, and S and A stay 0
           const float m_new = fmaxf(m_run, cmax * p.sl2);
           const float shift = m_new > -INFINITY ? m_new : 0.f;
@@ -454,16 +528,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (t == vc + i) tgt = __uint_as_float(a[i]);
           }
           if (KM > 0) {
-            const float least = tz[KL - 1];
             if (__any_sync(~0u, live && cmax > least)) {
-              uint32_t want = 0;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (live && __uint_as_float(a[i]) > least) want |= 1u << i;
-              for (uint32_t u = __reduce_or_sync(~0u, want); u; u &= u - 1) {
-                const int i = __ffs(u) - 1;
-                const float z = __uint_as_float(tmem_ld1(col + i));
-                insert<KL>(tz, ti, (want >> i) & 1u ? z : -INFINITY, vc + i);
+              for (int q = 0; q < 4; ++q) {
+                if (!__any_sync(~0u, live && m8[q] > least)) continue;
+                uint32_t want = over8(a, q, live ? least : INFINITY);
+                if (__any_sync(~0u, held + __popc(want) > kCands)) {
+                  insert_held();
+                  want = over8(a, q, live ? least : INFINITY);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t bit = (want >> i) & 1u;
+                  st_shared_if(bit, mine_at + held * (128 * sizeof(float2)), a[8 * q + i], vc + 8 * q + i);
+                  held += bit;
+                }
               }
             }
           }
@@ -471,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       release_acc<PAIR>(m, buf);
     }
+    if (KM > 0) insert_held();
     if (!PAIR && p.reps > 1) {
       // every product has completed and every copy been read: the ring is free
       Joint* joint = reinterpret_cast<Joint*>(ring);
@@ -805,16 +885,20 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   p.part = reinterpret_cast<float4*>(w + L.part);
   p.cand = reinterpret_cast<float2*>(w + L.cand);
   p.status = reinterpret_cast<uint32_t*>(w);
-  const auto kfn = top == 0   ? (sp.pair ? logp_fwd_kernel<0, true> : logp_fwd_kernel<0, false>)
-                   : top <= 8 ? (sp.pair ? logp_fwd_kernel<8, true> : logp_fwd_kernel<8, false>)
-                              : (sp.pair ? logp_fwd_kernel<kLogpMaxTop, true> : logp_fwd_kernel<kLogpMaxTop, false>);
-  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // lists of the next multiple of eight slots: inserting costs five instructions a slot
+  const auto kfn = top == 0    ? (sp.pair ? logp_fwd_kernel<0, true> : logp_fwd_kernel<0, false>)
+                   : top <= 8  ? (sp.pair ? logp_fwd_kernel<8, true> : logp_fwd_kernel<8, false>)
+                   : top <= 16 ? (sp.pair ? logp_fwd_kernel<16, true> : logp_fwd_kernel<16, false>)
+                   : top <= 24 ? (sp.pair ? logp_fwd_kernel<24, true> : logp_fwd_kernel<24, false>)
+                               : (sp.pair ? logp_fwd_kernel<kLogpMaxTop, true> : logp_fwd_kernel<kLogpMaxTop, false>);
+  const uint32_t smem = top == 0 ? kSmem : kSmemTop;
+  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sp.pair ? (N + 2 * kTok - 1) / (2 * kTok) * 2 : (N + kTok - 1) / kTok, sp.splits);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr = cluster_pair();
     cfg.attrs = &attr;

@@ -160,6 +160,22 @@ def test_infinities_and_nan_stay_in_their_rows(cuda_dev):
     assert (got[0][[3, 4]] == -np.inf).all() and got[0][5] == 0
 
 
+@pytest.mark.parametrize("N,top", [(2, 5), (2, 20), (150, 8), (150, 32)])
+def test_nan_rows_of_the_head_are_no_alternatives(N, top, cuda_dev):
+    """A head row of NaN spoils every token's sums, but the alternatives are the
+    other rows', in their order; whole groups of NaN rows among the first."""
+    V, D = 4000, 64
+    H, W, t = inputs(N, V, D, 19 + top)
+    W2 = W.copy()
+    dead = np.r_[0:40, 64:72, 133, 200:260, V - 1]
+    W2[dead] = np.nan
+    got = run(H, W2, t, cuda_dev, 1.0, top)
+    alive = np.setdiff1d(np.arange(V), dead)
+    order = alive[np.argsort(-(H @ W[alive].T), axis=1, kind="stable")[:, :top]]
+    assert (got[3] == order).all()
+    assert np.isnan(got[1]).all() and np.isnan(got[2]).all()
+
+
 def test_the_same_bits_again_and_in_a_graph(cuda_dev):
     """Two calls, a call on another stream, and a captured call replayed on
     new inputs give the same bits; two graphs keep workspaces of their own."""
@@ -214,6 +230,8 @@ BWD = [
     (1, 33, 64, True, True, 1.0), (2, 1, 64, True, True, 1.0), (5, 1000, 128, True, True, 0.7),
     (130, 1003, 192, True, True, 1.3), (300, 5000, 256, True, False, 1.0), (300, 5000, 256, False, True, 1.0),
     (96, 32003, 128, True, True, 1.0), (4500, 17000, 64, True, True, 1.0), (257, 130, 1088, True, True, 2.0),
+    # a last chunk of 100 vocabulary rows, fewer than dH's contraction has runs
+    (3000, 22372, 64, False, True, 1.0),
 ]
 
 
