@@ -615,16 +615,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int m0 = o.x, n0 = o.y;
       const int row = m0 + quarter * 32 + lane;
       if (through) {
-        // a box of 128 rows x 128 bytes at a time, through two buffers in turn
+        // a box of 128 rows x 128 bytes at a time, through two buffers in turn (the
+        // second CTA of a pair may lie past the last row)
         const int run = (cta + j * ctas) / p.per_split, step = f32 ? 32 : 64;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kGemmN && n0 + c0 < p.N; c0 += step, box ^= 1) {
+        for (int c0 = 0; m0 < p.M && c0 < kGemmN && n0 + c0 < p.N; c0 += step, box ^= 1) {
           if (issuer) bulk_wait_read1();  // the buffer's last copy has left it
           named_bar_sync(1, 128);
           store_box(tmem + lane_base + buf * kGemmN + c0, smem_u32(out) + box * 16384, quarter * 32 + lane, f32);
           fence_async_smem();
           named_bar_sync(1, 128);
-          if (issuer && m0 < p.M) {
+          if (issuer) {
             tma_store_3d(&tmC, out + box * 16384, n0 + c0, m0, run);
             bulk_commit();
           }
