@@ -65,10 +65,17 @@ struct Misc {
   int abort_flag;
 };
 
+// The boxes of a launch: `wide` units of W (or half of that many rows a CTA in
+// a pair) in tmW, `rest` in tmR for the shorter last tile of a split, and
+// `rows` tokens of H, `reps` times.
+struct Boxes {
+  int wide, rest, rows, reps;
+};
+
 struct FwdParams {
   int N, V, D, top;
   int units_per_split, splits;
-  int reps;   // 1, 2 or 4: how often the token tile's rows are repeated (see logp_fwd_kernel)
+  Boxes boxes;  // reps 1, 2 or 4: how often the token tile's rows are repeated (see logp_fwd_kernel)
   float sl2;  // log2(e) / temperature
   const int32_t* targets;
   float4* part;    // (splits, N) {m, S, A, the target's raw logit}
@@ -80,6 +87,7 @@ struct BwdParams {
   int N, V, D;
   int v_base, v_end;   // the chunk's vocabulary rows
   int tile_units;      // units of 32 rows per logit tile
+  Boxes boxes;
   int first;           // 1: this launch starts the call (clears the status word)
   float sl2, inv_t;
   const int32_t* targets;
@@ -176,51 +184,47 @@ __device__ __forceinline__ void teardown(uint32_t tmem) {
   }
 }
 
-// Warp 0, lane 0: 64-wide K slices of H and W through the ring. The tile's
-// tokens are one box of 128 / reps rows loaded `reps` times, one below the
-// other. A whole tile of W is one box, a shorter one its units one by one
-// (eight-row swizzle atoms, so the boxes' layouts join). In a pair each CTA
-// loads its own tokens and its half of the tile's vocabulary rows, the first
-// half in rank 0, and rank 0's barrier counts the bytes of both.
+// Warp 0, lane 0: 64-wide K slices of H and W through the ring, each as one
+// box: a TMA copy takes about two cycles a 128-byte row, rows past the tensor's
+// end included, so that is also what is spared: a tile's tokens are brought in
+// only up to the last one (eight-row swizzle atoms; the product's other rows
+// come from whatever the ring holds and are nobody's). The tokens of a tile
+// that repeats them come `reps` times, 128 / reps rows apart. In a pair each
+// CTA loads its own tokens and its half of the tile's vocabulary rows, the
+// first half in rank 0, and rank 0's barrier counts the bytes of both.
 template <bool PAIR, class TileOf>
 __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* ring, const CUtensorMap* tmH,
-                                           const CUtensorMap* tmW, const CUtensorMap* tmWu, int nt, int KS, int reps,
-                                           TileOf tile_of) {
+                                           const CUtensorMap* tmW, const CUtensorMap* tmR, int nt, int KS,
+                                           const Boxes bx, TileOf tile_of) {
   using R = Ring<PAIR>;
   prefetch_tmap(tmH);
   prefetch_tmap(tmW);
-  prefetch_tmap(tmWu);
+  prefetch_tmap(tmR);
   const uint32_t rank = PAIR ? cluster_rank() : 0;
   int it = 0;
   bool ok = true;
   for (int j = 0; ok && j < nt; ++j) {
     const Tile t = tile_of(j);
     const int w0 = t.u * kUnit + (PAIR ? (int)rank * t.units * (kUnit / 2) : 0);  // first vocabulary row here
+    // a box may hold more units than the tile (at the vocabulary's end): they are not used
+    const bool rest = t.units <= bx.rest;
+    const CUtensorMap* tm = rest ? tmR : tmW;
+    const uint32_t bytes = bx.reps * bx.rows * 128 + (rest ? bx.rest : bx.wide) * R::UNIT;
     for (int kc = 0; kc < KS; ++kc, ++it) {
       const int st = it % R::STAGES;
       if (!g.wait(&m.empty[st], ((it / R::STAGES) & 1) ^ 1, 50)) { ok = false; break; }
       uint8_t* sh = ring + st * R::STAGE;
       if (PAIR) {
         const uint32_t full = cluster_addr(&m.full[st], 0);
-        if (rank == 0) mbar_expect_tx(&m.full[st], 2 * (kSliceH + t.units * R::UNIT));
+        if (rank == 0) mbar_expect_tx(&m.full[st], 2 * bytes);
         tma_load_2d_pair(sh, tmH, full, kc * 64, t.tm * kTok);
-        if (t.units == kTileUnits) {
-          tma_load_2d_pair(sh + kSliceH, tmW, full, kc * 64, w0);
-        } else {
-          for (int x = 0; x < t.units; ++x)
-            tma_load_2d_pair(sh + kSliceH + x * R::UNIT, tmWu, full, kc * 64, w0 + x * (kUnit / 2));
-        }
+        tma_load_2d_pair(sh + kSliceH, tm, full, kc * 64, w0);
         continue;
       }
-      mbar_expect_tx(&m.full[st], kSliceH + t.units * R::UNIT);
-      for (int r = 0; r < reps; ++r)
-        tma_load_2d(sh + r * (kSliceH / reps), tmH, &m.full[st], kc * 64, t.tm * (kTok / reps));
-      if (t.units == kTileUnits) {
-        tma_load_2d(sh + kSliceH, tmW, &m.full[st], kc * 64, w0);
-      } else {
-        for (int x = 0; x < t.units; ++x)
-          tma_load_2d(sh + kSliceH + x * R::UNIT, tmWu, &m.full[st], kc * 64, w0 + x * kUnit);
-      }
+      mbar_expect_tx(&m.full[st], bytes);
+      tma_load_2d(sh + kSliceH, tm, &m.full[st], kc * 64, w0);
+      for (int r = 0; r < bx.reps; ++r)
+        tma_load_2d(sh + r * (kSliceH / bx.reps), tmH, &m.full[st], kc * 64, t.tm * (kTok / bx.reps));
     }
   }
   // No copy may still be landing when the CTA exits, and in a pair no arrival
@@ -322,7 +326,7 @@ template <int KL>
 __device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, int quarter, int lane, int groups,
                                             int token, bool lists) {
   float4 x = j.sums[quarter][lane];
-  for (int r = 1; r < p.reps; ++r) join(x, j.sums[quarter + r * groups][lane]);
+  for (int r = 1; r < p.boxes.reps; ++r) join(x, j.sums[quarter + r * groups][lane]);
   p.part[(size_t)blockIdx.y * p.N + token] = x;
   if (!lists) return;
   const int first = KL - p.top;  // slots before it hold no candidates
@@ -331,7 +335,7 @@ __device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, 
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     pos[r] = first;
-    head[r] = r < p.reps ? j.top[quarter + r * groups][first][lane] : make_float2(-INFINITY, __int_as_float(-1));
+    head[r] = r < p.boxes.reps ? j.top[quarter + r * groups][first][lane] : make_float2(-INFINITY, __int_as_float(-1));
   }
   float2* out = p.cand + ((size_t)token * p.splits + blockIdx.y) * p.top;
   for (int k = 0; k < p.top; ++k) {
@@ -405,7 +409,7 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int vc, int V, uint32
 template <int KM, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_fwd_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
-                    const __grid_constant__ CUtensorMap tmWu, const FwdParams p) {
+                    const __grid_constant__ CUtensorMap tmR, const FwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Misc& m = *reinterpret_cast<Misc*>(smem_raw);
   uint8_t* ring =
@@ -428,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, p.reps, tile_of);
+    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmR, nt, KS, p.boxes, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
   } else if (warp >= 4) {
     const int quarter = warp & 3;
-    const int groups = 4 / p.reps, share = quarter / groups;  // this warp's share of the columns
-    const int row0 = (int)blockIdx.x * (kTok / p.reps) + (quarter % groups) * 32, token = row0 + lane;
+    const int groups = 4 / p.boxes.reps, share = quarter / groups;  // this warp's share of the columns
+    const int row0 = (int)blockIdx.x * (kTok / p.boxes.reps) + (quarter % groups) * 32, token = row0 + lane;
     const bool live = token < p.N, any = row0 < p.N;
     const int t = live ? p.targets[token] : -1;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -476,13 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile tl = tile_of(j);
       if (KM > 0 && j == 0 && any) {
 #pragma unroll 1
-        for (int c = share; c < tl.units; c += p.reps) {
+        for (int c = share; c < tl.units; c += p.boxes.reps) {
           uint32_t a[32];
           load_chunk(tmem + lane_base + buf * 256 + c * 32, (tl.u + c) * kUnit, p.V, a);
           if (KM == 8) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) insert_value<KL>(tz, fmaxf(max_of<8>(a, q), -INFINITY));  // NaN as -inf
-          } else if (p.reps == 1) {
+          } else if (p.boxes.reps == 1) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) insert_value<KL>(tz, fmaxf(max_of<4>(a, q), -INFINITY));
           } else {
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (any) {
 #pragma unroll 1
-        for (int c = share; c < tl.units; c += p.reps) {
+        for (int c = share; c < tl.units; c += p.boxes.reps) {
           uint32_t a[32];
           const uint32_t col = tmem + lane_base + buf * 256 + c * 32;
           const int vc = (tl.u + c) * kUnit;
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       release_acc<PAIR>(m, buf);
     }
     if (KM > 0) insert_held();
-    if (!PAIR && p.reps > 1) {
+    if (!PAIR && p.boxes.reps > 1) {
       // every product has completed and every copy been read: the ring is free
       Joint* joint = reinterpret_cast<Joint*>(ring);
       joint->sums[quarter][lane] = make_float4(m_run, s_run, a_run, tgt);
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     logp_dz_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmWu, const BwdParams p) {
+                   const BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Misc& m = *reinterpret_cast<Misc*>(smem_raw);
   uint8_t* ring =
@@ -733,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmWu, nt, KS, 1, tile_of);
+    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmW, nt, KS, p.boxes, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
@@ -812,6 +816,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+// Rows of a token tile that a launch brings in.
+static int token_rows(int N) { return N < kTok ? (N + 7) / 8 * 8 : kTok; }
+
 // Most splits of the vocabulary: each at least one unit, and no more CTAs in
 // all than about sixteen a SM.
 int logp_max_splits(int N, int V) {
@@ -865,15 +872,15 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
                             float* top_logp, void* ws, cudaStream_t st) {
   const LogpPlan sp = logp_plan(N, V, sm_count());
   const LogpFwdLayout L = logp_fwd_layout(N, V, top);
-  CUtensorMap tH, tW, tWu;
-  const int reps = N <= 32 ? 4 : N <= 64 ? 2 : 1;
-  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok / reps) ||
-      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / (sp.pair ? 2 : 1)) ||
-      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit / (sp.pair ? 2 : 1)))
+  CUtensorMap tH, tW, tR;
+  const int cut = sp.pair ? 2 : 1, rest = sp.per % kTileUnits;
+  const Boxes bx{kTileUnits, rest, token_rows(N), N <= 32 ? 4 : N <= 64 ? 2 : 1};
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, bx.rows) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / cut) ||
+      !tmap_bf16_2d_sw128(&tR, head, D, V, (rest ? rest : kTileUnits) * kUnit / cut))
     return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(ws);
   FwdParams p{};
-  p.reps = reps;
+  p.boxes = bx;
   p.N = N;
   p.V = V;
   p.D = D;
@@ -903,7 +910,7 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
     cudaLaunchAttribute attr = cluster_pair();
     cfg.attrs = &attr;
     cfg.numAttrs = sp.pair ? 1 : 0;
-    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, tWu, p)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, tR, p)) != cudaSuccess) return e;
   }
   // a block per token while that fills less than two rounds of the SMs; else
   // as many tokens a block as 40 KB of lists hold, 8 at most
@@ -976,10 +983,8 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   dz_tile_units(TM2, first_rows, sms / 2, &paired);
   const bool pair = N > kTok && 2 * paired < 3 * single;  // as in logp_plan
   const int TM = pair ? TM2 : TM1, slots = pair ? sms / 2 : sms;
-  CUtensorMap tH, tW, tWu, tHb;
-  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, kTok) ||
-      !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / (pair ? 2 : 1)) ||
-      !tmap_bf16_2d_sw128(&tWu, head, D, V, kUnit / (pair ? 2 : 1)) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
+  CUtensorMap tH, tHb;
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, token_rows(N)) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
     return cudaErrorInvalidValue;
   const auto kfn = pair ? logp_dz_kernel<true> : logp_dz_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -997,6 +1002,9 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     p.v_end = cv0 + kc;
     long long cost = 0;
     p.tile_units = dz_tile_units(TM, kc, slots, &cost);
+    p.boxes = Boxes{p.tile_units, 0, token_rows(N), 1};
+    CUtensorMap tW;
+    if (!tmap_bf16_2d_sw128(&tW, head, D, V, p.tile_units * kUnit / (pair ? 2 : 1))) return cudaErrorInvalidValue;
     p.first = c == 0;
     p.sl2 = kLog2e / temperature;
     p.inv_t = 1.f / temperature;
@@ -1019,7 +1027,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     cfg.stream = st;
     cfg.attrs = pair ? attrs : attrs + 1;
     cfg.numAttrs = (pair ? 1 : 0) + (c == 0 ? 0 : 1);
-    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, tWu, p)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, p)) != cudaSuccess) return e;
     // dW rows of the chunk = dz^T H (the tokens are the contraction)
     if (dhead) {
       CUtensorMap tA;
