@@ -111,15 +111,16 @@ __device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// VEC elements as they lie in memory, their largest magnitude as the bits of an
+// VEC elements as they lie in memory (WIDE: taken 32 bytes at a time, which they
+// are then aligned to), their largest magnitude as the bits of an
 // fp32 value (NaN and infinity order above every number), and as fp32.
-template <typename T, int VEC>
+template <typename T, int VEC, bool WIDE = VEC == 16>
 struct Vec {
   static constexpr int W = VEC * sizeof(T) / 4;
   uint32_t w[W];
   __device__ __forceinline__ void load(const void* base, size_t e) {
     const T* p = static_cast<const T*>(base) + e;
-    if (VEC == 16) {
+    if constexpr (WIDE) {
 #pragma unroll
       for (int i = 0; i < W; i += 8) ld_32(reinterpret_cast<const uint32_t*>(p) + i, w + i);
     } else {
@@ -132,7 +133,7 @@ struct Vec {
   }
   __device__ __forceinline__ void store(void* base, size_t e) const {
     T* p = static_cast<T*>(base) + e;
-    if (VEC == 16) {
+    if constexpr (WIDE) {
 #pragma unroll
       for (int i = 0; i < W; i += 8) st_32(reinterpret_cast<uint32_t*>(p) + i, w + i);
     } else {
@@ -299,13 +300,13 @@ __device__ __forceinline__ float scale_of(float m) {
 }
 
 // LG lanes hold one block of LG * VEC elements.
-template <typename T, int FMT, int VEC, int LG>
+template <typename T, int FMT, int VEC, int LG, bool WIDE>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_save_kernel(const __grid_constant__ Tensors a) {
   using F = Format<FMT>;
   constexpr int U = kUnroll<VEC>, kShift = LG == 2 ? 1 : LG == 4 ? 2 : LG == 8 ? 3 : 4;
   uint32_t first;
   const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * U, &first);
-  Vec<T, VEC> v[U];
+  Vec<T, VEC, WIDE> v[U];
   Place at[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_save_kernel(const __grid_co
 
 // Vectors first .. of one tensor: codes and scales to T. shift = log2 of the
 // vectors in a block.
-template <typename T, int FMT, int VEC>
+template <typename T, int FMT, int VEC, bool WIDE>
 __device__ __forceinline__ void load_vectors(const Tensor& t, uint32_t first, int shift) {
   using F = Format<FMT>;
   constexpr int U = kLoadUnroll;
@@ -377,7 +378,7 @@ __device__ __forceinline__ void load_vectors(const Tensor& t, uint32_t first, in
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (!at[u].on) continue;
-    Vec<T, VEC> v;
+    Vec<T, VEC, WIDE> v;
 #pragma unroll
     for (int h = 0; h < VEC / 8; ++h) {
       float f[8];
@@ -393,11 +394,11 @@ __device__ __forceinline__ void load_vectors(const Tensor& t, uint32_t first, in
     v.store(const_cast<void*>(t.x), at[u].x);
   }
 }
-template <typename T, int FMT, int VEC>
+template <typename T, int FMT, int VEC, bool WIDE>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_load_kernel(const __grid_constant__ Tensors a, int shift) {
   uint32_t first;
   const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * kLoadUnroll, &first);
-  load_vectors<T, FMT, VEC>(t, first, shift);
+  load_vectors<T, FMT, VEC, WIDE>(t, first, shift);
 }
 
 // Start of the attention backward from 8-bit tensors, in one launch: the
@@ -427,12 +428,12 @@ constexpr int block_rows(int D) { return kCkptThreads / row_lanes(D) * row_unrol
 
 // VEC: of the load. WIDE: dout's rows start on 32 bytes.
 template <int D, int FMT, int VEC, bool WIDE>
-__global__ void __launch_bounds__(kCkptThreads, 5)
+__global__ void __launch_bounds__(kCkptThreads, VEC == 16 ? 5 : 4)
     bwd_ckpt_prologue_kernel(const __grid_constant__ Tensors a, uint32_t load_blocks, const DeltaArgs p, int shift) {
   if (blockIdx.x < load_blocks) {
     uint32_t first;
     const Tensor& t = tensor_of(a, blockIdx.x, kCkptThreads * kLoadUnroll, &first);
-    load_vectors<__nv_bfloat16, FMT, VEC>(t, first, shift);
+    load_vectors<__nv_bfloat16, FMT, VEC, VEC == 16>(t, first, shift);
     return;
   }
   using F = Format<FMT>;
@@ -540,38 +541,49 @@ uint32_t describe(const CkptTensor* x, int count, int G, int VEC, uint32_t per_b
 }
 int log2_of(int n) { return n == 2 ? 1 : n == 4 ? 2 : n == 8 ? 3 : 4; }
 
-template <typename T, int FMT, int VEC>
+// Whether vectors of eight fp32 elements start on 32 bytes.
+bool all_wide(const CkptTensor* x, int count) {
+  for (int i = 0; i < count; ++i)
+    if (!aligned32(x[i].x) || (x[i].N > 1 && x[i].s_n % 8) || (x[i].H > 1 && x[i].s_h % 8) || (x[i].B > 1 && x[i].s_b % 8))
+      return false;
+  return true;
+}
+
+template <typename T, int FMT, int VEC, bool WIDE>
 void save_launch(const CkptTensor* x, int count, int G, cudaStream_t st) {
   Tensors a{};
   const uint32_t blocks = describe(x, count, G, VEC, kCkptThreads * kUnroll<VEC>, true, &a);
   if (G == 32)
-    ckpt_save_kernel<T, FMT, VEC, 32 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 32 / VEC, WIDE><<<blocks, kCkptThreads, 0, st>>>(a);
   else if (G == 64)
-    ckpt_save_kernel<T, FMT, VEC, 64 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 64 / VEC, WIDE><<<blocks, kCkptThreads, 0, st>>>(a);
   else
-    ckpt_save_kernel<T, FMT, VEC, 128 / VEC><<<blocks, kCkptThreads, 0, st>>>(a);
+    ckpt_save_kernel<T, FMT, VEC, 128 / VEC, WIDE><<<blocks, kCkptThreads, 0, st>>>(a);
 }
-template <typename T>
-void save_any(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
+template <typename T, int FMT>
+void save_any(const CkptTensor* x, int count, int G, cudaStream_t st) {
   if (all_flat(x, count, G))
-    format == PA_CKPT_INT8 ? save_launch<T, PA_CKPT_INT8, 16>(x, count, G, st) : save_launch<T, PA_CKPT_E4M3, 16>(x, count, G, st);
+    save_launch<T, FMT, 16, true>(x, count, G, st);
+  else if (sizeof(T) == 4 && all_wide(x, count))
+    save_launch<T, FMT, 8, sizeof(T) == 4>(x, count, G, st);
   else
-    format == PA_CKPT_INT8 ? save_launch<T, PA_CKPT_INT8, 8>(x, count, G, st) : save_launch<T, PA_CKPT_E4M3, 8>(x, count, G, st);
+    save_launch<T, FMT, 8, false>(x, count, G, st);
 }
 
-template <typename T, int VEC>
-void load_launch(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
+template <typename T, int FMT, int VEC, bool WIDE>
+void load_launch(const CkptTensor* x, int count, int G, cudaStream_t st) {
   Tensors a{};
   const uint32_t blocks = describe(x, count, G, VEC, kCkptThreads * kLoadUnroll, false, &a);
-  const int shift = log2_of(G / VEC);
-  if (format == PA_CKPT_INT8)
-    ckpt_load_kernel<T, PA_CKPT_INT8, VEC><<<blocks, kCkptThreads, 0, st>>>(a, shift);
-  else
-    ckpt_load_kernel<T, PA_CKPT_E4M3, VEC><<<blocks, kCkptThreads, 0, st>>>(a, shift);
+  ckpt_load_kernel<T, FMT, VEC, WIDE><<<blocks, kCkptThreads, 0, st>>>(a, log2_of(G / VEC));
 }
-template <typename T>
-void load_any(const CkptTensor* x, int count, int format, int G, cudaStream_t st) {
-  all_flat(x, count, G) ? load_launch<T, 16>(x, count, format, G, st) : load_launch<T, 8>(x, count, format, G, st);
+template <typename T, int FMT>
+void load_any(const CkptTensor* x, int count, int G, cudaStream_t st) {
+  if (all_flat(x, count, G))
+    load_launch<T, FMT, 16, true>(x, count, G, st);
+  else if (sizeof(T) == 4 && all_wide(x, count))
+    load_launch<T, FMT, 8, sizeof(T) == 4>(x, count, G, st);
+  else
+    load_launch<T, FMT, 8, false>(x, count, G, st);
 }
 
 template <int D, int VEC>
@@ -595,12 +607,18 @@ cudaError_t prologue_launch(const CkptTensor* qkv, int format, int G, const Delt
 }  // namespace
 
 cudaError_t launch_ckpt_save(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st) {
-  f32 ? save_any<float>(x, count, format, block, st) : save_any<__nv_bfloat16>(x, count, format, block, st);
+  if (format == PA_CKPT_INT8)
+    f32 ? save_any<float, PA_CKPT_INT8>(x, count, block, st) : save_any<__nv_bfloat16, PA_CKPT_INT8>(x, count, block, st);
+  else
+    f32 ? save_any<float, PA_CKPT_E4M3>(x, count, block, st) : save_any<__nv_bfloat16, PA_CKPT_E4M3>(x, count, block, st);
   return cudaGetLastError();
 }
 
 cudaError_t launch_ckpt_load(const CkptTensor* x, int count, bool f32, int format, int block, cudaStream_t st) {
-  f32 ? load_any<float>(x, count, format, block, st) : load_any<__nv_bfloat16>(x, count, format, block, st);
+  if (format == PA_CKPT_INT8)
+    f32 ? load_any<float, PA_CKPT_INT8>(x, count, block, st) : load_any<__nv_bfloat16, PA_CKPT_INT8>(x, count, block, st);
+  else
+    f32 ? load_any<float, PA_CKPT_E4M3>(x, count, block, st) : load_any<__nv_bfloat16, PA_CKPT_E4M3>(x, count, block, st);
   return cudaGetLastError();
 }
 
