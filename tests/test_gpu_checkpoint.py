@@ -141,6 +141,21 @@ def test_strided_tensors_many_at_once_and_nothing_else_touched(fmt, cuda_dev):
     assert (dst == 7).all()
 
 
+@pytest.mark.parametrize("C", [4096, 4104])  # whole blocks, and a short one in each row
+def test_offsets_past_32_bits(C, cuda_dev):
+    """More than 2^32 bytes and 2^31 elements: the last rows are kept like any."""
+    N = (1 << 31) // C + 700
+    x = torch.empty(N, C, dtype=torch.bfloat16, device=cuda_dev)
+    x[:-1000] = 1
+    tail = torch.randn(1000, C, generator=torch.Generator(device=cuda_dev).manual_seed(3), device=cuda_dev).bfloat16()
+    x[-1000:] = tail
+    c, = pa.checkpoint_save([x], block=64)
+    y, = pa.checkpoint_load([c])
+    torch.cuda.synchronize()
+    check(tail, pa.Checkpoint(c.codes[-1000:], c.scales[-1000:], 64), y[-1000:])
+    assert (c.codes[:-1000].amin() == 127).item() and (y[:-1000].amin() == y[:-1000].amax()).item()
+
+
 def test_capture_and_streams(cuda_dev):
     x = torch.randn(300, 512, device=cuda_dev).bfloat16()
     want, = pa.checkpoint_load(pa.checkpoint_save([x]))

@@ -359,6 +359,38 @@ def test_the_mean_nll_is_the_cross_entropys(cuda_dev):
         assert (x.float() - y.float()).norm() <= 2.0 ** -7 * x.float().norm()
 
 
+def test_a_head_past_32_bit_offsets(cuda_dev):
+    """V * D beyond 2^31 elements, both directions, against fp64 on the device.
+    (The backward's tokens sit in one tile, its vocabulary in one chunk.)"""
+    N, V, D, top = 3, 540_001, 4096, 8
+    g = torch.Generator(device=cuda_dev).manual_seed(1)
+    w = torch.empty(V, D, dtype=torch.bfloat16, device=cuda_dev)
+    for a in range(0, V, 60_000):
+        n = min(60_000, V - a)
+        w[a:a + n] = torch.randint(-15, 16, (n, D), generator=g, device=cuda_dev).float() / 256
+    h = (torch.randint(-15, 16, (N, D), generator=g, device=cuda_dev).float() / 8).bfloat16()
+    t = torch.tensor([V - 1, 5, 500_000], dtype=torch.int32, device=cuda_dev)
+    logp, lse, ent, ids, alt = pa.token_logprobs_forward(h, w, t, top=top)
+    z = torch.cat([h.double() @ w[a:a + 60_000].double().T for a in range(0, V, 60_000)], 1)
+    lp = torch.log_softmax(z, 1)
+    want = [lp[torch.arange(N), t.long()], torch.logsumexp(z, 1), -(lp.exp() * lp).sum(1), torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top]]
+    # the bars of check(): V / 32 chunk sums are spread over the splits here
+    u = 2.0 ** -24
+    bar = 3 * 1.45 * z.abs().max().item() * u + 4 * u + u * (V / 32 / 100 + 32) + 8 * u * z.abs().max().item()
+    assert (logp.double() - want[0]).abs().max() <= bar and (lse.double() - want[1]).abs().max() <= bar
+    assert (ent.double() - want[2]).abs().max() <= bar * (2 + want[2].max() + math.log(V) + 1)
+    assert torch.equal(ids.long(), want[3])
+    gl = torch.tensor([1.0, -2.0, 0.5], device=cuda_dev)
+    dh, dw = pa.token_logprobs_backward(h, w, t, lse, ent, gl, 0.1 * gl)
+    dz = -lp.exp() * (gl.double()[:, None] + 0.1 * gl.double()[:, None] * (lp + want[2][:, None]))
+    dz[torch.arange(N), t.long()] += gl.double()
+    for a, b in ((0, 2000), (499_000, 501_000), (V - 2000, V)):
+        exact = dz[:, a:b].T @ h.double()
+        assert (dw[a:b].double() - exact).norm() <= 2.0 ** -8 * exact.norm()
+    exact = sum(dz[:, a:a + 60_000] @ w[a:a + 60_000].double() for a in range(0, V, 60_000))
+    assert (dh.double() - exact).norm() <= 2.0 ** -8 * exact.norm()
+
+
 def test_refused_shapes_and_devices(cuda_dev):
     h, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=cuda_dev), torch.zeros(9, 64, dtype=torch.bfloat16, device=cuda_dev)
     t = torch.zeros(4, dtype=torch.int32, device=cuda_dev)
