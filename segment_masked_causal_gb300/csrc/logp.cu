@@ -184,24 +184,32 @@ __device__ __forceinline__ void teardown(uint32_t tmem) {
   }
 }
 
-// Warp 0, lane 0: 64-wide K slices of H and W through the ring, each as one
-// box: a TMA copy takes about two cycles a 128-byte row, rows past the tensor's
-// end included, so that is also what is spared: a tile's tokens are brought in
-// only up to the last one (eight-row swizzle atoms; the product's other rows
-// come from whatever the ring holds and are nobody's). The tokens of a tile
-// that repeats them come `reps` times, 128 / reps rows apart. In a pair each
-// CTA loads its own tokens and its half of the tile's vocabulary rows, the
-// first half in rank 0, and rank 0's barrier counts the bytes of both.
-template <bool PAIR, class TileOf>
+// 64-wide K slices of H and W through the ring, each as one box, W's by lane 0
+// of warp 0 and H's by lane 0 of warp 2: one round of waiting, announcing and
+// issuing takes a thread about 320 cycles and each further copy 60, which is
+// near the 512 cycles of a slice's products. A copy itself costs its rows, past
+// the tensor's end or not, so a tile's tokens are brought in only up to the
+// last one (eight-row swizzle atoms; the product's other rows come from
+// whatever the ring holds and are nobody's). The tokens of a tile that repeats
+// them come `reps` times, 128 / reps rows apart. In a pair each CTA loads its
+// own tokens and its half of the tile's vocabulary rows, the first half in rank
+// 0, and rank 0's barrier counts the bytes of both.
+template <bool PAIR, bool TOKENS, class TileOf>
 __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* ring, const CUtensorMap* tmH,
                                            const CUtensorMap* tmW, const CUtensorMap* tmR, int nt, int KS,
                                            const Boxes bx, TileOf tile_of) {
   using R = Ring<PAIR>;
-  prefetch_tmap(tmH);
-  prefetch_tmap(tmW);
-  prefetch_tmap(tmR);
+  if (TOKENS) {
+    prefetch_tmap(tmH);
+  } else {
+    prefetch_tmap(tmW);
+    prefetch_tmap(tmR);
+  }
   const uint32_t rank = PAIR ? cluster_rank() : 0;
-  int it = 0;
+  const uint32_t full0 = PAIR ? cluster_addr(&m.full[0], 0) : smem_u32(&m.full[0]);
+  const int rep_rows = kTok / bx.reps;
+  int st = 0, it = 0;
+  uint32_t phase = 1;
   bool ok = true;
   for (int j = 0; ok && j < nt; ++j) {
     const Tile t = tile_of(j);
@@ -209,22 +217,28 @@ __device__ __forceinline__ void load_tiles(Misc& m, const Guard& g, uint8_t* rin
     // a box may hold more units than the tile (at the vocabulary's end): they are not used
     const bool rest = t.units <= bx.rest;
     const CUtensorMap* tm = rest ? tmR : tmW;
-    const uint32_t bytes = bx.reps * bx.rows * 128 + (rest ? bx.rest : bx.wide) * R::UNIT;
+    const uint32_t bytes = (PAIR ? 2 : 1) * (bx.reps * bx.rows * 128 + (rest ? bx.rest : bx.wide) * R::UNIT);
     for (int kc = 0; kc < KS; ++kc, ++it) {
-      const int st = it % R::STAGES;
-      if (!g.wait(&m.empty[st], ((it / R::STAGES) & 1) ^ 1, 50)) { ok = false; break; }
+      if (!g.wait(&m.empty[st], phase, TOKENS ? 55 : 50)) { ok = false; break; }
       uint8_t* sh = ring + st * R::STAGE;
-      if (PAIR) {
-        const uint32_t full = cluster_addr(&m.full[st], 0);
-        if (rank == 0) mbar_expect_tx(&m.full[st], 2 * bytes);
-        tma_load_2d_pair(sh, tmH, full, kc * 64, t.tm * kTok);
-        tma_load_2d_pair(sh + kSliceH, tm, full, kc * 64, w0);
-        continue;
+      const uint32_t full = full0 + st * 8;
+      if (TOKENS) {
+        if (PAIR)
+          tma_load_2d_pair(sh, tmH, full, kc * 64, t.tm * kTok);
+        else
+          for (int r = 0; r < bx.reps; ++r)
+            tma_load_2d(sh + r * rep_rows * 128, tmH, &m.full[st], kc * 64, t.tm * rep_rows);
+      } else {
+        if (rank == 0) mbar_expect_tx(&m.full[st], bytes);
+        if (PAIR)
+          tma_load_2d_pair(sh + kSliceH, tm, full, kc * 64, w0);
+        else
+          tma_load_2d(sh + kSliceH, tm, &m.full[st], kc * 64, w0);
       }
-      mbar_expect_tx(&m.full[st], bytes);
-      tma_load_2d(sh + kSliceH, tm, &m.full[st], kc * 64, w0);
-      for (int r = 0; r < bx.reps; ++r)
-        tma_load_2d(sh + r * (kSliceH / bx.reps), tmH, &m.full[st], kc * 64, t.tm * (kTok / bx.reps));
+      if (++st == R::STAGES) {
+        st = 0;
+        phase ^= 1;
+      }
     }
   }
   // No copy may still be landing when the CTA exits, and in a pair no arrival
@@ -432,7 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmR, nt, KS, p.boxes, tile_of);
+    if (lane == 0) load_tiles<PAIR, false>(m, g, ring, &tmH, &tmW, &tmR, nt, KS, p.boxes, tile_of);
+    __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) load_tiles<PAIR, true>(m, g, ring, &tmH, &tmW, &tmR, nt, KS, p.boxes, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
@@ -737,7 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) load_tiles<PAIR>(m, g, ring, &tmH, &tmW, &tmW, nt, KS, p.boxes, tile_of);
+    if (lane == 0) load_tiles<PAIR, false>(m, g, ring, &tmH, &tmW, &tmW, nt, KS, p.boxes, tile_of);
+    __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) load_tiles<PAIR, true>(m, g, ring, &tmH, &tmW, &tmW, nt, KS, p.boxes, tile_of);
     __syncwarp();
   } else if (warp == 1) {
     multiply_tiles<PAIR>(m, g, smem_u32(ring), tmem, nt, KS, tile_of);
