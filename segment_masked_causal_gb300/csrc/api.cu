@@ -837,12 +837,13 @@ const char* pa_status_string(pa_status s) {
     case PA_ERR_GQA: return "Hq must be a multiple of Hkv";
     case PA_ERR_SHAPE:
       return "bad shape (B, H, N > 0; B*Hq*N < 2^31; finite scale; N % 128 == 0 for the single-step calls; "
-             "strides >= D)";
+             "strides >= D; hidden size a multiple of 64; 0 <= top <= min(32, V); temperature > 0; checkpoints: "
+             "1 to 8 tensors, C % 8 == 0, block 32, 64 or 128)";
     case PA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case PA_ERR_WORKSPACE: return "workspace too small (see pa_workspace_bytes)";
     case PA_ERR_ARCH: return "device is not compute capability 10.3 (GB300)";
     case PA_ERR_CUDA: return "a CUDA call or kernel launch failed";
-    case PA_ERR_DTYPE: return "io dtype must be PA_IO_BF16 or PA_IO_F32";
+    case PA_ERR_DTYPE: return "io dtype must be PA_IO_BF16 or PA_IO_F32, a checkpoint format PA_CKPT_INT8 or PA_CKPT_E4M3";
     case PA_ERR_HOST_MEMORY: return "host memory for the call's scratch could not be allocated";
   }
   return "unknown status";

@@ -366,8 +366,9 @@ __global__ void __launch_bounds__(256) lce_merge_kernel(const LceParams p, int s
 // blockIdx.x + gridDim.x, ... in groups of kGemmGroup row blocks (M tiles
 // fastest inside a group, so a group's A panels stay in L2 while it walks
 // every N tile), K in steps of 64 through a
-// 4-stage TMA ring (A as one 128-row x 64 box, B as four 64-row x 64 boxes,
-// all 128-byte swizzled; elements past M, N or K read as zero), tcgen05
+// TMA ring (A as one 128-row x 64 box, B as four 64-row x 64 boxes, or two in
+// each CTA of a pair, all 128-byte swizzled; elements past M, N or K read as
+// zero; a warp each issues the copies of A and B), tcgen05
 // products into two 256-column fp32 TMEM accumulators used by alternate
 // tiles, so a tile's epilogue runs beside the next tile's products. The
 // epilogue (one thread per output row) stores bf16, or starts / adds to /
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(256) lce_merge_kernel(const LceParams p, int s
 constexpr int kGemmN = 256;                               // output columns per tile
 constexpr uint32_t kGemmA = 128 * 128;                    // 128 rows x 64 K, 16 KB
 constexpr uint32_t kGemmBHalf = 64 * 128;                 // 64 K rows x 64 N columns, 8 KB
-constexpr int kGemmThreads = 192;
+constexpr int kGemmThreads = 224;  // A's copies, products, four epilogue warps, B's copies
 // PAIR: two CTAs of a cluster form one product of 256 x 256, each loading its
 // own 128 rows of A and half of B's columns: 32 KB a K block instead of 48.
 template <bool PAIR>
@@ -518,32 +519,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 6) {
+    // A's copies by warp 0, which also announces the bytes of both, B's by warp 6
     if (lane == 0) {
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-      int it = 0;
+      const bool isA = warp == 0;
+      prefetch_tmap(isA ? &tmA : &tmB);
+      const uint32_t full0 = PAIR ? cluster_addr(&m.full[0], 0) : smem_u32(&m.full[0]);
+      int it = 0, st = 0;
+      uint32_t phase = 1;
       bool ok = true;
       for (int j = 0; ok && j < nt; ++j) {
         const int2 o = tile_origin(cta + j * ctas);
-        const int m0 = o.x, n0 = o.y;
+        const int m0 = o.x, n0 = o.y + 64 * rank * R::BBOXES;
         const int2 run = tile_run(cta + j * ctas);
         for (int kb = run.x; kb < run.y; ++kb, ++it) {
-          const int st = it % R::STAGES;
-          if (!g.wait(&m.empty[st], ((it / R::STAGES) & 1) ^ 1, 45)) { ok = false; break; }
+          if (!g.wait(&m.empty[st], phase, isA ? 45 : 49)) { ok = false; break; }
           uint8_t* sa = ring + st * R::STAGE;
-          if (PAIR) {  // rank 0's barrier counts the bytes of both
-            const uint32_t full = cluster_addr(&m.full[st], 0);
-            if (rank == 0) mbar_expect_tx(&m.full[st], 2 * R::STAGE);
-            tma_load_2d_pair(sa, &tmA, full, kb * 64, m0);
+          if (isA) {
+            if (rank == 0) mbar_expect_tx(&m.full[st], kPer * R::STAGE);  // rank 0's barrier counts the bytes of both CTAs
+            if (PAIR)
+              tma_load_2d_pair(sa, &tmA, full0 + st * 8, kb * 64, m0);
+            else
+              tma_load_2d(sa, &tmA, &m.full[st], kb * 64, m0);
+          } else {
+#pragma unroll
             for (int c = 0; c < R::BBOXES; ++c)
-              tma_load_2d_pair(sa + kGemmA + c * kGemmBHalf, &tmB, full, n0 + 64 * (rank * R::BBOXES + c), kb * 64);
-            continue;
+              if (PAIR)
+                tma_load_2d_pair(sa + kGemmA + c * kGemmBHalf, &tmB, full0 + st * 8, n0 + 64 * c, kb * 64);
+              else
+                tma_load_2d(sa + kGemmA + c * kGemmBHalf, &tmB, &m.full[st], n0 + 64 * c, kb * 64);
           }
-          mbar_expect_tx(&m.full[st], R::STAGE);
-          tma_load_2d(sa, &tmA, &m.full[st], kb * 64, m0);
-          for (int c = 0; c < R::BBOXES; ++c)
-            tma_load_2d(sa + kGemmA + c * kGemmBHalf, &tmB, &m.full[st], n0 + 64 * c, kb * 64);
+          if (++st == R::STAGES) {
+            st = 0;
+            phase ^= 1;
+          }
         }
       }
       // no copy may still be landing when the CTA exits (in a pair, no arrival of

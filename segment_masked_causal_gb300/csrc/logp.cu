@@ -42,8 +42,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The ring of K slices: one CTA per SM. PAIR: two CTAs form one product of 256
 // tokens x 256 vocabulary rows, each holding its own 128 tokens and half of the
 // vocabulary rows. A tile of 128 x 256 alone takes 48 KB a K slice into an SM
-// for 512 cycles of products, and an SM's port to the L2 moves 64 bytes a
-// cycle, 768 cycles: the tensor pipe is 60% busy. The pair takes 32 KB.
+// for 512 cycles of products; with every SM copying, the L2 gives each about 77
+// bytes a cycle (620 cycles), in a shared memory that the operands are read
+// from as well. The pair takes 32 KB.
 template <bool PAIR>
 struct Ring {
   static constexpr int STAGES = PAIR ? 6 : 4;
@@ -401,9 +402,8 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int vc, int V, uint32
 // filled with +inf, so that the smallest kept value is always in the last
 // slot: a 32-column chunk (then each eight of it) in which no lane's maximum
 // beats it is done with one vote. Otherwise each lane notes its columns that do
-// in a buffer of 32, and
-// only when some lane's would overflow do all lanes put theirs into their
-// lists, side by side. A row gets a new alternative ever more rarely (in
+// in a buffer of 32, and only when some lane's would overflow do all lanes put
+// theirs into their lists, side by side. A row gets a new alternative ever more rarely (in
 // column n with probability top / n), but one of a warp's 32 rows nearly
 // always does: inserting column by column, for the one or two lanes that want
 // it, took 777 tokens with 8 alternatives over V 50,257, D 1024 from 71 to
@@ -518,9 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = share; c < tl.units; c += p.boxes.reps) {
           uint32_t a[32];
-          const uint32_t col = tmem + lane_base + buf * 256 + c * 32;
           const int vc = (tl.u + c) * kUnit;
-          load_chunk(col, vc, p.V, a);
+          load_chunk(tmem + lane_base + buf * 256 + c * 32, vc, p.V, a);
           float m8[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) m8[q] = max_of<8>(a, q);
