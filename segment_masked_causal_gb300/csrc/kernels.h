@@ -151,9 +151,9 @@ constexpr int kLogpMaxTop = 32;
 int logp_max_splits(int N, int V);
 struct LogpPlan {
   bool pair;  // two CTAs per product
-  int splits, per;
+  int splits, per, width;  // units per split and per tile of it
 };
-LogpPlan logp_plan(int N, int V, int sms);
+LogpPlan logp_plan(int N, int V, int D, int sms);
 struct LogpFwdLayout {
   size_t part, cand, bytes;  // after the 256-byte status region
 };

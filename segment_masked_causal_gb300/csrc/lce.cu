@@ -730,19 +730,18 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float4* __restric
 #endif
 constexpr int kGemmPairBlocks = PA_GEMM_PAIR_BLOCKS;
 
-// Time of an M x N x K product cut into s runs of K, on `slots` SMs: waves x
-// (blocks per run + 8 for the pipeline's fill and the tile's epilogue), a
-// block on a pair two thirds of the time that it takes one CTA (see
-// GemmRing), in units of a third of that (0.09 us); and, with more than one
-// run, writing and reading the accumulators at 6.5 TB/s. < 0 where a run would
-// be empty.
+// Cycles of an M x N x K product cut into s runs of K, on `slots` SMs: waves x
+// (K blocks + 8 blocks' worth for the pipeline's fill and the tile's epilogue);
+// a block takes a pair 622 cycles (512 of products, with copies and operands in
+// one shared memory) and a CTA alone its copies' 664 (48 KB at 74 bytes a cycle); and, with more than one run, writing and
+// reading the accumulators at 6.5 TB/s. < 0 where a run would be empty.
 static double gemm_cost(int M, int N, int K, int slots, int s, bool pair) {
   const int KB = (K + 63) / 64, per = (KB + s - 1) / s;
   if ((KB + per - 1) / per != s || (pair && (M <= 128 || slots < 2 || per < kGemmPairBlocks))) return -1.0;
   const long long rows = pair ? 256 : 128, at_once = pair ? slots / 2 : slots;
   const long long tiles = ((M + rows - 1) / rows) * ((N + kGemmN - 1) / kGemmN);
   const long long waves = (tiles * s + at_once - 1) / at_once;
-  return (double)waves * (per + 8) * (pair ? 2 : 3) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 / 0.09 : 0.0);
+  return (double)waves * (per * (pair ? 622.0 : 664.0) + 8 * 512.0) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 * 1900 : 0.0);
 }
 
 int gemm_splits(int M, int N, int K, int slots) {

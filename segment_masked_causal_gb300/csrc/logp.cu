@@ -397,7 +397,7 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int vc, int V, uint32
 }
 
 // Forward. CTA (token tile blockIdx.x, split blockIdx.y) walks its split's
-// units in tiles of eight; the epilogue warps hold one token per thread. The
+// units in tiles of up to eight; the epilogue warps hold one token per thread. The
 // alternatives are kept in registers, KM slots of which the first KM - top are
 // filled with +inf, so that the smallest kept value is always in the last
 // slot: a 32-column chunk (then each eight of it) in which no lane's maximum
@@ -431,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int U = (p.V + kUnit - 1) / kUnit;
   const int u0 = (int)blockIdx.y * p.units_per_split, u1 = min(u0 + p.units_per_split, U);
-  const int nt = (u1 - u0 + kTileUnits - 1) / kTileUnits;  // >= 1 by construction of the grid
+  const int width = p.boxes.wide, nt = (u1 - u0 + width - 1) / width;  // >= 1 by construction of the grid
   const int KS = p.D / 64;
   const Guard g{&m.abort_flag, p.status};
   const auto tile_of = [&](int j) {
-    const int u = u0 + j * kTileUnits;
-    return Tile{(int)blockIdx.x, u, min(kTileUnits, u1 - u)};
+    const int u = u0 + j * width;
+    return Tile{(int)blockIdx.x, u, min(width, u1 - u)};
   };
   // The status word starts at 0: no wait can give up within 2 s of the launch.
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;
@@ -837,6 +837,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of a token tile that a launch brings in.
 static int token_rows(int N) { return N < kTok ? (N + 7) / 8 * 8 : kTok; }
+// How often a forward tile repeats its tokens.
+static int token_reps(int N) { return N <= 32 ? 4 : N <= 64 ? 2 : 1; }
 
 // Most splits of the vocabulary: each at least one unit, and no more CTAs in
 // all than about sixteen a SM.
@@ -848,33 +850,55 @@ int logp_max_splits(int N, int V) {
   return s < 1 ? 1 : s;
 }
 
-// The split that makes waves x (units per CTA + 8) smallest: a CTA's pipeline
-// fill and last epilogue take about as long as one tile of eight units. slots:
-// CTAs (or pairs of them) that run at once; rows: tokens of each.
-static LceSplit best_split(int N, int V, int slots, int rows, long long* cost_out) {
-  const int TM = (N + rows - 1) / rows, U = (V + kUnit - 1) / kUnit;
-  LceSplit best{1, U};
+// Cycles that a K slice of a tile of `units` takes a CTA (or a pair), as
+// measured: a round of waiting for a stage, announcing and issuing its copies,
+// 360; the products, 64 a unit and 110 for the shared memory that copies and
+// operands share (622 for 256 columns: a pair's 82% of the tensor pipe); the
+// copies, 74 bytes a cycle with every SM copying; and the head's rows out of
+// DRAM, 23 bytes a cycle and SM, shared by the `sharing` token tiles that read
+// them at about the same time.
+static long long slice_cycles(int units, bool pair, int token_bytes, int sharing) {
+  const int head_bytes = units * (int)(pair ? Ring<true>::UNIT : Ring<false>::UNIT);
+  long long c = 360;
+  for (const long long x :
+       {64ll * units + 110, (long long)(token_bytes + head_bytes) / 74, (long long)head_bytes / (23ll * sharing)})
+    if (x > c) c = x;
+  return c;
+}
+
+// The split of the vocabulary over `slots` CTAs (or pairs) at once that takes
+// the fewest cycles, tiles of a split about equal: waves x (the tiles' slices +
+// 12,000 and 400 a slice for a CTA's start, the pipeline's fill, the last
+// epilogue and the exit: 8,192 tokens over V 151,936, D 4096 took 5.60 ms in
+// three waves and 5.73 ms in eight that fill the SMs a little better).
+static LogpPlan best_plan(int N, int V, int D, int slots, bool pair, long long* cost_out) {
+  const int rows = pair ? 2 * kTok : kTok, TM = (N + rows - 1) / rows, U = (V + kUnit - 1) / kUnit;
+  const int token_bytes = token_rows(N) * 128 * token_reps(N);
+  LogpPlan best{pair, 1, U, kTileUnits};
   long long best_cost = -1;
   for (int s = 1, most = logp_max_splits(N, V); s <= most; ++s) {
     const int per = (U + s - 1) / s, used = (U + per - 1) / per;
-    const long long waves = ((long long)TM * used + slots - 1) / slots, cost = waves * (per + kTileUnits);
+    const int tiles = (per + kTileUnits - 1) / kTileUnits, width = (per + tiles - 1) / tiles;
+    const long long slices = (tiles - 1) * slice_cycles(width, pair, token_bytes, TM) +
+                             slice_cycles(per - (tiles - 1) * width, pair, token_bytes, TM);
+    const long long waves = ((long long)TM * used + slots - 1) / slots, cost = waves * ((slices + 400) * (D / 64) + 12000);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = LceSplit{used, per};
+      best = LogpPlan{pair, used, per, width};
     }
   }
   *cost_out = best_cost;
   return best;
 }
 
-// Pairs of CTAs where that is faster: a unit takes them two thirds of the time
-// (see Ring), but tokens come in rows of 256, so 777 of them are 1,024 rows
-// instead of 896. Up to 128 tokens the head's bytes are what takes the time.
-LogpPlan logp_plan(int N, int V, int sms) {
+// Pairs of CTAs where that is faster; tokens then come in rows of 256, so 777
+// of them are 1,024 rows instead of 896.
+LogpPlan logp_plan(int N, int V, int D, int sms) {
   long long single = 0, paired = 0;
-  const LceSplit a = best_split(N, V, sms, kTok, &single), b = best_split(N, V, sms / 2, 2 * kTok, &paired);
-  const bool pair = N > kTok && sms >= 2 && 2 * paired < 3 * single;
-  return pair ? LogpPlan{true, b.splits, b.per} : LogpPlan{false, a.splits, a.per};
+  const LogpPlan a = best_plan(N, V, D, sms, false, &single);
+  if (N <= kTok || sms < 2) return a;
+  const LogpPlan b = best_plan(N, V, D, sms / 2, true, &paired);
+  return paired < single ? b : a;
 }
 
 LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
@@ -889,13 +913,13 @@ LogpFwdLayout logp_fwd_layout(int N, int V, int top) {
 cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, const void* hidden, const void* head,
                             const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
                             float* top_logp, void* ws, cudaStream_t st) {
-  const LogpPlan sp = logp_plan(N, V, sm_count());
+  const LogpPlan sp = logp_plan(N, V, D, sm_count());
   const LogpFwdLayout L = logp_fwd_layout(N, V, top);
   CUtensorMap tH, tW, tR;
-  const int cut = sp.pair ? 2 : 1, rest = sp.per % kTileUnits;
-  const Boxes bx{kTileUnits, rest, token_rows(N), N <= 32 ? 4 : N <= 64 ? 2 : 1};
-  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, bx.rows) || !tmap_bf16_2d_sw128(&tW, head, D, V, kTileUnits * kUnit / cut) ||
-      !tmap_bf16_2d_sw128(&tR, head, D, V, (rest ? rest : kTileUnits) * kUnit / cut))
+  const int cut = sp.pair ? 2 : 1, rest = sp.per % sp.width;
+  const Boxes bx{sp.width, rest, token_rows(N), token_reps(N)};
+  if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, bx.rows) || !tmap_bf16_2d_sw128(&tW, head, D, V, sp.width * kUnit / cut) ||
+      !tmap_bf16_2d_sw128(&tR, head, D, V, (rest ? rest : sp.width) * kUnit / cut))
     return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(ws);
   FwdParams p{};
@@ -950,14 +974,15 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
                             top_logp);
 }
 
-// Units per vocabulary tile of the dz kernel: waves x (units + 1), the one for
-// a tile's fixed cost, is what the longest CTA (or pair) takes.
-static int dz_tile_units(int TM, int rows, int slots, long long* cost_out) {
-  const int units = (rows + kUnit - 1) / kUnit;
+// Units per vocabulary tile of the dz kernel: the fewest cycles for the CTA (or
+// pair) with the most tiles, 1,500 a tile beside its slices.
+static int dz_tile_units(int N, int rows, int D, int slots, bool pair, long long* cost_out) {
+  const int units = (rows + kUnit - 1) / kUnit, TM = (N + (pair ? 2 : 1) * kTok - 1) / ((pair ? 2 : 1) * kTok);
   int best = kTileUnits;
   long long best_cost = -1;
   for (int u = kTileUnits; u >= 4; --u) {
-    const long long pairs = (long long)TM * ((units + u - 1) / u), cost = (pairs + slots - 1) / slots * (u + 1);
+    const long long tiles = (long long)TM * ((units + u - 1) / u);
+    const long long cost = (tiles + slots - 1) / slots * (slice_cycles(u, pair, token_rows(N) * 128, TM) * (D / 64) + 1500);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = u;
@@ -998,9 +1023,9 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   const int sms = sm_count(), TM1 = (N + kTok - 1) / kTok, TM2 = (N + 2 * kTok - 1) / (2 * kTok);
   const int first_rows = V < L.vc ? V : L.vc;
   long long single = 0, paired = 0;
-  dz_tile_units(TM1, first_rows, sms, &single);
-  dz_tile_units(TM2, first_rows, sms / 2, &paired);
-  const bool pair = N > kTok && 2 * paired < 3 * single;  // as in logp_plan
+  dz_tile_units(N, first_rows, D, sms, false, &single);
+  if (N > kTok && sms >= 2) dz_tile_units(N, first_rows, D, sms / 2, true, &paired);
+  const bool pair = paired > 0 && paired < single;
   const int TM = pair ? TM2 : TM1, slots = pair ? sms / 2 : sms;
   CUtensorMap tH, tHb;
   if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, token_rows(N)) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
@@ -1020,7 +1045,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     p.v_base = cv0;
     p.v_end = cv0 + kc;
     long long cost = 0;
-    p.tile_units = dz_tile_units(TM, kc, slots, &cost);
+    p.tile_units = dz_tile_units(N, kc, D, slots, pair, &cost);
     p.boxes = Boxes{p.tile_units, 0, token_rows(N), 1};
     CUtensorMap tW;
     if (!tmap_bf16_2d_sw128(&tW, head, D, V, p.tile_units * kUnit / (pair ? 2 : 1))) return cudaErrorInvalidValue;
