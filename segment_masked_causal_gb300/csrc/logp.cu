@@ -604,39 +604,45 @@ __device__ __forceinline__ uint32_t ordered(float z) {
 
 // The splits' results of a token: their (m, S, A) in a fixed tree, then `top`
 // rounds that each take the largest head of the splits' lists (lowest row first
-// among equals) from shared memory. One warp per token and eight tokens a
+// among equals), staged in shared memory. One warp per token and eight tokens a
 // block, or, where tokens are few, a block per token (WPT = 8): reading the
 // lists is what takes the time, 3,000 entries for 20 alternatives of 149
 // splits, and eight warps have eight times the loads in flight. Each lane of
 // the token's first warp owns the splits lane, lane + 32, ....
+// 6.2 us for a token's five alternatives of 143 splits, 10.2 us for 17 tokens'
+// 20 of 149 (8.3 and 12.9 with the loads in three steps and heads in shared memory).
 constexpr int kListsPerLane = (kLogpMaxSplits + 31) / 32;
 template <int WPT>
 __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, float* __restrict__ logp,
                                                          float* __restrict__ lse, float* __restrict__ entropy,
                                                          int32_t* __restrict__ top_ids, float* __restrict__ top_logp) {
   extern __shared__ float2 lists[];  // per token: splits x top {logit, row}
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, tokens = (blockDim.x >> 5) / WPT, slot = (threadIdx.x >> 5) / WPT;
   const int token = blockIdx.x * tokens + slot;
   const int n = p.splits * p.top;
   float2* mine = lists + (size_t)slot * n;
-  const bool first = (threadIdx.x >> 5) % WPT == 0;
+  const bool first = (threadIdx.x >> 5) % WPT == 0 && token < p.N;
+  const int t = first ? p.targets[token] : -1;  // an input: read before the forward has ended
+  const bool scored = t >= 0 && t < p.V;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // everything that is read goes out at once
+  const float zt = scored ? p.part[(size_t)(t / kUnit / p.units_per_split) * p.N + token].w : 0.f;
   float4 q[kListsPerLane];
 #pragma unroll
   for (int l = 0; l < kListsPerLane; ++l) {
     const int s = lane + 32 * l;
-    q[l] = first && token < p.N && s < p.splits ? p.part[(size_t)s * p.N + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    q[l] = first && s < p.splits ? p.part[(size_t)s * p.N + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
   }
   if (token < p.N) {
     const float2* from = p.cand + (size_t)token * n;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x % (32 * WPT); i < n; i += 32 * WPT) mine[i] = from[i];
   }
   if (WPT > 1)
     __syncthreads();
   else
     __syncwarp();
-  if (token >= p.N || !first) return;
+  if (!first) return;
   float M = -INFINITY;
 #pragma unroll
   for (int l = 0; l < kListsPerLane; ++l) M = fmaxf(M, q[l].x);
@@ -659,56 +665,64 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
   const float l2 = log2f(S), ls = kLn2 * (M + l2);
   const auto log_p = [&](float z) { return kLn2 * (fmaf(z, p.sl2, -M) - l2); };
   if (lane == 0) {
-    const int t = p.targets[token];
-    float lp = 0.f;
-    if (t >= 0 && t < p.V) lp = log_p(p.part[(size_t)(t / kUnit / p.units_per_split) * p.N + token].w);
     const float h = kLn2 * (l2 - A / S);
-    logp[token] = lp;
+    logp[token] = scored ? log_p(zt) : 0.f;
     lse[token] = ls;
     entropy[token] = h < 0.f ? 0.f : h;  // rounding below the least entropy there is; NaN stays
   }
   if (p.top == 0) return;
-  int pos[kListsPerLane] = {};
-  uint32_t key[kListsPerLane];
-  const auto head = [&](int l) {  // 0: the list is at its end
+  // Each list's head and the entry behind it are kept in registers, so that a
+  // round is two warp reductions; lane k keeps the outcome of round k.
+  uint32_t key[kListsPerLane], row[kListsPerLane], next_key[kListsPerLane], next_row[kListsPerLane];
+  int at[kListsPerLane];  // entry after next
+  const auto fetch = [&](int l, int e, uint32_t& k, uint32_t& r) {  // key 0: the list is at its end
     const int s = lane + 32 * l;
-    if (s >= p.splits || pos[l] >= p.top) return 0u;
-    const float2 x = mine[s * p.top + pos[l]];
-    return __float_as_int(x.y) < 0 ? 0u : ordered(x.x);
+    k = 0;
+    r = 0xFFFFFFFFu;
+    if (s >= p.splits || e >= p.top) return;
+    const float2 x = mine[s * p.top + e];
+    r = (uint32_t)__float_as_int(x.y);
+    if (__float_as_int(x.y) >= 0) k = ordered(x.x);
   };
 #pragma unroll
-  for (int l = 0; l < kListsPerLane; ++l) key[l] = head(l);
+  for (int l = 0; l < kListsPerLane; ++l) {
+    fetch(l, 0, key[l], row[l]);
+    fetch(l, 1, next_key[l], next_row[l]);
+    at[l] = 2;
+  }
+  uint32_t my_key = 0, my_row = 0;
   for (int k = 0; k < p.top; ++k) {
-    uint32_t best = 0;
-    int at = 0, bl = 0;
+    uint32_t best = key[0], best_row = row[0];
+    int bl = 0;
 #pragma unroll
-    for (int l = 0; l < kListsPerLane; ++l)
+    for (int l = 1; l < kListsPerLane; ++l)
       if (key[l] > best) {  // the lower split of a lane's equal heads holds the lower rows
         best = key[l];
+        best_row = row[l];
         bl = l;
-        at = (lane + 32 * l) * p.top + pos[l];
       }
     const uint32_t most = __reduce_max_sync(~0u, best);
-    if (most == 0) {  // fewer logits above -inf than asked for
-      if (lane == 0) {
-        top_ids[(size_t)token * p.top + k] = -1;
-        top_logp[(size_t)token * p.top + k] = -INFINITY;
-      }
-      continue;
+    if (most == 0) break;  // fewer logits above -inf than asked for
+    const uint32_t low = __reduce_min_sync(~0u, best == most ? best_row : 0xFFFFFFFFu);
+    if (lane == k) {
+      my_key = most;
+      my_row = low;
     }
-    const float2 x = best == most ? mine[at] : make_float2(0.f, __int_as_float(-1));
-    const uint32_t low = __reduce_min_sync(~0u, (uint32_t)__float_as_int(x.y));
-    if ((uint32_t)__float_as_int(x.y) == low) {  // one lane: rows differ
-      top_ids[(size_t)token * p.top + k] = (int32_t)low;
-      top_logp[(size_t)token * p.top + k] = log_p(x.x);
+    if (best == most && best_row == low) {  // one lane: rows differ
 #pragma unroll
       for (int l = 0; l < kListsPerLane; ++l)
         if (l == bl) {
-          ++pos[l];
-          key[l] = head(l);
+          key[l] = next_key[l];
+          row[l] = next_row[l];
+          fetch(l, at[l]++, next_key[l], next_row[l]);
         }
     }
     __syncwarp();
+  }
+  if (lane < p.top) {
+    const float z = __uint_as_float(my_key & 0x80000000u ? my_key ^ 0x80000000u : ~my_key);
+    top_ids[(size_t)token * p.top + lane] = my_key ? (int32_t)my_row : -1;
+    top_logp[(size_t)token * p.top + lane] = my_key ? log_p(z) : -INFINITY;
   }
 }
 
