@@ -132,6 +132,7 @@ struct GemmCall {
   int M, N, K;
   int mode;          // GemmMode
   int splits;        // <= 1: one run
+  int sms;           // at most this many of the device's SMs; 0: all
   __nv_bfloat16* c;  // bf16 result (kStoreBf16: the product; kAccFinal: accumulator + product)
   float* acc;        // fp32 accumulator (kAccInit: set; kAccAdd: add; kAccFinal: read)
   uint32_t* status;
@@ -162,7 +163,8 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
                             const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
                             float* top_logp, void* ws, cudaStream_t st);
 struct LogpBwdLayout {
-  int vc, chunks, ld_dzt, splits;
+  int vc, chunks, ld_dzt;
+  int splits, splits_beside;  // runs of dH's contraction: on all SMs, and on those that dW leaves
   size_t acc, dz, dzt, bytes;
 };
 LogpBwdLayout logp_bwd_layout(int N, int V, int D);

@@ -767,6 +767,7 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (gc.sms > 0 && gc.sms < sms) sms = gc.sms;
   const double one = gemm_cost(gc.M, gc.N, gc.K, sms, splits, false), two = gemm_cost(gc.M, gc.N, gc.K, sms, splits, true);
   const bool pair = two >= 0 && two < one;
   const auto kfn = pair ? lce_gemm_kernel<true> : lce_gemm_kernel<false>;

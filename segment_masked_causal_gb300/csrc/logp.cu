@@ -1011,6 +1011,16 @@ static int dz_tile_units(int N, int rows, int D, int slots, bool pair, long long
   return best;
 }
 
+// SMs for dH where it runs beside dW from the start. With one token tile dW
+// only writes the head's gradient and dH only reads the head: one after the
+// other they leave DRAM idle at their ends and in the turn between them. Both
+// gradients of 96 tokens, in turn / dH on 56, 64 or 68 of 152 SMs: V 32,003,
+// D 2048 93 / 82, 84 or 87 us; V 151,936, D 4096 626 / 628, 618 or 638 us; V
+// 8,192, D 4096 63 / 55, 58 or 59 us. From two token tiles on the products take
+// their time on the tensor pipe, and halves of the SMs fit fewer tile counts
+// (192 tokens, V 32,003, D 2048 103 / 137 us).
+static int beside_sms(int sms) { return sms * 3 / 7 / 8 * 8; }
+
 LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   LogpBwdLayout L;
   // dz and dz^T of one chunk: at most 128 MiB each (L2 holds about one of
@@ -1022,9 +1032,12 @@ LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   L.vc = (int)vc;
   L.chunks = (V + L.vc - 1) / L.vc;
   L.ld_dzt = (N + 63) / 64 * 64;
-  L.splits = gemm_splits(N, D, L.vc < V ? L.vc : V, 152);
+  const int K = L.vc < V ? L.vc : V;
+  L.splits = gemm_splits(N, D, K, 152);
+  L.splits_beside = N <= kTok ? gemm_splits(N, D, K, beside_sms(152)) : L.splits;
+  const int most = L.splits > L.splits_beside ? L.splits : L.splits_beside;
   L.acc = 256;
-  L.dz = L.acc + (L.chunks > 1 || L.splits > 1 ? up256((size_t)L.splits * N * D * 4) : 0);
+  L.dz = L.acc + (L.chunks > 1 || most > 1 ? up256((size_t)most * N * D * 4) : 0);
   L.dzt = L.dz + up256((size_t)N * L.vc * 2);
   L.bytes = L.dzt + up256((size_t)L.vc * L.ld_dzt * 2);
   return L;
@@ -1040,6 +1053,8 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   __nv_bfloat16* dzt = reinterpret_cast<__nv_bfloat16*>(w + L.dzt);
   float* acc = reinterpret_cast<float*>(w + L.acc);
   const int sms = sm_count(), TM1 = (N + kTok - 1) / kTok, TM2 = (N + 2 * kTok - 1) / (2 * kTok);
+  // dW and dH side by side, each on its part of the SMs
+  const int apart = dhead && N <= kTok ? beside_sms(sms) : 0, splits = apart ? L.splits_beside : L.splits;
   const int first_rows = V < L.vc ? V : L.vc;
   long long single = 0, paired = 0;
   dz_tile_units(N, first_rows, D, sms, false, &single);
@@ -1103,10 +1118,11 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
       gc.c = static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D;
       gc.status = status;
       gc.order = kAfter;
+      gc.sms = apart ? sms - apart : 0;
       if ((e = launch_gemm(tA, tHb, gc, st)) != cudaSuccess) return e;
     }
     // dH += dz W[chunk] (the chunk's vocabulary rows are the contraction),
-    // the contraction cut into L.splits runs with an accumulator each
+    // the contraction cut into `splits` runs with an accumulator each
     CUtensorMap tA, tB;
     if (!tmap_bf16_2d_sw128_pitch(&tA, dz, kc, N, L.vc, 128) ||
         !tmap_bf16_2d_sw128(&tB, static_cast<const __nv_bfloat16*>(head) + (size_t)cv0 * D, D, kc, 64))
@@ -1115,8 +1131,9 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     gc.M = N;
     gc.N = D;
     gc.K = kc;
-    gc.splits = L.splits;
-    if (L.splits > 1)
+    gc.splits = splits;
+    gc.sms = apart;
+    if (splits > 1)
       gc.mode = c == 0 ? kAccInit : kAccAdd;
     else
       gc.mode = L.chunks == 1 ? kStoreBf16 : c == 0 ? kAccInit : c == L.chunks - 1 ? kAccFinal : kAccAdd;
@@ -1126,7 +1143,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     gc.order = dhead ? kBeside : kAfter;
     if ((e = launch_gemm(tA, tB, gc, st)) != cudaSuccess) return e;
   }
-  if (L.splits > 1) return launch_sum_splits(acc, L.splits, (size_t)N * D, static_cast<__nv_bfloat16*>(dhidden), st);
+  if (splits > 1) return launch_sum_splits(acc, splits, (size_t)N * D, static_cast<__nv_bfloat16*>(dhidden), st);
   return cudaSuccess;
 }
 
