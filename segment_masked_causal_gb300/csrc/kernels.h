@@ -131,6 +131,8 @@ enum GemmOrder : int { kInOrder = 0, kAfter = 1, kBeside = 2 };
 struct GemmCall {
   int M, N, K;
   int mode;          // GemmMode
+  const CUtensorMap* lo;  // null, or A's second term: the product of (A + lo) and B
+  bool stay;         // with lo, K <= 128 and one run: a CTA keeps its columns' B
   int splits;        // <= 1: one run
   int sms;           // at most this many of the device's SMs; 0: all
   __nv_bfloat16* c;  // bf16 result (kStoreBf16: the product; kAccFinal: accumulator + product)
@@ -139,9 +141,9 @@ struct GemmCall {
   int order;         // GemmOrder
 };
 cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st);
-// The number of runs that makes an M x N x K product shortest on `slots` SMs;
-// no run is empty.
-int gemm_splits(int M, int N, int K, int slots);
+// The number of runs that makes an M x N x K product (A in `terms` terms)
+// shortest on `slots` SMs; no run is empty.
+int gemm_splits(int M, int N, int K, int slots, int terms);
 cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st);
 
 // Token log probabilities. The vocabulary is cut into runs of whole units of
@@ -163,6 +165,7 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
                             const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* top_ids,
                             float* top_logp, void* ws, cudaStream_t st);
 struct LogpBwdLayout {
+  int terms;  // of dz, bf16 each
   int vc, chunks, ld_dzt;
   int splits, splits_beside;  // runs of dH's contraction: on all SMs, and on those that dW leaves
   size_t acc, dz, dzt, bytes;

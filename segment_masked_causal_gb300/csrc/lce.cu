@@ -384,16 +384,27 @@ constexpr uint32_t kGemmBHalf = 64 * 128;                 // 64 K rows x 64 N co
 constexpr int kGemmThreads = 224;  // A's copies, products, four epilogue warps, B's copies
 // PAIR: two CTAs of a cluster form one product of 256 x 256, each loading its
 // own 128 rows of A and half of B's columns: 32 KB a K block instead of 48.
-template <bool PAIR>
+// TWO: A is the sum of two bf16 matrices, which take the same block of B. STAY:
+// K is at most 128, a CTA takes its tiles column by column, and all of a column's
+// B stays behind the ring, which only A goes through (the head's gradient of 96
+// tokens in two terms: 102 us for both gradients with B in the ring, three
+// stages deep, 97 us so).
+template <bool PAIR, bool TWO, bool STAY>
 struct GemmRing {
-  static constexpr int STAGES = PAIR ? 6 : 4;
+  static_assert(PAIR ? !TWO && !STAY : TWO || !STAY, "the others are not built");
+  static constexpr int STAGES = PAIR ? 6 : STAY ? 4 : TWO ? 3 : 4;
   static constexpr int BBOXES = PAIR ? 2 : 4;  // boxes of 64 columns of B in this CTA
-  static constexpr uint32_t STAGE = kGemmA + BBOXES * kGemmBHalf;
-  static constexpr uint32_t BYTES = STAGES * STAGE;
+  static constexpr uint32_t BBLOCK = BBOXES * kGemmBHalf;
+  static constexpr uint32_t B = kGemmA, LO = kGemmA + (STAY ? 0 : BBLOCK);  // in a stage; LO: A's second term
+  static constexpr uint32_t STAGE = LO + (TWO ? kGemmA : 0);
+  static constexpr uint32_t BYTES = STAGES * STAGE + (STAY ? 2 * BBLOCK : 0);
 };
 constexpr uint32_t kGemmOut = 2 * 128 * 128;  // two boxes of 128 rows x 128 bytes on their way out
-constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + GemmRing<false>::BYTES + kGemmOut;
-static_assert(GemmRing<true>::BYTES == GemmRing<false>::BYTES && kGemmSmem <= 232448, "shared memory");
+constexpr uint32_t kGemmSmem = 1024 /* misc */ + 1024 /* alignment */ + GemmRing<false, false, false>::BYTES + kGemmOut;
+static_assert(GemmRing<true, false, false>::BYTES == GemmRing<false, false, false>::BYTES &&
+                  GemmRing<false, true, false>::BYTES == GemmRing<false, false, false>::BYTES &&
+                  GemmRing<false, true, true>::BYTES == GemmRing<false, false, false>::BYTES && kGemmSmem <= 232448,
+              "shared memory");
 
 // Row blocks per group of the tile order. Measured on the N = 8192,
 // V = 151,936, D = 4096 backward (38 launches a call), in one run: 20.95,
@@ -426,6 +437,7 @@ struct GemmParams {
 struct GemmMisc {
   uint64_t full[6], empty[6];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t b_full, b_empty;  // STAY
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
@@ -455,17 +467,18 @@ __device__ __forceinline__ void store_box(uint32_t taddr, uint32_t out, int r, b
   }
 }
 
-template <bool PAIR>
+template <bool PAIR, bool TWO, bool STAY>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    lce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmC, const GemmParams p) {
+    lce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmLo,
+                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
+                    const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   GemmMisc& m = *reinterpret_cast<GemmMisc*>(smem_raw);
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sRing = smem_u32(ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  using R = GemmRing<PAIR>;
+  using R = GemmRing<PAIR, TWO, STAY>;
   constexpr int kPer = PAIR ? 2 : 1, kRows = 128 * kPer, kGroup = kGemmGroup / kPer;
   const int cta = (int)blockIdx.x / kPer, ctas = (int)gridDim.x / kPer, rank = PAIR ? (int)blockIdx.x % 2 : 0;
   const int KB = (p.K + 63) / 64;
@@ -476,10 +489,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   };
   // this CTA's (or pair's) tiles: t = cta + j * ctas for j < nt (>= 1: the
   // grid is never larger than the tile count)
-  const int nt = (p.tiles - cta + ctas - 1) / ctas;
+  // STAY: t0 .. t0 + nt - 1, row blocks fastest
+  const int t0 = STAY ? (int)((long long)p.tiles * cta / ctas) : cta, dt = STAY ? 1 : ctas;
+  const int nt = STAY ? (int)((long long)p.tiles * (cta + 1) / ctas) - t0 : (p.tiles - cta + ctas - 1) / ctas;
   // first row (of this CTA) and column of tile t: group gi holds row blocks g0 .. g0 + gs - 1
   const auto tile_origin = [&](int t) -> int2 {
     t %= p.per_split;
+    if (STAY) return make_int2(t % p.m_tiles * kRows, t / p.m_tiles * kGemmN);
     const int gi = t / (kGroup * p.n_tiles), r = t - gi * kGroup * p.n_tiles;
     const int g0 = gi * kGroup, gs = min(kGroup, p.m_tiles - g0);
     return make_int2((g0 + r % gs) * kRows + rank * 128, (r / gs) * kGemmN);
@@ -496,6 +512,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(&m.acc_full[b], 1);
       mbar_init(&m.acc_empty[b], 128 * kPer);
     }
+    mbar_init(&m.b_full, 1);
+    mbar_init(&m.b_empty, 1);
     mbar_init(&m.fin, 1);
     fence_mbar_init();
   }
@@ -519,7 +537,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
 
-  if (warp == 0 || warp == 6) {
+  if (STAY && warp == 6) {
+    // B of each column of tiles, once the products of the column before have read theirs
+    if (lane == 0) {
+      prefetch_tmap(&tmB);
+      int columns = 0;
+      for (int j = 0; j < nt; ++j) {
+        const int n0 = tile_origin(t0 + j).y;
+        if (j > 0 && n0 == tile_origin(t0 + j - 1).y) continue;
+        if (!g.wait(&m.b_empty, (columns & 1) ^ 1, 49)) break;
+        mbar_expect_tx(&m.b_full, KB * R::BBLOCK);
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int c = 0; c < R::BBOXES; ++c)
+            tma_load_2d(ring + R::STAGES * R::STAGE + kb * R::BBLOCK + c * kGemmBHalf, &tmB, &m.b_full, n0 + 64 * c, kb * 64);
+        ++columns;
+      }
+      if (columns > 0) g.drain(&m.b_full, (columns - 1) & 1);  // no copy may still be landing when the CTA exits
+    }
+    __syncwarp();
+  } else if (warp == 0 || warp == 6) {
     // A's copies by warp 0, which also announces the bytes of both, B's by warp 6
     if (lane == 0) {
       const bool isA = warp == 0;
@@ -529,9 +566,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t phase = 1;
       bool ok = true;
       for (int j = 0; ok && j < nt; ++j) {
-        const int2 o = tile_origin(cta + j * ctas);
+        const int2 o = tile_origin(t0 + j * dt);
         const int m0 = o.x, n0 = o.y + 64 * rank * R::BBOXES;
-        const int2 run = tile_run(cta + j * ctas);
+        const int2 run = tile_run(t0 + j * dt);
         for (int kb = run.x; kb < run.y; ++kb, ++it) {
           if (!g.wait(&m.empty[st], phase, isA ? 45 : 49)) { ok = false; break; }
           uint8_t* sa = ring + st * R::STAGE;
@@ -541,13 +578,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               tma_load_2d_pair(sa, &tmA, full0 + st * 8, kb * 64, m0);
             else
               tma_load_2d(sa, &tmA, &m.full[st], kb * 64, m0);
+            if (TWO) tma_load_2d(sa + R::LO, &tmLo, &m.full[st], kb * 64, m0);
           } else {
 #pragma unroll
             for (int c = 0; c < R::BBOXES; ++c)
               if (PAIR)
-                tma_load_2d_pair(sa + kGemmA + c * kGemmBHalf, &tmB, full0 + st * 8, n0 + 64 * c, kb * 64);
+                tma_load_2d_pair(sa + R::B + c * kGemmBHalf, &tmB, full0 + st * 8, n0 + 64 * c, kb * 64);
               else
-                tma_load_2d(sa + kGemmA + c * kGemmBHalf, &tmB, &m.full[st], n0 + 64 * c, kb * 64);
+                tma_load_2d(sa + R::B + c * kGemmBHalf, &tmB, &m.full[st], n0 + 64 * c, kb * 64);
           }
           if (++st == R::STAGES) {
             st = 0;
@@ -565,21 +603,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool leader = lane == 0;
     constexpr uint32_t idC = idesc_bf16_f32(kRows, kGemmN, false, true);
     bool ok = true;
-    int it = 0;
+    int it = 0, columns = 0;
     for (int j = 0; ok && rank == 0 && j < nt; ++j) {  // rank 0 issues for both
       const int buf = j & 1;
       // accumulator buf is free once the epilogue has read tile j - 2 from it
       if (j >= 2 && !g.wait_warp(&m.acc_empty[buf], ((j - 2) >> 1) & 1, 48)) { ok = false; break; }
       if (PAIR) fence_cluster();  // half of the arrivals are the other CTA's
       tc_fence_after();
-      const int2 run = tile_run(cta + j * ctas);
+      const int2 run = tile_run(t0 + j * dt);
+      if (STAY && (j == 0 || tile_origin(t0 + j).y != tile_origin(t0 + j - 1).y)) {
+        if (!g.wait_warp(&m.b_full, columns & 1, 46)) { ok = false; break; }
+        ++columns;
+      }
       for (int kb = run.x; kb < run.y; ++kb, ++it) {
         const int st = it % R::STAGES;
         if (!g.wait_warp(&m.full[st], (it / R::STAGES) & 1, 46)) { ok = false; break; }
         tc_fence_after();
         const uint32_t sa = sRing + st * R::STAGE;
         const uint64_t ad = sdesc_sw128(sa, 16, 1024);
-        const uint64_t bd = sdesc_sw128(sa + kGemmA, kGemmBHalf, 1024);
+        const uint64_t bd = sdesc_sw128(STAY ? sRing + R::STAGES * R::STAGE + kb * R::BBLOCK : sa + R::B, kGemmBHalf, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           if (leader) {
@@ -589,10 +631,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             else
               umma_bf16(tmem + buf * kGemmN, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), idC, add);
           }
+        if (TWO) {
+          const uint64_t ld = sdesc_sw128(sa + R::LO, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (leader) umma_bf16(tmem + buf * kGemmN, sdesc_add(ld, kk * 32), sdesc_add(bd, kk * 2048), idC, 1u);
+        }
         if (leader) PAIR ? umma_commit_pair(&m.empty[st]) : umma_commit(&m.empty[st]);
         __syncwarp();
       }
       if (ok && leader) PAIR ? umma_commit_pair(&m.acc_full[buf]) : umma_commit(&m.acc_full[buf]);
+      if (STAY && ok && leader && j + 1 < nt && tile_origin(t0 + j).y != tile_origin(t0 + j + 1).y) umma_commit(&m.b_empty);
       __syncwarp();
     }
     if (leader && rank == 0) {
@@ -605,7 +654,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const bool f32 = p.mode == kAccInit, through = f32 || p.mode == kStoreBf16;
-    uint8_t* out = ring + R::STAGES * R::STAGE;
+    uint8_t* out = ring + R::BYTES;
     const bool issuer = threadIdx.x == 64;
     int box = 0;
     const auto release = [&](int buf) {
@@ -620,13 +669,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const bool ok = __all_sync(~0u, g.wait(&m.acc_full[buf], (j >> 1) & 1, 47));
       if (!ok) break;
       tc_fence_after();
-      const int2 o = tile_origin(cta + j * ctas);
+      const int2 o = tile_origin(t0 + j * dt);
       const int m0 = o.x, n0 = o.y;
       const int row = m0 + quarter * 32 + lane;
       if (through) {
         // a box of 128 rows x 128 bytes at a time, through two buffers in turn (the
         // second CTA of a pair may lie past the last row)
-        const int run = (cta + j * ctas) / p.per_split, step = f32 ? 32 : 64;
+        const int run = (t0 + j * dt) / p.per_split, step = f32 ? 32 : 64;
 #pragma unroll 1
         for (int c0 = 0; m0 < p.M && c0 < kGemmN && n0 + c0 < p.N; c0 += step, box ^= 1) {
           if (issuer) bulk_wait_read1();  // the buffer's last copy has left it
@@ -644,7 +693,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         continue;
       }
       // each run of K has an accumulator of its own
-      float* acc = p.acc + (size_t)((cta + j * ctas) / p.per_split) * p.M * p.ldacc;
+      float* acc = p.acc + (size_t)((t0 + j * dt) / p.per_split) * p.M * p.ldacc;
 #pragma unroll 1
       for (int c0 = 0; c0 < kGemmN; c0 += 32) {
         uint32_t a[32];
@@ -733,23 +782,24 @@ constexpr int kGemmPairBlocks = PA_GEMM_PAIR_BLOCKS;
 // Cycles of an M x N x K product cut into s runs of K, on `slots` SMs: waves x
 // (K blocks + 8 blocks' worth for the pipeline's fill and the tile's epilogue);
 // a block takes a pair 622 cycles (512 of products, with copies and operands in
-// one shared memory) and a CTA alone its copies' 664 (48 KB at 74 bytes a cycle); and, with more than one run, writing and
+// one shared memory) and a CTA alone its copies' 664 (48 KB at 74 bytes a cycle),
+// or 1,130 with A in two terms; and, with more than one run, writing and
 // reading the accumulators at 6.5 TB/s. < 0 where a run would be empty.
-static double gemm_cost(int M, int N, int K, int slots, int s, bool pair) {
+static double gemm_cost(int M, int N, int K, int slots, int s, bool pair, int terms) {
   const int KB = (K + 63) / 64, per = (KB + s - 1) / s;
-  if ((KB + per - 1) / per != s || (pair && (M <= 128 || slots < 2 || per < kGemmPairBlocks))) return -1.0;
+  if ((KB + per - 1) / per != s || (pair && (terms > 1 || M <= 128 || slots < 2 || per < kGemmPairBlocks))) return -1.0;
   const long long rows = pair ? 256 : 128, at_once = pair ? slots / 2 : slots;
   const long long tiles = ((M + rows - 1) / rows) * ((N + kGemmN - 1) / kGemmN);
   const long long waves = (tiles * s + at_once - 1) / at_once;
-  return (double)waves * (per * (pair ? 622.0 : 664.0) + 8 * 512.0) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 * 1900 : 0.0);
+  return (double)waves * (per * (pair ? 622.0 : terms > 1 ? 1130.0 : 664.0) + 8 * 512.0) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 * 1900 : 0.0);
 }
 
-int gemm_splits(int M, int N, int K, int slots) {
+int gemm_splits(int M, int N, int K, int slots, int terms) {
   int best = 1;
   double best_cost = -1;
   for (int s = 1; s <= 64 && s <= (K + 63) / 64; ++s)
     for (const bool pair : {false, true}) {
-      const double cost = gemm_cost(M, N, K, slots, s, pair);
+      const double cost = gemm_cost(M, N, K, slots, s, pair, terms);
       if (cost >= 0 && (best_cost < 0 || cost < best_cost)) {
         best_cost = cost;
         best = s;
@@ -768,9 +818,15 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (gc.sms > 0 && gc.sms < sms) sms = gc.sms;
-  const double one = gemm_cost(gc.M, gc.N, gc.K, sms, splits, false), two = gemm_cost(gc.M, gc.N, gc.K, sms, splits, true);
+  const int terms = gc.lo ? 2 : 1;
+  const double one = gemm_cost(gc.M, gc.N, gc.K, sms, splits, false, terms);
+  const double two = gemm_cost(gc.M, gc.N, gc.K, sms, splits, true, terms);
   const bool pair = two >= 0 && two < one;
-  const auto kfn = pair ? lce_gemm_kernel<true> : lce_gemm_kernel<false>;
+  if (gc.stay && (!gc.lo || KB > 2 || planes > 1)) return cudaErrorInvalidValue;
+  const auto kfn = pair      ? lce_gemm_kernel<true, false, false>
+                   : gc.stay ? lce_gemm_kernel<false, true, true>
+                   : gc.lo   ? lce_gemm_kernel<false, true, false>
+                             : lce_gemm_kernel<false, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   if (e != cudaSuccess) return e;
   const long long rows = pair ? 256 : 128, mt = (gc.M + rows - 1) / rows, ntl = (gc.N + kGemmN - 1) / kGemmN;
@@ -807,7 +863,7 @@ cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const Gemm
   cudaLaunchAttribute attrs[2] = {cluster_pair(), programmatic_launch()};
   cfg.attrs = pair ? attrs : attrs + 1;
   cfg.numAttrs = (pair ? 1 : 0) + (gc.order == kInOrder ? 0 : 1);
-  return cudaLaunchKernelEx(&cfg, kfn, tA, tB, tC, q);
+  return cudaLaunchKernelEx(&cfg, kfn, tA, gc.lo ? *gc.lo : tA, tB, tC, q);
 }
 
 cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st) {

@@ -36,6 +36,10 @@ constexpr int kUnit = kLogpUnit;           // vocabulary rows of one unit: what 
 constexpr int kTileUnits = 8;              // units per logit tile: 256 columns
 constexpr uint32_t kSliceH = kTok * 128;   // 128 x 64 bf16, 16 KB
 constexpr int kThreads = 256;
+// Eight epilogue warps, two a token quarter: the last tile's epilogue stands
+// behind its products (1,000 tokens over V 151,936, D 512: 564 us with four
+// warps, 547 with eight; 4,096 over V 32,003, D 64: 331 and 327).
+constexpr int kDzThreads = 384;
 constexpr uint32_t kTmemCols = 512;  // two 256-column fp32 accumulators
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -96,9 +100,9 @@ struct BwdParams {
   const float* entropy;    // read where g_entropy is given
   const float* g_logp;
   const float* g_entropy;  // may be null
-  __nv_bfloat16* dz;       // (N, ld_dz)
+  __nv_bfloat16* dz;       // (terms, N, ld_dz)
   int ld_dz;
-  __nv_bfloat16* dzt;      // (vc, ld_dzt), or null (frozen head)
+  __nv_bfloat16* dzt;      // (terms, ld_dz, ld_dzt), or null (frozen head)
   int ld_dzt;
   uint32_t* status;
 };
@@ -139,9 +143,9 @@ __device__ __forceinline__ void st_shared_if(uint32_t on, uint32_t addr, uint32_
 }
 
 // Barriers and TMEM. In a pair the full and acc_empty barriers of rank 0 serve
-// both CTAs; the others are each CTA's own.
+// both CTAs; the others are each CTA's own. `readers`: epilogue threads of a CTA.
 template <bool PAIR>
-__device__ __forceinline__ void setup(Misc& m) {
+__device__ __forceinline__ void setup(Misc& m, int readers) {
   if (threadIdx.x == 0) {
     m.abort_flag = 0;
     for (int s = 0; s < Ring<PAIR>::STAGES; ++s) {
@@ -150,7 +154,7 @@ __device__ __forceinline__ void setup(Misc& m) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&m.acc_full[b], 1);
-      mbar_init(&m.acc_empty[b], PAIR ? 256 : 128);
+      mbar_init(&m.acc_empty[b], PAIR ? 2 * readers : readers);
     }
     mbar_init(&m.fin, 1);
     fence_mbar_init();
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // The status word starts at 0: no wait can give up within 2 s of the launch.
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;
-  setup<PAIR>(m);
+  setup<PAIR>(m, kThreads - 128);
   // the merge may take its place on the SMs; it waits for this kernel's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = m.tmem_base;
@@ -735,13 +739,15 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 // exactly 0 in rows without a gradient and in columns past V. dz is rounded
 // to bf16, the operand type of the two products that follow (at most
 // 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
-// That and the results' own rounding, 1.6e-3 of the norm each, make 2.3e-3, and
-// up to 2.6e-3 where a few values at the targets carry it (96 tokens). dz as the
-// sum of two bf16 terms (2^-16 of the value) for up to 128 tokens, where the
-// products wait for the head, took 96 tokens over V 32,003, D 2048 from 94 to
-// 110 us; one term stayed.
-template <bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+// That and the results' own rounding, 1.6e-3 of the norm each, make 2.3e-3. But
+// the gradients of a few tokens hang on the few values at their targets, whose
+// roundings do not average out: 3.5e-3 for one token, 2.6e-3 for 96. So up to
+// 128 tokens, where the products wait for the head more than for the tensor pipe,
+// dz is the sum of two bf16 terms (2^-16 of the value): the results' rounding
+// alone is left, for 97 us instead of 84 (both gradients of 96 tokens over V
+// 32,003, D 2048).
+template <bool PAIR, int TERMS>
+__global__ void __launch_bounds__(kDzThreads, 1)
     logp_dz_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                    const BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -767,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait can give up within 2 s
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  setup<PAIR>(m);
+  setup<PAIR>(m, kDzThreads - 128);
   if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");  // the last chunk's products have read dz
   const uint32_t tmem = m.tmem_base;
 
@@ -797,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int v0 = tl.u * kUnit, c0v = v0 - p.v_base;  // column of v0 in the chunk
 #pragma unroll 1
-      for (int c0 = 0; c0 < tl.units * kUnit; c0 += 32) {
+      for (int c0 = (warp >> 2) % 2 * 32; c0 < tl.units * kUnit; c0 += 64) {  // every second unit
         uint32_t a[32];
         tmem_ld32(tmem + lane_base + buf * 256 + c0, a);
         const int vc = v0 + c0;
@@ -817,23 +823,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (!use || vc + i >= p.V) d[i] = 0.f;
         }
-        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
-        if (live) {
-          __nv_bfloat16* row = p.dz + (size_t)token * p.ld_dz + c0v + c0;
+        for (int term = 0; term < TERMS; ++term) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            w[i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+            if (term + 1 < TERMS) {  // what is left for the next term
+              d[2 * i] -= __uint_as_float(w[i] << 16);
+              d[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+          }
+          if (!live) continue;
+          __nv_bfloat16* row = p.dz + ((size_t)term * p.N + token) * p.ld_dz + c0v + c0;
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             if (vc + 8 * u < p.V)
               *reinterpret_cast<uint4*>(row + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-          if (p.dzt) {
-            __nv_bfloat16* colp = p.dzt + (size_t)(c0v + c0) * p.ld_dzt + token;
+          if (!p.dzt) continue;
+          __nv_bfloat16* colp = p.dzt + ((size_t)term * p.ld_dz + c0v + c0) * p.ld_dzt + token;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (vc + i < p.V)
-                colp[(size_t)i * p.ld_dzt] =
-                    __ushort_as_bfloat16((unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu));
-          }
+          for (int i = 0; i < 32; ++i)
+            if (vc + i < p.V)
+              colp[(size_t)i * p.ld_dzt] =
+                  __ushort_as_bfloat16((unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu));
         }
       }
       release_acc<PAIR>(m, buf);
@@ -1014,32 +1027,34 @@ static int dz_tile_units(int N, int rows, int D, int slots, bool pair, long long
 // SMs for dH where it runs beside dW from the start. With one token tile dW
 // only writes the head's gradient and dH only reads the head: one after the
 // other they leave DRAM idle at their ends and in the turn between them. Both
-// gradients of 96 tokens, in turn / dH on 56, 64 or 68 of 152 SMs: V 32,003,
-// D 2048 93 / 82, 84 or 87 us; V 151,936, D 4096 626 / 628, 618 or 638 us; V
-// 8,192, D 4096 63 / 55, 58 or 59 us. From two token tiles on the products take
-// their time on the tensor pipe, and halves of the SMs fit fewer tile counts
-// (192 tokens, V 32,003, D 2048 103 / 137 us).
-static int beside_sms(int sms) { return sms * 3 / 7 / 8 * 8; }
+// gradients of 96 tokens with dz in one term, in turn / side by side: V 32,003,
+// D 2048 94 / 84 us; V 8,192, D 4096 63 / 58 us. From two token tiles on the
+// products take their time on the tensor pipe, and halves of the SMs fit fewer
+// tile counts (192 tokens, V 32,003, D 2048 103 / 137 us). With two terms, dH on
+// 64, 72 or 80 of 152 SMs, 1 and 96 tokens: V 32,003, D 2048 89 and 98, 85 and
+// 98, 90 and 103 us; V 151,936, D 4096 702 and 730, 654 and 714, 666 and 763 us.
+static int beside_sms(int sms) { return sms / 2 / 8 * 8; }
 
 LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   LogpBwdLayout L;
   // dz and dz^T of one chunk: at most 128 MiB each (L2 holds about one of
   // them), in whole vocabulary tiles
   const long long vmax = (long long)(V + 255) / 256 * 256;
-  long long vc = (1ll << 26) / N / 256 * 256;
+  L.terms = N <= kTok ? 2 : 1;
+  long long vc = (1ll << 26) / (L.terms * (long long)N) / 256 * 256;
   if (vc > vmax) vc = vmax;
   if (vc < 256) vc = 256;
   L.vc = (int)vc;
   L.chunks = (V + L.vc - 1) / L.vc;
   L.ld_dzt = (N + 63) / 64 * 64;
   const int K = L.vc < V ? L.vc : V;
-  L.splits = gemm_splits(N, D, K, 152);
-  L.splits_beside = N <= kTok ? gemm_splits(N, D, K, beside_sms(152)) : L.splits;
+  L.splits = gemm_splits(N, D, K, 152, L.terms);
+  L.splits_beside = N <= kTok ? gemm_splits(N, D, K, beside_sms(152), L.terms) : L.splits;
   const int most = L.splits > L.splits_beside ? L.splits : L.splits_beside;
   L.acc = 256;
   L.dz = L.acc + (L.chunks > 1 || most > 1 ? up256((size_t)most * N * D * 4) : 0);
-  L.dzt = L.dz + up256((size_t)N * L.vc * 2);
-  L.bytes = L.dzt + up256((size_t)L.vc * L.ld_dzt * 2);
+  L.dzt = L.dz + up256((size_t)L.terms * N * L.vc * 2);
+  L.bytes = L.dzt + up256((size_t)L.terms * L.vc * L.ld_dzt * 2);
   return L;
 }
 
@@ -1064,7 +1079,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
   CUtensorMap tH, tHb;
   if (!tmap_bf16_2d_sw128(&tH, hidden, D, N, token_rows(N)) || !tmap_bf16_2d_sw128(&tHb, hidden, D, N, 64))
     return cudaErrorInvalidValue;
-  const auto kfn = pair ? logp_dz_kernel<true> : logp_dz_kernel<false>;
+  const auto kfn = L.terms > 1 ? logp_dz_kernel<false, 2> : pair ? logp_dz_kernel<true, 1> : logp_dz_kernel<false, 1>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attrs[2] = {cluster_pair(), programmatic_launch()};
@@ -1100,7 +1115,7 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     const long long pairs = (long long)TM * ((units + p.tile_units - 1) / p.tile_units);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((pairs < slots ? (int)pairs : slots) * (pair ? 2 : 1));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kDzThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = pair ? attrs : attrs + 1;
@@ -1108,9 +1123,13 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     if ((e = cudaLaunchKernelEx(&cfg, kfn, tH, tW, p)) != cudaSuccess) return e;
     // dW rows of the chunk = dz^T H (the tokens are the contraction)
     if (dhead) {
-      CUtensorMap tA;
-      if (!tmap_bf16_2d_sw128_pitch(&tA, dzt, N, kc, L.ld_dzt, 128)) return cudaErrorInvalidValue;
+      CUtensorMap tA, tLo;
+      if (!tmap_bf16_2d_sw128_pitch(&tA, dzt, N, kc, L.ld_dzt, 128) ||
+          (L.terms > 1 && !tmap_bf16_2d_sw128_pitch(&tLo, dzt + (size_t)L.vc * L.ld_dzt, N, kc, L.ld_dzt, 128)))
+        return cudaErrorInvalidValue;
       GemmCall gc{};
+      gc.lo = L.terms > 1 ? &tLo : nullptr;
+      gc.stay = L.terms > 1;
       gc.M = kc;
       gc.N = D;
       gc.K = N;
@@ -1123,11 +1142,13 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     }
     // dH += dz W[chunk] (the chunk's vocabulary rows are the contraction),
     // the contraction cut into `splits` runs with an accumulator each
-    CUtensorMap tA, tB;
+    CUtensorMap tA, tLo, tB;
     if (!tmap_bf16_2d_sw128_pitch(&tA, dz, kc, N, L.vc, 128) ||
+        (L.terms > 1 && !tmap_bf16_2d_sw128_pitch(&tLo, dz + (size_t)N * L.vc, kc, N, L.vc, 128)) ||
         !tmap_bf16_2d_sw128(&tB, static_cast<const __nv_bfloat16*>(head) + (size_t)cv0 * D, D, kc, 64))
       return cudaErrorInvalidValue;
     GemmCall gc{};
+    gc.lo = L.terms > 1 ? &tLo : nullptr;
     gc.M = N;
     gc.N = D;
     gc.K = kc;
