@@ -449,8 +449,9 @@ pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_
  * NULL (all 0), entropy then too. A target outside [0, V) leaves only the
  * entropy's part; a token without any gradient has a dhidden row of exact
  * zeros. Every row of hidden is a factor in dhead, so a padding row holds
- * finite values even where its gradient is 0. The vocabulary is taken in chunks as in pa_lce_bwd (the
- * logits are formed again, dz of a chunk is held in bf16), in a fixed order.
+ * finite values even where its gradient is 0. The vocabulary is taken in chunks
+ * as in pa_lce_bwd (the logits are formed again, dz of a chunk is held in bf16,
+ * up to 128 tokens as the sum of two bf16 terms), in a fixed order.
  * ws >= pa_logp_bwd_workspace_bytes(N, V, D). Arguments, execution and errors
  * otherwise as pa_logp_fwd.
  */
