@@ -451,7 +451,9 @@ pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_
  * zeros. Every row of hidden is a factor in dhead, so a padding row holds
  * finite values even where its gradient is 0. The vocabulary is taken in chunks
  * as in pa_lce_bwd (the logits are formed again, dz of a chunk is held in bf16,
- * up to 128 tokens as the sum of two bf16 terms), in a fixed order.
+ * up to 128 tokens as the sum of two bf16 terms), in a fixed order: the same
+ * call gives the same bits (with dhead NULL, dhidden of up to 128 tokens is
+ * summed in another order).
  * ws >= pa_logp_bwd_workspace_bytes(N, V, D). Arguments, execution and errors
  * otherwise as pa_logp_fwd.
  */

@@ -356,6 +356,37 @@ def test_backward_frozen_head_bits_and_graph(cuda_dev):
         assert torch.equal(gh, dh) and torch.equal(gw, dw)
 
 
+@pytest.mark.parametrize("N", [1, 100])
+def test_few_tokens_bits_graph_and_two_streams(N, cuda_dev):
+    """The head's and the states' gradients of few tokens run side by side: the
+    same bits again, replayed, and in two calls at once on streams of their own."""
+    V, D = 20011, 576
+    H, W, t = inputs(N, V, D, 16)
+    h, w, tt = dev_bf16(H, cuda_dev), dev_bf16(W, cuda_dev), torch.from_numpy(t).to(cuda_dev)
+    _, lse, ent, _, _ = pa.token_logprobs_forward(h, w, tt)
+    g, e = (torch.from_numpy(x.astype(np.float32)).to(cuda_dev) for x in upstream(N, t, V, 4, True))
+    dh, dw = pa.token_logprobs_backward(h, w, tt, lse, ent, g, e)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gh, gw = pa.token_logprobs_backward(h, w, tt, lse, ent, g, e)
+    for _ in range(2):
+        gh.zero_()
+        gw.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(gh, dh) and torch.equal(gw, dw)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    made = [[], []]
+    for _ in range(4):
+        for s, m in zip(streams, made):
+            with torch.cuda.stream(s):
+                m.append(pa.token_logprobs_backward(h, w, tt, lse, ent, g, e))
+    torch.cuda.synchronize()
+    for m in made:
+        for x, y in m:
+            assert torch.equal(x, dh) and torch.equal(y, dw)
+
+
 def test_the_mean_nll_is_the_cross_entropys(cuda_dev):
     """At temperature 1 logp is minus the cross-entropy's NLL, and its gradient
     the cross-entropy's with the sign turned."""
