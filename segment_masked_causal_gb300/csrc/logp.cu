@@ -16,7 +16,9 @@
 // A = sum 2^t t, so that lse = ln 2 (m + log2 S) and H = ln 2 (log2 S - A / S):
 // A is a sum of terms that are all <= 0 and vanish at both ends, so nothing
 // cancels in it. A larger maximum m' = m + d turns (S, A) into
-// (S 2^-d, (A - d S) 2^-d).
+// (S 2^-d, (A - d S) 2^-d). Both sums carry what their additions lose: with one
+// likely token S is near 1, and of a hundred thousand others at 1e-9, which add
+// 1e-4 in all, 32 columns together are less than half a step of it.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -327,6 +329,16 @@ struct Joint {
 };
 static_assert(sizeof(Joint) <= Ring<false>::BYTES, "fits the ring");
 
+// sum * f + x into sum, and what the product and the addition have rounded off
+// into lost (Knuth, "The Art of Computer Programming" 2, 4.2.2: the error of an
+// addition is itself a float). The intrinsics keep them from being fused.
+__device__ __forceinline__ void add_kept(float& sum, float& lost, float f, float x) {
+  const float p = __fmul_rn(sum, f), s = __fadd_rn(p, x), b = __fsub_rn(s, p);
+  const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(s, b)), __fsub_rn(x, b));
+  lost = fmaf(lost, f, __fadd_rn(fmaf(sum, f, -p), e));
+  sum = s;
+}
+
 // (m, S, A) of two disjoint sets of columns as that of both.
 __device__ __forceinline__ void join(float4& x, const float4& y) {
   const float m = fmaxf(x.x, y.x);
@@ -490,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       held = 0;
       least = fmaxf(least, tz[KL - 1]);
     };
-    float m_run = -INFINITY, s_run = 0.f, a_run = 0.f, tgt = 0.f;
+    float m_run = -INFINITY, s_run = 0.f, a_run = 0.f, s_lost = 0.f, a_lost = 0.f, tgt = 0.f;
     const uint64_t sl2 = f2(p.sl2, p.sl2);
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -543,8 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float2 ss = f2_split(s2), aa = f2_split(a2);
           const float d = m_run > -INFINITY ? m_run - shift : 0.f, sc = ex2(d);
-          a_run = fmaf(fmaf(d, s_run, a_run), sc, aa.x + aa.y);
-          s_run = fmaf(s_run, sc, ss.x + ss.y);
+          a_run = fmaf(d, s_run, a_run);
+          a_lost = fmaf(d, s_lost, a_lost);
+          add_kept(a_run, a_lost, sc, aa.x + aa.y);
+          add_kept(s_run, s_lost, sc, ss.x + ss.y);
           m_run = m_new;
           if (t >= vc && t < vc + 32) {
 #pragma unroll
@@ -574,6 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       release_acc<PAIR>(m, buf);
     }
+    s_run += s_lost;
+    a_run += a_lost;
     if (KM > 0) insert_held();
     if (!PAIR && p.boxes.reps > 1) {
       // every product has completed and every copy been read: the ring is free

@@ -132,6 +132,61 @@ def test_a_sure_token(cuda_dev):
     assert abs(got[2][2]) <= 2.0 ** -22 and abs(got[0][2]) <= 2.0 ** -22
 
 
+# A token of logit a at its dominant row and -a at the V - 1 others, with g = 2a / T
+# the gap in nats: S = 1 + tail, tail = (V - 1) exp(-g), so
+#   logp = -ln(1 + tail), entropy = ln(1 + tail) + g tail / (1 + tail).
+# In units of 2^-24 the sum S, which lies in [1, 2), loses at most half a step (one
+# unit) in each addition on the way of the large term: 16 inside its own chunk of
+# 32 columns, one at the split's end, 3 where the columns are shared by four warps,
+# 9 in the merge; the exponential of the dominant term itself is within 2^-22 of 1
+# (4 units). What the additions between the chunks lose is kept beside the sum. The
+# small terms are each off by ln 2 * 2^-24 (3 * 1.45 a / T) for the argument and 2^-22
+# for the exponential, and so is their sum A = sum 2^t t, which loses 16 + 3 + 9
+# units of itself in additions, relative to |A| = g tail. So logp is within
+# 40 (1 + tail) units, and the entropy within 40 + 80 (1 + g) tail (tail <= 1).
+def check_dominant(N, V, T, dev):
+    D = 64
+    amp = np.arange(8 * 16, 12 * 16 + 1) / 16 * T  # gaps of 16 to 24
+    amp = np.round(amp * 16) / 16
+    first = [0, V // 3, V - 1, 31]  # the dominant row, by the token's column
+    a = amp[(np.arange(N) * 37) % len(amp)]
+    g = 2 * a / T
+    tail = (V - 1) * np.exp(-g)
+    a = np.where(tail <= 1, a, amp[-1])
+    g = 2 * a / T
+    tail = (V - 1) * np.exp(-g)
+    col = np.arange(N) % 4
+    h = torch.zeros(N, D, dtype=torch.bfloat16)
+    h[torch.arange(N), torch.from_numpy(col)] = torch.from_numpy(a).to(torch.bfloat16)
+    assert (h.double().sum(1).numpy() == a).all()
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device=dev)
+    w[:, :4] = -1
+    for c, r in enumerate(first):
+        w[r, c] = 1
+    t = torch.tensor([first[c] for c in col], dtype=torch.int32)
+    logp, lse, ent, ids, alt = (x.cpu().double().numpy() for x in pa.token_logprobs_forward(
+        h.to(dev), w, t.to(dev), temperature=T, top=1))
+    assert (ids[:, 0] == t.numpy()).all()
+    u = 2.0 ** -24
+    e_logp, e_ent = -np.log1p(tail), np.log1p(tail) + g * tail / (1 + tail)
+    for got, want, bar, n in ((logp, e_logp, 40 * u * (1 + tail), "logp"), (alt[:, 0], e_logp, 40 * u * (1 + tail), "top_logp"),
+                              (lse, a / T + np.log1p(tail), 40 * u * (1 + tail) + 4 * u * a / T, "lse"),
+                              (ent, e_ent, u * (40 + 80 * (1 + g) * tail), "entropy")):
+        err = np.abs(got - want)
+        print(f"{n}: max err {err.max():.2e}, {(err / bar).max():.2f} of its bar")
+        assert (err <= bar).all(), n
+
+
+# one token to many: columns shared by four, two and no warps, CTA pairs; splits of
+# 100 to 1,000 chunks of 32 columns
+@pytest.mark.parametrize("N,V", [(1, 4_000_000), (60, 2_000_000), (100, 1_000_000), (1500, 400_000), (8192, 151_936)])
+@pytest.mark.parametrize("T", [1.0, 0.5])
+def test_a_likely_tokens_tail_is_summed(N, V, T, cuda_dev):
+    """Thousands of tokens of 1e-9 each behind a likely one, whose probability
+    alone is nearly 1: what they add in all is not rounded away chunk by chunk."""
+    check_dominant(N, V, T, cuda_dev)
+
+
 def test_infinities_and_nan_stay_in_their_rows(cuda_dev):
     N, V, D = 6, 300, 64
     H, W, t = inputs(N, V, D, 9)
