@@ -11,12 +11,15 @@
 // "The fused cross-entropy loss"), writes dz of a vocabulary chunk in bf16
 // and multiplies it out with the GEMM of lce.cu.
 //
-// Forward: one pass over the vocabulary. With m the running maximum of the
-// scaled logits in base 2 (t = z log2 e - m), a row keeps S = sum 2^t and
-// A = sum 2^t t, so that lse = ln 2 (m + log2 S) and H = ln 2 (log2 S - A / S):
+// Forward: one pass over the vocabulary. With x the unscaled logits, m their
+// running maximum and t = (x - m) log2 e / T, a row keeps S = sum 2^t and
+// A = sum 2^t t, so that lse = m / T + ln 2 log2 S and H = ln 2 (log2 S - A / S):
 // A is a sum of terms that are all <= 0 and vanish at both ends, so nothing
-// cancels in it. A larger maximum m' = m + d turns (S, A) into
-// (S 2^-d, (A - d S) 2^-d). Both sums carry what their additions lose: with one
+// cancels in it. A maximum larger by -d (in t's units) turns (S, A) into
+// (S 2^d, (A + d S) 2^d). The difference is taken before the scaling: t is 0 at
+// the maximum and nowhere above, however large the logits (those of a masked
+// vocabulary row may be the type's lowest value, and a product of that rounds by
+// 1e30). 2^d is 0 from d = -150 on, so d is cut at kFar: d S stays finite. Both sums carry what their additions lose: with one
 // likely token S is near 1, and of a hundred thousand others at 1e-9, which add
 // 1e-4 in all, 32 columns together are less than half a step of it.
 #include <cuda.h>
@@ -44,6 +47,7 @@ constexpr int kThreads = 256;
 constexpr int kDzThreads = 384;
 constexpr uint32_t kTmemCols = 512;  // two 256-column fp32 accumulators
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFar = -30000.f;  // 2^t and 2^t t are 0 here
 
 // The ring of K slices: one CTA per SM. PAIR: two CTAs form one product of 256
 // tokens x 256 vocabulary rows, each holding its own 128 tokens and half of the
@@ -83,7 +87,7 @@ struct FwdParams {
   int N, V, D, top;
   int units_per_split, splits;
   Boxes boxes;  // reps 1, 2 or 4: how often the token tile's rows are repeated (see logp_fwd_kernel)
-  float sl2;  // log2(e) / temperature
+  float sl2, inv_t;  // log2(e) / temperature, 1 / temperature
   const int32_t* targets;
   float4* part;    // (splits, N) {m, S, A, the target's raw logit}
   float2* cand;    // (N, splits, top) {raw logit, vocabulary row or -1}, largest first
@@ -339,10 +343,15 @@ __device__ __forceinline__ void add_kept(float& sum, float& lost, float f, float
   sum = s;
 }
 
+// d of a sum kept under the maximum `was` when that becomes m (0 before there is one).
+__device__ __forceinline__ float shift_of(float was, float m, float sl2) {
+  return was > -INFINITY ? fmaxf((was - m) * sl2, kFar) : 0.f;
+}
+
 // (m, S, A) of two disjoint sets of columns as that of both.
-__device__ __forceinline__ void join(float4& x, const float4& y) {
+__device__ __forceinline__ void join(float4& x, const float4& y, float sl2) {
   const float m = fmaxf(x.x, y.x);
-  const float dx = x.x > -INFINITY ? x.x - m : 0.f, dy = y.x > -INFINITY ? y.x - m : 0.f;
+  const float dx = shift_of(x.x, m, sl2), dy = shift_of(y.x, m, sl2);
   const float sx = ex2(dx), sy = ex2(dy);
   x.z = fmaf(fmaf(dx, x.y, x.z), sx, fmaf(dy, y.y, y.z) * sy);
   x.y = fmaf(x.y, sx, y.y * sy);
@@ -357,7 +366,7 @@ template <int KL>
 __device__ __forceinline__ void write_joint(const FwdParams& p, const Joint& j, int quarter, int lane, int groups,
                                             int token, bool lists) {
   float4 x = j.sums[quarter][lane];
-  for (int r = 1; r < p.boxes.reps; ++r) join(x, j.sums[quarter + r * groups][lane]);
+  for (int r = 1; r < p.boxes.reps; ++r) join(x, j.sums[quarter + r * groups][lane], p.sl2);
   p.part[(size_t)blockIdx.y * p.N + token] = x;
   if (!lists) return;
   const int first = KL - p.top;  // slots before it hold no candidates
@@ -541,20 +550,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) m8[q] = max_of<8>(a, q);
           const float cmax = fmaxf(fmax3(m8[0], m8[1], m8[2]), m8[3]);
           // a row with nothing but -inf so far: the shift is 0, and S and A stay 0
-          const float m_new = fmaxf(m_run, cmax * p.sl2);
+          const float m_new = fmaxf(m_run, cmax);
           const float shift = m_new > -INFINITY ? m_new : 0.f;
           const uint64_t off = f2(-shift, -shift);
           uint64_t s2 = 0ull, a2 = 0ull;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 x = f2_split(fma2(f2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), sl2, off));
+            const float2 x = f2_split(mul2(add2(f2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), off), sl2));
             const uint64_t e = f2(ex2(x.x), ex2(x.y));
             s2 = add2(s2, e);
-            // 2^t t -> 0 as t -> -inf: a finite factor keeps 0 * inf out (2^-30000 is 0)
-            a2 = fma2(e, f2(fmaxf(x.x, -30000.f), fmaxf(x.y, -30000.f)), a2);
+            // 2^t t -> 0 as t -> -inf: a finite factor keeps 0 * inf out
+            a2 = fma2(e, f2(fmaxf(x.x, kFar), fmaxf(x.y, kFar)), a2);
           }
           const float2 ss = f2_split(s2), aa = f2_split(a2);
-          const float d = m_run > -INFINITY ? m_run - shift : 0.f, sc = ex2(d);
+          const float d = shift_of(m_run, shift, p.sl2), sc = ex2(d);
           a_run = fmaf(d, s_run, a_run);
           a_lost = fmaf(d, s_lost, a_lost);
           add_kept(a_run, a_lost, sc, aa.x + aa.y);
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
   float S = 0.f, A = 0.f;
 #pragma unroll
   for (int l = 0; l < kListsPerLane; ++l) {
-    const float d = q[l].x > -INFINITY ? q[l].x - M : 0.f, sc = exp2f(d);
+    const float d = shift_of(q[l].x, M, p.sl2), sc = exp2f(d);
     S = fmaf(q[l].y, sc, S);
     A = fmaf(fmaf(d, q[l].y, q[l].z), sc, A);
   }
@@ -681,9 +690,9 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
     A += __shfl_xor_sync(~0u, A, o);
   }
   // From the logit and not from lse: a likely token's log probability is a
-  // small difference, and M's own rounding is in S as well, so it cancels here.
-  const float l2 = log2f(S), ls = kLn2 * (M + l2);
-  const auto log_p = [&](float z) { return kLn2 * (fmaf(z, p.sl2, -M) - l2); };
+  // small difference, which lse would have rounded off.
+  const float l2 = log2f(S), ls = fmaf(M, p.inv_t, kLn2 * l2);
+  const auto log_p = [&](float z) { return kLn2 * fmaf(z - M, p.sl2, -l2); };
   if (lane == 0) {
     const float h = kLn2 * (l2 - A / S);
     logp[token] = scored ? log_p(zt) : 0.f;
@@ -827,7 +836,7 @@ __global__ void __launch_bounds__(kDzThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float x = fmaf(__uint_as_float(a[i]), p.sl2, -l2);
-          d[i] = ex2(x) * fmaf(cB, fmaxf(x, -30000.f), cA);
+          d[i] = ex2(x) * fmaf(cB, fmaxf(x, kFar), cA);
         }
         if (t >= vc && t < vc + 32) {
 #pragma unroll
@@ -979,6 +988,7 @@ cudaError_t launch_logp_fwd(int N, int V, int D, float temperature, int top, con
   p.units_per_split = sp.per;
   p.splits = sp.splits;
   p.sl2 = kLog2e / temperature;
+  p.inv_t = 1.f / temperature;
   p.targets = targets;
   p.part = reinterpret_cast<float4*>(w + L.part);
   p.cand = reinterpret_cast<float2*>(w + L.cand);

@@ -215,6 +215,69 @@ def test_infinities_and_nan_stay_in_their_rows(cuda_dev):
     assert (got[0][[3, 4]] == -np.inf).all() and got[0][5] == 0
 
 
+@pytest.mark.parametrize("N", [1, 40, 100, 300])
+@pytest.mark.parametrize("low,T", [(-1e38, 1.0), (-1e38, 0.7), (-3.3e38, 1.0), (-3.3e38, 2.0), (-1e34, 2.0), (-3e34, 1.0),
+                                   (-1e12, 0.5), (-5e9, 1.0)])
+def test_rows_masked_by_the_types_lowest_values(N, low, T, cuda_dev):
+    """Vocabulary rows taken out by a bias of about the lowest bf16 value: whole
+    chunks, tiles and splits of nothing but such logits, the first ones among
+    them, count for nothing, whichever way low log2(e) / T rounds. (Their own logits differ by less than fp32 holds
+    there, so only the other rows are asked for as alternatives.)"""
+    V, D, top = 20_000, 64, 8
+    H, W, t = inputs(N, V, D, 23)
+    H[:, 0], W[:, 0] = 1, 0
+    low = float(torch.tensor(low, dtype=torch.bfloat16))
+    keep = np.r_[300:340, 9000:9005, 9100, 15_000:15_032, V - 3]
+    masked = np.setdiff1d(np.arange(V), keep)
+    t = keep[t % len(keep)].astype(np.int32)
+    t[-1] = -1
+    e_logp, e_lse, e_ent, e_ids, e_alt = logprobs.forward(H, W[keep], np.where(t < 0, -1, np.searchsorted(keep, t)), T, top)
+    z = np.abs(H @ W[keep].T).max() / T
+    W[masked, 0] = low
+    got = run(H, W, t, cuda_dev, T, top)
+    check(got, [e_logp, e_lse, e_ent, keep[e_ids], e_alt], V, z)
+    # and their gradients are zero
+    h, w, tt = dev_bf16(H, cuda_dev), dev_bf16(W, cuda_dev), torch.from_numpy(t).to(cuda_dev)
+    _, lse, ent, _, _ = pa.token_logprobs_forward(h, w, tt, temperature=T)
+    g = torch.from_numpy(synth.normals(3, 65, N).astype(np.float32)).to(cuda_dev)
+    dh, dw = pa.token_logprobs_backward(h, w, tt, lse, ent, g, 0.3 * g, temperature=T)
+    dh, dw = dh.double().cpu().numpy(), dw.double().cpu().numpy()
+    assert np.isfinite(dh).all() and (dw[masked] == 0).all()
+    eh, ew = logprobs.backward(H, W[keep], np.where(t < 0, -1, np.searchsorted(keep, t)), g.double().cpu().numpy(),
+                               (0.3 * g).double().cpu().numpy(), T)
+    assert np.linalg.norm(dw[keep] - ew) <= 2.0 ** -8 * np.linalg.norm(ew)
+    assert np.linalg.norm(dh[:, 1:] - eh[:, 1:]) <= 2.0 ** -8 * np.linalg.norm(eh[:, 1:])
+
+
+
+@pytest.mark.parametrize("N", [1, 40, 100, 300])
+@pytest.mark.parametrize("low,T", [(-1e38, 1.0), (-1e38, 0.7), (-3.3e38, 2.0), (3e34, 1.0), (-5e9, 0.5), (0.0, 1e-20)])
+def test_tokens_with_nothing_but_masked_logits(N, low, T, cuda_dev):
+    """Logits that are all the same, however large: the softmax is uniform and
+    lse is the logit itself as far as fp32 holds it. The last: a temperature so
+    small that only the largest logits count, 100 equal ones of 199/64 in rows
+    1, 201, ...; the target's is 1, and exact like the others."""
+    V, D, top = 20_000, 64, 8
+    H, W = np.zeros((N, D)), np.zeros((V, D))
+    H[:, 0] = 1
+    low = float(torch.tensor(low, dtype=torch.bfloat16))
+    W[:, 0] = low
+    t = (np.arange(N) * 41 % V).astype(np.int32)
+    if low == 0:
+        W[:, 0], t[:] = (-np.arange(V) % 200) / 64, 7
+        W[7, 0] = 1
+    logp, lse, ent, ids, alt = run(H, W, t, cuda_dev, T, top)
+    bar = 2.0 ** -24 * (V / 32 + 32)
+    if low == 0:
+        assert np.abs(logp.astype(np.float64) * T * 64 / (64 - 199) - 1).max() <= 2.0 ** -22
+        assert np.abs(ent - math.log(100)).max() <= bar and np.abs(alt + math.log(100)).max() <= bar
+        assert (ids == 1 + 200 * np.arange(top)).all() and np.abs(lse.astype(np.float64) * T * 64 / 199 - 1).max() <= 2.0 ** -22
+    else:
+        assert np.abs(logp + math.log(V)).max() <= bar and np.abs(ent - math.log(V)).max() <= 12 * bar
+        assert (ids == np.arange(top)).all() and np.abs(alt + math.log(V)).max() <= bar
+        assert np.abs(lse / (low / T) - 1).max() <= 2.0 ** -22
+
+
 @pytest.mark.parametrize("N,top", [(2, 5), (2, 20), (150, 8), (150, 32)])
 def test_nan_rows_of_the_head_are_no_alternatives(N, top, cuda_dev):
     """A head row of NaN spoils every token's sums, but the alternatives are the
