@@ -1063,16 +1063,19 @@ static int beside_sms(int sms) { return sms / 2 / 8 * 8; }
 
 LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   LogpBwdLayout L;
-  // dz and dz^T of one chunk: at most 128 MiB each (L2 holds about one of
-  // them), in whole vocabulary tiles
+  // dz of one chunk takes at most 128 MiB (about what L2 holds), and dz^T, whose
+  // rows are padded to whole runs of 64 tokens, at most 256; in whole vocabulary
+  // tiles, of which there is one at least (so both are more past 262,144 tokens).
   const long long vmax = (long long)(V + 255) / 256 * 256;
   L.terms = N <= kTok ? 2 : 1;
-  long long vc = (1ll << 26) / (L.terms * (long long)N) / 256 * 256;
+  L.ld_dzt = (N + 63) / 64 * 64;
+  long long vc = (1ll << 26) / (L.terms * (long long)N);
+  if (vc > (1ll << 27) / (L.terms * (long long)L.ld_dzt)) vc = (1ll << 27) / (L.terms * (long long)L.ld_dzt);
+  vc = vc / 256 * 256;
   if (vc > vmax) vc = vmax;
   if (vc < 256) vc = 256;
   L.vc = (int)vc;
   L.chunks = (V + L.vc - 1) / L.vc;
-  L.ld_dzt = (N + 63) / 64 * 64;
   const int K = L.vc < V ? L.vc : V;
   L.splits = gemm_splits(N, D, K, 152, L.terms);
   L.splits_beside = N <= kTok ? gemm_splits(N, D, K, beside_sms(152), L.terms) : L.splits;

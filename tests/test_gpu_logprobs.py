@@ -431,6 +431,17 @@ def test_gradients_of_few_tokens_are_exact_but_for_their_own_rounding(N, V, D, h
     check_grads(bwd(H, W, t, g, e, cuda_dev, T, head), H, W, t, g, e, T, dz_step=2.0 ** -16)
 
 
+@pytest.mark.parametrize("N,head", [(3, True), (3, False), (70, True)])
+def test_few_tokens_over_a_vocabulary_of_two_chunks(N, head, cuda_dev):
+    """The transposed dz, padded to 64 tokens a row, bounds the chunk: 2^20 rows
+    for 3 tokens and 2^19 for 70."""
+    V, D = (1 << 20 if N <= 64 else 1 << 19) + 1003, 64
+    H, W, t = inputs(N, V, D, N)
+    t[0], t[2] = V - 1, V - 1003
+    g, e = upstream(N, t, V, N, True)
+    check_grads(bwd(H, W, t, g, e, cuda_dev, 1.0, head), H, W, t, g, e, 1.0, dz_step=2.0 ** -16)
+
+
 def test_backward_matches_the_oracle_and_differences(cuda_dev):
     """Against the oracle's gradient, and the change of the loss along it:
     for a step s along the direction of the gradient itself the loss changes by

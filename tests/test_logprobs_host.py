@@ -141,3 +141,12 @@ def test_splits_cover_the_vocabulary_within_the_workspace(N, V, L):
     assert used <= most and (used - 1) * per < U <= used * per
     for top in (0, min(V, 32)):
         assert L.pa_logp_workspace_bytes(N, V, 64, top) >= 256 + used * N * (16 + 8 * top)
+
+
+@pytest.mark.parametrize("N", [1, 2, 63, 64, 65, 128, 129, 1000, 4096, 100_000, 1 << 18])
+@pytest.mark.parametrize("V", [1, 32003, 540_001, 1_100_000, 1 << 25, 1 << 30])
+def test_backward_workspace_is_bounded(N, V, L):
+    """One chunk's dz takes 128 MiB at most and its transposed copy, whose rows
+    are whole runs of 64 tokens, 256 MiB; beside them dH's accumulators, one for
+    each of up to 64 runs of the contraction (the D = 64 of them here)."""
+    assert 0 < L.pa_logp_bwd_workspace_bytes(N, V, 64) <= (384 << 20) + 64 * N * 64 * 4 + 4096
