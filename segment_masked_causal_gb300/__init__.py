@@ -741,8 +741,11 @@ def _ckpt_of(x, codes, scales, at):
         raise ValueError("a checkpointed tensor has 1 to 4 dims, the last contiguous")
     if not x.get_device() == codes.get_device() == scales.get_device() == at:
         raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
-    return _CKPT_FIELDS.pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *_ONES[pad], *shape, *_ZEROS[pad],
-                             *stride[:-1])
+    try:
+        return _CKPT_FIELDS.pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), *_ONES[pad], *shape, *_ZEROS[pad],
+                                 *stride[:-1])
+    except struct.error:
+        raise PAError(4, f"a dimension of {tuple(shape)} is past 2^31 - 1") from None
 
 
 def _ckpt_call(fn, parts, io, fmt, block, stream):

@@ -116,3 +116,13 @@ def test_python_refusals():
     with pytest.raises(ValueError, match="block"):
         pa.checkpoint_save([c.bfloat16()], block=50)
     assert pa.checkpoint_save([]) == [] and pa.checkpoint_load([]) == []
+
+
+def test_a_dimension_past_31_bits_is_refused():
+    """Tensors without storage: only their shapes matter. 1-D, and as one of four dims."""
+    for shape in ((1 << 31,), (1, 1, (1 << 31) + 8, 8)):
+        x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+        c = torch.empty(shape, dtype=torch.int8, device="meta")
+        s = torch.empty((*shape[:-1], -(-shape[-1] // 64)), device="meta")
+        with pytest.raises(pa.PAError, match="2\\^31"):
+            pa._ckpt_of(x, c, s, x.get_device())
