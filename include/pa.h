@@ -440,6 +440,15 @@ pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_
                       int32_t* top_ids, float* top_logp, void* ws, size_t ws_bytes, pa_stream_t stream);
 
 /*
+ * How pa_logp_fwd cuts its work on a device of `sms` SMs (host only, for tests
+ * and profiling): plan[0] 1 where two CTAs form one product of 256 tokens, 0
+ * where one forms 128; plan[1] the splits of the vocabulary; plan[2] the units
+ * of 32 vocabulary rows of a split, plan[3] those of a logit tile (at most 8).
+ * A function of its arguments alone. Errors: PA_ERR_SHAPE, PA_ERR_NULL.
+ */
+pa_status pa_logp_plan(int32_t N, int32_t V, int32_t D, int32_t sms, int32_t* plan);
+
+/*
  * Its backward: for L = sum_i g_logp[i] * logp[i] + g_entropy[i] * entropy[i]
  *   dz[i, v]   = (g_logp[i] ([v == targets[i]] - p) - g_entropy[i] p (ln p + entropy[i])) / temperature
  *   dhidden[i] = sum_v dz[i, v] head[v]      (N, D) bf16, overwritten

@@ -37,7 +37,7 @@ EXPORTS = ["pa_workspace_bytes", "pa_fwd", "pa_bwd", "pa_fwd_causal", "pa_bwd_ca
            "pa_fwd_tiles", "pa_bwd_delta", "pa_bwd_dq", "pa_bwd_dkv", "pa_bwd_noalloc", "pa_device_status",
            "pa_selftest_wait_timeout", "pa_selftest_exp2_fma", "pa_pack_first_fit", "pa_workspace_bytes_strided", "pa_fwd_strided",
            "pa_bwd_strided", "pa_lce_workspace_bytes", "pa_lce_fwd", "pa_lce_bwd_workspace_bytes", "pa_lce_bwd",
-           "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_logp_workspace_bytes", "pa_logp_fwd",
+           "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_logp_workspace_bytes", "pa_logp_plan", "pa_logp_fwd",
            "pa_logp_bwd_workspace_bytes", "pa_logp_bwd", "pa_ckpt_save", "pa_ckpt_load", "pa_bwd_ckpt_workspace_bytes",
            "pa_bwd_ckpt", "pa_status_string"]
 
@@ -135,6 +135,8 @@ def lib():
             L.pa_logp_workspace_bytes.restype = S
             L.pa_logp_fwd.argtypes = [I32, I32, I32, F, I32, P, P, P, P, P, P, P, P, P, S, P]
             L.pa_logp_fwd.restype = ctypes.c_int
+            L.pa_logp_plan.argtypes = [I32, I32, I32, I32, P]
+            L.pa_logp_plan.restype = ctypes.c_int
             L.pa_logp_bwd_workspace_bytes.argtypes = [I32, I32, I32]
             L.pa_logp_bwd_workspace_bytes.restype = S
             L.pa_logp_bwd.argtypes = [I32, I32, I32, F, P, P, P, P, P, P, P, P, P, P, S, P]
@@ -604,6 +606,17 @@ def _want(t, shape, name):
 @functools.lru_cache(maxsize=256)  # a function of the numbers alone
 def pa_logp_workspace_bytes(N, V, D, top=0) -> int:
     return int(lib().pa_logp_workspace_bytes(int(N), int(V), int(D), int(top)))
+
+
+def pa_logp_plan(N, V, D, sms=None):
+    """How the forward cuts its work: (pairs of CTAs, splits, units of 32 rows
+    per split, units per logit tile); sms defaults to the current device's."""
+    import torch
+    if sms is None:
+        sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    plan = (ctypes.c_int32 * 4)()
+    _check(lib().pa_logp_plan(int(N), int(V), int(D), int(sms), plan))
+    return bool(plan[0]), plan[1], plan[2], plan[3]
 
 
 def pa_logp_fwd(hidden, head, targets, logp, lse, entropy, top_ids, top_logp, ws, temperature=1.0, top=0, stream=None):

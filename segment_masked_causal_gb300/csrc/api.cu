@@ -633,6 +633,17 @@ pa_status pa_logp_fwd(int32_t N, int32_t V, int32_t D, float temperature, int32_
              : PA_ERR_CUDA;
 }
 
+pa_status pa_logp_plan(int32_t N, int32_t V, int32_t D, int32_t sms, int32_t* plan) {
+  if (!logp_dims_ok(N, V, D) || sms < 1) return PA_ERR_SHAPE;
+  if (!plan) return PA_ERR_NULL;
+  const pa::LogpPlan p = pa::logp_plan(N, V, D, sms);
+  plan[0] = p.pair;
+  plan[1] = p.splits;
+  plan[2] = p.per;
+  plan[3] = p.width;
+  return PA_OK;
+}
+
 size_t pa_logp_bwd_workspace_bytes(int32_t N, int32_t V, int32_t D) {
   if (!logp_dims_ok(N, V, D)) return 0;
   return pa::logp_bwd_layout(N, V, D).bytes;

@@ -150,3 +150,29 @@ def test_backward_workspace_is_bounded(N, V, L):
     are whole runs of 64 tokens, 256 MiB; beside them dH's accumulators, one for
     each of up to 64 runs of the contraction (the D = 64 of them here)."""
     assert 0 < L.pa_logp_bwd_workspace_bytes(N, V, 64) <= (384 << 20) + 64 * N * 64 * 4 + 4096
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 66, 148, 152, 160])
+@pytest.mark.parametrize("N", [1, 8, 32, 33, 64, 65, 127, 128, 129, 256, 257, 777, 1500, 8192, 100_000, 1 << 30])
+def test_the_forwards_plan_covers_the_vocabulary(N, sms, L):
+    """What the launch takes: every unit of 32 rows lies in one split and none is
+    empty; tiles are 1 to 8 units wide and none of a split's is empty; the splits'
+    partial results (16 bytes a token, 8 for each alternative) fit the workspace,
+    and a token's lists the 40 KB of shared memory that the merge gives them."""
+    for V in (1, 31, 32, 33, 255, 256, 257, 1000, 5003, 32003, 50257, 151936, 1_000_001, 1 << 25, 1 << 30):
+        for D in (64, 128, 512, 4096, 16384):
+            pair, splits, per, width = pa.pa_logp_plan(N, V, D, sms)
+            U = -(-V // 32)
+            assert 1 <= splits <= 160 and (splits - 1) * per < U <= splits * per
+            assert 1 <= width <= 8 and width <= per and per - (-(-per // width) - 1) * width >= 1
+            assert not pair or (N > 128 and sms >= 2)
+            for top in (0, min(V, 32)):
+                assert L.pa_logp_workspace_bytes(N, V, D, top) >= 256 + splits * N * (16 + 8 * top)
+                assert splits * top * 8 <= 40960
+
+
+def test_plan_refusals(L):
+    out = (ctypes.c_int32 * 4)()
+    assert L.pa_logp_plan(0, 10, 64, 152, out) == 4 and L.pa_logp_plan(1, 10, 65, 152, out) == 4
+    assert L.pa_logp_plan(1, 10, 64, 0, out) == 4 and L.pa_logp_plan(1, 10, 64, 152, None) == 1
+    assert L.pa_logp_plan(1, 10, 64, 152, out) == 0
