@@ -103,6 +103,69 @@ def test_forward_matches_oracle(N, V, D, top, T, cuda_dev):
     check(got, want, V, np.abs(H @ W.T).max() / T)
 
 
+def on_device(H, W, t, T, top, dev):
+    """The oracle's forward in fp64 on the device, for sizes that take the host long."""
+    h, w, tt = (torch.from_numpy(np.ascontiguousarray(x)).to(dev) for x in (H, W, t))
+    got = [[] for _ in range(5)]
+    for a in range(0, len(t), 256):
+        raw = h[a:a + 256] @ w.T
+        lp = torch.log_softmax(raw / T, 1)
+        ti = tt[a:a + 256].long()
+        scored = (ti >= 0) & (ti < len(W))
+        logp = lp.gather(1, torch.where(scored, ti, 0)[:, None])[:, 0]
+        ids = torch.sort(raw, dim=1, descending=True, stable=True).indices[:, :top]
+        for g, x in zip(got, (torch.where(scored, logp, 0.0), torch.logsumexp(raw / T, 1), -(lp.exp() * lp).sum(1), ids,
+                              lp.gather(1, ids))):
+            g.append(x.cpu().numpy())
+    return [np.concatenate(g) for g in got], (h @ w.T).abs().max().item() / T
+
+
+# Pairs of CTAs with lists of 8, 16, 24 and 32 slots over several tiles of a split
+# (both accumulators, each used again); single CTAs whose tile holds the tokens
+# once, twice and four times; merges with fewer than eight tokens a block (more
+# than 304 tokens with more than 640 entries each)
+LISTS = [
+    # N, V, D, top, pairs, least tiles of a split, merge with fewer tokens a block
+    (1500, 20_000, 128, 8, True, 7, False), (700, 30_011, 128, 16, True, 5, False), (257, 151_936, 128, 3, False, 12, False),
+    (400, 30_000, 64, 24, True, 4, True), (1000, 50_257, 256, 32, True, 11, False), (310, 60_000, 64, 20, False, 5, True),
+    (600, 50_257, 64, 5, False, 7, False), (128, 151_936, 64, 12, False, 4, False), (70, 90_001, 64, 20, False, 3, False),
+    (100, 90_001, 64, 8, False, 3, False), (40, 90_001, 64, 20, False, 3, False), (64, 90_001, 64, 32, False, 3, False),
+    (20, 140_000, 64, 9, False, 4, False),
+]
+
+
+def planned(N, V, D, top, pair, tiles, small_merge):
+    """That the launch takes the form the case is there for, on 152 SMs."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        return
+    is_pair, splits, per, width = pa.pa_logp_plan(N, V, D)
+    assert is_pair == pair and -(-per // width) >= tiles and (N > 304 and splits * top > 640) == small_merge
+
+
+@pytest.mark.parametrize("case", LISTS, ids=lambda c: "-".join(map(str, c[:4])))
+@pytest.mark.parametrize("order", ["random", "ties", "rising", "falling"])
+def test_alternatives_over_tiles_splits_and_pairs(case, order, cuda_dev):
+    """Random logits; a head whose rows come again and again, so that equal logits
+    lie in other chunks, tiles and splits; logits that rise along the vocabulary,
+    where every column enters the list, and that fall."""
+    N, V, D, top = case[:4]
+    planned(*case)
+    H, W, t = inputs(N, V, D, N + V + top)
+    if order == "ties":
+        W = W[np.arange(V) % 911]
+    elif order in ("rising", "falling"):
+        # z = s v, s = +-2^-12: exact, since v = 1024 a + 4 b + c with a, b, c of eight bits
+        H[:], W[:] = 0, 0
+        v = np.arange(V)
+        W[:, 0], W[:, 1], W[:, 2] = v // 1024, v // 4 % 256, v % 4
+        H[:, :3] = np.array([0.25, 2.0 ** -10, 2.0 ** -12])
+        H[(np.arange(N) % 5 == 0) ^ (order == "falling")] *= -1
+    T = 1.0 if order != "ties" else 0.7
+    got = run(H, W, t, cuda_dev, T, top)
+    want, Z = on_device(H, W, t, T, top, cuda_dev)
+    check(got, want, V, Z)
+
+
 def test_ties_and_uniform_logits(cuda_dev):
     """Zero states make every logit equal: the lowest rows win, the entropy is
     ln V. Rows of the head that repeat tie exactly."""
