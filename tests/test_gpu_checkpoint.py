@@ -141,6 +141,35 @@ def test_strided_tensors_many_at_once_and_nothing_else_touched(fmt, cuda_dev):
     assert (dst == 7).all()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("block", [32, 64, 128])
+def test_fp32_strides_and_alignments(block, fmt, cuda_dev):
+    """Every form of the fp32 kernels' accesses: whole tensors of whole blocks,
+    rows on 32 bytes with gaps or short blocks, rows on 16 bytes only (a start
+    16 bytes past a 32-byte boundary, a row stride of 4 mod 8 elements)."""
+    g = torch.Generator(device=cuda_dev).manual_seed(4)
+    mem = torch.randn(2, 37, 5, 96, generator=g, device=cuda_dev)
+    wide = torch.randn(60, 268, generator=g, device=cuda_dev)  # 4 mod 8 elements a row
+    flat = torch.randn(60 * 136 + 4, generator=g, device=cuda_dev)
+    off = flat[4:].view(60, 136)
+    for xs in ([mem.transpose(1, 2), mem.transpose(1, 2)[:, 1:4], mem[:, :, 2], mem[1]],  # 32-byte rows
+               [off], [off[:, :128]], [wide[:, :128]], [wide[:, 4:140], wide[::3, 8:264], wide[7:8, :8], mem[0]],
+               [flat[4:132]], [torch.randn(33, 256, generator=g, device=cuda_dev)]):
+        assert all(x.data_ptr() % 16 == 0 for x in xs)
+        kept = pa.checkpoint_save(xs, format=fmt, block=block)
+        ys = pa.checkpoint_load(kept)
+        torch.cuda.synchronize()
+        for x, c, y in zip(xs, kept, ys):
+            check(x, c, y)
+    # into rows on 16 bytes, whose neighbours stay
+    dst = torch.full((60, 268), 7.0, device=cuda_dev)
+    kept = pa.checkpoint_save([wide[:, 4:140]], format=fmt, block=block)
+    pa.checkpoint_load(kept, out=[dst[:, 4:140]])
+    torch.cuda.synchronize()
+    check(wide[:, 4:140], kept[0], dst[:, 4:140])
+    assert (dst[:, :4] == 7).all() and (dst[:, 140:] == 7).all()
+
+
 @pytest.mark.parametrize("C", [4096, 4104])  # whole blocks, and a short one in each row
 def test_offsets_past_32_bits(C, cuda_dev):
     """More than 2^32 bytes and 2^31 elements: the last rows are kept like any."""
@@ -263,6 +292,100 @@ def test_backward_from_checkpoint_matches_oracle(case, cuda_dev):
     again = pa.backward_from_checkpoint(*kept, do, lse, seg)
     for x, y in zip(got, again):
         assert torch.equal(x, y)
+
+
+# Rounding normals to bf16 costs 1.66e-3 of their norm (the mean of a uniform error
+# of half a step, 2^-8 of the power of two below). dv takes P and itself, dq and dk
+# dS and themselves, in bf16: two roundings, 2.35e-3. What else there is, fp32 sums
+# and exponentials, is below 1e-5. P rounded before it enters dS would make it
+# three, 2.87e-3, and an error of delta of 1% where dout is about out (delta is then
+# as large as any <dO, v>) much more. So 2.6e-3 is the bar; for a sample's spread,
+# over 10^4 elements and more, 1% of that.
+TWO_ROUNDINGS = 2.6e-3
+
+LONG = [
+    (1, 4, 1, 1500, 128, (100, 900), "int8", 64, "bhnd"), (2, 4, 2, 1000, 96, (64, 300), "e4m3", 32, "bnhd"),
+    (1, 2, 2, 1301, 64, None, "int8", 128, "bnhd"), (1, 6, 2, 1024, 128, None, "e4m3", 128, "bhnd"),
+    (3, 2, 1, 640, 64, (1, 60), "int8", 32, "bhnd"),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("like_out", [False, True])
+def test_gradients_from_checkpoints_are_two_roundings_off(case, like_out, cuda_dev):
+    B, Hq, Hkv, N, D, lens, fmt, block, order = case
+    q, k, v, do = (_rows(N + D, 80 + i, B, H, N, D, order, cuda_dev) for i, H in enumerate((Hq, Hkv, Hkv, Hq)))
+    seg = None
+    if lens:
+        ids = np.stack([synth.lengths_to_ids(synth.uniform_lengths(N + b, N, *lens)) for b in range(B)]).astype(np.int32)
+        seg = torch.from_numpy(ids).to(cuda_dev)
+    out, lse = pa.forward(q, k, v, seg)
+    if like_out:
+        do = (out.float() + 0.1 * do.float()).bfloat16()
+    kept = pa.checkpoint_save([q, k, v, out], format=fmt, block=block)
+    got = pa.backward_from_checkpoint(*kept, do, lse, seg)
+    torch.cuda.synchronize()
+    for x, y, n in zip(got, _oracle(kept, do, lse, seg, D), ("dq", "dk", "dv")):
+        rel = np.linalg.norm(f64(x) - y) / np.linalg.norm(y)
+        print(f"{n}: relL2 {rel:.2e}")
+        assert rel <= TWO_ROUNDINGS, n
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_backward_with_rows_on_16_bytes(D, cuda_dev):
+    """dout and its gradient with a row stride of 8 mod 16 elements and a start 16
+    bytes past a 32-byte boundary; then a workspace that starts so, too."""
+    B, Hq, Hkv, N = 2, 4, 2, 300
+    q, k, v, do, seg, out, lse, kept = _case(B, Hq, Hkv, N, D, True, "int8", 64, "bhnd", cuda_dev)
+    want = pa.backward_from_checkpoint(*kept, do, lse, seg)
+    flat = torch.full((B * N * (Hq * D + 8) + 8,), 3.0, dtype=torch.bfloat16, device=cuda_dev)
+    odd = flat[8:].as_strided((B, Hq, N, D), (N * (Hq * D + 8), D, Hq * D + 8, 1))
+    odd.copy_(do)
+    assert odd.data_ptr() % 32 == 16
+    got = pa.backward_from_checkpoint(*kept, odd, lse, seg)
+    n = pa.pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D)
+    ws = torch.empty(n + 16, dtype=torch.uint8, device=cuda_dev)[16:]
+    assert ws.data_ptr() % 32 == 16
+    again = pa.backward_from_checkpoint(*kept, do, lse, seg, ws=ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    for x, y, z in zip(want, got, again):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("B,N", [(4100, 100), (1, 524_417), (2, 300_001)])
+def test_backward_behind_the_tile_table_of_many_tiles(B, N, cuda_dev):
+    """More than 4,096 tiles: the table and the work lists take a kernel each. dv
+    has the bits of pa_bwd on the loaded tensors, dq and dk differ by out's
+    rounding inside delta and dk's by P's; rows at both ends against the oracle."""
+    Hq, Hkv, D = 2, 1, 64
+    g = torch.Generator(device=cuda_dev).manual_seed(6)
+    q, k, v, do = (torch.randn(B, H, N, D, generator=g, device=cuda_dev).bfloat16() for H in (Hq, Hkv, Hkv, Hq))
+    lens = torch.randint(1, 200, (B, N // 90 + 2), generator=g, device=cuda_dev)
+    seg = torch.searchsorted(lens.cumsum(1), torch.arange(N, device=cuda_dev).expand(B, N).contiguous(), right=True).int()
+    out, lse = pa.forward(q, k, v, seg)
+    kept = pa.checkpoint_save([q, k, v, out])
+    ws = torch.empty(pa.pa_bwd_ckpt_workspace_bytes(B, Hq, Hkv, N, D), dtype=torch.uint8, device=cuda_dev)
+    got = pa.backward_from_checkpoint(*kept, do, lse, seg, ws=ws)
+    again = pa.backward_from_checkpoint(*kept, do, lse, seg)
+    lq, lk, lv, lo = pa.checkpoint_load(kept)
+    want = pa.backward(lq, lk, lv, lo, do, lse, seg)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    assert torch.equal(got[2], want[2]) and all(torch.equal(x, y) for x, y in zip(got, again))
+    for x, y in zip(got, want):
+        assert (x.float() - y.float()).norm() <= 2.0 ** -7 * x.float().norm()
+    # whole segments at the start of the first row and the end of the last
+    for b, last in ((0, False), (B - 1, True)):
+        ids = seg[b].cpu().numpy()
+        cut = np.flatnonzero(np.diff(ids)) + 1
+        r = np.s_[cut[cut >= N - 400][0] if N > 400 else 0:] if last else np.s_[:(cut[cut <= 400][-1] if N > 400 else N)]
+        sub = [pa.Checkpoint(c.codes[b:b + 1, :, r].contiguous(), c.scales[b:b + 1, :, r].contiguous(), c.block) for c in kept]
+        w = _oracle(sub, do[b:b + 1, :, r], lse[b:b + 1, :, r], seg[b:b + 1, r], D)
+        for x, y, n in zip(got, w, ("dq", "dk", "dv")):
+            rel = np.linalg.norm(f64(x[b:b + 1, :, r]) - y) / np.linalg.norm(y)
+            print(f"{n}: relL2 {rel:.2e}")
+            assert rel <= TWO_ROUNDINGS, n
 
 
 def test_backward_is_pa_bwds_on_what_a_load_gives(cuda_dev):
