@@ -505,6 +505,36 @@ def test_few_tokens_over_a_vocabulary_of_two_chunks(N, head, cuda_dev):
     check_grads(bwd(H, W, t, g, e, cuda_dev, 1.0, head), H, W, t, g, e, 1.0, dz_step=2.0 ** -16)
 
 
+@pytest.mark.parametrize("N", [5, 300])
+def test_the_widest_hidden_size(N, cuda_dev):
+    """D = 16,384, both directions."""
+    V, D = 1003, 16384
+    H, W, t = inputs(N, V, D, 41)
+    check(run(H, W, t, cuda_dev, 1.0, 8), logprobs.forward(H, W, t, 1.0, 8), V, np.abs(H @ W.T).max())
+    g, e = upstream(N, t, V, 41, True)
+    check_grads(bwd(H, W, t, g, e, cuda_dev, 1.0, True), H, W, t, g, e, 1.0, dz_step=2.0 ** -16 if N <= 128 else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("T", [1e-3, 30.0, 1e30, 3e38])
+def test_temperatures_far_from_one(T, cuda_dev):
+    """Nearly greedy to uniform; the gradient's 1 / T with it (where 1 / T is a
+    number that bf16 holds to eight bits)."""
+    N, V, D = 9, 3000, 64
+    H, W, t = inputs(N, V, D, 43)
+    check(run(H, W, t, cuda_dev, T, 4), logprobs.forward(H, W, t, T, 4), V, np.abs(H @ W.T).max() / T)
+    if T <= 1e30:
+        g, e = upstream(N, t, V, 43, True)
+        dh, dw = bwd(H, W, t, g, e, cuda_dev, T, True)
+        eh, ew = logprobs.backward(H, W, t, g, e, T)
+        assert np.linalg.norm(dw - ew) <= 2.0 ** -8 * np.linalg.norm(ew)
+        # a token's row: p is off by 2^-24 (3 * 1.45 Z) of itself through z and lse, and
+        # at T = 1e-3, Z is some thousands: 1e-3 of what dz is made of before it cancels
+        Z = np.abs(H @ W.T).max() / T
+        size = np.linalg.norm(np.abs(g)[:, None] / T * np.abs(W).max(0), axis=1) * 2 + np.linalg.norm(eh, axis=1)
+        bar = 2.0 ** -8 * np.linalg.norm(eh, axis=1) + 2.0 ** -24 * (8 * Z + 64) * size * (1 + np.abs(e) * Z)
+        assert (np.linalg.norm(dh - eh, axis=1) <= bar).all()
+
+
 def test_backward_matches_the_oracle_and_differences(cuda_dev):
     """Against the oracle's gradient, and the change of the loss along it:
     for a step s along the direction of the gradient itself the loss changes by
