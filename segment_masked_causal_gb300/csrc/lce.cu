@@ -772,12 +772,9 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float4* __restric
 // Fewest K blocks of a run for which pairs are taken: below, a tile is mostly
 // its epilogue, and the cluster's barriers cost more than the loads that a pair
 // saves. Both gradients over V 32,003, D 2048 in us, pairs always / never / from
-// 8 blocks on: 96 tokens 107 / 95 / 95, 256 tokens 128 / 120 / 117, 512 tokens
-// 185 / 192 / 185, 2,048 tokens 471 / 491 / 471.
-#ifndef PA_GEMM_PAIR_BLOCKS
-#define PA_GEMM_PAIR_BLOCKS 8
-#endif
-constexpr int kGemmPairBlocks = PA_GEMM_PAIR_BLOCKS;
+// 8 blocks on: 256 tokens 128 / 120 / 117, 512 tokens 185 / 192 / 185, 2,048
+// tokens 471 / 491 / 471. (A in two terms, up to 128 tokens, takes no pairs.)
+constexpr int kGemmPairBlocks = 8;
 
 // Cycles of an M x N x K product cut into s runs of K, on `slots` SMs: waves x
 // (K blocks + 8 blocks' worth for the pipeline's fill and the tile's epilogue);
