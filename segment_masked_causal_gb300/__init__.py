@@ -690,7 +690,8 @@ def token_logprobs_backward(hidden, head, targets, lse, entropy, g_logp, g_entro
     """Gradients of sum(g_logp * logp + g_entropy * entropy) into hidden and
     head: (dhidden, dhead), dhead None when the head does not train. hidden
     may be a Checkpoint (of a (N, D) tensor): its values are brought back for
-    the call."""
+    the call. The gradients are bf16, about 1.7e-3 of their norm off for up to
+    128 tokens and 2.4e-3 for more (see include/pa.h)."""
     import torch
     if isinstance(hidden, Checkpoint):
         hidden = checkpoint_load([hidden])[0]

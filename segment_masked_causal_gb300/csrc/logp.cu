@@ -16,12 +16,18 @@
 // A = sum 2^t t, so that lse = m / T + ln 2 log2 S and H = ln 2 (log2 S - A / S):
 // A is a sum of terms that are all <= 0 and vanish at both ends, so nothing
 // cancels in it. A maximum larger by -d (in t's units) turns (S, A) into
-// (S 2^d, (A + d S) 2^d). The difference is taken before the scaling: t is 0 at
-// the maximum and nowhere above, however large the logits (those of a masked
-// vocabulary row may be the type's lowest value, and a product of that rounds by
-// 1e30). 2^d is 0 from d = -150 on, so d is cut at kFar: d S stays finite. Both sums carry what their additions lose: with one
-// likely token S is near 1, and of a hundred thousand others at 1e-9, which add
-// 1e-4 in all, 32 columns together are less than half a step of it.
+// (S 2^d, (A + d S) 2^d).
+//   The difference is taken before the scaling, so that t is 0 at the maximum,
+// nowhere above, and off by its own rounding only, however large the logits: those
+// of a masked vocabulary row may be the type's lowest value, whose product with
+// log2 e / T rounds by 1e30. It costs an addition for two columns: 777 tokens over
+// V 50,257, D 1024 60.9 -> 61.7 us, and 73.2 -> 76.9 us where the epilogue is all
+// there is (4,096 tokens, V 32,003, D 64). 2^d is 0 from d = -150 on, so d is cut
+// at kFar, and d S stays finite.
+//   Both sums carry what their additions lose: with one likely token S is near 1,
+// and of a hundred thousand others at 1e-9, which add 1e-4 in all, 32 columns
+// together are less than half a step of it (8,192 tokens over V 151,936 were 4e-5
+// off, now 9e-7; no time that could be measured).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -432,11 +438,12 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int vc, int V, uint32
 // column n with probability top / n), but one of a warp's 32 rows nearly
 // always does: inserting column by column, for the one or two lanes that want
 // it, took 777 tokens with 8 alternatives over V 50,257, D 1024 from 71 to
-// 144 us; with the buffers it is 103 us. Most of a list's insertions come from
+// 144 us; with the buffers it was 103 us. Most of a list's insertions come from
 // the first columns, so the first tile is read twice: the top-th largest of
 // its groups' maxima (two, four or eight columns each) is a value that `top`
-// columns reach, and only columns that reach it are taken: 99 us (and 17 tokens
-// with 20 of them over V 151,936, D 4096 205 us instead of 211).
+// columns reach, and only columns that reach it are taken: 99 us then, 89 us with
+// the loaders and plans that came after (and 17 tokens with 20 of them over V
+// 151,936, D 4096 205 us instead of 211).
 //
 // A TMEM lane is read by one warp of the four alone, so with few tokens most
 // epilogue warps would have none. For N <= 64 (32) the tile holds the tokens'
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
 // exactly 0 in rows without a gradient and in columns past V. dz is rounded
 // to bf16, the operand type of the two products that follow (at most
 // 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
-// That and the results' own rounding, 1.6e-3 of the norm each, make 2.3e-3. But
+// That and the results' own rounding, 1.66e-3 of the norm each, make 2.35e-3. But
 // the gradients of a few tokens hang on the few values at their targets, whose
 // roundings do not average out: 3.5e-3 for one token, 2.6e-3 for 96. So up to
 // 128 tokens, where the products wait for the head more than for the tensor pipe,
