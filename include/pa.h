@@ -470,7 +470,8 @@ pa_status pa_logp_plan(int32_t N, int32_t V, int32_t D, int32_t sms, int32_t* pl
  * tokens and by 2^-8 (its rounding to bf16) from 129 on, where a second term
  * would double two of the three products; the results are rounded to bf16. Of
  * a gradient's norm that is about 1.7e-3 (the results' rounding alone) and
- * 2.4e-3. p is formed from lse in fp32, which adds about 2^-22 |lse| of p.
+ * 2.4e-3. p is formed from lse in fp32, which adds about 2^-22 |lse| of p (and
+ * is taken as 1 where it comes out larger).
  * ws >= pa_logp_bwd_workspace_bytes(N, V, D): up to 262,144 tokens a chunk's dz
  * takes at most 128 MiB of it and its transposed copy 256 MiB (laid out with
  * dhead NULL too), beside dhidden's fp32 accumulators. Arguments, execution and

@@ -762,15 +762,24 @@ __global__ void __launch_bounds__(256) logp_merge_kernel(const FwdParams p, floa
   }
 }
 
+// min(x, 0); NaN stays.
+__device__ __forceinline__ float not_above_0(float x) {
+  float r;
+  asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Backward, one chunk of the vocabulary: one CTA per SM over the chunk's
 // (token tile, vocabulary tile) pairs; the vocabulary tiles have eight units,
 // or fewer where that makes the longest CTA shorter (few tokens). Each
 // recomputed logit becomes
 //   dz = p (cA + cB log2 p) + [v = t] g / T,
 //   cA = -(g + e H) / T,  cB = -e ln 2 / T,
-// exactly 0 in rows without a gradient and in columns past V. dz is rounded
-// to bf16, the operand type of the two products that follow (at most
-// 2^-8 of the value, as in the cross-entropy's backward; sums stay in fp32).
+// exactly 0 in rows without a gradient and in columns past V. p is cut at 1: from
+// logits of 2^24 on the roundings of z and lse alone could make it anything up to
+// infinity, and with one such token the whole head's gradient. dz is rounded to
+// bf16, the operand type of the two products that follow (at most 2^-8 of the
+// value, as in the cross-entropy's backward; sums stay in fp32).
 // That and the results' own rounding, 1.66e-3 of the norm each, make 2.35e-3. But
 // the gradients of a few tokens hang on the few values at their targets, whose
 // roundings do not average out: 3.5e-3 for one token, 2.6e-3 for 96. So up to
@@ -842,7 +851,7 @@ __global__ void __launch_bounds__(kDzThreads, 1)
         float d[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float x = fmaf(__uint_as_float(a[i]), p.sl2, -l2);
+          const float x = not_above_0(fmaf(__uint_as_float(a[i]), p.sl2, -l2));
           d[i] = ex2(x) * fmaf(cB, fmaxf(x, kFar), cA);
         }
         if (t >= vc && t < vc + 32) {

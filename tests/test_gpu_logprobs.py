@@ -535,6 +535,42 @@ def test_temperatures_far_from_one(T, cuda_dev):
         assert (np.linalg.norm(dh - eh, axis=1) <= bar).all()
 
 
+@pytest.mark.parametrize("N", [9, 100, 300])
+@pytest.mark.parametrize("low", [-5e9, -1e12, 5e9, -1e34, -3e34, -1e38, 3e34])
+def test_a_token_whose_lse_fp32_cannot_hold_spoils_no_other(N, low, cuda_dev):
+    """Tokens whose logits are all of about `low`: lse rounds to that, and what
+    p = exp(z - lse) is, fp32 cannot tell; but it is not above 1, so the gradients
+    stay finite (but for column 0 of the tokens themselves, which sums 3,000 dz of
+    order 1 times `low`: 1e38 and more), and the other tokens' are what they are
+    without."""
+    V, D = 3000, 64
+    H, W, t = inputs(N, V, D, 47)
+    t = np.where(t < 0, 3, t % V).astype(np.int32)
+    H[:, 0], W[:, 0] = 0, float(torch.tensor(low, dtype=torch.bfloat16))
+    bad = np.arange(N) % 7 == 2
+    H[bad, 0] = 1
+    g, e = upstream(N, t, V, 47, True)
+    dh, dw = bwd(H, W, t, g, e, cuda_dev, 1.0, True)
+    assert np.isfinite(dh[:, 1:]).all() and np.isfinite(dh[~bad]).all() and np.isfinite(dw).all()
+    # columns 1 on of the others' rows (their column 0 sums dz times the huge column,
+    # where dz is 0 in all but its rounding)
+    eh, _ = logprobs.backward(H[~bad], W, t[~bad], g[~bad], e[~bad], 1.0)
+    assert np.linalg.norm((dh[~bad] - eh)[:, 1:]) <= 2.0 ** -8 * np.linalg.norm(eh[:, 1:])
+
+
+@pytest.mark.parametrize("N", [9, 300])
+def test_a_nan_state_shows_in_its_gradient_alone(N, cuda_dev):
+    V, D = 3000, 64
+    H, W, t = inputs(N, V, D, 53)
+    g, e = upstream(N, t, V, 53, True)
+    want, _ = bwd(H, W, t, g, e, cuda_dev, 1.0, True)
+    H2 = H.copy()
+    H2[4, 7] = np.nan
+    got, dw = bwd(H2, W, t, g, e, cuda_dev, 1.0, True)
+    others = np.arange(N) != 4
+    assert np.isnan(got[4]).all() and np.isnan(dw).all() and (got[others] == want[others]).all()
+
+
 def test_backward_matches_the_oracle_and_differences(cuda_dev):
     """Against the oracle's gradient, and the change of the loss along it:
     for a step s along the direction of the gradient itself the loss changes by
