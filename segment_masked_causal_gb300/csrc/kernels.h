@@ -142,8 +142,13 @@ struct GemmCall {
 };
 cudaError_t launch_gemm(const CUtensorMap& tA, const CUtensorMap& tB, const GemmCall& gc, cudaStream_t st);
 // The number of runs that makes an M x N x K product (A in `terms` terms)
-// shortest on `slots` SMs; no run is empty.
+// shortest on `slots` SMs; no run is empty, or longer than gemm_least_runs's.
 int gemm_splits(int M, int N, int K, int slots, int terms);
+// The fewest runs of at most 65,536 terms, none empty. The tensor cores cut what
+// an addition of 16 products to an fp32 sum leaves over, always towards zero: a run
+// loses about 2e-8 of its sum at each (8.6 million tokens in one run left dW 1.0e-2
+// of its norm short), 8e-5 at this length.
+int gemm_least_runs(int K);
 cudaError_t launch_sum_splits(const float* acc, int splits, size_t n, __nv_bfloat16* out, cudaStream_t st);
 
 // Token log probabilities. The vocabulary is cut into runs of whole units of
@@ -168,7 +173,8 @@ struct LogpBwdLayout {
   int terms;  // of dz, bf16 each
   int vc, chunks, ld_dzt;
   int splits, splits_beside;  // runs of dH's contraction: on all SMs, and on those that dW leaves
-  size_t acc, dz, dzt, bytes;
+  int splits_w;               // runs of dW's
+  size_t acc, acc_w, dz, dzt, bytes;
 };
 LogpBwdLayout logp_bwd_layout(int N, int V, int D);
 cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* hidden, const void* head,

@@ -791,10 +791,21 @@ static double gemm_cost(int M, int N, int K, int slots, int s, bool pair, int te
   return (double)waves * (per * (pair ? 622.0 : terms > 1 ? 1130.0 : 664.0) + 8 * 512.0) + (s > 1 ? (double)s * M * N * 8 / 6.5e6 * 1900 : 0.0);
 }
 
+int gemm_least_runs(int K) {
+  const int KB = (K + 63) / 64;
+  int runs = (KB + 1023) / 1024;
+  for (;;) {  // runs of equal length may be fewer than asked for
+    const int per = (KB + runs - 1) / runs, used = (KB + per - 1) / per;
+    if (used == runs) return runs;
+    runs = used;
+  }
+}
+
 int gemm_splits(int M, int N, int K, int slots, int terms) {
-  int best = 1;
+  const int least = gemm_least_runs(K);
+  int best = least;
   double best_cost = -1;
-  for (int s = 1; s <= 64 && s <= (K + 63) / 64; ++s)
+  for (int s = least; s <= 64 && s <= (K + 63) / 64; ++s)
     for (const bool pair : {false, true}) {
       const double cost = gemm_cost(M, N, K, slots, s, pair, terms);
       if (cost >= 0 && (best_cost < 0 || cost < best_cost)) {

@@ -1096,8 +1096,10 @@ LogpBwdLayout logp_bwd_layout(int N, int V, int D) {
   L.splits = gemm_splits(N, D, K, 152, L.terms);
   L.splits_beside = N <= kTok ? gemm_splits(N, D, K, beside_sms(152), L.terms) : L.splits;
   const int most = L.splits > L.splits_beside ? L.splits : L.splits_beside;
+  L.splits_w = gemm_least_runs(N);
   L.acc = 256;
-  L.dz = L.acc + (L.chunks > 1 || most > 1 ? up256((size_t)most * N * D * 4) : 0);
+  L.acc_w = L.acc + (L.chunks > 1 || most > 1 ? up256((size_t)most * N * D * 4) : 0);
+  L.dz = L.acc_w + (L.splits_w > 1 ? up256((size_t)L.splits_w * K * D * 4) : 0);
   L.dzt = L.dz + up256((size_t)L.terms * N * L.vc * 2);
   L.bytes = L.dzt + up256((size_t)L.terms * L.vc * L.ld_dzt * 2);
   return L;
@@ -1178,8 +1180,10 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
       gc.M = kc;
       gc.N = D;
       gc.K = N;
-      gc.mode = kStoreBf16;
+      gc.mode = L.splits_w > 1 ? kAccInit : kStoreBf16;
+      gc.splits = L.splits_w;
       gc.c = static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D;
+      gc.acc = reinterpret_cast<float*>(w + L.acc_w);
       gc.status = status;
       gc.order = kAfter;
       gc.sms = apart ? sms - apart : 0;
@@ -1208,6 +1212,11 @@ cudaError_t launch_logp_bwd(int N, int V, int D, float temperature, const void* 
     gc.status = status;
     gc.order = dhead ? kBeside : kAfter;
     if ((e = launch_gemm(tA, tB, gc, st)) != cudaSuccess) return e;
+    // behind dH, which ends no earlier than dW
+    if (dhead && L.splits_w > 1 &&
+        (e = launch_sum_splits(reinterpret_cast<float*>(w + L.acc_w), L.splits_w, (size_t)kc * D,
+                               static_cast<__nv_bfloat16*>(dhead) + (size_t)cv0 * D, st)) != cudaSuccess)
+      return e;
   }
   if (splits > 1) return launch_sum_splits(acc, splits, (size_t)N * D, static_cast<__nv_bfloat16*>(dhidden), st);
   return cudaSuccess;

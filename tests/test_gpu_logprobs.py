@@ -694,6 +694,49 @@ def test_a_head_past_32_bit_offsets(cuda_dev):
     assert (dh.double() - exact).norm() <= 2.0 ** -8 * exact.norm()
 
 
+def test_tokens_past_32_bit_offsets(cuda_dev):
+    """A chunk's dz and its transposed copy beyond 2^31 elements (8.6 million tokens
+    by 256 vocabulary rows, two chunks), against fp64 on the device."""
+    N, V, D, top = 8_600_003, 300, 64, 2
+    gen = torch.Generator(device=cuda_dev).manual_seed(2)
+    h = (torch.randint(-15, 16, (N, D), generator=gen, device=cuda_dev, dtype=torch.int8).bfloat16() / 8)
+    w = (torch.randint(-15, 16, (V, D), generator=gen, device=cuda_dev).float() / 32).bfloat16()
+    t = torch.randint(-1, V, (N,), generator=gen, device=cuda_dev, dtype=torch.int32)
+    g = torch.randn(N, generator=gen, device=cuda_dev)
+    e = 0.5 * torch.randn(N, generator=gen, device=cuda_dev)
+    logp, lse, ent, ids, alt = pa.token_logprobs_forward(h, w, t, top=top)
+    ws = torch.empty(pa.pa_logp_bwd_workspace_bytes(N, V, D), dtype=torch.uint8, device=cuda_dev)
+    dh, dw = pa.token_logprobs_backward(h, w, t, lse, ent, g, e, ws=ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    del ws
+    u, wd = 2.0 ** -24, w.double()
+    exact_w, err_h, norm_h = torch.zeros(V, D, dtype=torch.float64, device=cuda_dev), 0.0, 0.0
+    for a in range(0, N, 400_000):
+        s = slice(a, min(N, a + 400_000))
+        hd, ti = h[s].double(), t[s].long()
+        raw = hd @ wd.T
+        lp = torch.log_softmax(raw, 1)
+        en = -(lp.exp() * lp).sum(1)
+        scored = ti >= 0
+        want = torch.where(scored, lp.gather(1, ti.clamp(min=0)[:, None])[:, 0], 0.0)
+        Z = raw.abs().max().item()
+        bar = 3 * 1.45 * Z * u + 4 * u + u * (V / 32 + 32) + 8 * u * (Z + math.log(V))
+        assert (logp[s].double() - want).abs().max() <= bar
+        assert (lse[s].double() - torch.logsumexp(raw, 1)).abs().max() <= bar
+        assert (ent[s].double() - en).abs().max() <= bar * (3 + 2 * math.log(V))
+        assert torch.equal(ids[s].long(), torch.sort(raw, dim=1, descending=True, stable=True).indices[:, :top])
+        gs = torch.where(scored, g[s], 0.0).double()
+        dz = -lp.exp() * (gs[:, None] + e[s].double()[:, None] * (lp + en[:, None]))
+        dz.scatter_add_(1, ti.clamp(min=0)[:, None], gs[:, None])
+        x = dz @ wd
+        err_h += (dh[s].double() - x).square().sum().item()
+        norm_h += x.square().sum().item()
+        exact_w += dz.T @ hd
+    assert err_h ** 0.5 <= 2.0 ** -8 * norm_h ** 0.5
+    assert (dw.double() - exact_w).norm() <= 2.0 ** -8 * exact_w.norm()
+
+
 def test_refused_shapes_and_devices(cuda_dev):
     h, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=cuda_dev), torch.zeros(9, 64, dtype=torch.bfloat16, device=cuda_dev)
     t = torch.zeros(4, dtype=torch.int32, device=cuda_dev)
