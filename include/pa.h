@@ -430,7 +430,10 @@ pa_status pa_lce_bwd(int32_t N, int32_t V, int32_t D, const void* hidden, const 
  * NaN or +inf logit makes the token's lse, logp and entropy NaN. Finite logits
  * may have any size, a mask's lowest values included. A token's sums keep what
  * their additions round off, so logp of a likely token carries what all the
- * unlikely ones add, to about 1e-6.
+ * unlikely ones add, to about 1e-6. The logits themselves are the tensor cores'
+ * fp32 sums, which are cut towards zero at each 16 of D, by about 2e-8 of the sum
+ * (normals at D = 4096: lse is 2e-5 off for logits of up to 10 and 2e-4 for logits
+ * of up to 43, and a tenth of that at D = 256).
  * Device pointers, caller-owned, 16-byte aligned; ws >=
  * pa_logp_workspace_bytes(N, V, D, top), its first 4 bytes the status word.
  * Asynchronous on `stream`; results do not depend on timing.
