@@ -551,6 +551,149 @@ pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t fo
                       const float* lse, const int32_t* seg, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
                       pa_stream_t stream);
 
+/*
+ * Rotary positions: what the attention's queries and keys are turned by before
+ * they meet. The first `rot` elements of a head form rot / 2 pairs; at position p
+ * pair i, of frequency f_i radians a position, becomes
+ *   y1 = a (x1 cos(p f_i) - x2 sin(p f_i)),   y2 = a (x2 cos(p f_i) + x1 sin(p f_i))
+ * and the elements past rot stay as they are. PA_ROPE_HALF pairs element i with
+ * i + rot / 2, PA_ROPE_INTERLEAVED 2i with 2i + 1.
+ *
+ * pa_rotary_frequencies (host only) fills f_i = theta^(-2i / rot), i < rot / 2, with
+ * `scaling` for contexts longer than those trained on:
+ *   PA_ROPE_PLAIN   as they are
+ *   PA_ROPE_LINEAR  f_i / factor
+ *   PA_ROPE_BASE    theta * factor^(rot / (rot - 2)) in theta's place: the slowest
+ *                   pair comes out factor times slower, the fastest as it was
+ *   PA_ROPE_BANDS   by the turns r_i = original f_i / (2 pi) that a pair makes over
+ *                   the `original` context: f_i / factor up to r_i = low, f_i from
+ *                   r_i = high on, linear in r_i between
+ * Arguments that a scaling does not name are not looked at.
+ * pa_rotary_init (host only) makes the description that the kernels take, from any
+ * frequencies (finite) and the amplitude a (1 as a rule). The angle is formed
+ * from a 64-bit binary fraction of a turn, so it is as exact at far positions
+ * as at near ones (about 5e-8 radians).
+ *   rot : a multiple of 8 in [8, 128]
+ * Errors: PA_ERR_NULL, PA_ERR_SHAPE (rot; theta, factor, original or frequencies
+ * not finite and positive, negative frequencies allowed in pa_rotary_init; low >=
+ * high; PA_ROPE_BASE with rot 2 or less; an amplitude that is not finite),
+ * PA_ERR_DTYPE (layout or scaling).
+ */
+#define PA_ROPE_MAX_PAIRS 64
+#define PA_ROPE_MAX_TENSORS 4
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+typedef enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BASE = 2, PA_ROPE_BANDS = 3 } pa_rope_scaling;
+typedef struct {
+  int32_t rot, layout;
+  float amplitude;
+  int32_t ready;                      /* set by pa_rotary_init                   */
+  uint64_t turns[PA_ROPE_MAX_PAIRS];  /* 2^64 * (f_i / 2 pi), whole turns dropped */
+} pa_rotary;
+pa_status pa_rotary_frequencies(int32_t rot, int32_t scaling, double theta, double factor, double original, double low,
+                                double high, double* frequencies);
+pa_status pa_rotary_init(pa_rotary* rotary, int32_t rot, int32_t layout, const double* frequencies, double amplitude);
+
+/*
+ * Positions of packed rows: positions[b, n] = n minus the first token of the run of
+ * equal ids that token n of row b lies in. So each segment of a packed row counts
+ * from 0 (an id that comes back later in the row starts a run of its own there).
+ *   seg, positions : (B, N) int32, contiguous, 16-byte aligned; B * N < 2^31
+ * Errors: PA_ERR_SHAPE, PA_ERR_NULL, PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+pa_status pa_positions(int32_t B, int32_t N, const int32_t* seg, int32_t* positions, pa_stream_t stream);
+
+/*
+ * Rotates up to PA_ROPE_MAX_TENSORS tensors (q and k of a layer, say) in one launch.
+ * `backward` non-zero takes gradients back: the rotation by minus the angle with
+ * the same amplitude, so dx is written from dy given as x.
+ *   x, y : (B, H, N, D), element (b, h, n, c) at b*x_b + h*x_h + n*x_n + c (y_* for y),
+ *          bf16 or fp32 (io_dtype, one for all); y may be x with the same strides and
+ *          overlaps no tensor of the call otherwise. fp32 arithmetic; bf16 results are
+ *          rounded once. Strides of dimensions larger than one are >= D and
+ *          multiples of 16 bytes.
+ *   positions : (B, N) int32, any values, 4-byte aligned; NULL: position n
+ * D a multiple of 8 in [rot, 256]; B * N < 2^31; H in [1, 65535].
+ * Errors: PA_ERR_NULL, PA_ERR_SHAPE (also count, and a rotary that pa_rotary_init did
+ * not fill), PA_ERR_DTYPE, PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t H;
+  int64_t x_b, x_h, x_n, y_b, y_h, y_n;
+} pa_rope_tensor;
+pa_status pa_rope(const pa_rotary* rotary, int32_t count, const pa_rope_tensor* tensors, int32_t B, int32_t N, int32_t D,
+                  int32_t io_dtype, const int32_t* positions, int32_t backward, pa_stream_t stream);
+
+/*
+ * A paged cache of keys and values, for generating from the model that is trained.
+ * The cache is a pool of pages of `page` tokens; sequence s holds its token j in row
+ * j % page of page page_table[s, j / page]. A step brings T rows of new tokens,
+ * the sequences' one behind the other: rows q_start[s] .. q_start[s + 1] - 1 are
+ * sequence s's last tokens, kv_len[s] its tokens with the new ones counted. So
+ * row i of them has position kv_len[s] - (q_start[s + 1] - q_start[s]) + i. One new
+ * token a sequence, a few, a chunk of a prompt, none, and any mixture are alike.
+ *   q          : (T, Hq, D) bf16     element (t, h, c) at t*q_t + h*q_h + c
+ *   k, v       : (T, Hkv, D) bf16    the new tokens', at t*n_t + h*n_h + c
+ *   out, q_out : (T, Hq, D) bf16     at t*o_t + h*o_h + c
+ *   k_pages, v_pages : (pages, Hkv, page, D) bf16, at p*p_p + h*p_h + n*p_n + c; either
+ *                order of heads and tokens in memory, by the strides
+ *   page_table : (S, width) int32    q_start : (S + 1) int32, rising    kv_len : (S) int32
+ * The three are read on the device, so a captured step is replayed with new
+ * lengths. Whatever they hold, no call reads or writes outside the tensors
+ * described: q_start is taken within [0, T], a negative kv_len as 0, and tokens past
+ * width * page, or on a page number outside [0, pages), are not in the cache:
+ * they are neither written nor attended (pages given back at the start of a long
+ * context, say, marked with -1). Rows of q before q_start[0] and from q_start[S] on
+ * belong to nobody: their outputs stay as they were.
+ * D is 64, 96 or 128; page 16, 32, 64, 128 or 256; S, T, pages, width >= 1 (T = 0
+ * returns PA_OK without a launch); width * page < 2^31 - 256; S < 2^24. Strides of dimensions
+ * larger than one are >= D and multiples of 8; pointers are 16-byte aligned (page_table,
+ * q_start and kv_len 4-byte aligned).
+ */
+typedef struct {
+  int32_t S, T, Hq, Hkv, D;
+  int32_t pages, page, width;
+  float scale; /* softmax scale; <= 0 selects 1/sqrt(D) */
+} pa_paged_dims;
+typedef struct {
+  int64_t q_t, q_h, n_t, n_h, o_t, o_h, p_p, p_h, p_n;
+} pa_paged_strides;
+
+/*
+ * Writes the new tokens' keys and values into their places in the cache, the keys
+ * rotated on the way, and their queries rotated into q_out. `rotary` NULL: nothing is
+ * rotated. q may be NULL, q_out then too; q_out may be q with the same strides.
+ * positions (T) int32 replaces the tokens' places as what they are rotated by; NULL:
+ * their places. A token that has no place in the cache leaves only its q_out. Two
+ * tokens of one place (a page listed for two sequences) leave either's values.
+ * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA, PA_ERR_SHAPE (also rot > D),
+ * PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+pa_status pa_paged_append(const pa_paged_dims* dims, const pa_paged_strides* strides, const pa_rotary* rotary,
+                          const void* q, const void* k, const void* v, const int32_t* page_table, const int32_t* q_start,
+                          const int32_t* kv_len, const int32_t* positions, void* q_out, void* k_pages, void* v_pages,
+                          pa_stream_t stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds theirs too, see
+ * pa_paged_append). For row i of sequence s, at position p, over the keys j <= p that
+ * are in the cache, query head h reading kv head h / (Hq / Hkv):
+ *   lse[t, h] = ln sum_j exp(scale <q, k_j>)      out = sum_j exp(scale <q, k_j> - lse) v_j
+ * A row that sees no key has out 0 and lse -inf. lse (T, Hq) fp32, contiguous. What a page
+ * holds past a sequence's tokens may be anything (NaN too); the keys and values
+ * up to kv_len are finite. P enters the second product in bf16; sums and maxima are
+ * fp32. Hq / Hkv is at most 128.
+ * ws >= pa_paged_workspace_bytes(D) bytes, its first 4 the status word; a
+ * workspace belongs to one stream at a time. The same call gives the same bits.
+ * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA (also Hq / Hkv > 128), PA_ERR_SHAPE, PA_ERR_ALIGN,
+ * PA_ERR_WORKSPACE, PA_ERR_ARCH, PA_ERR_CUDA.
+ */
+size_t pa_paged_workspace_bytes(int32_t D);
+pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* strides, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len,
+                       void* out, float* lse, void* ws, size_t ws_bytes, pa_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* pa_status_string(pa_status s);
 

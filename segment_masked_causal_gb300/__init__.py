@@ -33,13 +33,17 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_HEAD_DIM", 3: "PA_ERR_G
 PA_IO_BF16, PA_IO_F32 = 0, 1
 PA_CKPT_INT8, PA_CKPT_E4M3 = 0, 1
 PA_CKPT_MAX_TENSORS = 8
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+PA_ROPE_MAX_TENSORS, PA_ROPE_MAX_PAIRS = 4, 64
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 EXPORTS = ["pa_workspace_bytes", "pa_fwd", "pa_bwd", "pa_fwd_causal", "pa_bwd_causal", "pa_build_tile_table",
            "pa_fwd_tiles", "pa_bwd_delta", "pa_bwd_dq", "pa_bwd_dkv", "pa_bwd_noalloc", "pa_device_status",
            "pa_selftest_wait_timeout", "pa_selftest_exp2_fma", "pa_pack_first_fit", "pa_workspace_bytes_strided", "pa_fwd_strided",
            "pa_bwd_strided", "pa_lce_workspace_bytes", "pa_lce_fwd", "pa_lce_bwd_workspace_bytes", "pa_lce_bwd",
            "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_logp_workspace_bytes", "pa_logp_plan", "pa_logp_fwd",
            "pa_logp_bwd_workspace_bytes", "pa_logp_bwd", "pa_ckpt_save", "pa_ckpt_load", "pa_bwd_ckpt_workspace_bytes",
-           "pa_bwd_ckpt", "pa_status_string"]
+           "pa_bwd_ckpt", "pa_rotary_frequencies", "pa_rotary_init", "pa_positions", "pa_rope", "pa_paged_append",
+           "pa_paged_workspace_bytes", "pa_paged_fwd", "pa_status_string"]
 
 
 class LibraryMissing(RuntimeError):
@@ -70,6 +74,25 @@ class pa_ckpt_tensor(ctypes.Structure):
 
 class pa_ckpt(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class pa_rotary(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * PA_ROPE_MAX_PAIRS)]
+
+
+class pa_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("x_b", ctypes.c_int64), ("x_h", ctypes.c_int64), ("x_n", ctypes.c_int64),
+                ("y_b", ctypes.c_int64), ("y_h", ctypes.c_int64), ("y_n", ctypes.c_int64)]
+
+
+class pa_paged_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "T", "Hq", "Hkv", "D", "pages", "page", "width")] + [("scale", ctypes.c_float)]
+
+
+class pa_paged_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("q_t", "q_h", "n_t", "n_h", "o_t", "o_h", "p_p", "p_h", "p_n")]
 
 
 _lib = None
@@ -150,6 +173,22 @@ def lib():
             L.pa_bwd_ckpt_workspace_bytes.restype = S
             L.pa_bwd_ckpt.argtypes = [D, ST, I32, I32, CK, CK, CK, CK, P, P, P, P, P, P, P, S, P]
             L.pa_bwd_ckpt.restype = ctypes.c_int
+            DB = ctypes.c_double
+            L.pa_rotary_frequencies.argtypes = [I32, I32, DB, DB, DB, DB, DB, P]
+            L.pa_rotary_frequencies.restype = ctypes.c_int
+            L.pa_rotary_init.argtypes = [P, I32, I32, P, DB]
+            L.pa_rotary_init.restype = ctypes.c_int
+            L.pa_positions.argtypes = [I32, I32, P, P, P]
+            L.pa_positions.restype = ctypes.c_int
+            L.pa_rope.argtypes = [P, I32, P, I32, I32, I32, I32, P, I32, P]  # an array of pa_rope_tensor, or its bytes
+            L.pa_rope.restype = ctypes.c_int
+            PD, PS = ctypes.POINTER(pa_paged_dims), ctypes.POINTER(pa_paged_strides)
+            L.pa_paged_append.argtypes = [PD, PS, P, P, P, P, P, P, P, P, P, P, P, P]
+            L.pa_paged_append.restype = ctypes.c_int
+            L.pa_paged_workspace_bytes.argtypes = [I32]
+            L.pa_paged_workspace_bytes.restype = S
+            L.pa_paged_fwd.argtypes = [PD, PS, P, P, P, P, P, P, P, P, P, S, P]
+            L.pa_paged_fwd.restype = ctypes.c_int
             L.pa_pack_first_fit.argtypes = [P, P, I32, P, I32, I32, I32, U64, U64, P, P, P, P, P, P, P]
             L.pa_pack_first_fit.restype = ctypes.c_int
             L.pa_status_string.argtypes = [ctypes.c_int]
@@ -908,6 +947,271 @@ def backward_from_checkpoint(q, k, v, out, dout, lse, seg=None, scale=0.0, ws=No
     dk, dv = (torch.empty_strided(shape, stride, dtype=dout.dtype, device=dout.device) for _ in range(2))
     pa_bwd_ckpt(q, k, v, out, dout, lse, seg, dq, dk, dv, ws, scale)
     return dq, dk, dv
+
+
+# -------------------------------------------------------- rotary positions
+class Rotary:
+    """Rotary positions on the first `rot` elements of a head, in pairs of
+    halves or of neighbours (interleaved): frequencies theta^(-2i / rot) with
+    `scaling` "plain", "linear", "base" or "bands" by `factor` (see
+    include/pa.h; "bands" takes original, low and high), or the given
+    `frequencies` (rot / 2 radians a position). `amplitude` multiplies cosine and
+    sine. Holds no device memory."""
+    __slots__ = ("c", "ref", "rot", "interleaved", "amplitude", "frequencies")
+
+    def __init__(self, rot, theta=10000.0, interleaved=False, scaling="plain", factor=1.0, original=0.0, low=1.0, high=32.0,
+                 amplitude=1.0, frequencies=None):
+        rot = int(rot)
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+        if frequencies is None:
+            f = (ctypes.c_double * PA_ROPE_MAX_PAIRS)()
+            _check(lib().pa_rotary_frequencies(rot, ROPE_SCALINGS[scaling], float(theta), float(factor), float(original),
+                                               float(low), float(high), f))
+        else:
+            if scaling != "plain":
+                raise ValueError("frequencies come as they are used: no scaling beside them")
+            given = [float(x) for x in frequencies]
+            if len(given) != rot // 2 or len(given) > PA_ROPE_MAX_PAIRS:
+                raise ValueError(f"frequencies must be rot / 2 = {rot // 2} numbers (at most {PA_ROPE_MAX_PAIRS}), got {len(given)}")
+            f = (ctypes.c_double * PA_ROPE_MAX_PAIRS)(*given)
+        self.c = pa_rotary()
+        _check(lib().pa_rotary_init(ctypes.byref(self.c), rot, int(bool(interleaved)), f, float(amplitude)))
+        self.ref = ctypes.byref(self.c)
+        self.rot, self.interleaved, self.amplitude = rot, bool(interleaved), float(amplitude)
+        self.frequencies = tuple(f[:rot // 2])
+
+
+def pa_positions(seg, positions, stream=None):
+    """positions[b, n] = n minus the start of its run of equal ids; both (B, N) int32."""
+    import torch
+    if seg.dim() != 2:
+        raise ValueError("seg must be (B, N)")
+    _want(positions, seg.shape, "positions")
+    _on_current_device(seg, positions)
+    _check(lib().pa_positions(*seg.shape, _ptr(seg, torch.int32, "seg"), _ptr(positions, torch.int32, "positions"),
+                              _stream(stream)))
+
+
+def segment_positions(seg):
+    """Positions of packed rows from their segment ids, counting from 0 in each
+    segment: (B, N) int32."""
+    import torch
+    positions = torch.empty_like(seg, memory_format=torch.contiguous_format)
+    pa_positions(seg, positions)
+    return positions
+
+
+_ROPE_FIELDS = struct.Struct("PPi4xqqqqqq")  # pa_rope_tensor
+
+
+def pa_rope(tensors, out, rotary, positions=None, backward=False, stream=None):
+    """Rotate the (B, H, N, D) tensors into `out` (which may be the tensors
+    themselves), or take their gradients back; see include/pa.h."""
+    import torch
+    tensors, out = list(tensors), list(out)
+    if len(tensors) != len(out):
+        raise ValueError("one output per tensor")
+    if not tensors:
+        return
+    x0, parts, at = tensors[0], [], torch.cuda.current_device()
+    if x0.dim() != 4:
+        raise ValueError("tensors must be (B, H, N, D)")
+    B, _, N, D = x0.shape
+    dtype, io = _io_dtype(x0)
+    for x, y in zip(tensors, out):
+        if x.dim() != 4 or x.shape[0] != B or x.shape[2:] != x0.shape[2:] or y.shape != x.shape:
+            raise ValueError("the tensors of one call are (B, H, N, D) with one B, N and D, and out has their shapes")
+        if x.dtype != dtype or y.dtype != dtype:
+            raise ValueError("the tensors of one call share their type")
+        if not x.get_device() == y.get_device() == at:
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+        xs, ys = x.stride(), y.stride()
+        if xs[3] != 1 or ys[3] != 1:
+            raise ValueError("the tensors' last dim must be contiguous")
+        parts.append(_ROPE_FIELDS.pack(x.data_ptr(), y.data_ptr(), x.shape[1], *xs[:3], *ys[:3]))
+    pos = None
+    if positions is not None:
+        _want(positions, (B, N), "positions")
+        _on_current_device(positions)
+        pos = _ptr(positions, torch.int32, "positions")
+    st, fn = _stream(stream), lib().pa_rope
+    for i in range(0, len(parts), PA_ROPE_MAX_TENSORS):
+        some = parts[i:i + PA_ROPE_MAX_TENSORS]
+        _check(fn(rotary.ref, len(some), b"".join(some), B, N, D, io, pos, int(backward), st))
+
+
+def rotary_forward(tensors, rotary, positions=None, out=None):
+    """The (B, H, N, D) tensors (q and k, say; bf16 or fp32, any strides with
+    the last dim contiguous) rotated to their positions ((B, N) int32, or None
+    for 0, 1, ...), as new tensors in the same memory order or into `out`."""
+    import torch
+    tensors = list(tensors)
+    out = [torch.empty_like(x) for x in tensors] if out is None else list(out)
+    pa_rope(tensors, out, rotary, positions)
+    return out
+
+
+def rotary_backward(grads, rotary, positions=None, out=None):
+    """Gradients of rotary_forward's inputs from those of its outputs."""
+    import torch
+    grads = list(grads)
+    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    pa_rope(grads, out, rotary, positions, backward=True)
+    return out
+
+
+# -------------------------------------------------------------- paged cache
+class PagedCache:
+    """Pages of keys and values: two (pages, Hkv, page, D) bf16 tensors on one
+    device with the same strides, the last dim contiguous; (pages, page, Hkv, D)
+    memory comes as its transpose(1, 2). Holds the tensors."""
+    __slots__ = ("k", "v", "pages", "Hkv", "page", "D", "strides", "device_index")
+
+    def __init__(self, k_pages, v_pages):
+        import torch
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be (pages, Hkv, page, D)")
+        if k_pages.dtype != torch.bfloat16 or v_pages.dtype != torch.bfloat16:
+            raise ValueError(f"k_pages and v_pages must be bfloat16, got {k_pages.dtype} and {v_pages.dtype}")
+        if k_pages.stride() != v_pages.stride() or k_pages.stride(3) != 1:
+            raise ValueError("k_pages and v_pages must share their strides, the last dim contiguous")
+        if k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must be on one device")
+        self.k, self.v, self.device_index = k_pages, v_pages, k_pages.get_device()
+        self.pages, self.Hkv, self.page, self.D = k_pages.shape
+        self.strides = k_pages.stride()[:3]
+
+
+def _rows_of(t, H, D, at, name):
+    """A (T, H, D) bf16 tensor on device `at`, its last dim contiguous: its token and head strides."""
+    import torch
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError(f"{name} must be (T, {H}, {D}), got {tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.get_device() != at:
+        raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at}), got {name} on {t.device}")
+    s_t, s_h, s_c = t.stride()
+    if s_c != 1:
+        raise ValueError(f"{name}'s last dim must be contiguous")
+    return s_t, s_h
+
+
+def _paged_tables(cache, page_table, q_start, kv_len, at):
+    """S and width, the step's three arrays checked."""
+    import torch
+    i32 = torch.int32
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (S, width)")
+    S, width = page_table.shape
+    if q_start.shape != (S + 1,) or kv_len.shape != (S,):
+        raise ValueError(f"q_start must be {(S + 1,)} and kv_len {(S,)}, got {tuple(q_start.shape)} and {tuple(kv_len.shape)}")
+    if not page_table.dtype == q_start.dtype == kv_len.dtype == i32:
+        raise ValueError("page_table, q_start and kv_len must be int32")
+    if not page_table.get_device() == q_start.get_device() == kv_len.get_device() == cache.device_index == at:
+        raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+    if not (page_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()):
+        raise ValueError("page_table, q_start and kv_len must be contiguous")
+    return S, width
+
+
+def pa_paged_append(cache, q, k, v, page_table, q_start, kv_len, rotary=None, positions=None, q_out=None, stream=None):
+    """New tokens' keys and values into the cache, their queries rotated into
+    q_out (see include/pa.h); q and q_out may both be None."""
+    import torch
+    at = torch.cuda.current_device()
+    S, width = _paged_tables(cache, page_table, q_start, kv_len, at)
+    n = _rows_of(k, cache.Hkv, cache.D, at, "k")
+    T = k.shape[0]
+    m = _rows_of(v, cache.Hkv, cache.D, at, "v")
+    if v.shape[0] != T or (T > 1 and m[0] != n[0]) or (cache.Hkv > 1 and m[1] != n[1]):
+        raise ValueError("v must have k's shape and strides")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    Hq, qs, os_ = cache.Hkv, (cache.D, cache.D), (cache.D, cache.D)
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs, os_ = _rows_of(q, Hq, cache.D, at, "q"), _rows_of(q_out, Hq, cache.D, at, "q_out")
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError(f"q and q_out must have k's {T} rows")
+    else:
+        qs = os_ = (cache.D * Hq, cache.D)
+    pos = None
+    if positions is not None:
+        _want(positions, (T,), "positions")
+        _on_current_device(positions)
+        pos = _ptr(positions, torch.int32, "positions")
+    d = pa_paged_dims(S, T, Hq, cache.Hkv, cache.D, cache.pages, cache.page, width, 0.0)
+    _check(lib().pa_paged_append(ctypes.byref(d), ctypes.byref(pa_paged_strides(*qs, *n, *os_, *cache.strides)),
+                                 None if rotary is None else rotary.ref, None if q is None else q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), pos,
+                                 None if q_out is None else q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
+                                 _stream(stream)))
+
+
+def paged_append(cache, q, k, v, page_table, q_start, kv_len, rotary=None, positions=None, q_out=None):
+    """Write a step's new keys (T, Hkv, D), rotated, and values into their places
+    in the cache and return the queries (T, Hq, D) rotated to their positions (in
+    q_out, which may be q, or a new tensor whose rows behind the last sequence are
+    not set; None for q None). Sequence s's new tokens are rows q_start[s] to
+    q_start[s + 1] - 1, the last of its kv_len[s] tokens; page_table (S, width)
+    lists its pages. All int32 on the device."""
+    import torch
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    pa_paged_append(cache, q, k, v, page_table, q_start, kv_len, rotary, positions, q_out)
+    return q_out
+
+
+@functools.lru_cache(maxsize=16)  # a function of the number alone
+def pa_paged_workspace_bytes(D) -> int:
+    return int(lib().pa_paged_workspace_bytes(int(D)))
+
+
+def paged_workspace(q, cache):
+    """A device workspace for paged_forward on q and cache (uint8; any lengths)."""
+    import torch
+    n = pa_paged_workspace_bytes(cache.D)
+    if n == 0:
+        raise PAError(2, "head dim must be 64, 96 or 128")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def pa_paged_fwd(q, cache, page_table, q_start, kv_len, out, lse, ws, scale=0.0, stream=None):
+    """Attention of a step's queries over the cache (see include/pa.h): out (T, Hq,
+    D) bf16 and lse (T, Hq) fp32 are outputs."""
+    import torch
+    at = torch.cuda.current_device()
+    S, width = _paged_tables(cache, page_table, q_start, kv_len, at)
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    qs, os_ = _rows_of(q, Hq, cache.D, at, "q"), _rows_of(out, Hq, cache.D, at, "out")
+    T = q.shape[0]
+    if out.shape[0] != T or lse.shape != (T, Hq):
+        raise ValueError(f"out must have q's shape and lse be {(T, Hq)}, got {tuple(out.shape)} and {tuple(lse.shape)}")
+    if lse.get_device() != at or ws.get_device() != at:
+        raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+    d = pa_paged_dims(S, T, Hq, cache.Hkv, cache.D, cache.pages, cache.page, width, scale)
+    _check(lib().pa_paged_fwd(ctypes.byref(d), ctypes.byref(pa_paged_strides(*qs, 0, 0, *os_, *cache.strides)), q.data_ptr(),
+                              cache.k.data_ptr(), cache.v.data_ptr(), page_table.data_ptr(), q_start.data_ptr(),
+                              kv_len.data_ptr(), out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(ws, torch.uint8, "ws"),
+                              ws.numel(), _stream(stream)))
+
+
+def paged_forward(q, cache, page_table, q_start, kv_len, scale=0.0, out=None, lse=None, ws=None):
+    """Attention of a step's new tokens over the paged cache, their own keys and
+    values among it (paged_append). q (T, Hq, D) bf16, rows as in paged_append;
+    returns (out, lse), lse (T, Hq) fp32. Rows of no sequence are left as they
+    are (not set, in new outputs)."""
+    import torch
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = paged_workspace(q, cache)
+    pa_paged_fwd(q, cache, page_table, q_start, kv_len, out, lse, ws, scale)
+    return out, lse
 
 
 def pa_status_string(code: int) -> str:

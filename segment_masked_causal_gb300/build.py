@@ -20,8 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["api.cu", "prologue.cu", "stage.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkv.cu", "bwd_fused.cu", "noalloc.cu",
-           "lce.cu", "logp.cu", "ckpt.cu", "pack.cpp"]
-HEADERS = ["sm103.cuh", "common.cuh", "kernels.h", "tmap.h"]
+           "lce.cu", "logp.cu", "ckpt.cu", "rope.cu", "append.cu", "paged.cu", "pack.cpp"]
+HEADERS = ["sm103.cuh", "common.cuh", "kernels.h", "tmap.h", "rope.cuh", "paged.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -804,6 +804,181 @@ pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t fo
   return PA_OK;
 }
 
+// ------------------------------------------------------ rotary positions
+static bool rot_ok(int32_t rot) { return rot >= 8 && rot <= 2 * PA_ROPE_MAX_PAIRS && rot % 8 == 0; }
+static bool positive(double x) { return std::isfinite(x) && x > 0.0; }
+constexpr int32_t kRotaryReady = 0x526f7461;
+
+pa_status pa_rotary_frequencies(int32_t rot, int32_t scaling, double theta, double factor, double original, double low,
+                                double high, double* frequencies) {
+  if (!rot_ok(rot) || !positive(theta)) return PA_ERR_SHAPE;
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_BANDS) return PA_ERR_DTYPE;
+  if (scaling != PA_ROPE_PLAIN && !positive(factor)) return PA_ERR_SHAPE;
+  if (scaling == PA_ROPE_BANDS && (!positive(original) || !std::isfinite(low) || !std::isfinite(high) || low >= high))
+    return PA_ERR_SHAPE;
+  if (!frequencies) return PA_ERR_NULL;
+  if (scaling == PA_ROPE_BASE) theta *= std::pow(factor, (double)rot / (rot - 2));
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(theta, -2.0 * i / rot);
+    if (scaling == PA_ROPE_LINEAR) f /= factor;
+    if (scaling == PA_ROPE_BANDS) {
+      const double turns = original * f / 6.283185307179586476925, x = (turns - low) / (high - low);
+      const double keep = x < 0 ? 0 : x > 1 ? 1 : x;
+      f = f / factor * (1 - keep) + f * keep;
+    }
+    frequencies[i] = f;
+  }
+  return PA_OK;
+}
+
+pa_status pa_rotary_init(pa_rotary* rotary, int32_t rot, int32_t layout, const double* frequencies, double amplitude) {
+  if (!rot_ok(rot) || !std::isfinite(amplitude) || !std::isfinite((float)amplitude)) return PA_ERR_SHAPE;
+  if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_DTYPE;
+  if (!rotary || !frequencies) return PA_ERR_NULL;
+  for (int i = 0; i < rot / 2; ++i)
+    if (!std::isfinite(frequencies[i])) return PA_ERR_SHAPE;
+  pa_rotary r{};
+  r.rot = rot;
+  r.layout = layout;
+  r.amplitude = (float)amplitude;
+  r.ready = kRotaryReady;
+  for (int i = 0; i < rot / 2; ++i) {
+    double t = frequencies[i] / 6.283185307179586476925;
+    t -= std::floor(t);
+    // a double below 1 is at most 1 - 2^-53; a tiny negative frequency can come out as 1
+    r.turns[i] = t >= 1.0 ? 0 : (uint64_t)(t * 18446744073709551616.0);
+  }
+  *rotary = r;
+  return PA_OK;
+}
+static bool rotary_ok(const pa_rotary* r) {
+  return r->ready == kRotaryReady && rot_ok(r->rot) && (r->layout == PA_ROPE_HALF || r->layout == PA_ROPE_INTERLEAVED);
+}
+
+pa_status pa_positions(int32_t B, int32_t N, const int32_t* seg, int32_t* positions, pa_stream_t stream) {
+  if (B <= 0 || N <= 0 || (int64_t)B * N > 0x7fffffff) return PA_ERR_SHAPE;
+  if (!seg || !positions) return PA_ERR_NULL;
+  if (!aligned16(seg) || !aligned16(positions)) return PA_ERR_ALIGN;
+  const pa_status why = device_ok();
+  if (why != PA_OK) return why;
+  return pa::launch_positions(B, N, seg, positions, cu(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_rope(const pa_rotary* rotary, int32_t count, const pa_rope_tensor* tensors, int32_t B, int32_t N, int32_t D,
+                  int32_t io_dtype, const int32_t* positions, int32_t backward, pa_stream_t stream) {
+  if (!rotary || !tensors) return PA_ERR_NULL;
+  if (count < 1 || count > PA_ROPE_MAX_TENSORS || B <= 0 || N <= 0 || (int64_t)B * N > 0x7fffffff) return PA_ERR_SHAPE;
+  if (!rotary_ok(rotary) || D < rotary->rot || D > 256 || D % 8 != 0) return PA_ERR_SHAPE;
+  pa_status why = io_ok(io_dtype);
+  if (why != PA_OK) return why;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u) return PA_ERR_ALIGN;
+  const int unit = io_dtype == PA_IO_F32 ? 4 : 8;
+  for (int i = 0; i < count; ++i) {
+    const pa_rope_tensor& t = tensors[i];
+    if (t.H <= 0 || t.H > 65535) return PA_ERR_SHAPE;
+    const int32_t n[3] = {B, t.H, N};
+    const int64_t s[2][3] = {{t.x_b, t.x_h, t.x_n}, {t.y_b, t.y_h, t.y_n}};
+    for (const auto& side : s)
+      for (int k = 0; k < 3; ++k)
+        if (n[k] > 1 && side[k] < D) return PA_ERR_SHAPE;
+    for (const auto& side : s)
+      for (int k = 0; k < 3; ++k)
+        if (n[k] > 1 && side[k] % unit != 0) return PA_ERR_ALIGN;
+    if (!t.x || !t.y) return PA_ERR_NULL;
+    if (!aligned16(t.x) || !aligned16(t.y)) return PA_ERR_ALIGN;
+    if (t.x == t.y)  // in place: each element is read and written by one thread
+      for (int k = 0; k < 3; ++k)
+        if (n[k] > 1 && s[0][k] != s[1][k]) return PA_ERR_SHAPE;
+  }
+  if ((why = device_ok()) != PA_OK) return why;
+  return pa::launch_rope(*rotary, tensors, count, B, N, D, io_dtype == PA_IO_F32, backward != 0, positions, cu(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// ------------------------------------------------------ paged cache
+// Dims, and the strides of dimensions larger than one.
+static pa_status paged_checks(const pa_paged_dims* d, const pa_paged_strides* s, bool fresh) {
+  if (!d || !s) return PA_ERR_NULL;
+  if (d->S <= 0 || d->S >= (1 << 24) || d->T < 0 || d->Hq <= 0 || d->Hkv <= 0 || d->pages <= 0 || d->width <= 0)
+    return PA_ERR_SHAPE;
+  if (d->D != 64 && d->D != 96 && d->D != 128) return PA_ERR_HEAD_DIM;
+  if (d->Hq % d->Hkv != 0) return PA_ERR_GQA;
+  if (d->page < 16 || d->page > 256 || (d->page & (d->page - 1))) return PA_ERR_SHAPE;
+  if ((int64_t)d->width * d->page >= 0x7fffffff - 256 || !std::isfinite(d->scale) || d->Hq > 65535) return PA_ERR_SHAPE;
+  const int64_t n[9] = {d->T, d->Hq, fresh ? d->T : 0, fresh ? d->Hkv : 0, d->T, d->Hq, d->pages, d->Hkv, d->page};
+  const int64_t x[9] = {s->q_t, s->q_h, s->n_t, s->n_h, s->o_t, s->o_h, s->p_p, s->p_h, s->p_n};
+  for (int i = 0; i < 9; ++i)
+    if (n[i] > 1 && (x[i] < d->D || x[i] >= (int64_t(1) << 38))) return PA_ERR_SHAPE;
+  for (int i = 0; i < 9; ++i)
+    if (n[i] > 1 && x[i] % 8 != 0) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+static pa::PagedArgs paged_args(const pa_paged_dims* d, const pa_paged_strides* s, const int32_t* page_table,
+                                const int32_t* q_start, const int32_t* kv_len) {
+  const auto used = [&](int64_t n, int64_t x) { return n > 1 ? x : (int64_t)d->D; };  // a dimension of one has any stride
+  pa::PagedArgs p{};
+  p.S = d->S, p.T = d->T, p.Hq = d->Hq, p.Hkv = d->Hkv, p.D = d->D, p.G = d->Hq / d->Hkv;
+  p.pages = d->pages, p.page = d->page, p.width = d->width;
+  p.scale_log2 = (d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)d->D)) * 1.4426950408889634f;
+  p.q_t = used(d->T, s->q_t), p.q_h = used(d->Hq, s->q_h);
+  p.o_t = used(d->T, s->o_t), p.o_h = used(d->Hq, s->o_h);
+  p.p_p = used(d->pages, s->p_p), p.p_h = used(d->Hkv, s->p_h), p.p_n = s->p_n;
+  p.page_table = page_table, p.q_start = q_start, p.kv_len = kv_len;
+  return p;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+pa_status pa_paged_append(const pa_paged_dims* dims, const pa_paged_strides* strides, const pa_rotary* rotary,
+                          const void* q, const void* k, const void* v, const int32_t* page_table, const int32_t* q_start,
+                          const int32_t* kv_len, const int32_t* positions, void* q_out, void* k_pages, void* v_pages,
+                          pa_stream_t stream) {
+  pa_status why = paged_checks(dims, strides, true);
+  if (why != PA_OK) return why;
+  if (rotary && (!rotary_ok(rotary) || rotary->rot > dims->D)) return PA_ERR_SHAPE;
+  if (dims->T == 0) return PA_OK;  // tensors without elements have no address
+  for (const void* x : {k, v, (const void*)page_table, (const void*)q_start, (const void*)kv_len, (const void*)k_pages,
+                        (const void*)v_pages})
+    if (!x) return PA_ERR_NULL;
+  if (!q != !q_out) return PA_ERR_NULL;
+  for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_pages, (const void*)v_pages})
+    if (!aligned16(x)) return PA_ERR_ALIGN;
+  for (const void* x : {page_table, q_start, kv_len, positions})
+    if (!aligned4(x)) return PA_ERR_ALIGN;
+  const pa::PagedArgs p = paged_args(dims, strides, page_table, q_start, kv_len);
+  if (q && q == q_out && (p.q_t != p.o_t || p.q_h != p.o_h)) return PA_ERR_SHAPE;
+  if ((why = device_ok()) != PA_OK) return why;
+  const int64_t n_t = dims->T > 1 ? strides->n_t : dims->D, n_h = dims->Hkv > 1 ? strides->n_h : dims->D;
+  return pa::launch_append(p, rotary, q, k, v, n_t, n_h, positions, q_out, k_pages, v_pages, cu(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+size_t pa_paged_workspace_bytes(int32_t D) { return D == 64 || D == 96 || D == 128 ? pa::paged_ws_bytes(D) : 0; }
+
+pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* strides, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len,
+                       void* out, float* lse, void* ws, size_t ws_bytes, pa_stream_t stream) {
+  pa_status why = paged_checks(dims, strides, false);
+  if (why != PA_OK) return why;
+  if (dims->Hq / dims->Hkv > 128) return PA_ERR_GQA;
+  if (dims->T == 0) return PA_OK;
+  for (const void* x : {q, k_pages, v_pages, (const void*)page_table, (const void*)q_start, (const void*)kv_len,
+                        (const void*)out, (const void*)lse, (const void*)ws})
+    if (!x) return PA_ERR_NULL;
+  for (const void* x : {q, k_pages, v_pages, (const void*)out, (const void*)lse, (const void*)ws})
+    if (!aligned16(x)) return PA_ERR_ALIGN;
+  for (const void* x : {page_table, q_start, kv_len})
+    if (!aligned4(x)) return PA_ERR_ALIGN;
+  if (ws_bytes < pa_paged_workspace_bytes(dims->D)) return PA_ERR_WORKSPACE;
+  if ((why = device_ok()) != PA_OK) return why;
+  return pa::launch_paged_fwd(paged_args(dims, strides, page_table, q_start, kv_len), q, k_pages, v_pages, out, lse, ws,
+                              cu(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 pa_status pa_selftest_wait_timeout(void* ws, size_t ws_bytes, pa_stream_t stream) {
   if (!ws) return PA_ERR_NULL;
   if (!aligned16(ws)) return PA_ERR_ALIGN;
@@ -845,16 +1020,18 @@ const char* pa_status_string(pa_status s) {
     case PA_OK: return "ok";
     case PA_ERR_NULL: return "a required pointer is NULL";
     case PA_ERR_HEAD_DIM: return "head dim must be 64, 96 or 128";
-    case PA_ERR_GQA: return "Hq must be a multiple of Hkv";
+    case PA_ERR_GQA: return "Hq must be a multiple of Hkv (paged attention: at most 128 times)";
     case PA_ERR_SHAPE:
       return "bad shape (B, H, N > 0; B*Hq*N < 2^31; finite scale; N % 128 == 0 for the single-step calls; "
              "strides >= D; hidden size a multiple of 64; 0 <= top <= min(32, V); temperature > 0; checkpoints: "
-             "1 to 8 tensors, C % 8 == 0, block 32, 64 or 128)";
+             "1 to 8 tensors, C % 8 == 0, block 32, 64 or 128; rotary: 1 to 4 tensors, rot a multiple of 8 in [8, 128], "
+             "D a multiple of 8 in [rot, 256]; paged cache: page 16, 32, 64, 128 or 256, see the call)";
     case PA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case PA_ERR_WORKSPACE: return "workspace too small (see pa_workspace_bytes)";
     case PA_ERR_ARCH: return "device is not compute capability 10.3 (GB300)";
     case PA_ERR_CUDA: return "a CUDA call or kernel launch failed";
-    case PA_ERR_DTYPE: return "io dtype must be PA_IO_BF16 or PA_IO_F32, a checkpoint format PA_CKPT_INT8 or PA_CKPT_E4M3";
+    case PA_ERR_DTYPE: return "io dtype must be PA_IO_BF16 or PA_IO_F32, a checkpoint format PA_CKPT_INT8 or PA_CKPT_E4M3, a rotary layout or "
+                             "scaling one of its enum";
     case PA_ERR_HOST_MEMORY: return "host memory for the call's scratch could not be allocated";
   }
   return "unknown status";

@@ -198,4 +198,24 @@ cudaError_t launch_bwd_ckpt_prologue(const AttnParams& p, int D, const RowStride
                                      const void* out_codes, const float* out_scales, int format, int block,
                                      cudaStream_t st);
 
+// Rotary positions (rope.cu).
+using RopeTensor = pa_rope_tensor;
+cudaError_t launch_rope(const pa_rotary& rope, const RopeTensor* t, int count, int B, int N, int D, bool f32, bool backward,
+                        const int32_t* positions, cudaStream_t st);
+cudaError_t launch_positions(int B, int N, const int32_t* seg, int32_t* positions, cudaStream_t st);
+
+// A step's rows and the paged cache (append.cu, paged.cu); element strides.
+struct PagedArgs {
+  int S, T, Hq, Hkv, D, G;
+  int pages, page, width;
+  float scale_log2;  // scale * log2(e)
+  int64_t q_t, q_h, o_t, o_h, p_p, p_h, p_n;
+  const int32_t *page_table, *q_start, *kv_len;
+};
+cudaError_t launch_append(const PagedArgs& p, const pa_rotary* rope, const void* q, const void* k, const void* v, int64_t n_t,
+                          int64_t n_h, const int32_t* positions, void* q_out, void* k_pages, void* v_pages, cudaStream_t st);
+size_t paged_ws_bytes(int D);
+cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                             void* ws, cudaStream_t st);
+
 }  // namespace pa

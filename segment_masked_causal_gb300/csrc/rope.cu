@@ -1,0 +1,198 @@
+// rope.cu -- positions of packed rows, and rotary positions applied to queries
+// and keys, forward and backward.
+//
+// Both are bound by memory: the rotation reads and writes each element once.
+// A thread holds the cosines and sines of one unit of pairs at one token
+// (rope.cuh) and takes that unit of many heads, so that they are computed once
+// for a run of heads; four heads' loads are in flight at a time. The backward is
+// the rotation by minus the angle (a rotation's transpose), times the same
+// amplitude.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "rope.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeArgs {
+  pa_rotary rope;
+  RopeTensor t[PA_ROPE_MAX_TENSORS];
+  int count, heads;       // tensors, and their heads in all
+  int run;                // heads per block
+  int64_t tokens;         // B * N
+  int N, units, turning;  // units per row: `turning` ones of pairs, then eight elements each
+  const int32_t* positions;
+  float sign;
+};
+
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
+  const int per = kRopeThreads / p.units;
+  const int at = threadIdx.x / p.units, u = threadIdx.x - at * p.units;
+  const int64_t token = (int64_t)blockIdx.x * per + at;
+  if (at >= per || token >= p.tokens) return;
+  const int64_t b = token / p.N, n = token - b * p.N;
+  const int rot = p.rope.rot, half = rot / 2;
+  const bool turn = u < p.turning;
+  float c[VEC], s[VEC];
+  if (turn) {
+    const int32_t pos = p.positions ? p.positions[token] : (int32_t)n;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      rope_cos_sin(p.rope.turns[u * VEC + i], pos, p.rope.amplitude, c[i], s[i]);
+      s[i] *= p.sign;
+    }
+  }
+  int h = blockIdx.y * p.run;  // among all tensors' heads
+  const int end = min(h + p.run, p.heads);
+  int k = 0, first = 0;  // tensor, and its first head
+  while (h < end) {
+    while (h >= first + p.t[k].H) first += p.t[k++].H;
+    const RopeTensor& t = p.t[k];
+    const int stop = min(end, first + t.H);
+    const T* x = static_cast<const T*>(t.x) + b * t.x_b + n * t.x_n + (int64_t)(h - first) * t.x_h;
+    T* y = static_cast<T*>(t.y) + b * t.y_b + n * t.y_n + (int64_t)(h - first) * t.y_h;
+    constexpr int U = 4;
+    if (turn) {
+      for (; h < stop; h += U, x += U * t.x_h, y += U * t.y_h) {
+        RopeUnit<T, VEC, INTER> r[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (h + i < stop) r[i].load(x + i * t.x_h, u, half);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (h + i < stop) {
+            r[i].rotate(c, s);
+            r[i].store(y + i * t.y_h, u, half);
+          }
+      }
+    } else {
+      const int e = rot + 8 * (u - p.turning);
+      for (; h < stop; h += U, x += U * t.x_h, y += U * t.y_h) {
+        PlainUnit<T> r[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (h + i < stop) r[i].load(x + i * t.x_h + e);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (h + i < stop) r[i].store(y + i * t.y_h + e);
+      }
+    }
+    h = stop;
+  }
+}
+
+template <typename T, int VEC>
+cudaError_t launch_vec(RopeArgs& a, cudaStream_t st) {
+  a.turning = a.rope.rot / (2 * VEC);
+  const int64_t blocks = (a.tokens + kRopeThreads / a.units - 1) / (kRopeThreads / a.units);
+  // Heads of a block: all of them, or fewer where the tokens alone do not fill the device.
+  const int64_t want = 152 * 8;
+  a.run = (int)std::min<int64_t>(a.heads, std::max<int64_t>(4, (int64_t)a.heads * blocks / want));
+  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.run - 1) / a.run));
+  if (a.rope.layout == PA_ROPE_INTERLEAVED)
+    rope_kernel<T, VEC, true><<<grid, kRopeThreads, 0, st>>>(a);
+  else
+    rope_kernel<T, VEC, false><<<grid, kRopeThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Position of each token in its run of equal ids. A block takes 1,024 tokens of
+// a row; a thread's latest start of a run at or before each of its four tokens
+// comes from a scan of maxima, and the block looks back from its first token,
+// 4,096 ids at a time, for the start that the scan does not see.
+constexpr int kPosThreads = 256, kPosPer = 4, kPosTile = kPosThreads * kPosPer, kPosBack = 16;
+
+__device__ __forceinline__ int block_max(int v, int* sh) {
+  v = __reduce_max_sync(~0u, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int m = sh[0];
+#pragma unroll
+  for (int i = 1; i < kPosThreads / 32; ++i) m = max(m, sh[i]);
+  return m;
+}
+
+__global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* __restrict__ seg,
+                                                                int32_t* __restrict__ positions, int N, int tiles) {
+  __shared__ int sh[kPosThreads / 32];
+  const int b = blockIdx.x / tiles, n0 = (blockIdx.x - b * tiles) * kPosTile;
+  const int32_t* row = seg + (int64_t)b * N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto starts = [&](int n) { return n == 0 || row[n] != row[n - 1]; };
+  int at[kPosPer];  // latest start at or before token n0 + 4 thread + i, as far as this thread sees
+  int last = -1;
+#pragma unroll
+  for (int i = 0; i < kPosPer; ++i) {
+    const int n = n0 + threadIdx.x * kPosPer + i;
+    if (n < N && starts(n)) last = n;
+    at[i] = last;
+  }
+  int before = last;  // inclusive scan over the warp, then over the block
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, before, o);
+    if (lane >= o) before = max(before, v);
+  }
+  if (lane == 31) sh[warp] = before;
+  int excl = __shfl_up_sync(~0u, before, 1);
+  if (lane == 0) excl = -1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) excl = max(excl, sh[w]);
+  int from = -1;  // start of the run that the block's first token continues
+  if (!starts(n0)) {
+    for (int hi = n0; hi > 0 && from < 0; hi -= kPosThreads * kPosBack) {
+      int found = -1;
+#pragma unroll
+      for (int j = 0; j < kPosBack; ++j) {
+        const int n = hi - 1 - (j * kPosThreads + (int)threadIdx.x);
+        if (n >= 0 && starts(n)) found = max(found, n);
+      }
+      from = block_max(found, sh);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPosPer; ++i) {
+    const int n = n0 + threadIdx.x * kPosPer + i;
+    if (n < N) positions[(int64_t)b * N + n] = n - max(max(at[i], excl), from);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const pa_rotary& rope, const RopeTensor* t, int count, int B, int N, int D, bool f32, bool backward,
+                        const int32_t* positions, cudaStream_t st) {
+  RopeArgs a{};
+  a.rope = rope;
+  a.count = count;
+  bool in_place = true;
+  for (int i = 0; i < count; ++i) {
+    a.t[i] = t[i];
+    a.heads += t[i].H;
+    in_place = in_place && t[i].x == t[i].y;
+  }
+  a.tokens = (int64_t)B * N;
+  a.N = N;
+  a.positions = positions;
+  a.sign = backward ? -1.f : 1.f;
+  // Units of eight pairs where the rotated part is a whole number of them; fp32
+  // ones of four are as many bytes.
+  const int vec = f32 || rope.rot % 16 ? 4 : 8;
+  a.units = rope.rot / (2 * vec) + (in_place ? 0 : (D - rope.rot) / 8);
+  if (f32) return launch_vec<float, 4>(a, st);
+  return vec == 8 ? launch_vec<__nv_bfloat16, 8>(a, st) : launch_vec<__nv_bfloat16, 4>(a, st);
+}
+
+cudaError_t launch_positions(int B, int N, const int32_t* seg, int32_t* positions, cudaStream_t st) {
+  const int tiles = (N + kPosTile - 1) / kPosTile;
+  positions_kernel<<<(unsigned)((int64_t)B * tiles), kPosThreads, 0, st>>>(seg, positions, N, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace pa
