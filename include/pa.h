@@ -646,7 +646,7 @@ pa_status pa_rope(const pa_rotary* rotary, int32_t count, const pa_rope_tensor* 
  * they are neither written nor attended (pages given back at the start of a long
  * context, say, marked with -1). Rows of q before q_start[0] and from q_start[S] on
  * belong to nobody: their outputs stay as they were.
- * D is 64, 96 or 128; page 16, 32, 64, 128 or 256; S, T, pages, width >= 1 (T = 0
+ * D is 64, 96 or 128; page 16, 32, 64, 128 or 256; S, pages, width >= 1; T <= 2^30 (0
  * returns PA_OK without a launch); width * page < 2^31 - 256; S < 2^24. Strides of dimensions
  * larger than one are >= D and multiples of 8; pointers are 16-byte aligned (page_table,
  * q_start and kv_len 4-byte aligned).
@@ -683,7 +683,7 @@ pa_status pa_paged_append(const pa_paged_dims* dims, const pa_paged_strides* str
  * A row that sees no key has out 0 and lse -inf. lse (T, Hq) fp32, contiguous. What a page
  * holds past a sequence's tokens may be anything (NaN too); the keys and values
  * up to kv_len are finite. P enters the second product in bf16; sums and maxima are
- * fp32. Hq / Hkv is at most 128.
+ * fp32. Hq / Hkv is at most 128, and (T + S) Hkv (width page + T + 512) at most 4e18.
  * ws >= pa_paged_workspace_bytes(D) bytes, its first 4 the status word; a
  * workspace belongs to one stream at a time. The same call gives the same bits.
  * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA (also Hq / Hkv > 128), PA_ERR_SHAPE, PA_ERR_ALIGN,

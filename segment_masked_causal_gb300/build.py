@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["api.cu", "prologue.cu", "stage.cu", "fwd.cu", "bwd_dq.cu", "bwd_dkv.cu", "bwd_fused.cu", "noalloc.cu",
            "lce.cu", "logp.cu", "ckpt.cu", "rope.cu", "append.cu", "paged.cu", "pack.cpp"]
-HEADERS = ["sm103.cuh", "common.cuh", "kernels.h", "tmap.h", "rope.cuh", "paged.cuh"]
+HEADERS = ["sm103.cuh", "common.cuh", "kernels.h", "tmap.h", "rope.cuh", "paged.cuh", "softmax.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

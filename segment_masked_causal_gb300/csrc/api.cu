@@ -901,7 +901,7 @@ pa_status pa_rope(const pa_rotary* rotary, int32_t count, const pa_rope_tensor* 
 // Dims, and the strides of dimensions larger than one.
 static pa_status paged_checks(const pa_paged_dims* d, const pa_paged_strides* s, bool fresh) {
   if (!d || !s) return PA_ERR_NULL;
-  if (d->S <= 0 || d->S >= (1 << 24) || d->T < 0 || d->Hq <= 0 || d->Hkv <= 0 || d->pages <= 0 || d->width <= 0)
+  if (d->S <= 0 || d->S >= (1 << 24) || d->T < 0 || d->T > (1 << 30) || d->Hq <= 0 || d->Hkv <= 0 || d->pages <= 0 || d->width <= 0)
     return PA_ERR_SHAPE;
   if (d->D != 64 && d->D != 96 && d->D != 128) return PA_ERR_HEAD_DIM;
   if (d->Hq % d->Hkv != 0) return PA_ERR_GQA;
@@ -963,6 +963,8 @@ pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* stride
   pa_status why = paged_checks(dims, strides, false);
   if (why != PA_OK) return why;
   if (dims->Hq / dims->Hkv > 128) return PA_ERR_GQA;
+  // the costs that deal out the work are 64-bit sums of keys over tiles and kv heads
+  if (((double)dims->T + dims->S) * dims->Hkv * ((double)dims->width * dims->page + dims->T + 512) > 4e18) return PA_ERR_SHAPE;
   if (dims->T == 0) return PA_OK;
   for (const void* x : {q, k_pages, v_pages, (const void*)page_table, (const void*)q_start, (const void*)kv_len,
                         (const void*)out, (const void*)lse, (const void*)ws})

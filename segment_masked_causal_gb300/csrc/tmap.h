@@ -77,6 +77,23 @@ inline bool tmap_bf16_bhnd_sw128(CUtensorMap* m, const void* base, uint64_t D, u
   return r == CUDA_SUCCESS;
 }
 
+// A 4-D bf16 tensor of dims d[0] (contiguous) .. d[3] with element strides s[0] ..
+// s[2] of the outer three, read in boxes of 64 x box[0] x box[1] x 1 with the
+// 128-byte swizzle. What lies past a dim reads as zero.
+inline bool tmap_bf16_4d_sw128(CUtensorMap* m, const void* base, const uint64_t (&d)[4], const int64_t (&s)[3],
+                               const uint32_t (&box)[2]) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {d[0], d[1], d[2], d[3]};
+  cuuint64_t strides[3] = {(cuuint64_t)s[0] * 2, (cuuint64_t)s[1] * 2, (cuuint64_t)s[2] * 2};
+  cuuint32_t b[4] = {64, box[0], box[1], 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, b, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // `planes` planes of `rows` rows x `inner` contiguous bf16 or fp32 elements
 // (16-byte multiples), in boxes of 128 rows x 128 bytes of one plane with the
 // 128-byte swizzle; what lies past `inner` or `rows` is dropped from stores.

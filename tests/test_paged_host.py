@@ -63,7 +63,7 @@ def strides(**kw):
 
 
 BAD_SHAPES = [dict(S=0), dict(S=1 << 24), dict(T=-1), dict(Hq=0), dict(Hkv=0), dict(pages=0), dict(width=0), dict(page=8),
-              dict(page=48), dict(page=512), dict(page=0), dict(width=1 << 27), dict(scale=math.inf), dict(Hq=65538)]
+              dict(page=48), dict(page=512), dict(page=0), dict(width=1 << 27), dict(scale=math.inf), dict(Hq=65538), dict(T=(1 << 30) + 1)]
 
 
 @pytest.mark.parametrize("call", ["append", "fwd"])
