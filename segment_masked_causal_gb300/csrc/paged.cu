@@ -1,10 +1,10 @@
 // paged.cu -- attention of a step's new tokens over a paged cache, for sm_103a.
 //
-// Rows. A tile has the TQ = 128 / G new tokens (rounded down) of one sequence times
-// the G query heads of one kv head: row r is token r / G, head r % G, which is the
-// order in which one TMA box {64, G, TQ} brings q. So keys and values are read once
-// for all heads that share them, a single token fills G rows, and a long chunk
-// fills 128. An item is (sequence, tile, kv head); a visit is 128 of its keys.
+// Rows. A tile is floor(128 / G) new tokens of one sequence times the G query heads of
+// one kv head: row r is token r / G, head r % G, which is the order in which one TMA box
+// {64, G, tokens} brings q. So keys and values are read once for all heads that share
+// them, a single token fills G rows and a long chunk 128. An item is (sequence, two
+// neighbouring tiles or what is left of them, kv head); a visit is 128 of its keys.
 //
 // Work. What there is to do is known on the device only (a step's lengths change
 // while it is replayed from a graph), and it is dealt out evenly: every item has
@@ -15,16 +15,27 @@
 // unnormalised) in the workspace, at most two a CTA; a second kernel joins them. So
 // one long context spreads over all SMs as evenly as many short ones.
 //
-// Visits. As in fwd.cu: S = Q K^T into one of two TMEM buffers, softmax in two
-// warpgroups that take the visits in turn (one thread a row), P from TMEM, O += P V in
-// TMEM, lazy rescaling. The pipeline runs on from item to item: the next item's K and V are
-// loaded, and its S formed, while the last one's O is written. Pages arrive by TMA, one
-// box per page and 64 columns, a lane each, the page numbers loaded a visit ahead. Rows
-// past a sequence's tokens and pages that are not there are masked in S; their rows of
-// V are set to zero in shared memory before the product, because 0 * NaN is NaN.
+// Visits. Two streams, each with an S buffer and an O accumulator in TMEM and a softmax
+// warpgroup, one thread a row: S = Q K^T, P = 2^(S log2e scale - m) as bf16 over S, O += P V
+// with P from TMEM. While one stream is in its softmax, the tensor cores work for the
+// other. An item of two tiles gives each stream a tile, and both take every visit (K and
+// V are read from shared memory for 256 rows); an item of one tile has its visits dealt out to
+// the streams in turn, whose sums and O are joined at its end. No stream ever waits for
+// the other's maximum, and O is rescaled, lazily, between a stream's own products.
+//
+// Few rows. A TMEM lane belongs to one warp of four, so where an item has at most 32
+// rows the tile holds them four times and each of a group's warps takes 32 of a visit's
+// 128 keys (its P has zeros for the others); the four parts of a row are joined
+// at the item's end as well.
+//
+// The pipeline runs on from item to item: the next item's Q, K and V are loaded while the
+// last one's O is written. Pages arrive by TMA, one box per page and 64 columns, a lane
+// each, the page numbers loaded a visit ahead. Rows past a sequence's tokens and pages
+// that are not there are masked in S; their rows of V are set to zero in shared memory
+// before the product, because 0 * NaN is NaN.
 //
 // Warp roles: 0 Q and K producer, 1 V producer, 2 S issuer and TMEM owner, 3 PV
-// issuer, 4..7 and 8..11 the softmax groups.
+// issuer, 4..7 and 8..11 the softmax groups of streams 0 and 1.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,49 +50,64 @@
 namespace pa {
 namespace {
 
-constexpr int kCtas = 160;       // at most; the workspace's layout has room for as many
+constexpr int kCtas = 160;  // at most; the workspace's layout has room for as many
 constexpr int kThreads = 384;
 // Cost of an item besides its keys, in keys: what Q's load, the pipeline's turn and the
 // epilogue take.
 constexpr int kItemCost = 256;
-constexpr int kLeastVisits = 2;  // of a part of an item
-constexpr int kLeastCost = 512;  // of a CTA
+constexpr int kLeastVisits = 2;   // of a part of an item
+constexpr int kLeastCostLog = 9;  // of a CTA, log2
+constexpr int kFew = 32;          // rows of an item that the tile holds four times
+constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
 template <int D>
 struct Layout {
   static constexpr int DL = D == 64 ? 64 : 128;  // columns of a tile in shared memory
   static constexpr int NC = DL / 64;             // 64-column chunks
-  static constexpr int NSK = 3, NSV = 2;
+  static constexpr int NS = D == 64 ? 4 : 2;     // stages of K, and of V
   static constexpr uint32_t CHUNK = 128 * 128;
   static constexpr uint32_t TB = NC * CHUNK;
-  static constexpr uint32_t OFF_K = TB, OFF_V = OFF_K + NSK * TB;
-  static constexpr uint32_t MISC = 8192;
-  static constexpr uint32_t SMEM = OFF_V + NSV * TB + MISC + 1024;
-  static constexpr uint32_t TM_O = 0, TM_S = 128, TM_P = 384, TMEM_COLS = 512;
+  static constexpr uint32_t OFF_K = 2 * TB, OFF_V = OFF_K + NS * TB, OFF_STAGE = OFF_V + NS * TB;
+  static constexpr uint32_t MISC = 4096;
+  static constexpr uint32_t SMEM = OFF_STAGE + 8 * kStage + MISC + 1024;
+  // TMEM: a stream's O, and its S with P over the first half of it
+  static constexpr uint32_t TM_O = 0, TM_S = 256, TMEM_COLS = 512;
 };
 
 // A place on the line of work: before visit kt of item (s, i, h), of nkt visits.
 struct Bound {
   int s, i, h, kt, nkt;
+  SeqRows r;
 };
 
+// A part of an item, as the K producer hands it to the other warps; nt 0 ends the run.
+struct Item {
+  int row0, nt, h;    // first row of q, tokens, kv head
+  int s;              // sequence
+  int kt0, kt1, nkt;  // visits of the part, and of the item
+  int cap, seen0;     // keys in the cache; keys that the first token sees
+};
+constexpr int kItems = 4;
+
 struct Misc {
-  uint64_t q_full, q_free, k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], mh_full[2][4], sums_full, o_free, fin_s, fin_pv;
+  uint64_t q_full[2], q_free[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], sums[2], group[2], fin_s, fin_pv;
+  uint64_t item_full[kItems], item_free[kItems];
   uint32_t tmem_base;
   int abort_flag;
   Bound ends[2];
   long long scan[kThreads / 32];
-  float mh[2][128];          // [visit parity][row]: row maximum in use after the visit
-  float sums[2][2][2][128];  // [item parity][group][l, lr][row]
+  Item items[kItems];
+  uint32_t k_bad[4], v_bad[4], s_bad[2];  // missing pages of the visit in a stage, or in a stream's S
+  float stat[2][2][128];                  // [stream][maximum, sum][row]
 };
 
 // Partial results of a CTA: slot 0 of the item that its run begins inside of, slot 1 of
 // the one that it ends inside of. O as float4 of row r, columns 4c .. 4c + 3 at [c][r].
 struct Partial {
-  float m[128], l[128], lr[128];
+  float m[256], l[256];
 };
-__host__ __device__ constexpr size_t partial_bytes(int D) { return sizeof(Partial) + (size_t)128 * D * 4; }
+__host__ __device__ constexpr size_t partial_bytes(int D) { return sizeof(Partial) + (size_t)256 * D * 4; }
 constexpr size_t kOffRecords = 256, kOffPartials = kOffRecords + kCtas * sizeof(int4);
 
 // What a CTA left: the item that it began and did not end, if any (s, i, h, else s = -1),
@@ -90,37 +116,43 @@ enum Head : int { kWhole = 0, kGoesOn = 1, kEnds = 2, kEmpty = 3 };
 
 struct FwdArgs {
   PagedArgs p;
-  int TQ, page_shift;
+  int TQ;   // tokens of a tile; an item has two of them
+  int TQf;  // tokens of one that has few rows
+  int page_shift;
   __nv_bfloat16* out;
   float* lse;
   uint8_t* ws;
 };
 
-__device__ __forceinline__ int tiles_of(const FwdArgs& a, int ql) { return (ql + a.TQ - 1) / a.TQ; }
-// Visits of tile i of a sequence's tiles: the keys that its last token sees.
+__device__ __forceinline__ int items_of(const FwdArgs& a, int ql) {
+  const int n = 2 * a.TQ;
+  return ql <= n ? (ql > 0) : (ql + n - 1) / n;
+}
+// Visits of item i of a sequence: the keys that its last token sees.
 __device__ __forceinline__ int visits_of(const FwdArgs& a, const SeqRows& r, int i) {
-  const int ql = r.b - r.a, e = min(r.base() + min(ql, (i + 1) * a.TQ), a.p.width * a.p.page);
+  const int ql = r.b - r.a, e = min(r.base() + min(ql, (i + 1) * 2 * a.TQ), a.p.width * a.p.page);
   return e <= kTile ? 1 : (e + kTile - 1) / kTile;
 }
-// Costs of a sequence's items of one kv head: tile i's and all before it.
+// Costs of a sequence's items of one kv head: item i's and all before it.
 struct Costs {
   long long A;
-  int ql, n, TQ;
+  int ql, n, per;
   __device__ __forceinline__ Costs(const FwdArgs& a, const SeqRows& r) {
     ql = r.b - r.a;
-    n = tiles_of(a, ql);
-    TQ = a.TQ;
+    n = items_of(a, ql);
+    per = 2 * a.TQ;
     A = (long long)min(max(r.base(), 0), a.p.width * a.p.page) + kItemCost;
   }
-  __device__ __forceinline__ long long before(int i) const { return A * i + (long long)TQ * i * (i + 1) / 2; }
-  __device__ __forceinline__ long long of(int i) const { return A + (i == n - 1 ? ql : TQ * (i + 1)); }
+  __device__ __forceinline__ long long before(int i) const { return A * i + (long long)per * i * (i + 1) / 2; }
+  __device__ __forceinline__ long long of(int i) const { return A + (i == n - 1 ? ql : per * (i + 1)); }
   __device__ __forceinline__ long long all() const { return n ? before(n - 1) + of(n - 1) : 0; }
 };
 
-// Where `x` of sequence s's cost lies. A cut that would leave fewer than kLeastVisits on
+// Where `x` of sequence s's cost lies: a function of x alone that never falls as x rises,
+// so that the end of one run is the start of the next (which is all that the fp32
+// quotients have to be good for). A cut that would leave fewer than kLeastVisits on
 // one of its sides moves to the item's end on that side.
-__device__ Bound place(const FwdArgs& a, int s, long long x) {
-  const SeqRows r = seq_rows(a.p, s);
+__device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r, long long x) {
   const Costs c(a, r);
   const int H = a.p.Hkv;
   int i = 0;
@@ -133,12 +165,16 @@ __device__ Bound place(const FwdArgs& a, int s, long long x) {
   }
   x -= c.before(i) * H;
   const long long of = c.of(i);
+  int h = min((int)__fdividef((float)x, (float)of), H - 1);
+  while (h > 0 && h * of > x) --h;
+  while (h < H - 1 && (h + 1) * of <= x) ++h;
   Bound b;
   b.s = s;
   b.i = i;
-  b.h = (int)min(x / of, (long long)H - 1);
+  b.h = h;
+  b.r = r;
   b.nkt = visits_of(a, r, i);
-  b.kt = (int)min((x - b.h * of) * b.nkt / of, (long long)b.nkt - 1);
+  b.kt = min((int)(__fdividef((float)(x - h * of), (float)of) * (float)b.nkt), b.nkt - 1);
   if (b.kt < kLeastVisits)
     b.kt = 0;
   else if (b.nkt - b.kt < kLeastVisits)
@@ -146,45 +182,46 @@ __device__ Bound place(const FwdArgs& a, int s, long long x) {
   return b;
 }
 
-// Both ends of this CTA's run, by all threads.
-__device__ void find_ends(const FwdArgs& a, Misc& m) {
+// Both ends of this CTA's run, by all threads. mine: the rows of sequence threadIdx.x.
+__device__ __forceinline__ void find_ends(const FwdArgs& a, Misc& m, SeqRows mine) {
   const int S = a.p.S, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long total = 0, x[2] = {0, 0};
-  for (int pass = 0; pass < 2; ++pass) {  // the sum, then the places in it
-    long long run = 0;
+  unsigned long long total = 0, x[2] = {0, 0};
+  for (int pass = S <= kThreads ? 1 : 0; pass < 2; ++pass) {  // the sum (at once with the rest where it can), then the places
+    unsigned long long run = 0;
     for (int s0 = 0; s0 < S; s0 += kThreads) {
       const int s = s0 + tid;
-      long long mine = 0;
-      if (s < S) mine = Costs(a, seq_rows(a.p, s)).all() * a.p.Hkv;
-      long long v = mine;
+      if (s0 > 0 || pass > 0) {
+        if (s < S && S > kThreads) mine = seq_rows(a.p, s);
+      }
+      const unsigned long long cost = s < S ? Costs(a, mine).all() * a.p.Hkv : 0;
+      unsigned long long v = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(~0u, v, o);
+        const unsigned long long u = __shfl_up_sync(~0u, v, o);
         if (lane >= o) v += u;
       }
-      if (lane == 31) m.scan[warp] = v;
+      if (lane == 31) m.scan[warp] = (long long)v;
       __syncthreads();
-      long long before = run;
+      unsigned long long before = run;
+#pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) {
-        const long long u = m.scan[w];
+        const unsigned long long u = (unsigned long long)m.scan[w];
         if (w < warp) before += u;
         run += u;
       }
       v += before;  // inclusive
-      if (S <= kThreads) {  // everything is here already: no second pass over memory
-        total = run;
-        pass = 1;
-      }
+      if (S <= kThreads) total = run;
       if (pass == 1) {
         if (s0 == 0) {
-          const long long P = max(1ll, min((long long)gridDim.x, total / kLeastCost)), per = total / P, rest = total % P;
+          const uint32_t P = (uint32_t)max(1ull, min((unsigned long long)gridDim.x, total >> kLeastCostLog));
           for (int e = 0; e < 2; ++e) {
-            const long long c = min((long long)blockIdx.x + e, P);
-            x[e] = per * c + rest * c / P;
+            const uint32_t c = blockIdx.x + e;
+            x[e] = c >= P ? total : __umul64hi(total, (unsigned long long)(c * (0xFFFFFFFFu / P + 1)) << 32);
           }
         }
+#pragma unroll 1
         for (int e = 0; e < 2; ++e)
-          if (mine > 0 && x[e] >= v - mine && x[e] < v) m.ends[e] = place(a, s, x[e] - (v - mine));
+          if (x[e] >= v - cost && x[e] < v) m.ends[e] = place(a, s, mine, (long long)(x[e] - (v - cost)));
       }
       __syncthreads();
     }
@@ -195,96 +232,143 @@ __device__ void find_ends(const FwdArgs& a, Misc& m) {
 // The parts of items in a CTA's run, in order.
 struct Walk {
   const FwdArgs& a;
-  Bound at, end;
   SeqRows r;
-  int n;         // tiles of the sequence
+  int s, i, h;   // the item
+  int n;         // items of the sequence and kv head
   int kt0, kt1;  // visits of this part
-  __device__ __forceinline__ Walk(const FwdArgs& a_, const Misc& m) : a(a_), at(m.ends[0]), end(m.ends[1]) {
-    r.a = r.b = r.kv = n = 0;
-    if (at.s < a.p.S) load();
-    kt0 = kt1 = 0;
+  int nkt;       // and of the item
+  __device__ __forceinline__ Walk(const FwdArgs& a_, const Misc& m) : a(a_) {
+    const Bound &b = m.ends[0], &e = m.ends[1];
+    s = b.s, i = b.i, h = b.h, kt0 = b.kt, r = b.r;
+    es = e.s, ei = e.i, eh = e.h, ek = e.kt;
+    n = items_of(a, r.b - r.a);
+    kt1 = nkt = 0;
     first = true;
   }
   // To the next part; false when there is none.
   __device__ __forceinline__ bool next() {
     for (;;) {
-      if (!first) step();
-      if (at.s >= a.p.S || (at.s == end.s && at.i == end.i && at.h == end.h && end.kt == 0) || past()) return false;
-      kt0 = first ? at.kt : 0;
+      if (!first) {
+        step();
+        kt0 = 0;
+      }
       first = false;
-      at.nkt = visits_of(a, r, at.i);
-      const bool last = at.s == end.s && at.i == end.i && at.h == end.h;
-      kt1 = last ? end.kt : at.nkt;
-      if (last) end.s = -1;  // nothing behind this one
+      const bool last = s == es && i == ei && h == eh;
+      if (s >= a.p.S || es < 0 || (last && ek == 0)) return false;
+      nkt = visits_of(a, r, i);
+      kt1 = last ? ek : nkt;
+      if (last) es = -1;  // nothing behind this one
       if (kt0 < kt1) return true;
     }
   }
-  __device__ __forceinline__ int nkt() const { return at.nkt; }
-  __device__ __forceinline__ int row0() const { return r.a + at.i * a.TQ; }                      // the tile's first row of q
-  __device__ __forceinline__ int tokens() const { return min(a.TQ, r.b - r.a - at.i * a.TQ); }  // and its tokens
-  __device__ __forceinline__ int first_seen() const { return r.base() + at.i * a.TQ + 1; }      // keys that its first one sees
-  __device__ __forceinline__ int cap() const { return min(r.kv, a.p.width * a.p.page); }        // keys in the cache
+  __device__ __forceinline__ Item item() const {
+    const int t0 = i * 2 * a.TQ;
+    return Item{r.a + t0, min(2 * a.TQ, r.b - r.a - t0), h, s, kt0, kt1, nkt, min(r.kv, a.p.width * a.p.page),
+                r.base() + t0 + 1};
+  }
 
  private:
   bool first;
-  __device__ __forceinline__ bool past() const { return end.s < 0; }
-  __device__ __forceinline__ void load() {
-    r = seq_rows(a.p, at.s);
-    n = tiles_of(a, r.b - r.a);
-  }
+  int es, ei, eh, ek;  // the run's end
   __device__ __forceinline__ void step() {
-    if (++at.h < a.p.Hkv) return;
-    at.h = 0;
-    if (++at.i < n) return;
-    at.i = 0;
-    for (++at.s; at.s < a.p.S; ++at.s) {
-      load();
+    if (++h < a.p.Hkv) return;
+    h = 0;
+    if (++i < n) return;
+    i = 0;
+    for (++s; s < a.p.S; ++s) {
+      r = seq_rows(a.p, s);
+      n = items_of(a, r.b - r.a);
       if (n > 0) return;
     }
   }
 };
 
-// A lane's page of visit kt: its number, or -1 (not there, or past the sequence's keys).
+// A lane's page of visit kt as the table has it; -1 past the sequence's keys. What it
+// returns is looked at a visit later, so that nobody stands and waits for it.
 __device__ __forceinline__ int page_of(const FwdArgs& a, int s, int kt, int cap, int lane, int per) {
   const int key = kt * kTile + lane * a.p.page;
-  if (lane >= per || key >= cap) return -1;
-  const int id = __ldg(a.p.page_table + (int64_t)s * a.p.width + (key >> a.page_shift));
-  return id >= 0 && id < a.p.pages ? id : -1;
+  int id = -1;
+  if (lane < per && key < cap) id = __ldg(a.p.page_table + (int64_t)s * a.p.width + (key >> a.page_shift));
+  return id;
 }
-// Pages of visit kt within the sequence's keys that are not in the cache, a bit each.
-__device__ __forceinline__ uint32_t missing(const FwdArgs& a, int id, int kt, int cap, int lane, int per) {
-  return __ballot_sync(~0u, lane < per && kt * kTile + lane * a.p.page < cap && id < 0);
-}
+// A producer's lanes: lane l brings chunk l / per of page l % per of a visit.
+struct PageLanes {
+  int per, box, page, chunk, lane;
+  __device__ __forceinline__ PageLanes(const FwdArgs& a, int lane_, int NC) {
+    per = a.p.page >= kTile ? 1 : kTile / a.p.page;
+    box = min(a.p.page, kTile);
+    page = lane_ % per;
+    chunk = lane_ / per;
+    lane = chunk < NC ? page : per;
+  }
+};
 
-// Keys k0 .. k0+31 that a row with `seen` keys does not see, and those of missing
-// pages (bits of 16 keys: the low one for the first 16), out of its scores.
-__device__ __forceinline__ void hide32(uint32_t (&x)[32], int k0, int seen, uint32_t bad) {
-#pragma unroll
-  for (int c = 0; c < 32; ++c)
-    x[c] = (k0 + c < seen && !((c < 16 ? bad : bad >> 1) & 1)) ? x[c] : __float_as_uint(-INFINITY);
+// Bits of the 32 keys from k0 on (of visit kt, its keys k0 + ...) that a row with `seen`
+// keys sees and whose pages are there.
+__device__ __forceinline__ uint32_t seen32(int seen, int k0, int in_visit, uint32_t bad, int page_shift) {
+  const int n = seen - k0;
+  uint32_t m = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+  if (bad) {
+    if ((bad >> (in_visit >> page_shift)) & 1) m &= 0xFFFF0000u;
+    if ((bad >> ((in_visit + 16) >> page_shift)) & 1) m &= 0x0000FFFFu;
+  }
+  return m;
 }
-// The missing pages' bits as bits of 16 keys each.
-__device__ __forceinline__ uint32_t by16(uint32_t bad, int page_shift) {
-  uint32_t r = 0;
-  for (int e = 0; e < 8; ++e) r |= ((bad >> ((e * 16) >> page_shift)) & 1u) << e;
-  return r;
+__device__ __forceinline__ void hide32(uint32_t (&x)[32], uint32_t m) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) x[c] = (m >> c) & 1 ? x[c] : __float_as_uint(-INFINITY);
 }
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
+__device__ __forceinline__ void warp_arrive2(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(bar);
+    mbar_arrive(bar);
+  }
+}
+__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2, int c3) {
-  tma_load_bhnd(dst, m, bar, c0, c1, c2, c3);
+// A softmax thread's running state: the maximum in use and the weights' sums.
+struct Running {
+  float m;
+  uint64_t l2;  // two partial sums
+};
+// Takes the running maximum on for scores whose largest (scaled) is ms; returns what O, if it
+// holds anything, has to be multiplied with where `rescale` comes out true (for the whole warp).
+__device__ __forceinline__ float advance(Running& u, float ms, bool& rescale) {
+  rescale = __any_sync(~0u, ms > u.m + 8.f);
+  float f = 1.f;
+  if (rescale) {
+    const float m_new = fmaxf(u.m, ms);
+    f = u.m == m_new ? 1.f : weight(u.m, m_new);
+    u.l2 = mul2(u.l2, f2(f, f));
+    u.m = m_new;
+  }
+  return f;
+}
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(tO + c0, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+    tmem_st32(tO + c0, v);
+  }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs a) {
+    paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmF,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ FwdArgs a) {
   using L = Layout<D>;
-  constexpr int NSK = L::NSK, NSV = L::NSV, NC = L::NC;
+  constexpr int NS = L::NS, NC = L::NC;
   static_assert(sizeof(Misc) <= L::MISC, "misc region");
   static_assert(L::SMEM <= 232448, "shared memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -293,36 +377,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + sizeof(Misc) + 1023) & ~uintptr_t(1023));
   uint8_t *bK = base + L::OFF_K, *bV = base + L::OFF_V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t* status = reinterpret_cast<uint32_t*>(a.ws);
-  const Guard g{&m.abort_flag, status};
+  const Guard g{&m.abort_flag, reinterpret_cast<uint32_t*>(a.ws)};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  SeqRows mine{0, 0, 0};
+  if ((int)threadIdx.x < a.p.S) mine = seq_rows(a.p, threadIdx.x);
 
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) *status = 0;
+    if (blockIdx.x == 0) *g.status = 0;
     m.abort_flag = 0;
-    mbar_init(&m.q_full, 1);
-    mbar_init(&m.q_free, 1);
-    for (int s = 0; s < NSK; ++s) {
+#pragma unroll 1
+    for (int s = 0; s < NS; ++s) {
       mbar_init(&m.k_full[s], 1);
       mbar_init(&m.k_empty[s], 1);
-    }
-    for (int s = 0; s < NSV; ++s) {
       mbar_init(&m.v_full[s], 1);
       mbar_init(&m.v_empty[s], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&m.s_full[s], 1);
-      mbar_init(&m.s_free[s], 4);  // the four warps of the group that owns the visit
-      mbar_init(&m.p_full[s], 4);
+      mbar_init(&m.q_full[s], 1);
+      mbar_init(&m.q_free[s], 1);
+      mbar_init(&m.s_full[s], 2);  // the S issuer itself, and its products
+      mbar_init(&m.p_full[s], 4);  // the four warps of the stream's group
       mbar_init(&m.pv_done[s], 1);
-      for (int q = 0; q < 4; ++q) mbar_init(&m.mh_full[s][q], 1);
+      mbar_init(&m.o_free[s], 8);  // both groups' warps, or those of one group twice
+      mbar_init(&m.sums[s], 4);
+      mbar_init(&m.group[s], 4);
+      m.ends[s] = Bound{a.p.S, 0, 0, 0, 0, SeqRows{0, 0, 0}};
     }
-    mbar_init(&m.sums_full, 8);
-    mbar_init(&m.o_free, 8);
+#pragma unroll 1
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(&m.item_full[s], 1);
+      mbar_init(&m.item_free[s], kThreads / 32 - 1);
+    }
     mbar_init(&m.fin_s, 1);
     mbar_init(&m.fin_pv, 1);
     fence_mbar_init();
-    m.ends[0] = m.ends[1] = Bound{a.p.S, 0, 0, 0, 0};
+  }
+  if (threadIdx.x == 32) {
+    prefetch_tmap(&tmF);
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
   }
   if (warp == 2) {
     tmem_alloc(&m.tmem_base, L::TMEM_COLS);
@@ -332,112 +427,172 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
-  find_ends(a, m);
+  find_ends(a, m, mine);
 
-  const int per = a.p.page >= kTile ? 1 : kTile / a.p.page;  // pages of a visit
-  const int box = min(a.p.page, kTile);                      // and the rows of one
-  Walk w(a, m);
+  // All roles count alike: ic the items, vc the visits (K and V stages; an item of one tile gives
+  // visit vc to stream vc & 1), n[g] those of stream g, qt the Q buffer of the next item of one tile.
+  int ic = 0, vc = 0;
+  bool ok = true;
+  const auto next_item = [&](Item& it) {
+    const int slot = ic % kItems;
+    ok = g.wait_warp(&m.item_full[slot], (ic / kItems) & 1, 18);
+    if (!ok) return false;
+    it = m.items[slot];
+    warp_arrive(&m.item_free[slot], lane);
+    ++ic;
+    return it.nt > 0;
+  };
+  const auto is_pair = [&](const Item& it) { return it.nt > a.TQ; };
+  const auto is_few = [&](const Item& it) { return it.nt * a.p.G <= kFew; };
   if (warp == 0) {
     // ------------------------------------------------------ Q and K producer
     if (lane == 0) {  // what the second kernel has to know
-      const Bound b = m.ends[0], e = m.ends[1];
+      const Bound &b = m.ends[0], &e = m.ends[1];
       const bool same = b.s == e.s && b.i == e.i && b.h == e.h;
-      const bool inside = b.kt > 0 && b.kt < b.nkt;
       int4 rec = make_int4(-1, 0, 0, kWhole);
-      if (inside) rec.w = !same ? kEnds : e.kt == b.kt ? kEmpty : e.kt == e.nkt ? kEnds : kGoesOn;
+      if (b.kt > 0 && b.kt < b.nkt) rec.w = !same ? kEnds : e.kt == b.kt ? kEmpty : e.kt == e.nkt ? kEnds : kGoesOn;
       if (e.kt > 0 && e.kt < e.nkt && !(same && b.kt > 0)) rec = make_int4(e.s, e.i, e.h, rec.w);
       reinterpret_cast<int4*>(a.ws + kOffRecords)[blockIdx.x] = rec;
-      prefetch_tmap(&tmQ);
-      prefetch_tmap(&tmK);
     }
     __syncwarp();
-    const int pl = lane % per, ch = lane / per;
-    const int mine = ch < NC ? pl : per;  // this lane's page of a visit
-    int vc = 0, items = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      const int cap = w.cap();
-      int id = page_of(a, w.at.s, w.kt0, cap, mine, per);
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++vc) {
-        const int now = id, sk = vc % NSK;
-        if (kt + 1 < w.kt1) id = page_of(a, w.at.s, kt + 1, cap, mine, per);
-        const uint32_t boxes = __popc(__ballot_sync(~0u, now >= 0));
-        if (!g.wait_warp(&m.k_empty[sk], ((vc / NSK) & 1) ^ 1, 1)) { ok = false; break; }
-        if (lane == 0) mbar_expect_tx(&m.k_full[sk], boxes * box * 128);
-        __syncwarp();
-        if (now >= 0)
-          tma_load_4d(bK + sk * L::TB + ch * L::CHUNK + pl * box * 128, &tmK, &m.k_full[sk], ch * 64,
-                      (kt * kTile) & (a.p.page - 1) & ~(kTile - 1), w.at.h, now);
-        if (kt == w.kt0) {  // Q once the last item's S products have read theirs
-          if (items > 0 && !g.wait_warp(&m.q_free, (items - 1) & 1, 2)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_expect_tx(&m.q_full, NC * a.TQ * a.p.G * 128);
-            for (int c = 0; c < NC; ++c)
-              tma_load_4d(base + c * L::CHUNK, &tmQ, &m.q_full, c * 64, 0, w.row0(), w.at.h);
+    const PageLanes pl(a, lane, NC);
+    Walk w(a, m);
+    int used[2] = {0, 0}, qt = 0;  // uses of the Q buffers
+    for (bool more = true; ok && more;) {
+      more = w.next();
+      Item it = more ? w.item() : Item{};
+      const int slot = ic % kItems;
+      if (ic >= kItems && !(ok = g.wait_warp(&m.item_free[slot], (ic / kItems - 1) & 1, 19))) break;
+      if (lane == 0) {
+        m.items[slot] = it;
+        mbar_arrive(&m.item_full[slot]);
+      }
+      __syncwarp();
+      ++ic;
+      if (!more) break;
+      const bool pair = is_pair(it), few = is_few(it);
+      int id = page_of(a, it.s, it.kt0, it.cap, pl.lane, pl.per);
+      // Q goes ahead of the item's first K where two buffers take turns, and behind it where
+      // both wait for the last item's products.
+      const int visits = it.kt1 - it.kt0, q_at = pair ? 1 : 0;
+#pragma unroll 1
+      for (int v = 0; ok && v < max(visits, q_at + 1); ++v) {
+        if (v == q_at) {
+#pragma unroll 1
+          for (int t = 0; ok && t <= q_at; ++t) {
+            const int b = pair ? t : qt;
+            if (used[b] > 0 && !(ok = g.wait_warp(&m.q_free[b], (used[b] - 1) & 1, 2))) break;
+            if (lane == 0) mbar_expect_tx(&m.q_full[b], NC * a.p.G * 128 * (few ? 4 * a.TQf : a.TQ));
+            __syncwarp();
+            const int c = lane >> 2, q = lane & 3;  // a lane a box
+            if (c < NC && (few || q == 0))
+              tma_load_bhnd(base + b * L::TB + c * L::CHUNK + q * kFew * 128, few ? &tmF : &tmQ, &m.q_full[b], c * 64, 0,
+                            it.row0 + t * a.TQ, it.h);
+            ++used[b];
           }
-          __syncwarp();
-          ++items;
+          if (!pair) qt ^= 1;
+          if (!ok) break;
         }
+        if (v >= visits) break;
+        const int kt = it.kt0 + v, now = id, sk = vc % NS;
+        if (v + 1 < visits) id = page_of(a, it.s, kt + 1, it.cap, pl.lane, pl.per);
+        const bool there = (uint32_t)now < (uint32_t)a.p.pages;
+        const uint32_t boxes = __ballot_sync(~0u, there);
+        const uint32_t bad = __ballot_sync(~0u, lane < pl.per && kt * kTile + lane * a.p.page < it.cap && !there);
+        if (!(ok = g.wait_warp(&m.k_empty[sk], ((vc / NS) & 1) ^ 1, 1))) break;
+        if (lane == 0) {
+          m.k_bad[sk] = bad;
+          mbar_expect_tx(&m.k_full[sk], __popc(boxes) * pl.box * 128);
+        }
+        __syncwarp();
+        if (there)
+          tma_load_bhnd(bK + sk * L::TB + pl.chunk * L::CHUNK + pl.page * pl.box * 128, &tmK, &m.k_full[sk], pl.chunk * 64,
+                        (kt * kTile) & (a.p.page - 1) & ~(kTile - 1), it.h, now);
+        ++vc;
       }
     }
     if (lane == 0) {  // no copy may still be landing when the CTA exits
-      if (items > 0) g.drain(&m.q_full, (items - 1) & 1);
-      for (int i = (vc > NSK ? vc - NSK : 0); i < vc; ++i) g.drain(&m.k_full[i % NSK], (i / NSK) & 1);
+      for (int b = 0; b < 2; ++b)
+        if (used[b] > 0) g.drain(&m.q_full[b], (used[b] - 1) & 1);
+      for (int i = (vc > NS ? vc - NS : 0); i < vc; ++i) g.drain(&m.k_full[i % NS], (i / NS) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ V producer
-    if (lane == 0) prefetch_tmap(&tmV);
-    const int pl = lane % per, ch = lane / per;
-    const int mine = ch < NC ? pl : per;
-    int vc = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      const int cap = w.cap();
-      int id = page_of(a, w.at.s, w.kt0, cap, mine, per);
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++vc) {
-        const int now = id, sv = vc % NSV;
-        if (kt + 1 < w.kt1) id = page_of(a, w.at.s, kt + 1, cap, mine, per);
-        const uint32_t boxes = __popc(__ballot_sync(~0u, now >= 0));
-        if (!g.wait_warp(&m.v_empty[sv], ((vc / NSV) & 1) ^ 1, 3)) { ok = false; break; }
-        if (lane == 0) mbar_expect_tx(&m.v_full[sv], boxes * box * 128);
+    const PageLanes pl(a, lane, NC);
+    Item it;
+    while (ok && next_item(it)) {
+      int id = page_of(a, it.s, it.kt0, it.cap, pl.lane, pl.per);
+      for (int kt = it.kt0; kt < it.kt1; ++kt, ++vc) {
+        const int now = id, sv = vc % NS;
+        if (kt + 1 < it.kt1) id = page_of(a, it.s, kt + 1, it.cap, pl.lane, pl.per);
+        const bool there = (uint32_t)now < (uint32_t)a.p.pages;
+        const uint32_t boxes = __ballot_sync(~0u, there);
+        const uint32_t bad = __ballot_sync(~0u, lane < pl.per && kt * kTile + lane * a.p.page < it.cap && !there);
+        if (!(ok = g.wait_warp(&m.v_empty[sv], ((vc / NS) & 1) ^ 1, 3))) break;
+        if (lane == 0) {
+          m.v_bad[sv] = bad;
+          mbar_expect_tx(&m.v_full[sv], __popc(boxes) * pl.box * 128);
+        }
         __syncwarp();
-        if (now >= 0)
-          tma_load_4d(bV + sv * L::TB + ch * L::CHUNK + pl * box * 128, &tmV, &m.v_full[sv], ch * 64,
-                      (kt * kTile) & (a.p.page - 1) & ~(kTile - 1), w.at.h, now);
+        if (there)
+          tma_load_bhnd(bV + sv * L::TB + pl.chunk * L::CHUNK + pl.page * pl.box * 128, &tmV, &m.v_full[sv], pl.chunk * 64,
+                        (kt * kTile) & (a.p.page - 1) & ~(kTile - 1), it.h, now);
       }
     }
     if (lane == 0)
-      for (int i = (vc > NSV ? vc - NSV : 0); i < vc; ++i) g.drain(&m.v_full[i % NSV], (i / NSV) & 1);
+      for (int i = (vc > NS ? vc - NS : 0); i < vc; ++i) g.drain(&m.v_full[i % NS], (i / NS) & 1);
     __syncwarp();
   } else if (warp == 2) {
     // -------------------------------------------------------------- S issuer
     const bool leader = lane == 0;
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
     const uint64_t qd = sdesc_sw128(smem_u32(base), 16, 1024);
-    int vc = 0, items = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      if (!g.wait_warp(&m.q_full, items & 1, 4)) { ok = false; break; }
-      ++items;
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++vc) {
-        const int sb = vc & 1, sk = vc % NSK;
-        if (vc >= 2 && !g.wait_warp(&m.s_free[sb], ((vc - 2) >> 1) & 1, 5)) { ok = false; break; }
-        if (!g.wait_warp(&m.k_full[sk], (vc / NSK) & 1, 6)) { ok = false; break; }
-        tc_fence_after();
+    int n[2] = {0, 0}, used[2] = {0, 0}, qt = 0;
+    Item it;
+    while (ok && next_item(it)) {
+      const bool pair = is_pair(it);
+      for (int t = 0; ok && t < (pair ? 2 : 1); ++t) {
+        const int b = pair ? t : qt;
+        ok = g.wait_warp(&m.q_full[b], used[b] & 1, 4);
+        ++used[b];
+      }
+      for (int kt = it.kt0; ok && kt < it.kt1; ++kt, ++vc) {
+        const int sk = vc % NS;
+        if (!(ok = g.wait_warp(&m.k_full[sk], (vc / NS) & 1, 6))) break;
+        const uint32_t bad = m.k_bad[sk];
         const uint64_t kd = sdesc_sw128(smem_u32(bK + sk * L::TB), 16, 1024);
+        const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
+#pragma unroll 1
+        for (int gs = lo; gs <= hi; ++gs) {
+          // the stream's last P, which lies over its S, has been read
+          if (n[gs] > 0 && !(ok = g.wait_warp(&m.pv_done[gs], (n[gs] - 1) & 1, 5))) break;
+          ++n[gs];
+          tc_fence_after();
+          if (leader) {
+            const uint64_t qb = sdesc_add(qd, (pair ? gs : qt) * L::TB);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = (kk >> 2) * L::CHUNK + (kk & 3) * 32;
-          if (leader) umma_bf16(tmem + L::TM_S + sb * 128, sdesc_add(qd, ko), sdesc_add(kd, ko), idS, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t ko = (kk >> 2) * L::CHUNK + (kk & 3) * 32;
+              umma_bf16(tmem + L::TM_S + gs * 128, sdesc_add(qb, ko), sdesc_add(kd, ko), idS, kk > 0 ? 1u : 0u);
+            }
+            m.s_bad[gs] = bad;
+            mbar_arrive(&m.s_full[gs]);
+            umma_commit(&m.s_full[gs]);
+          }
+          __syncwarp();
         }
+        if (!ok) break;
         if (leader) {
-          umma_commit(&m.s_full[sb]);
           umma_commit(&m.k_empty[sk]);
-          if (kt + 1 == w.kt1) umma_commit(&m.q_free);
+          if (kt + 1 == it.kt1) {
+            if (pair || qt == 0) umma_commit(&m.q_free[0]);
+            if (pair || qt == 1) umma_commit(&m.q_free[1]);
+          }
         }
         __syncwarp();
       }
+      if (!pair) qt ^= 1;
     }
     if (leader) {
       umma_commit(&m.fin_s);
@@ -448,19 +603,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- PV issuer
     const bool leader = lane == 0;
     constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
-    int vc = 0, items = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      const int cap = w.cap();
-      int id = page_of(a, w.at.s, w.kt0, cap, lane, per);
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++vc) {
-        const int now = id, sb = vc & 1, sv = vc % NSV;
-        if (kt + 1 < w.kt1) id = page_of(a, w.at.s, kt + 1, cap, lane, per);
-        const uint32_t bad = missing(a, now, kt, cap, lane, per);
-        if (!g.wait_warp(&m.v_full[sv], (vc / NSV) & 1, 7)) { ok = false; break; }
-        const int there = cap - kt * kTile;  // rows of this visit that hold keys
+    int n[2] = {0, 0}, uses[2] = {0, 0};  // visits of the streams, and items that their O has held
+    Item it;
+    while (ok && next_item(it)) {
+      const bool pair = is_pair(it);
+      bool fresh[2] = {true, true};
+      for (int kt = it.kt0; kt < it.kt1; ++kt, ++vc) {
+        const int sv = vc % NS;
+        if (!(ok = g.wait_warp(&m.v_full[sv], (vc / NS) & 1, 7))) break;
+        const uint32_t bad = m.v_bad[sv];
+        const int there = it.cap - kt * kTile;  // rows of this visit that hold keys
         if (bad || there < kTile) {
           // zeros where there are none: eight lanes a row of 128 bytes
+#pragma unroll 1
           for (int r = lane >> 3; r < kTile; r += 4)
             if (r >= there || (bad >> (r >> a.page_shift)) & 1)
               for (int c = 0; c < NC; ++c)
@@ -468,22 +623,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
         }
-        if (kt == w.kt0) {  // O is free once the last item's has been read
-          if (items > 0 && !g.wait_warp(&m.o_free, (items - 1) & 1, 8)) { ok = false; break; }
-          ++items;
-        }
-        if (!g.wait_warp(&m.p_full[sb], (vc >> 1) & 1, 9)) { ok = false; break; }
-        tc_fence_after();
         const uint64_t vd = sdesc_sw128(smem_u32(bV + sv * L::TB), L::CHUNK, 1024);
+        const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
+#pragma unroll 1
+        for (int gs = lo; gs <= hi; ++gs) {
+          if (fresh[gs]) {  // O is free once its last item's has been read
+            if (uses[gs] > 0 && !(ok = g.wait_warp(&m.o_free[gs], (uses[gs] - 1) & 1, 8))) break;
+            ++uses[gs];
+          }
+          if (!(ok = g.wait_warp(&m.p_full[gs], n[gs] & 1, 9))) break;
+          ++n[gs];
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (leader)
-            umma_bf16_ta(tmem + L::TM_O, tmem + L::TM_P + sb * 64 + kk * 8, sdesc_add(vd, kk * 2048), idO,
-                         (kt > w.kt0 || kk > 0) ? 1u : 0u);
-        if (leader) {
-          umma_commit(&m.pv_done[sb]);
-          umma_commit(&m.v_empty[sv]);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_ta(tmem + L::TM_O + gs * 128, tmem + L::TM_S + gs * 128 + kk * 8, sdesc_add(vd, kk * 2048), idO,
+                           (!fresh[gs] || kk > 0) ? 1u : 0u);
+            umma_commit(&m.pv_done[gs]);
+          }
+          fresh[gs] = false;
+          __syncwarp();
         }
+        if (!ok) break;
+        if (leader) umma_commit(&m.v_empty[sv]);
         __syncwarp();
       }
     }
@@ -496,170 +658,233 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------- softmax
     const int grp = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const int tok = r / a.p.G, gh = r - tok * a.p.G;
-    const int warp_tok = (quarter * 32) / a.p.G;  // the token of the warp's first row
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tO = tmem + lane_base + L::TM_O;
+    const uint32_t tO = tmem + lane_base + L::TM_O, tS = tmem + lane_base + L::TM_S + grp * 128;
     const float sl2 = a.p.scale_log2;
-    int vc = 0, items = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      const int cap = w.cap(), first_seen = min(w.first_seen(), cap), nt = w.tokens();
-      const int seen = min(w.first_seen() + tok, cap);
-      const bool active = warp_tok < nt;  // some row of this warp is a token's
-      float m_w = -INFINITY;              // the maximum this group's sums are taken against
-      uint64_t l2 = 0ull, lr2 = 0ull;     // exact and bf16-rounded weight sums
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++vc) {
-        if ((vc & 1) != grp) continue;
-        const int id = page_of(a, w.at.s, kt, cap, lane, per);
-        ok = g.wait_warp(&m.s_full[grp], (vc >> 1) & 1, 10);
-        if (!ok) break;
+    const uint64_t sc = f2(sl2, sl2);
+    int nv = 0, gp = 0, ex[2] = {0, 0};  // visits of this stream, phases of its group's barrier, uses of the streams' statistics
+    Item it;
+    while (ok && next_item(it)) {
+      const bool pair = is_pair(it), few = is_few(it);
+      const int t0 = pair ? grp * a.TQ : 0;  // this stream's first token of the item
+      const int rl = few ? lane : r, tok = t0 + rl / a.p.G;
+      const int first_seen = min(it.seen0 + t0, it.cap);  // keys that the first one sees
+      const int seen = min(it.seen0 + tok, it.cap);
+      const bool active = few || t0 + quarter * 32 / a.p.G < it.nt;  // some row of this warp is a token's
+      const int visits = it.kt1 - it.kt0, step = pair ? 1 : 2;
+      Running u{-INFINITY, 0ull};
+      int kt = it.kt0 + (pair || (vc & 1) == grp ? 0 : 1);
+      vc += visits;
+      const bool part = kt < it.kt1;  // this stream has visits of the item
+      bool any = false;
+      for (; kt < it.kt1; kt += step, ++nv) {
+        if (!(ok = g.wait_warp(&m.s_full[grp], nv & 1, 10))) break;
         if (!active) {  // in step with the others, nothing to do
-          warp_arrive(&m.s_free[grp], lane);
-          warp_arrive(&m.mh_full[grp][quarter], lane);
-          if (vc >= 2 && !(ok = g.wait_warp(&m.pv_done[grp], ((vc - 2) >> 1) & 1, 11))) break;
           warp_arrive(&m.p_full[grp], lane);
           continue;
         }
         tc_fence_after();
-        uint32_t x0[32], x1[32], x2[32], x3[32];
-        tmem_ld128(tmem + lane_base + L::TM_S + grp * 128, x0, x1, x2, x3);
-        tc_fence_before();
-        warp_arrive(&m.s_free[grp], lane);
-        const uint32_t bad = missing(a, id, kt, cap, lane, per);
+        const uint32_t bad = m.s_bad[grp];
         const bool masked = bad || (kt + 1) * kTile > first_seen;
-        if (masked) {
-          const uint32_t b16 = by16(bad, a.page_shift);
-          const int k0 = kt * kTile;
-          hide32(x0, k0, seen, b16);
-          hide32(x1, k0 + 32, seen, b16 >> 2);
-          hide32(x2, k0 + 64, seen, b16 >> 4);
-          hide32(x3, k0 + 96, seen, b16 >> 6);
-        }
-        const float ms = fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2;
-        float m_prev = -INFINITY;
-        if (kt > w.kt0) {  // the maximum in use after the previous visit, from the other group
-          ok = g.wait_warp(&m.mh_full[grp ^ 1][quarter], ((vc - 1) >> 1) & 1, 12);
-          if (!ok) break;
-          m_prev = m.mh[grp ^ 1][r];
-        }
-        const bool rescale = __any_sync(~0u, ms > m_prev + 8.f);
-        const float m_new = rescale ? fmaxf(m_prev, ms) : m_prev;
-        m.mh[grp][r] = m_new;
-        warp_arrive(&m.mh_full[grp][quarter], lane);
-        if (m_w != m_new) {
-          const float f = (m_w == -INFINITY) ? 0.f : ex2(m_w - m_new);
-          l2 = mul2(l2, f2(f, f));
-          lr2 = mul2(lr2, f2(f, f));
-          m_w = m_new;
-        }
-        const float moff = (m_new == -INFINITY) ? 0.f : m_new;
-        const uint64_t sc = f2(sl2, sl2), off = f2(-moff, -moff);
-        const uint32_t tP = tmem + lane_base + L::TM_P + grp * 64;
-        if (vc >= 2) {
-          ok = g.wait_warp(&m.pv_done[grp], ((vc - 2) >> 1) & 1, 13);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        uint64_t t2 = 0ull, tr2 = 0ull;
-        // O's normaliser takes the rounded weights where a row may have few keys, see fwd.cu
-        if (masked) {
-          exp_store32<true>(x0, sc, off, tP, t2, tr2);
-          exp_store32<true>(x1, sc, off, tP + 16, t2, tr2);
-          exp_store32<true>(x2, sc, off, tP + 32, t2, tr2);
-          exp_store32<true>(x3, sc, off, tP + 48, t2, tr2);
-        } else {
-          exp_store32<false>(x0, sc, off, tP, t2, tr2);
-          exp_store32<false>(x1, sc, off, tP + 16, t2, tr2);
-          exp_store32<false>(x2, sc, off, tP + 32, t2, tr2);
-          exp_store32<false>(x3, sc, off, tP + 48, t2, tr2);
-          tr2 = t2;
-        }
-        l2 = add2(l2, t2);
-        lr2 = add2(lr2, tr2);
-        if (rescale && kt > w.kt0) {  // O holds earlier visits: rescale it once their PV is done
-          const float alpha = (m_prev == -INFINITY) ? 0.f : ex2(m_prev - m_new);
-          ok = g.wait_warp(&m.pv_done[grp ^ 1], ((vc - 1) >> 1) & 1, 14);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(tO + c0, v);
+        const int k0 = kt * kTile;
+        bool rescale;
+        uint64_t t2 = 0ull, none = 0ull;
+        float f;
+        if (few) {
+          uint32_t x[32];
+          tmem_ld32(tS + quarter * 32, x);
+          if (masked) hide32(x, seen32(seen, k0 + quarter * 32, quarter * 32, bad, a.page_shift));
+          f = advance(u, max32(x) * sl2, rescale);
+          const float moff = (u.m == -INFINITY) ? 0.f : u.m;
+          exp_store32<false>(x, sc, f2(-moff, -moff), tS + quarter * 16, t2, none);
+          const uint32_t zero[16] = {};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st32(tO + c0, v);
+          for (int q = 1; q < 4; ++q) tmem_st16_nowait(tS + ((quarter + q) & 3) * 16, zero);
+        } else {
+          uint32_t x0[32], x1[32], x2[32], x3[32];
+          tmem_ld128(tS, x0, x1, x2, x3);
+          if (masked) {
+            hide32(x0, seen32(seen, k0, 0, bad, a.page_shift));
+            hide32(x1, seen32(seen, k0 + 32, 32, bad, a.page_shift));
+            hide32(x2, seen32(seen, k0 + 64, 64, bad, a.page_shift));
+            hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
           }
+          f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, rescale);
+          const float moff = (u.m == -INFINITY) ? 0.f : u.m;
+          const uint64_t off = f2(-moff, -moff);
+          exp_store32<false>(x0, sc, off, tS, t2, none);
+          exp_store32<false>(x1, sc, off, tS + 16, t2, none);
+          exp_store32<false>(x2, sc, off, tS + 32, t2, none);
+          exp_store32<false>(x3, sc, off, tS + 48, t2, none);
         }
+        u.l2 = add2(u.l2, t2);
+        // the stream's last product has ended (its S was formed after it), so O stands still
+        if (rescale && any) scale_o<D>(tO + grp * 128, f);
+        any = true;
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&m.p_full[grp], lane);
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      // The final maximum is the one the last visit's group handed on; both groups take
-      // their sums to it, add them up and write half of O each.
-      const int last = vc - 1, ip = items & 1;
-      ok = g.wait_warp(&m.mh_full[last & 1][quarter], (last >> 1) & 1, 15);
-      if (!ok) break;
-      const float m_fin = active ? m.mh[last & 1][r] : -INFINITY;
-      const float f = (m_w == m_fin) ? 1.f : (m_w == -INFINITY ? 0.f : ex2(m_w - m_fin));
-      const float2 lp = f2_split(l2), lrp = f2_split(lr2);
-      m.sums[ip][grp][0][r] = (lp.x + lp.y) * f;
-      m.sums[ip][grp][1][r] = (lrp.x + lrp.y) * f;
-      warp_arrive(&m.sums_full, lane);
-      ok = g.wait_warp(&m.sums_full, items & 1, 16) && g.wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, 17);
-      if (!ok) break;
-      ++items;
+      if (!part) {  // the other stream's item alone
+        ++ex[grp ^ 1];
+        continue;
+      }
+      if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 11))) break;
       tc_fence_after();
-      // both groups add the two groups' sums in the same order
-      const float lt = m.sums[ip][0][0][r] + m.sums[ip][1][0][r], lrt = m.sums[ip][0][1][r] + m.sums[ip][1][1][r];
-      const bool whole = w.kt0 == 0 && w.kt1 == w.nkt();
-      const bool mine = tok < nt;
-      const int c_lo = grp * (L::DL / 2), c_hi = min(c_lo + L::DL / 2, D);
-      if (active) {
-        const float inv = lrt > 0.f ? 1.f / lrt : 0.f;
-        const int64_t row = w.row0() + tok;
-        const int head = w.at.h * a.p.G + gh;
-        __nv_bfloat16* po = a.out + row * a.p.o_t + (int64_t)head * a.p.o_h;
-        uint8_t* slot = a.ws + kOffPartials + ((size_t)blockIdx.x * 2 + (w.kt0 == 0 ? 1 : 0)) * partial_bytes(D);
-        float4* part = reinterpret_cast<float4*>(slot + sizeof(Partial));
+      const float2 lp = f2_split(u.l2);
+      float M = u.m, lt = lp.x + lp.y, f[2] = {1.f, 1.f};
+      const bool halves = !pair && visits > 1;  // two streams' O to be joined, half of the columns each
+      const bool whole = it.kt1 - it.kt0 == it.nkt;
+      if (!pair) {
+        // what the rows' other parts have to know: of the other stream, and of a few rows' warps
+        m.stat[grp][0][r] = M;
+        m.stat[grp][1][r] = lt;
+        tc_fence_before();
+        warp_arrive(&m.sums[grp], lane);
+        if (!(ok = g.wait_warp(&m.sums[grp], ex[grp] & 1, 12))) break;
+        ++ex[grp];
+        if (halves) {
+          if (!(ok = g.wait_warp(&m.sums[grp ^ 1], ex[grp ^ 1] & 1, 13))) break;
+          ++ex[grp ^ 1];
+        }
+        tc_fence_after();
+        M = -INFINITY, lt = 0.f;
+        const int at0 = few ? lane : r, parts = few ? 4 : 1;
+#pragma unroll 1
+        for (int k = 0; k < 2 * parts; ++k)
+          if (halves || (k & 1) == grp) M = fmaxf(M, m.stat[k & 1][0][at0 + (k >> 1) * 32]);
+#pragma unroll 1
+        for (int k = 0; k < 2 * parts; ++k)
+          if (halves || (k & 1) == grp)
+            lt = fmaf(m.stat[k & 1][1][at0 + (k >> 1) * 32], weight(m.stat[k & 1][0][at0 + (k >> 1) * 32], M), lt);
+        f[0] = weight(m.stat[0][0][r], M);
+        f[1] = weight(m.stat[1][0][r], M);
+      }
+      const float fo = whole ? (lt > 0.f ? 1.f / lt : 0.f) : 1.f;
+      const float fa = (halves ? f[0] : grp ? f[1] : f[0]) * fo, fb = f[1] * fo;
+      const int c_lo = halves ? grp * (L::DL / 2) : 0, c_hi = halves ? min(c_lo + L::DL / 2, D) : D;
+      const uint32_t tA = tO + (halves ? 0 : grp * 128), tB = tO + 128;
+      const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
+      const bool mine_row = row < rows && rl < a.TQ * a.p.G;
+      const int64_t t = it.row0 + tok;
+      const int head = it.h * a.p.G + row % a.p.G;
+      uint8_t* slot = a.ws + kOffPartials + ((size_t)blockIdx.x * 2 + (it.kt0 == 0 ? 1 : 0)) * partial_bytes(D);
+      float4* po = reinterpret_cast<float4*>(slot + sizeof(Partial));
+      if (mine_row && c_lo == 0 && (!few || quarter == 0)) {
+        if (whole) {
+          a.lse[t * a.p.Hq + head] = M * 0.6931471805599453f + logf(lt);
+        } else {
+          Partial& pt = *reinterpret_cast<Partial*>(slot);
+          pt.m[row] = M;
+          pt.l[row] = lt;
+        }
+      }
+      unsigned long long dst = reinterpret_cast<unsigned long long>(a.out + t * a.p.o_t + (int64_t)head * a.p.o_h);
+      if (few) {
+        // the four parts of a row meet in shared memory, cs columns at a time
+        const int cs = rows > 16 ? 16 : rows > 8 ? 32 : 64, ld = cs + 4;
+        float* st = reinterpret_cast<float*>(base + L::OFF_STAGE + grp * 4 * kStage);
+        constexpr int part_ld = kStage / 4;
+#pragma unroll 1
+        for (int c0 = c_lo; ok && c0 < c_hi; c0 += cs) {
+          const int width = min(cs, c_hi - c0);
+#pragma unroll 1
+          for (int c = 0; c < width; c += 16) {
+            uint32_t v[16], v2[16];
+            tmem_ld16(tA + c0 + c, v);
+            if (halves) {
+              tmem_ld16(tB + c0 + c, v2);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v2[e]), fb, __uint_as_float(v[e]) * fa));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fa);
+            }
+            if (lane < rows) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                st_shared_v4(smem_u32(st + quarter * part_ld + lane * ld + c + e), v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+            __syncwarp();
+          }
+          warp_arrive(&m.group[grp], lane);
+          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 14))) break;
+          ++gp;
+          const int q4 = width / 4;
+#pragma unroll 1
+          for (int e = threadIdx.x & 127; e < rows * q4; e += 128) {
+            const int rr = e / q4, c = (e - rr * q4) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 z = *reinterpret_cast<const float4*>(st + q * part_ld + rr * ld + c);
+              y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            if (whole) {
+              const int tk = rr / a.p.G;
+              __nv_bfloat16* o = a.out + (it.row0 + tk) * a.p.o_t + (int64_t)(it.h * a.p.G + rr - tk * a.p.G) * a.p.o_h + c0 + c;
+              *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            } else {
+              po[(size_t)((c0 + c) / 4) * 256 + rr] = y;
+            }
+          }
+          warp_arrive(&m.group[grp], lane);
+          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 15))) break;
+          ++gp;
+        }
+        if (!ok) break;
+      } else if (active) {
+        uint8_t* stage = base + L::OFF_STAGE + (warp - 4) * kStage;
 #pragma unroll 1
         for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
           uint32_t v[32];
-          tmem_ld32(tO + c0, v);
-          if (mine && whole) {
+          tmem_ld32(tA + c0, v);
+          if (halves) {
+            uint32_t v2[32];
+            tmem_ld32(tB + c0, v2);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v2[e]), fb, __uint_as_float(v[e]) * fa));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fa);
+          }
+          if (whole) {
+            // through shared memory, so that four lanes write 64 neighbouring bytes of a row
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              st_shared_v4(smem_u32(stage + lane * 80 + q * 16),
+                           pack_bf16x2(__uint_as_float(v[q * 8 + 0]), __uint_as_float(v[q * 8 + 1])),
+                           pack_bf16x2(__uint_as_float(v[q * 8 + 2]), __uint_as_float(v[q * 8 + 3])),
+                           pack_bf16x2(__uint_as_float(v[q * 8 + 4]), __uint_as_float(v[q * 8 + 5])),
+                           pack_bf16x2(__uint_as_float(v[q * 8 + 6]), __uint_as_float(v[q * 8 + 7])));
+            __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint4 y;
-              y.x = pack_bf16x2(__uint_as_float(v[q * 8 + 0]) * inv, __uint_as_float(v[q * 8 + 1]) * inv);
-              y.y = pack_bf16x2(__uint_as_float(v[q * 8 + 2]) * inv, __uint_as_float(v[q * 8 + 3]) * inv);
-              y.z = pack_bf16x2(__uint_as_float(v[q * 8 + 4]) * inv, __uint_as_float(v[q * 8 + 5]) * inv);
-              y.w = pack_bf16x2(__uint_as_float(v[q * 8 + 6]) * inv, __uint_as_float(v[q * 8 + 7]) * inv);
-              *reinterpret_cast<uint4*>(po + c0 + q * 8) = y;
+              const int from = q * 8 + (lane >> 2);
+              const uint4 y = *reinterpret_cast<const uint4*>(stage + from * 80 + (lane & 3) * 16);
+              const unsigned long long to = __shfl_sync(~0u, dst, from);
+              if (__shfl_sync(~0u, (int)mine_row, from))
+                *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(to) + c0 + (lane & 3) * 8) = y;
             }
-          } else if (mine) {
+          } else if (mine_row) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              part[(size_t)(c0 / 4 + q) * 128 + r] =
+              po[(size_t)(c0 / 4 + q) * 256 + row] =
                   make_float4(__uint_as_float(v[q * 4]), __uint_as_float(v[q * 4 + 1]), __uint_as_float(v[q * 4 + 2]),
                               __uint_as_float(v[q * 4 + 3]));
           }
           __syncwarp();
         }
-        if (mine && grp == 0) {
-          if (whole) {
-            a.lse[row * a.p.Hq + head] = m_fin * 0.6931471805599453f + logf(lt);
-          } else {
-            Partial& pt = *reinterpret_cast<Partial*>(slot);
-            pt.m[r] = m_fin;
-            pt.l[r] = lt;
-            pt.lr[r] = lrt;
-          }
-        }
       }
       tc_fence_before();
-      warp_arrive(&m.o_free, lane);
+      if (halves) {
+        warp_arrive(&m.o_free[0], lane);
+        warp_arrive(&m.o_free[1], lane);
+      } else {
+        warp_arrive2(&m.o_free[grp], lane);
+      }
     }
   }
   tc_fence_before();
@@ -670,22 +895,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the item that CTA blockIdx.x began and did not end.
+// Joins the parts of the item that CTA blockIdx.x began and did not end, 32 of its rows a
+// block: the parts' weights once, then O.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ FwdArgs a) {
-  __shared__ int heads[kCtas];
-  __shared__ int slots[kCtas];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ FwdArgs a) {
+  __shared__ int heads[kCtas], slots[kCtas];
+  __shared__ float wt[kCtas][kJoinRows], sum[kJoinRows], top[kJoinRows];
   __shared__ int count;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4* recs = reinterpret_cast<const int4*>(a.ws + kOffRecords);
   const int4 rec = recs[blockIdx.x];
   if (rec.x < 0) return;
-  const int P = gridDim.x;
-  for (int c = blockIdx.x + 1 + threadIdx.x; c < P; c += 256) heads[c] = recs[c].w;
+  const int P = gridDim.x, tid = threadIdx.x;
+  for (int c = blockIdx.x + 1 + tid; c < P; c += kJoinThreads) heads[c] = recs[c].w;
+  const SeqRows r = seq_rows(a.p, rec.x);
+  const int row0 = r.a + rec.y * 2 * a.TQ, all = min(2 * a.TQ, r.b - row0) * a.p.G;
+  const int first = blockIdx.y * kJoinRows, rows = min(kJoinRows, all - first);
+  if (rows <= 0) return;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     int n = 0;
     slots[n++] = blockIdx.x * 2 + 1;
+#pragma unroll 1
     for (int c = blockIdx.x + 1; c < P; ++c) {
       if (heads[c] != kEmpty) slots[n++] = c * 2;
       if (heads[c] != kGoesOn && heads[c] != kEmpty) break;
@@ -693,32 +925,56 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     count = n;
   }
   __syncthreads();
-  const SeqRows r = seq_rows(a.p, rec.x);
-  const int row0 = r.a + rec.y * a.TQ, nt = min(a.TQ, r.b - row0), rows = nt * a.p.G, n = count;
+  const int n = count;
   const uint8_t* parts = a.ws + kOffPartials;
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * (D / 4); e += gridDim.y * 256) {
-    const int c = e / rows, row = e - c * rows;
-    float M = -INFINITY;
-    for (int k = 0; k < n; ++k) M = fmaxf(M, reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D))->m[row]);
-    float l = 0.f, lr = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
+#pragma unroll 1
+  for (int e = tid; e < n * rows; e += kJoinThreads) {
+    const int k = e / rows, row = e - k * rows;
+    wt[k][row] = reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D))->m[first + row];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int row = tid >> 5; row < rows; row += kJoinThreads / 32) {  // a warp a row
+    const int lane = tid & 31;
+    float M = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, wt[k][row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+#pragma unroll 1
+    for (int k = lane; k < n; k += 32) {
       const Partial& pt = *reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D));
-      const float4 v = reinterpret_cast<const float4*>(&pt + 1)[(size_t)c * 128 + row];
-      const float w = pt.m[row] == -INFINITY ? 0.f : ex2(pt.m[row] - M);
-      l = fmaf(pt.l[row], w, l);
-      lr = fmaf(pt.lr[row], w, lr);
-      o.x = fmaf(v.x, w, o.x);
-      o.y = fmaf(v.y, w, o.y);
-      o.z = fmaf(v.z, w, o.z);
-      o.w = fmaf(v.w, w, o.w);
+      const float x = weight(wt[k][row], M);
+      wt[k][row] = x;
+      l = fmaf(pt.l[first + row], x, l);
     }
-    const float inv = lr > 0.f ? 1.f / lr : 0.f;
-    const int tok = row / a.p.G, head = rec.z * a.p.G + (row - tok * a.p.G);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    if (lane == 0) {
+      sum[row] = l;
+      top[row] = M;
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int e = tid; e < rows * (D / 4); e += kJoinThreads) {
+    const int c = e / rows, row = e - c * rows;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float4 v = reinterpret_cast<const float4*>(parts + slots[k] * partial_bytes(D) + sizeof(Partial))[c * 256 + first + row];
+      const float x = wt[k][row];
+      o.x = fmaf(v.x, x, o.x);
+      o.y = fmaf(v.y, x, o.y);
+      o.z = fmaf(v.z, x, o.z);
+      o.w = fmaf(v.w, x, o.w);
+    }
+    const float l = sum[row], inv = l > 0.f ? 1.f / l : 0.f;
+    const int tok = (first + row) / a.p.G, head = rec.z * a.p.G + (first + row - tok * a.p.G);
     const int64_t at = row0 + tok;
     *reinterpret_cast<uint2*>(a.out + at * a.p.o_t + (int64_t)head * a.p.o_h + c * 4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (c == 0) a.lse[at * a.p.Hq + head] = M * 0.6931471805599453f + logf(l);
+    if (c == 0) a.lse[at * a.p.Hq + head] = top[row] * 0.6931471805599453f + logf(l);
   }
 }
 
@@ -734,24 +990,24 @@ template <int D>
 cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const void* v_pages, cudaStream_t st) {
   using L = Layout<D>;
   const PagedArgs& p = a.p;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tf, tk, tv;
   const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.T, (uint64_t)p.Hkv};
   const int64_t qs[3] = {p.q_h, p.q_t, p.Hkv > 1 ? p.G * p.q_h : D};
-  const uint32_t qbox[2] = {(uint32_t)p.G, (uint32_t)a.TQ};
+  const uint32_t qbox[2] = {(uint32_t)p.G, (uint32_t)a.TQ}, fbox[2] = {(uint32_t)p.G, (uint32_t)a.TQf};
   const uint64_t kd[4] = {(uint64_t)D, (uint64_t)p.page, (uint64_t)p.Hkv, (uint64_t)p.pages};
   const int64_t ks[3] = {p.p_n, p.p_h, p.p_p};
   const uint32_t kbox[2] = {(uint32_t)std::min(p.page, kTile), 1};
-  if (!tmap_bf16_4d_sw128(&tq, q, qd, qs, qbox) || !tmap_bf16_4d_sw128(&tk, k_pages, kd, ks, kbox) ||
-      !tmap_bf16_4d_sw128(&tv, v_pages, kd, ks, kbox))
+  if (!tmap_bf16_4d_sw128(&tq, q, qd, qs, qbox) || !tmap_bf16_4d_sw128(&tf, q, qd, qs, fbox) ||
+      !tmap_bf16_4d_sw128(&tk, k_pages, kd, ks, kbox) || !tmap_bf16_4d_sw128(&tv, v_pages, kd, ks, kbox))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sm_count(), kCtas);
-  paged_kernel<D><<<ctas, kThreads, L::SMEM, st>>>(tq, tk, tv, a);
+  paged_kernel<D><<<ctas, kThreads, L::SMEM, st>>>(tq, tf, tk, tv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, 4);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas, (2 * a.TQ * p.G + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr = programmatic_launch();
   cfg.attrs = &attr;
@@ -768,6 +1024,7 @@ cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pa
   FwdArgs a{};
   a.p = p;
   a.TQ = kTile / p.G;
+  a.TQf = std::max(1, kFew / p.G);
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
