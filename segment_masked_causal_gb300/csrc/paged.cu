@@ -23,16 +23,16 @@
 // the streams in turn, whose sums and O are joined at its end. No stream ever waits for
 // the other's maximum, and O is rescaled, lazily, between a stream's own products.
 //
-// Few rows. A TMEM lane belongs to one warp of four, so where an item has at most 32
+// Few rows. A TMEM lane belongs to one warp of four, so where an item has at most eight
 // rows the tile holds them four times and each of a group's warps takes 32 of a visit's
 // 128 keys (its P has zeros for the others); the four parts of a row are joined
-// at the item's end as well.
+// at the item's end as well. With more rows that join costs more than it saves.
 //
 // The pipeline runs on from item to item: the next item's Q, K and V are loaded while the
 // last one's O is written. Pages arrive by TMA, one box per page and 64 columns, a lane
 // each, the page numbers loaded a visit ahead. Rows past a sequence's tokens and pages
-// that are not there are masked in S; their rows of V are set to zero in shared memory
-// before the product, because 0 * NaN is NaN.
+// that are not there are masked in S, and the second product leaves out the steps of 16
+// keys without any; what is left of the last one's rows of V is set to zero.
 //
 // Warp roles: 0 Q and K producer, 1 V producer, 2 S issuer and TMEM owner, 3 PV
 // issuer, 4..7 and 8..11 the softmax groups of streams 0 and 1.
@@ -57,7 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kItemCost = 256;
 constexpr int kLeastVisits = 2;   // of a part of an item
 constexpr int kLeastCostLog = 9;  // of a CTA, log2
-constexpr int kFew = 32;          // rows of an item that the tile holds four times
+constexpr int kFew = 8;           // rows of an item that the tile holds four times
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
 template <int D>
@@ -96,7 +96,6 @@ struct Misc {
   uint32_t tmem_base;
   int abort_flag;
   Bound ends[2];
-  long long scan[kThreads / 32];
   Item items[kItems];
   uint32_t k_bad[4], v_bad[4], s_bad[2];  // missing pages of the visit in a stage, or in a stream's S
   float stat[2][2][128];                  // [stream][maximum, sum][row]
@@ -182,51 +181,67 @@ __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r
   return b;
 }
 
-// Both ends of this CTA's run, by all threads. mine: the rows of sequence threadIdx.x.
-__device__ __forceinline__ void find_ends(const FwdArgs& a, Misc& m, SeqRows mine) {
-  const int S = a.p.S, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned long long total = 0, x[2] = {0, 0};
-  for (int pass = S <= kThreads ? 1 : 0; pass < 2; ++pass) {  // the sum (at once with the rest where it can), then the places
-    unsigned long long run = 0;
-    for (int s0 = 0; s0 < S; s0 += kThreads) {
-      const int s = s0 + tid;
-      if (s0 > 0 || pass > 0) {
-        if (s < S && S > kThreads) mine = seq_rows(a.p, s);
-      }
-      const unsigned long long cost = s < S ? Costs(a, mine).all() * a.p.Hkv : 0;
-      unsigned long long v = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long u = __shfl_up_sync(~0u, v, o);
-        if (lane >= o) v += u;
-      }
-      if (lane == 31) m.scan[warp] = (long long)v;
-      __syncthreads();
-      unsigned long long before = run;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const unsigned long long u = (unsigned long long)m.scan[w];
-        if (w < warp) before += u;
-        run += u;
-      }
-      v += before;  // inclusive
-      if (S <= kThreads) total = run;
-      if (pass == 1) {
-        if (s0 == 0) {
-          const uint32_t P = (uint32_t)max(1ull, min((unsigned long long)gridDim.x, total >> kLeastCostLog));
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t c = blockIdx.x + e;
-            x[e] = c >= P ? total : __umul64hi(total, (unsigned long long)(c * (0xFFFFFFFFu / P + 1)) << 32);
-          }
-        }
-#pragma unroll 1
-        for (int e = 0; e < 2; ++e)
-          if (x[e] >= v - cost && x[e] < v) m.ends[e] = place(a, s, mine, (long long)(x[e] - (v - cost)));
-      }
-      __syncthreads();
-    }
-    total = run;
+// Both ends of this CTA's run, by one warp: the sum of all costs, then the sequences that the
+// ends lie in, 32 at a time, then the two places, a lane each.
+__device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], int lane) {
+  const int S = a.p.S;
+  const unsigned long long H = a.p.Hkv;
+  unsigned long long total = 0;
+  SeqRows r{0, 0, 0};
+#pragma unroll 2
+  for (int s = lane; s < S; s += 32) {
+    r = seq_rows(a.p, s);
+    total += Costs(a, r).all() * H;
   }
+  const unsigned long long own = total;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  const uint32_t P = (uint32_t)max(1ull, min((unsigned long long)gridDim.x, total >> kLeastCostLog));
+  // x of lanes 0 and 1: where the run starts and ends
+  const uint32_t c = blockIdx.x + (lane & 1);
+  unsigned long long x = c >= P ? total : __umul64hi(total, (unsigned long long)(c * (0xFFFFFFFFu / P + 1)) << 32);
+  const unsigned long long x0 = __shfl_sync(~0u, x, 0), x1 = __shfl_sync(~0u, x, 1);
+  int at = S;             // the sequence of this lane's x
+  SeqRows rows{0, 0, 0};  // and its rows
+  unsigned long long run = 0;
+  uint32_t open = 3;
+#pragma unroll 1
+  for (int s0 = 0; s0 < S && open; s0 += 32) {
+    unsigned long long v = own;
+    if (S > 32) {
+      v = 0;
+      if (s0 + lane < S) {
+        r = seq_rows(a.p, s0 + lane);
+        v = Costs(a, r).all() * H;
+      }
+    }
+    const unsigned long long cost = v;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += u;
+    }
+    v += run;
+    run = __shfl_sync(~0u, v, 31);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const unsigned long long xe = e ? x1 : x0;
+      const uint32_t hit = __ballot_sync(~0u, xe >= v - cost && xe < v);
+      if (hit) {
+        const int from = __ffs(hit) - 1;
+        const SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
+        const unsigned long long before = __shfl_sync(~0u, v - cost, from);
+        if (lane == e) {
+          at = s0 + from;
+          rows = t;
+          x -= before;
+        }
+        open &= ~(1u << e);
+      }
+    }
+  }
+  if (lane < 2) ends[lane] = at < S ? place(a, at, rows, (long long)x) : Bound{S, 0, 0, 0, 0, SeqRows{0, 0, 0}};
+  __syncwarp();
 }
 
 // The parts of items in a CTA's run, in order.
@@ -339,8 +354,9 @@ struct Running {
 };
 // Takes the running maximum on for scores whose largest (scaled) is ms; returns what O, if it
 // holds anything, has to be multiplied with where `rescale` comes out true (for the whole warp).
-__device__ __forceinline__ float advance(Running& u, float ms, bool& rescale) {
-  rescale = __any_sync(~0u, ms > u.m + 8.f);
+// Only `mine` rows have a say: what the others hold may be left over from anything.
+__device__ __forceinline__ float advance(Running& u, float ms, bool mine, bool& rescale) {
+  rescale = __any_sync(~0u, mine && ms > u.m + 8.f);
   float f = 1.f;
   if (rescale) {
     const float m_new = fmaxf(u.m, ms);
@@ -379,11 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Guard g{&m.abort_flag, reinterpret_cast<uint32_t*>(a.ws)};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  SeqRows mine{0, 0, 0};
-  if ((int)threadIdx.x < a.p.S) mine = seq_rows(a.p, threadIdx.x);
-
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) *g.status = 0;
     m.abort_flag = 0;
 #pragma unroll 1
     for (int s = 0; s < NS; ++s) {
@@ -402,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.o_free[s], 8);  // both groups' warps, or those of one group twice
       mbar_init(&m.sums[s], 4);
       mbar_init(&m.group[s], 4);
-      m.ends[s] = Bound{a.p.S, 0, 0, 0, 0, SeqRows{0, 0, 0}};
     }
 #pragma unroll 1
     for (int s = 0; s < kItems; ++s) {
@@ -423,11 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&m.tmem_base, L::TMEM_COLS);
     tmem_relinquish();
   }
+  // Up to here nothing that the kernels ahead write was looked at.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0 && blockIdx.x == 0) *g.status = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
-  find_ends(a, m, mine);
 
   // All roles count alike: ic the items, vc the visits (K and V stages; an item of one tile gives
   // visit vc to stream vc & 1), n[g] those of stream g, qt the Q buffer of the next item of one tile.
@@ -446,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto is_few = [&](const Item& it) { return it.nt * a.p.G <= kFew; };
   if (warp == 0) {
     // ------------------------------------------------------ Q and K producer
+    find_ends(a, m.ends, lane);
     if (lane == 0) {  // what the second kernel has to know
       const Bound &b = m.ends[0], &e = m.ends[1];
       const bool same = b.s == e.s && b.i == e.i && b.h == e.h;
@@ -486,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             const int c = lane >> 2, q = lane & 3;  // a lane a box
             if (c < NC && (few || q == 0))
-              tma_load_bhnd(base + b * L::TB + c * L::CHUNK + q * kFew * 128, few ? &tmF : &tmQ, &m.q_full[b], c * 64, 0,
+              tma_load_bhnd(base + b * L::TB + c * L::CHUNK + q * 32 * 128, few ? &tmF : &tmQ, &m.q_full[b], c * 64, 0,
                             it.row0 + t * a.TQ, it.h);
             ++used[b];
           }
@@ -611,17 +625,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kt = it.kt0; kt < it.kt1; ++kt, ++vc) {
         const int sv = vc % NS;
         if (!(ok = g.wait_warp(&m.v_full[sv], (vc / NS) & 1, 7))) break;
+        // The product takes the steps of 16 keys that hold some. Rows past the last key in its
+        // step are set to zero (0 * NaN is NaN); a visit without any key takes one step of zeros.
+        const int there = it.cap - kt * kTile;
+        uint32_t steps = there >= kTile ? 0xFFu : there <= 0 ? 0u : (1u << ((there + 15) >> 4)) - 1u;
         const uint32_t bad = m.v_bad[sv];
-        const int there = it.cap - kt * kTile;  // rows of this visit that hold keys
-        if (bad || there < kTile) {
-          // zeros where there are none: eight lanes a row of 128 bytes
+        if (bad) {
 #pragma unroll 1
-          for (int r = lane >> 3; r < kTile; r += 4)
-            if (r >= there || (bad >> (r >> a.page_shift)) & 1)
-              for (int c = 0; c < NC; ++c)
-                st_shared_v4(smem_u32(bV + sv * L::TB + c * L::CHUNK + r * 128 + (lane & 7) * 16), 0, 0, 0, 0);
+          for (int kk = 0; kk < 8; ++kk)
+            if ((bad >> ((kk * 16) >> a.page_shift)) & 1) steps &= ~(1u << kk);
+        }
+        if (there < kTile || steps == 0) {
+          const int r0 = steps == 0 ? 0 : there, r1 = steps == 0 ? 16 : (there + 15) & ~15;
+          for (int e = r0 * 128 + lane * 16; e < r1 * 128; e += 512)
+            for (int c = 0; c < NC; ++c) st_shared_v4(smem_u32(bV + sv * L::TB + c * L::CHUNK + e), 0, 0, 0, 0);
           fence_async_smem();
           __syncwarp();
+          if (steps == 0) steps = 1;
         }
         const uint64_t vd = sdesc_sw128(smem_u32(bV + sv * L::TB), L::CHUNK, 1024);
         const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
@@ -634,11 +654,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = g.wait_warp(&m.p_full[gs], n[gs] & 1, 9))) break;
           ++n[gs];
           tc_fence_after();
-          if (leader) {
+          const uint32_t tO = tmem + L::TM_O + gs * 128, tP = tmem + L::TM_S + gs * 128;
+          if (leader && steps == 0xFFu) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ta(tmem + L::TM_O + gs * 128, tmem + L::TM_S + gs * 128 + kk * 8, sdesc_add(vd, kk * 2048), idO,
-                           (!fresh[gs] || kk > 0) ? 1u : 0u);
+              umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (!fresh[gs] || kk > 0) ? 1u : 0u);
+          } else if (leader) {
+            bool add = !fresh[gs];
+#pragma unroll 1
+            for (int kk = 0; kk < 8; ++kk)
+              if ((steps >> kk) & 1) {
+                umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, add ? 1u : 0u);
+                add = true;
+              }
+          }
+          if (leader) {
             umma_commit(&m.pv_done[gs]);
           }
           fresh[gs] = false;
@@ -668,6 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool pair = is_pair(it), few = is_few(it);
       const int t0 = pair ? grp * a.TQ : 0;  // this stream's first token of the item
       const int rl = few ? lane : r, tok = t0 + rl / a.p.G;
+      const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
+      const bool mine_row = row < rows && rl < a.TQ * a.p.G;
       const int first_seen = min(it.seen0 + t0, it.cap);  // keys that the first one sees
       const int seen = min(it.seen0 + tok, it.cap);
       const bool active = few || t0 + quarter * 32 / a.p.G < it.nt;  // some row of this warp is a token's
@@ -694,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x[32];
           tmem_ld32(tS + quarter * 32, x);
           if (masked) hide32(x, seen32(seen, k0 + quarter * 32, quarter * 32, bad, a.page_shift));
-          f = advance(u, max32(x) * sl2, rescale);
+          f = advance(u, max32(x) * sl2, mine_row, rescale);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           exp_store32<false>(x, sc, f2(-moff, -moff), tS + quarter * 16, t2, none);
           const uint32_t zero[16] = {};
@@ -709,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             hide32(x2, seen32(seen, k0 + 64, 64, bad, a.page_shift));
             hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
           }
-          f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, rescale);
+          f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, mine_row, rescale);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           const uint64_t off = f2(-moff, -moff);
           exp_store32<false>(x0, sc, off, tS, t2, none);
@@ -731,12 +763,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ex[grp ^ 1];
         continue;
       }
-      if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 11))) break;
-      tc_fence_after();
-      const float2 lp = f2_split(u.l2);
-      float M = u.m, lt = lp.x + lp.y, f[2] = {1.f, 1.f};
       const bool halves = !pair && visits > 1;  // two streams' O to be joined, half of the columns each
       const bool whole = it.kt1 - it.kt0 == it.nkt;
+      const int c_lo = halves ? grp * (L::DL / 2) : 0, c_hi = halves ? min(c_lo + L::DL / 2, D) : D;
+      const int64_t t = it.row0 + tok;
+      const int head = it.h * a.p.G + rl - (tok - t0) * a.p.G;
+      uint8_t* slot = a.ws + kOffPartials + ((size_t)blockIdx.x * 2 + (it.kt0 == 0 ? 1 : 0)) * partial_bytes(D);
+      float4* po = reinterpret_cast<float4*>(slot + sizeof(Partial));
+      const unsigned long long dst = reinterpret_cast<unsigned long long>(a.out + t * a.p.o_t + (int64_t)head * a.p.o_h);
+      const float2 lp = f2_split(u.l2);
+      float M = u.m, lt = lp.x + lp.y, fa = 1.f, fb = 0.f;
+      if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 11))) break;
+      tc_fence_after();
       if (!pair) {
         // what the rows' other parts have to know: of the other stream, and of a few rows' warps
         m.stat[grp][0][r] = M;
@@ -750,28 +788,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++ex[grp ^ 1];
         }
         tc_fence_after();
-        M = -INFINITY, lt = 0.f;
-        const int at0 = few ? lane : r, parts = few ? 4 : 1;
-#pragma unroll 1
-        for (int k = 0; k < 2 * parts; ++k)
-          if (halves || (k & 1) == grp) M = fmaxf(M, m.stat[k & 1][0][at0 + (k >> 1) * 32]);
-#pragma unroll 1
-        for (int k = 0; k < 2 * parts; ++k)
-          if (halves || (k & 1) == grp)
-            lt = fmaf(m.stat[k & 1][1][at0 + (k >> 1) * 32], weight(m.stat[k & 1][0][at0 + (k >> 1) * 32], M), lt);
-        f[0] = weight(m.stat[0][0][r], M);
-        f[1] = weight(m.stat[1][0][r], M);
+        const float *sa = m.stat[halves ? 0 : grp][0], *sb = m.stat[halves ? 1 : grp][0];  // a stream alone counts once
+        const float ma = sa[r], mb = sb[r];
+        const float nb = halves ? 1.f : 0.f;
+        if (few) {
+          float x[8], y[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            x[q] = sa[q * 32 + lane], x[q + 4] = sb[q * 32 + lane];
+            y[q] = sa[128 + q * 32 + lane], y[q + 4] = sb[128 + q * 32 + lane] * nb;
+          }
+          M = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+          lt = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) lt = fmaf(y[k], weight(x[k], M), lt);
+        } else {
+          M = fmaxf(ma, mb);
+          lt = fmaf(sa[128 + r], weight(ma, M), sb[128 + r] * nb * weight(mb, M));
+        }
+        fa = weight(ma, M);
+        fb = weight(mb, M);
       }
-      const float fo = whole ? (lt > 0.f ? 1.f / lt : 0.f) : 1.f;
-      const float fa = (halves ? f[0] : grp ? f[1] : f[0]) * fo, fb = f[1] * fo;
-      const int c_lo = halves ? grp * (L::DL / 2) : 0, c_hi = halves ? min(c_lo + L::DL / 2, D) : D;
+      if (whole) {
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        fa *= inv;
+        fb *= inv;
+      }
       const uint32_t tA = tO + (halves ? 0 : grp * 128), tB = tO + 128;
-      const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
-      const bool mine_row = row < rows && rl < a.TQ * a.p.G;
-      const int64_t t = it.row0 + tok;
-      const int head = it.h * a.p.G + row % a.p.G;
-      uint8_t* slot = a.ws + kOffPartials + ((size_t)blockIdx.x * 2 + (it.kt0 == 0 ? 1 : 0)) * partial_bytes(D);
-      float4* po = reinterpret_cast<float4*>(slot + sizeof(Partial));
       if (mine_row && c_lo == 0 && (!few || quarter == 0)) {
         if (whole) {
           a.lse[t * a.p.Hq + head] = M * 0.6931471805599453f + logf(lt);
@@ -781,54 +824,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           pt.l[row] = lt;
         }
       }
-      unsigned long long dst = reinterpret_cast<unsigned long long>(a.out + t * a.p.o_t + (int64_t)head * a.p.o_h);
       if (few) {
-        // the four parts of a row meet in shared memory, cs columns at a time
-        const int cs = rows > 16 ? 16 : rows > 8 ? 32 : 64, ld = cs + 4;
+        // the four parts of a row meet in shared memory, 64 columns at a time
+        constexpr int ld = 68, part_ld = kStage / 4;
         float* st = reinterpret_cast<float*>(base + L::OFF_STAGE + grp * 4 * kStage);
-        constexpr int part_ld = kStage / 4;
+        const int e = threadIdx.x & 127, rr = e >> 4, c4 = (e & 15) * 4, tk = rr / a.p.G;
+        __nv_bfloat16* o = a.out + (it.row0 + tk) * a.p.o_t + (int64_t)(it.h * a.p.G + rr - tk * a.p.G) * a.p.o_h;
 #pragma unroll 1
-        for (int c0 = c_lo; ok && c0 < c_hi; c0 += cs) {
-          const int width = min(cs, c_hi - c0);
+        for (int c0 = c_lo; ok && c0 < c_hi; c0 += 64) {
 #pragma unroll 1
-          for (int c = 0; c < width; c += 16) {
-            uint32_t v[16], v2[16];
-            tmem_ld16(tA + c0 + c, v);
+          for (int c = 0; c < 64 && c0 + c < c_hi; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tA + c0 + c, v);
             if (halves) {
-              tmem_ld16(tB + c0 + c, v2);
+              uint32_t v2[32];
+              tmem_ld32(tB + c0 + c, v2);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v2[e]), fb, __uint_as_float(v[e]) * fa));
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(__uint_as_float(v2[k]), fb, __uint_as_float(v[k]) * fa));
             } else {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fa);
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fa);
             }
             if (lane < rows) {
+              float* to = st + quarter * part_ld + lane * ld + c;
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                st_shared_v4(smem_u32(st + quarter * part_ld + lane * ld + c + e), v[e], v[e + 1], v[e + 2], v[e + 3]);
+              for (int k = 0; k < 32; k += 4) st_shared_v4(smem_u32(to + k), v[k], v[k + 1], v[k + 2], v[k + 3]);
             }
             __syncwarp();
           }
           warp_arrive(&m.group[grp], lane);
           if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 14))) break;
           ++gp;
-          const int q4 = width / 4;
-#pragma unroll 1
-          for (int e = threadIdx.x & 127; e < rows * q4; e += 128) {
-            const int rr = e / q4, c = (e - rr * q4) * 4;
+          if (rr < rows && c0 + c4 < c_hi) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float4 z = *reinterpret_cast<const float4*>(st + q * part_ld + rr * ld + c);
+              const float4 z = *reinterpret_cast<const float4*>(st + q * part_ld + rr * ld + c4);
               y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
             }
-            if (whole) {
-              const int tk = rr / a.p.G;
-              __nv_bfloat16* o = a.out + (it.row0 + tk) * a.p.o_t + (int64_t)(it.h * a.p.G + rr - tk * a.p.G) * a.p.o_h + c0 + c;
-              *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-            } else {
-              po[(size_t)((c0 + c) / 4) * 256 + rr] = y;
-            }
+            if (whole)
+              *reinterpret_cast<uint2*>(o + c0 + c4) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            else
+              po[(size_t)((c0 + c4) / 4) * 256 + rr] = y;
           }
           warp_arrive(&m.group[grp], lane);
           if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 15))) break;
@@ -896,57 +933,79 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the item that CTA blockIdx.x began and did not end, 32 of its rows a
-// block: the parts' weights once, then O.
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+// block. What it reads hangs on the records alone, so that all of it is under way after one
+// round trip: a thread takes four columns of a row, of every n-th part where rows are few.
+constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinAhead = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ FwdArgs a) {
-  __shared__ int heads[kCtas], slots[kCtas];
+  __shared__ int slots[kCtas + 1];
   __shared__ float wt[kCtas][kJoinRows], sum[kJoinRows], top[kJoinRows];
+  __shared__ float4 share[kJoinThreads];
   __shared__ int count;
+  constexpr int C4 = D / 4;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4* recs = reinterpret_cast<const int4*>(a.ws + kOffRecords);
-  const int4 rec = recs[blockIdx.x];
+  const int P = gridDim.x, tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
+  const int4 rec = recs[b];
   if (rec.x < 0) return;
-  const int P = gridDim.x, tid = threadIdx.x;
-  for (int c = blockIdx.x + 1 + tid; c < P; c += kJoinThreads) heads[c] = recs[c].w;
   const SeqRows r = seq_rows(a.p, rec.x);
+  if (tid < 32) {  // the parts: this CTA's, then the following ones' up to the one that ends the item
+    int n = 1;
+    bool more = true;
+#pragma unroll 1
+    for (int c0 = b + 1; more && c0 < P; c0 += 32) {
+      const int c = c0 + lane, head = c < P ? recs[c].w : kWhole;
+      const uint32_t stop = __ballot_sync(~0u, head != kGoesOn && head != kEmpty);
+      const uint32_t upto = stop ? (2u << (__ffs(stop) - 1)) - 1u : ~0u;  // lanes up to the first that ends it
+      const uint32_t part = __ballot_sync(~0u, head == kGoesOn || head == kEnds) & upto;
+      if ((part >> lane) & 1) slots[n + __popc(part & ((1u << lane) - 1u))] = c * 2;
+      n += __popc(part);
+      more = stop == 0;
+    }
+    if (lane == 0) {
+      slots[0] = b * 2 + 1;
+      count = n;
+    }
+  }
   const int row0 = r.a + rec.y * 2 * a.TQ, all = min(2 * a.TQ, r.b - row0) * a.p.G;
   const int first = blockIdx.y * kJoinRows, rows = min(kJoinRows, all - first);
   if (rows <= 0) return;
   __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    slots[n++] = blockIdx.x * 2 + 1;
-#pragma unroll 1
-    for (int c = blockIdx.x + 1; c < P; ++c) {
-      if (heads[c] != kEmpty) slots[n++] = c * 2;
-      if (heads[c] != kGoesOn && heads[c] != kEmpty) break;
-    }
-    count = n;
-  }
-  __syncthreads();
-  const int n = count;
+  const int n = count, E = rows * C4;
   const uint8_t* parts = a.ws + kOffPartials;
+  const int groups = E >= kJoinThreads ? 1 : kJoinThreads / E;  // threads of an element
+  const int grp = groups == 1 ? 0 : tid / E, e0 = groups == 1 ? tid : tid - grp * E;
+  const auto o_of = [&](int k, int e) {
+    const int c = e / rows, row = e - c * rows;
+    return reinterpret_cast<const float4*>(parts + slots[k] * partial_bytes(D) + sizeof(Partial)) + c * 256 + first + row;
+  };
+  float4 ahead[kJoinAhead];
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i)
+    if (grp < groups && e0 < E && grp + i * groups < n) ahead[i] = *o_of(grp + i * groups, e0);
+  // the parts' weights, a warp a row
 #pragma unroll 1
-  for (int e = tid; e < n * rows; e += kJoinThreads) {
-    const int k = e / rows, row = e - k * rows;
-    wt[k][row] = reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D))->m[first + row];
-  }
-  __syncthreads();
+  for (int row = tid >> 5; row < rows; row += kJoinThreads / 32) {
+    const auto stat = [&](int k) { return reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D)); };
+    float M = -INFINITY, l = 0.f, m0 = -INFINITY, l0 = 0.f;
+    if (lane < n) {
+      m0 = stat(lane)->m[first + row];
+      l0 = stat(lane)->l[first + row];
+    }
+    M = m0;
 #pragma unroll 1
-  for (int row = tid >> 5; row < rows; row += kJoinThreads / 32) {  // a warp a row
-    const int lane = tid & 31;
-    float M = -INFINITY, l = 0.f;
-#pragma unroll 1
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, wt[k][row]);
+    for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, stat(k)->m[first + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    const float w0 = weight(m0, M);
+    if (lane < n) wt[lane][row] = w0;
+    l = l0 * w0;
 #pragma unroll 1
-    for (int k = lane; k < n; k += 32) {
-      const Partial& pt = *reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D));
-      const float x = weight(wt[k][row], M);
+    for (int k = lane + 32; k < n; k += 32) {
+      const float x = weight(stat(k)->m[first + row], M);
       wt[k][row] = x;
-      l = fmaf(pt.l[first + row], x, l);
+      l = fmaf(stat(k)->l[first + row], x, l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
@@ -957,17 +1016,31 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   }
   __syncthreads();
 #pragma unroll 1
-  for (int e = tid; e < rows * (D / 4); e += kJoinThreads) {
+  for (int e = e0; e < E; e += kJoinThreads) {  // (one round where threads share an element)
     const int c = e / rows, row = e - c * rows;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float4 v = reinterpret_cast<const float4*>(parts + slots[k] * partial_bytes(D) + sizeof(Partial))[c * 256 + first + row];
-      const float x = wt[k][row];
+    const auto add = [&](const float4& v, float x) {
       o.x = fmaf(v.x, x, o.x);
       o.y = fmaf(v.y, x, o.y);
       o.z = fmaf(v.z, x, o.z);
       o.w = fmaf(v.w, x, o.w);
+    };
+    if (grp < groups) {
+      int k = grp;
+      if (e == e0) {
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i, k += groups)
+          if (k < n) add(ahead[i], wt[k][row]);
+      }
+#pragma unroll 4
+      for (; k < n; k += groups) add(*o_of(k, e), wt[k][row]);
+    }
+    if (groups > 1) {
+      share[tid] = o;
+      __syncthreads();
+      if (grp > 0) break;
+#pragma unroll 1
+      for (int i = 1; i < groups; ++i) add(share[i * E + e], 1.f);
     }
     const float l = sum[row], inv = l > 0.f ? 1.f / l : 0.f;
     const int tok = (first + row) / a.p.G, head = rec.z * a.p.G + (first + row - tok * a.p.G);
@@ -1003,15 +1076,20 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
   cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sm_count(), kCtas);
-  paged_kernel<D><<<ctas, kThreads, L::SMEM, st>>>(tq, tf, tk, tv, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, (2 * a.TQ * p.G + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
+  // Both programmatic: each waits for the kernel ahead before it reads or writes memory
+  // that others write, and lets the next one start its prologue early.
   cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::SMEM;
+  cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, tq, tf, tk, tv, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(ctas, (2 * a.TQ * p.G + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
 }
 
