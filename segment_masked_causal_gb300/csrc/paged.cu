@@ -117,7 +117,7 @@ struct FwdArgs {
   PagedArgs p;
   int TQ;   // tokens of a tile; an item has two of them
   int TQf;  // tokens of one that has few rows
-  int page_shift;
+  int page_shift, cost_shift;
   __nv_bfloat16* out;
   float* lse;
   uint8_t* ws;
@@ -132,7 +132,7 @@ __device__ __forceinline__ int visits_of(const FwdArgs& a, const SeqRows& r, int
   const int ql = r.b - r.a, e = min(r.base() + min(ql, (i + 1) * 2 * a.TQ), a.p.width * a.p.page);
   return e <= kTile ? 1 : (e + kTile - 1) / kTile;
 }
-// Costs of a sequence's items of one kv head: item i's and all before it.
+// Costs of a sequence's items of one kv head: item i's and all before it, in keys.
 struct Costs {
   long long A;
   int ql, n, per;
@@ -144,15 +144,19 @@ struct Costs {
   }
   __device__ __forceinline__ long long before(int i) const { return A * i + (long long)per * i * (i + 1) / 2; }
   __device__ __forceinline__ long long of(int i) const { return A + (i == n - 1 ? ql : per * (i + 1)); }
-  __device__ __forceinline__ long long all() const { return n ? before(n - 1) + of(n - 1) : 0; }
+  // of the whole sequence and all kv heads, in units of 2^shift keys: the sum over a step fits 31 bits
+  __device__ __forceinline__ uint32_t scaled(const FwdArgs& a) const {
+    return n ? max(1u, (uint32_t)((before(n - 1) + of(n - 1)) * a.p.Hkv >> a.cost_shift)) : 0u;
+  }
 };
 
 // Where `x` of sequence s's cost lies: a function of x alone that never falls as x rises,
 // so that the end of one run is the start of the next (which is all that the fp32
 // quotients have to be good for). A cut that would leave fewer than kLeastVisits on
 // one of its sides moves to the item's end on that side.
-__device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r, long long x) {
+__device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r, uint32_t units) {
   const Costs c(a, r);
+  long long x = (long long)units << a.cost_shift;
   const int H = a.p.Hkv;
   int i = 0;
   for (int hi = c.n; hi - i > 1;) {
@@ -181,66 +185,70 @@ __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r
   return b;
 }
 
-// Both ends of this CTA's run, by one warp: the sum of all costs, then the sequences that the
-// ends lie in, 32 at a time, then the two places, a lane each.
-__device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], int lane) {
-  const int S = a.p.S;
-  const unsigned long long H = a.p.Hkv;
-  unsigned long long total = 0;
+// Both ends of this CTA's run. Every thread adds up the costs of its share of the sequences
+// (neighbours); warp 0 finds the thread's share that an end lies in, then the sequence in it and
+// the place, a lane for each end. sums: room for a number a thread.
+__device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], uint32_t* sums) {
+  const int S = a.p.S, tid = threadIdx.x, lane = tid & 31, share = (S + kThreads - 1) / kThreads;
+  uint32_t mine = 0;
   SeqRows r{0, 0, 0};
-#pragma unroll 2
-  for (int s = lane; s < S; s += 32) {
-    r = seq_rows(a.p, s);
-    total += Costs(a, r).all() * H;
+#pragma unroll 1
+  for (int k = 0; k < share; ++k)
+    if (tid * share + k < S) {
+      r = seq_rows(a.p, tid * share + k);
+      mine += Costs(a, r).scaled(a);
+    }
+  if (S > 32) {
+    sums[tid] = mine;
+    __syncthreads();
   }
-  const unsigned long long own = total;
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  const uint32_t P = (uint32_t)max(1ull, min((unsigned long long)gridDim.x, total >> kLeastCostLog));
-  // x of lanes 0 and 1: where the run starts and ends
-  const uint32_t c = blockIdx.x + (lane & 1);
-  unsigned long long x = c >= P ? total : __umul64hi(total, (unsigned long long)(c * (0xFFFFFFFFu / P + 1)) << 32);
-  const unsigned long long x0 = __shfl_sync(~0u, x, 0), x1 = __shfl_sync(~0u, x, 1);
-  int at = S;             // the sequence of this lane's x
-  SeqRows rows{0, 0, 0};  // and its rows
-  unsigned long long run = 0;
-  uint32_t open = 3;
-#pragma unroll 1
-  for (int s0 = 0; s0 < S && open; s0 += 32) {
-    unsigned long long v = own;
-    if (S > 32) {
-      v = 0;
-      if (s0 + lane < S) {
-        r = seq_rows(a.p, s0 + lane);
-        v = Costs(a, r).all() * H;
-      }
-    }
-    const unsigned long long cost = v;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long u = __shfl_up_sync(~0u, v, o);
-      if (lane >= o) v += u;
-    }
-    v += run;
-    run = __shfl_sync(~0u, v, 31);
+  if (tid >= 32) return;
+  // a lane's part of the sums, and what lies before it
+  const int per = S > 32 ? kThreads / 32 : 1;
+  if (S > 32) {
+    mine = 0;
+#pragma unroll 4
+    for (int k = 0; k < per; ++k) mine += sums[lane * per + k];
+  }
+  uint32_t v = mine;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const unsigned long long xe = e ? x1 : x0;
-      const uint32_t hit = __ballot_sync(~0u, xe >= v - cost && xe < v);
-      if (hit) {
-        const int from = __ffs(hit) - 1;
-        const SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
-        const unsigned long long before = __shfl_sync(~0u, v - cost, from);
-        if (lane == e) {
-          at = s0 + from;
-          rows = t;
-          x -= before;
-        }
-        open &= ~(1u << e);
-      }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += u;
+  }
+  const uint32_t total = __shfl_sync(~0u, v, 31);
+  const uint32_t P = max(1u, min(gridDim.x, total >> (kLeastCostLog > a.cost_shift ? kLeastCostLog - a.cost_shift : 0)));
+  const uint32_t c = blockIdx.x + (lane & 1);
+  uint32_t x = c >= P ? total : __umulhi(total, c * (0xFFFFFFFFu / P + 1));  // of lanes 0 and 1
+  int at = S;
+  uint32_t left = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t xe = __shfl_sync(~0u, x, e), hit = __ballot_sync(~0u, xe >= v - mine && xe < v);
+    const int from = hit ? __ffs(hit) - 1 : 0;
+    const uint32_t before = __shfl_sync(~0u, v - mine, from);
+    const SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
+    if (lane == e && hit) {
+      at = from;
+      left = xe - before;
+      if (S <= 32) ends[e].r = t;
     }
   }
-  if (lane < 2) ends[lane] = at < S ? place(a, at, rows, (long long)x) : Bound{S, 0, 0, 0, 0, SeqRows{0, 0, 0}};
+  if (lane < 2) {
+    SeqRows t{0, 0, 0};
+    if (at < S && S <= 32) t = ends[lane].r;
+    if (at < S && S > 32) {
+      int k = at * per;  // the thread's share, then the sequence in it
+      while (left >= sums[k]) left -= sums[k++];
+      for (at = k * share;; ++at) {
+        t = seq_rows(a.p, at);
+        const uint32_t cost = Costs(a, t).scaled(a);
+        if (left < cost) break;
+        left -= cost;
+      }
+    }
+    ends[lane] = at < S ? place(a, at, t, left) : Bound{S, 0, 0, 0, 0, SeqRows{0, 0, 0}};
+  }
   __syncwarp();
 }
 
@@ -369,12 +377,12 @@ __device__ __forceinline__ float advance(Running& u, float ms, bool mine, bool& 
 template <int D>
 __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
 #pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t v[32];
-    tmem_ld32(tO + c0, v);
+  for (int c0 = 0; c0 < D; c0 += 16) {  // few at a time: the scores stay in registers beside them
+    uint32_t v[16];
+    tmem_ld16(tO + c0, v);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-    tmem_st32(tO + c0, v);
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+    tmem_st16(tO + c0, v);
   }
 }
 
@@ -441,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
+  find_ends(a, m.ends, reinterpret_cast<uint32_t*>(base + L::OFF_STAGE));
 
   // All roles count alike: ic the items, vc the visits (K and V stages; an item of one tile gives
   // visit vc to stream vc & 1), n[g] those of stream g, qt the Q buffer of the next item of one tile.
@@ -459,7 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto is_few = [&](const Item& it) { return it.nt * a.p.G <= kFew; };
   if (warp == 0) {
     // ------------------------------------------------------ Q and K producer
-    find_ends(a, m.ends, lane);
     if (lane == 0) {  // what the second kernel has to know
       const Bound &b = m.ends[0], &e = m.ends[1];
       const bool same = b.s == e.s && b.i == e.i && b.h == e.h;
@@ -471,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     const PageLanes pl(a, lane, NC);
     Walk w(a, m);
-    int used[2] = {0, 0}, qt = 0;  // uses of the Q buffers
+    uint32_t used = 0, odd = 0;  // bits of the Q buffers: whether they were used, the parity of that
+    int qt = 0;
     for (bool more = true; ok && more;) {
       more = w.next();
       Item it = more ? w.item() : Item{};
@@ -495,14 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int t = 0; ok && t <= q_at; ++t) {
             const int b = pair ? t : qt;
-            if (used[b] > 0 && !(ok = g.wait_warp(&m.q_free[b], (used[b] - 1) & 1, 2))) break;
+            if ((used >> b) & 1 && !(ok = g.wait_warp(&m.q_free[b], ((odd >> b) & 1) ^ 1, 2))) break;
             if (lane == 0) mbar_expect_tx(&m.q_full[b], NC * a.p.G * 128 * (few ? 4 * a.TQf : a.TQ));
             __syncwarp();
             const int c = lane >> 2, q = lane & 3;  // a lane a box
             if (c < NC && (few || q == 0))
               tma_load_bhnd(base + b * L::TB + c * L::CHUNK + q * 32 * 128, few ? &tmF : &tmQ, &m.q_full[b], c * 64, 0,
                             it.row0 + t * a.TQ, it.h);
-            ++used[b];
+            used |= 1u << b;
+            odd ^= 1u << b;
           }
           if (!pair) qt ^= 1;
           if (!ok) break;
@@ -527,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {  // no copy may still be landing when the CTA exits
       for (int b = 0; b < 2; ++b)
-        if (used[b] > 0) g.drain(&m.q_full[b], (used[b] - 1) & 1);
+        if ((used >> b) & 1) g.drain(&m.q_full[b], ((odd >> b) & 1) ^ 1);
       for (int i = (vc > NS ? vc - NS : 0); i < vc; ++i) g.drain(&m.k_full[i % NS], (i / NS) & 1);
     }
     __syncwarp();
@@ -562,14 +572,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = lane == 0;
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
     const uint64_t qd = sdesc_sw128(smem_u32(base), 16, 1024);
-    int n[2] = {0, 0}, used[2] = {0, 0}, qt = 0;
+    // bits of the streams: whether they had a visit, the parity of their visits; of the Q buffers' uses
+    uint32_t had = 0, odd = 0, q_odd = 0;
+    int qt = 0;
     Item it;
     while (ok && next_item(it)) {
       const bool pair = is_pair(it);
+#pragma unroll 1
       for (int t = 0; ok && t < (pair ? 2 : 1); ++t) {
         const int b = pair ? t : qt;
-        ok = g.wait_warp(&m.q_full[b], used[b] & 1, 4);
-        ++used[b];
+        ok = g.wait_warp(&m.q_full[b], (q_odd >> b) & 1, 4);
+        q_odd ^= 1u << b;
       }
       for (int kt = it.kt0; ok && kt < it.kt1; ++kt, ++vc) {
         const int sk = vc % NS;
@@ -580,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int gs = lo; gs <= hi; ++gs) {
           // the stream's last P, which lies over its S, has been read
-          if (n[gs] > 0 && !(ok = g.wait_warp(&m.pv_done[gs], (n[gs] - 1) & 1, 5))) break;
-          ++n[gs];
+          if ((had >> gs) & 1 && !(ok = g.wait_warp(&m.pv_done[gs], ((odd >> gs) & 1) ^ 1, 5))) break;
+          had |= 1u << gs;
+          odd ^= 1u << gs;
           tc_fence_after();
           if (leader) {
             const uint64_t qb = sdesc_add(qd, (pair ? gs : qt) * L::TB);
@@ -617,11 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- PV issuer
     const bool leader = lane == 0;
     constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
-    int n[2] = {0, 0}, uses[2] = {0, 0};  // visits of the streams, and items that their O has held
+    // bits of the streams: the parity of their visits, whether O held an item, the parity of those
+    uint32_t odd = 0, held = 0, held_odd = 0;
     Item it;
     while (ok && next_item(it)) {
       const bool pair = is_pair(it);
-      bool fresh[2] = {true, true};
+      uint32_t fresh = 3;
       for (int kt = it.kt0; kt < it.kt1; ++kt, ++vc) {
         const int sv = vc % NS;
         if (!(ok = g.wait_warp(&m.v_full[sv], (vc / NS) & 1, 7))) break;
@@ -647,20 +662,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
 #pragma unroll 1
         for (int gs = lo; gs <= hi; ++gs) {
-          if (fresh[gs]) {  // O is free once its last item's has been read
-            if (uses[gs] > 0 && !(ok = g.wait_warp(&m.o_free[gs], (uses[gs] - 1) & 1, 8))) break;
-            ++uses[gs];
+          const uint32_t bit = 1u << gs;
+          if (fresh & bit) {  // O is free once its last item's has been read
+            if (held & bit && !(ok = g.wait_warp(&m.o_free[gs], ((held_odd >> gs) & 1) ^ 1, 8))) break;
+            held |= bit;
+            held_odd ^= bit;
           }
-          if (!(ok = g.wait_warp(&m.p_full[gs], n[gs] & 1, 9))) break;
-          ++n[gs];
-          tc_fence_after();
           const uint32_t tO = tmem + L::TM_O + gs * 128, tP = tmem + L::TM_S + gs * 128;
-          if (leader && steps == 0xFFu) {
+          bool add = !(fresh & bit);
+          if (!(ok = g.wait_warp(&m.p_full[gs], (odd >> gs) & 1, 9))) break;
+          tc_fence_after();
+          if (steps == 0xFFu) {
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (!fresh[gs] || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (add || kk > 0) ? 1u : 0u);
+            }
           } else if (leader) {
-            bool add = !fresh[gs];
 #pragma unroll 1
             for (int kk = 0; kk < 8; ++kk)
               if ((steps >> kk) & 1) {
@@ -668,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 add = true;
               }
           }
-          if (leader) {
-            umma_commit(&m.pv_done[gs]);
-          }
-          fresh[gs] = false;
+          __syncwarp();
+          if (!ok) break;
+          odd ^= bit;
+          fresh &= ~bit;
+          if (leader) umma_commit(&m.pv_done[gs]);
           __syncwarp();
         }
         if (!ok) break;
@@ -692,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_base + L::TM_O, tS = tmem + lane_base + L::TM_S + grp * 128;
     const float sl2 = a.p.scale_log2;
     const uint64_t sc = f2(sl2, sl2);
-    int nv = 0, gp = 0, ex[2] = {0, 0};  // visits of this stream, phases of its group's barrier, uses of the streams' statistics
+    // visits of this stream, phases of its group's barrier, uses of its statistics and of the other's
+    int nv = 0, gp = 0, ex = 0, ex_other = 0;
     Item it;
     while (ok && next_item(it)) {
       const bool pair = is_pair(it), few = is_few(it);
@@ -727,6 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + quarter * 32, x);
           if (masked) hide32(x, seen32(seen, k0 + quarter * 32, quarter * 32, bad, a.page_shift));
           f = advance(u, max32(x) * sl2, mine_row, rescale);
+          if (rescale && any) scale_o<D>(tO + grp * 128, f);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           exp_store32<false>(x, sc, f2(-moff, -moff), tS + quarter * 16, t2, none);
           const uint32_t zero[16] = {};
@@ -742,6 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
           }
           f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, mine_row, rescale);
+          // the stream's last product has ended (its S was formed after it), so O stands still
+          if (rescale && any) scale_o<D>(tO + grp * 128, f);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           const uint64_t off = f2(-moff, -moff);
           exp_store32<false>(x0, sc, off, tS, t2, none);
@@ -750,8 +773,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           exp_store32<false>(x3, sc, off, tS + 48, t2, none);
         }
         u.l2 = add2(u.l2, t2);
-        // the stream's last product has ended (its S was formed after it), so O stands still
-        if (rescale && any) scale_o<D>(tO + grp * 128, f);
         any = true;
         tmem_wait_st();
         tc_fence_before();
@@ -760,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
       if (!part) {  // the other stream's item alone
-        ++ex[grp ^ 1];
+        ++ex_other;
         continue;
       }
       const bool halves = !pair && visits > 1;  // two streams' O to be joined, half of the columns each
@@ -781,11 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.stat[grp][1][r] = lt;
         tc_fence_before();
         warp_arrive(&m.sums[grp], lane);
-        if (!(ok = g.wait_warp(&m.sums[grp], ex[grp] & 1, 12))) break;
-        ++ex[grp];
+        if (!(ok = g.wait_warp(&m.sums[grp], ex & 1, 12))) break;
+        ++ex;
         if (halves) {
-          if (!(ok = g.wait_warp(&m.sums[grp ^ 1], ex[grp ^ 1] & 1, 13))) break;
-          ++ex[grp ^ 1];
+          if (!(ok = g.wait_warp(&m.sums[grp ^ 1], ex_other & 1, 13))) break;
+          ++ex_other;
         }
         tc_fence_after();
         const float *sa = m.stat[halves ? 0 : grp][0], *sb = m.stat[halves ? 1 : grp][0];  // a stream alone counts once
@@ -1104,6 +1125,8 @@ cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pa
   a.TQ = kTile / p.G;
   a.TQf = std::max(1, kFew / p.G);
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
+  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * ((double)p.width * p.page + p.T + 2 * kItemCost);
+  while (most > 2147483648.0 * (double)(1ull << a.cost_shift)) ++a.cost_shift;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(ws);
