@@ -56,7 +56,7 @@ constexpr int kThreads = 384;
 // epilogue take.
 constexpr int kItemCost = 256;
 constexpr int kLeastVisits = 2;   // of a part of an item
-constexpr int kLeastCostLog = 9;  // of a CTA, log2
+constexpr int kLeastCost = 512;   // of a CTA
 constexpr int kFew = 8;           // rows of an item that the tile holds four times
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
@@ -75,17 +75,19 @@ struct Layout {
 };
 
 // A place on the line of work: before visit kt of item (s, i, h), of nkt visits.
-struct Bound {
-  int s, i, h, kt, nkt;
+struct alignas(16) Bound {
+  int s, i, h, kt;
+  int nkt;
   SeqRows r;
 };
 
 // A part of an item, as the K producer hands it to the other warps; nt 0 ends the run.
-struct Item {
+struct alignas(16) Item {
   int row0, nt, h;    // first row of q, tokens, kv head
   int s;              // sequence
   int kt0, kt1, nkt;  // visits of the part, and of the item
   int cap, seen0;     // keys in the cache; keys that the first token sees
+  int unused[3];
 };
 constexpr int kItems = 4;
 
@@ -117,7 +119,10 @@ struct FwdArgs {
   PagedArgs p;
   int TQ;   // tokens of a tile; an item has two of them
   int TQf;  // tokens of one that has few rows
-  int page_shift, cost_shift;
+  int page_shift;
+  int ctas;
+  int least_cost;    // of a CTA, in units
+  float cost_scale;  // units a key: a power of two
   __nv_bfloat16* out;
   float* lse;
   uint8_t* ws;
@@ -132,52 +137,48 @@ __device__ __forceinline__ int visits_of(const FwdArgs& a, const SeqRows& r, int
   const int ql = r.b - r.a, e = min(r.base() + min(ql, (i + 1) * 2 * a.TQ), a.p.width * a.p.page);
   return e <= kTile ? 1 : (e + kTile - 1) / kTile;
 }
-// Costs of a sequence's items of one kv head: item i's and all before it, in keys.
+// Costs of a sequence's items of one kv head, in keys: item i's and all before it. They are
+// fp32, since they only have to be the same in every CTA, and never to fall as i rises.
 struct Costs {
-  long long A;
-  int ql, n, per;
+  float A, per;
+  int ql, n;
   __device__ __forceinline__ Costs(const FwdArgs& a, const SeqRows& r) {
     ql = r.b - r.a;
     n = items_of(a, ql);
-    per = 2 * a.TQ;
-    A = (long long)min(max(r.base(), 0), a.p.width * a.p.page) + kItemCost;
+    per = (float)(2 * a.TQ);
+    A = (float)min(max(r.base(), 0), a.p.width * a.p.page) + (float)kItemCost;
   }
-  __device__ __forceinline__ long long before(int i) const { return A * i + (long long)per * i * (i + 1) / 2; }
-  __device__ __forceinline__ long long of(int i) const { return A + (i == n - 1 ? ql : per * (i + 1)); }
-  // of the whole sequence and all kv heads, in units of 2^shift keys: the sum over a step fits 31 bits
+  __device__ __forceinline__ float before(int i) const { return (A + 0.5f * per * (float)(i + 1)) * (float)i; }
+  __device__ __forceinline__ float of(int i) const { return A + (i == n - 1 ? (float)ql : per * (float)(i + 1)); }
+  // of the whole sequence and all kv heads, in units of 2^shift keys: the sum over a step fits 32 bits
   __device__ __forceinline__ uint32_t scaled(const FwdArgs& a) const {
-    return n ? max(1u, (uint32_t)((before(n - 1) + of(n - 1)) * a.p.Hkv >> a.cost_shift)) : 0u;
+    return n ? max(1u, __float2uint_rd((before(n - 1) + of(n - 1)) * (float)a.p.Hkv * a.cost_scale)) : 0u;
   }
 };
 
-// Where `x` of sequence s's cost lies: a function of x alone that never falls as x rises,
-// so that the end of one run is the start of the next (which is all that the fp32
-// quotients have to be good for). A cut that would leave fewer than kLeastVisits on
-// one of its sides moves to the item's end on that side.
+// Where `units` of sequence s's cost lie: a function of them that never falls as they rise,
+// so that the end of one run is the start of the next. A cut that would leave fewer than
+// kLeastVisits on one of its sides moves to the item's end on that side.
 __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r, uint32_t units) {
   const Costs c(a, r);
-  long long x = (long long)units << a.cost_shift;
-  const int H = a.p.Hkv;
+  const float H = (float)a.p.Hkv, x = __fdividef((float)units, a.cost_scale * H);  // of one kv head's line
   int i = 0;
   for (int hi = c.n; hi - i > 1;) {
     const int mid = i + (hi - i) / 2;
-    if (c.before(mid) * H <= x)
+    if (c.before(mid) <= x)
       i = mid;
     else
       hi = mid;
   }
-  x -= c.before(i) * H;
-  const long long of = c.of(i);
-  int h = min((int)__fdividef((float)x, (float)of), H - 1);
-  while (h > 0 && h * of > x) --h;
-  while (h < H - 1 && (h + 1) * of <= x) ++h;
+  // the heads of an item one behind the other
+  const float part = fmaxf(__fdividef((x - c.before(i)) * H, c.of(i)), 0.f);
   Bound b;
   b.s = s;
   b.i = i;
-  b.h = h;
+  b.h = min((int)part, a.p.Hkv - 1);
   b.r = r;
   b.nkt = visits_of(a, r, i);
-  b.kt = min((int)(__fdividef((float)(x - h * of), (float)of) * (float)b.nkt), b.nkt - 1);
+  b.kt = min((int)((part - (float)b.h) * (float)b.nkt), b.nkt - 1);
   if (b.kt < kLeastVisits)
     b.kt = 0;
   else if (b.nkt - b.kt < kLeastVisits)
@@ -217,7 +218,7 @@ __device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], ui
     if (lane >= o) v += u;
   }
   const uint32_t total = __shfl_sync(~0u, v, 31);
-  const uint32_t P = max(1u, min(gridDim.x, total >> (kLeastCostLog > a.cost_shift ? kLeastCostLog - a.cost_shift : 0)));
+  const uint32_t P = max(1u, min(gridDim.x, total / (uint32_t)a.least_cost));
   const uint32_t c = blockIdx.x + (lane & 1);
   uint32_t x = c >= P ? total : __umulhi(total, c * (0xFFFFFFFFu / P + 1));  // of lanes 0 and 1
   int at = S;
@@ -261,7 +262,7 @@ struct Walk {
   int kt0, kt1;  // visits of this part
   int nkt;       // and of the item
   __device__ __forceinline__ Walk(const FwdArgs& a_, const Misc& m) : a(a_) {
-    const Bound &b = m.ends[0], &e = m.ends[1];
+    const Bound b = m.ends[0], e = m.ends[1];
     s = b.s, i = b.i, h = b.h, kt0 = b.kt, r = b.r;
     es = e.s, ei = e.i, eh = e.h, ek = e.kt;
     n = items_of(a, r.b - r.a);
@@ -287,7 +288,7 @@ struct Walk {
   __device__ __forceinline__ Item item() const {
     const int t0 = i * 2 * a.TQ;
     return Item{r.a + t0, min(2 * a.TQ, r.b - r.a - t0), h, s, kt0, kt1, nkt, min(r.kv, a.p.width * a.p.page),
-                r.base() + t0 + 1};
+                r.base() + t0 + 1, {0, 0, 0}};
   }
 
  private:
@@ -459,7 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = ic % kItems;
     ok = g.wait_warp(&m.item_full[slot], (ic / kItems) & 1, 18);
     if (!ok) return false;
-    it = m.items[slot];
+    const int4* from = reinterpret_cast<const int4*>(&m.items[slot]);
+    int4* to = reinterpret_cast<int4*>(&it);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) to[k] = from[k];
     warp_arrive(&m.item_free[slot], lane);
     ++ic;
     return it.nt > 0;
@@ -669,22 +673,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             held_odd ^= bit;
           }
           const uint32_t tO = tmem + L::TM_O + gs * 128, tP = tmem + L::TM_S + gs * 128;
-          bool add = !(fresh & bit);
+          const bool add = !(fresh & bit);
           if (!(ok = g.wait_warp(&m.p_full[gs], (odd >> gs) & 1, 9))) break;
           tc_fence_after();
-          if (steps == 0xFFu) {
-            if (leader) {
+          if (leader) {
+            if (steps == 0xFFu) {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (add || kk > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                if ((steps >> kk) & 1)
+                  umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (add || (steps & ((1u << kk) - 1u))) ? 1u : 0u);
             }
-          } else if (leader) {
-#pragma unroll 1
-            for (int kk = 0; kk < 8; ++kk)
-              if ((steps >> kk) & 1) {
-                umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, add ? 1u : 0u);
-                add = true;
-              }
           }
           __syncwarp();
           if (!ok) break;
@@ -846,15 +848,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (few) {
-        // the four parts of a row meet in shared memory, 64 columns at a time
-        constexpr int ld = 68, part_ld = kStage / 4;
+        // the four parts of a row meet in shared memory, as many columns at a time as there is room for
+        const int cs = rows > 4 ? 64 : 128, ld = cs + 4, f4 = cs == 64 ? 4 : 5;
+        constexpr int part_ld = kStage / 4;
         float* st = reinterpret_cast<float*>(base + L::OFF_STAGE + grp * 4 * kStage);
-        const int e = threadIdx.x & 127, rr = e >> 4, c4 = (e & 15) * 4, tk = rr / a.p.G;
+        const int e = threadIdx.x & 127, rr = e >> f4, c4 = (e & ((1 << f4) - 1)) * 4, tk = rr / a.p.G;
         __nv_bfloat16* o = a.out + (it.row0 + tk) * a.p.o_t + (int64_t)(it.h * a.p.G + rr - tk * a.p.G) * a.p.o_h;
 #pragma unroll 1
-        for (int c0 = c_lo; ok && c0 < c_hi; c0 += 64) {
+        for (int c0 = c_lo; ok && c0 < c_hi; c0 += cs) {
 #pragma unroll 1
-          for (int c = 0; c < 64 && c0 + c < c_hi; c += 32) {
+          for (int c = 0; c < cs && c0 + c < c_hi; c += 32) {
             uint32_t v[32];
             tmem_ld32(tA + c0 + c, v);
             if (halves) {
@@ -888,9 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
               po[(size_t)((c0 + c4) / 4) * 256 + rr] = y;
           }
-          warp_arrive(&m.group[grp], lane);
-          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 15))) break;
-          ++gp;
+          if (c0 + cs < c_hi) {  // (the last step's sync is the next item's way here)
+            warp_arrive(&m.group[grp], lane);
+            if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 15))) break;
+            ++gp;
+          }
         }
         if (!ok) break;
       } else if (active) {
@@ -1096,7 +1101,7 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
-  const int ctas = std::min(sm_count(), kCtas);
+  const int ctas = a.ctas;
   // Both programmatic: each waits for the kernel ahead before it reads or writes memory
   // that others write, and lets the next one start its prologue early.
   cudaLaunchAttribute attr = programmatic_launch();
@@ -1108,7 +1113,7 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, tq, tf, tk, tv, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, (2 * a.TQ * p.G + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(ctas, (std::min(2 * a.TQ, p.T) * p.G + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
@@ -1125,8 +1130,13 @@ cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pa
   a.TQ = kTile / p.G;
   a.TQf = std::max(1, kFew / p.G);
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
-  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * ((double)p.width * p.page + p.T + 2 * kItemCost);
-  while (most > 2147483648.0 * (double)(1ull << a.cost_shift)) ++a.cost_shift;
+  // All that a step can cost: the units that its sum is counted in, and the CTAs that it can keep busy.
+  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * ((double)p.width * p.page + 2.0 * a.TQ + kItemCost);
+  double unit = 1;
+  while (most > 2e9 * unit) unit *= 2;
+  a.cost_scale = (float)(1 / unit);
+  a.least_cost = std::max(1, (int)(kLeastCost / unit));
+  a.ctas = (int)std::min<double>(std::min(sm_count(), kCtas), std::max(1.0, most / kLeastCost));
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(ws);
