@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "kernels.h"
 #include "paged.cuh"
@@ -18,7 +19,7 @@
 namespace pa {
 namespace {
 
-constexpr int kAppendThreads = 256, kStarts = 1024;
+constexpr int kAppendThreads = 128, kStarts = 1024;
 
 struct AppendArgs {
   PagedArgs p;
@@ -28,46 +29,17 @@ struct AppendArgs {
   int64_t n_t, n_h;
   const int32_t* positions;
   int heads, run;      // q's, k's and v's heads one behind the other, and how many a block takes
-  int units, turning;  // units per row: `turning` ones of pairs, then eight elements each
+  RopeUnits u;
 };
-
-// Heads h .. stop - 1 of one token: `turn` units rotated, others copied.
-template <int VEC, bool INTER>
-__device__ __forceinline__ void move_heads(const __nv_bfloat16* x, int64_t xs, __nv_bfloat16* y, int64_t ys, int n, bool pairs,
-                                           bool turn, int u, int half, int e, const float (&c)[VEC], const float (&s)[VEC]) {
-  constexpr int U = 4;
-  if (pairs) {
-    for (int h = 0; h < n; h += U, x += U * xs, y += U * ys) {
-      RopeUnit<__nv_bfloat16, VEC, INTER> r[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < n) r[i].load(x + i * xs, u, half);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < n) {
-          if (turn) r[i].rotate(c, s);
-          r[i].store(y + i * ys, u, half);
-        }
-    }
-  } else {
-    for (int h = 0; h < n; h += U, x += U * xs, y += U * ys) {
-      PlainUnit<__nv_bfloat16> r[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < n) r[i].load(x + i * xs + e);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < n) r[i].store(y + i * ys + e);
-    }
-  }
-}
 
 template <int VEC, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ int starts[kStarts + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const PagedArgs& p = a.p;
-  const int per = kAppendThreads / a.units;
-  const int at = threadIdx.x / a.units, u = threadIdx.x - at * a.units;
+  const int per = kAppendThreads / a.u.units;
+  const int at = threadIdx.x / a.u.units, u = threadIdx.x - at * a.u.units;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool small = p.S <= kStarts;
   if (small) {
     for (int i = threadIdx.x; i <= p.S; i += kAppendThreads) starts[i] = p.q_start[i];
@@ -93,32 +65,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const int id = p.page_table[(int64_t)s * p.width + slot / p.page];
     if (id >= 0 && id < p.pages) place = id * p.p_p + (int64_t)(slot % p.page) * p.p_n;
   }
-  const int rot = a.rope.rot, half = rot / 2, e = rot + 8 * (u - a.turning);
-  const bool pairs = u < a.turning;
+  const RopeUnit<__nv_bfloat16, VEC, INTER> unit(p.D, a.rope.rot, a.u.turning, u);
   float c[VEC], sn[VEC];
-  if (pairs) {
+  if (unit.turn) {
     const int32_t pos = a.positions ? a.positions[t] : slot;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) rope_cos_sin(a.rope.turns[u * VEC + i], pos, a.rope.amplitude, c[i], sn[i]);
   }
-  const int nq = a.q ? p.Hq : 0;
-  int h = blockIdx.y * a.run;
-  const int end = min(h + a.run, a.heads);
-  if (h < nq) {
-    const int stop = min(end, nq);
-    move_heads<VEC, INTER>(a.q + t * p.q_t + h * p.q_h, p.q_h, a.q_out + t * p.o_t + h * p.o_h, p.o_h, stop - h, pairs, true, u,
-                           half, e, c, sn);
-    h = stop;
-  }
-  if (place < 0) return;
-  for (int which = 0; which < 2; ++which) {  // keys, values
-    const int first = nq + which * p.Hkv, stop = min(end, first + p.Hkv);
-    if (h >= first && h < stop) {
-      move_heads<VEC, INTER>((which ? a.v : a.k) + t * a.n_t + (h - first) * a.n_h, a.n_h,
-                             (which ? a.v_pages : a.k_pages) + place + (h - first) * p.p_h, p.p_h, stop - h, pairs, which == 0,
-                             u, half, e, c, sn);
-      h = stop;
-    }
+  // this block's heads of q, k and v, one behind the other
+  const int nq = a.q ? p.Hq : 0, begin = blockIdx.y * a.run, end = min(begin + a.run, a.heads);
+#pragma unroll 1
+  for (int which = 0; which < 3; ++which) {
+    const int first = which == 0 ? 0 : nq + (which - 1) * p.Hkv, last = which == 0 ? nq : first + p.Hkv;
+    const int h0 = max(begin, first), n = min(end, last) - h0, h = h0 - first;
+    if (n <= 0 || (which > 0 && place < 0)) continue;
+    const __nv_bfloat16* x = which == 0 ? a.q + t * p.q_t + h * p.q_h : (which == 1 ? a.k : a.v) + t * a.n_t + h * a.n_h;
+    __nv_bfloat16* y = which == 0 ? a.q_out + t * p.o_t + h * p.o_h : (which == 1 ? a.k_pages : a.v_pages) + place + h * p.p_h;
+    unit.move(x, which == 0 ? p.q_h : a.n_h, y, which == 0 ? p.o_h : p.p_h, n, unit.turn && which < 2, c, sn);
   }
 }
 
@@ -139,18 +102,32 @@ cudaError_t launch_append(const PagedArgs& p, const pa_rotary* rope, const void*
   a.n_h = n_h;
   a.positions = positions;
   a.heads = (q ? p.Hq : 0) + 2 * p.Hkv;
-  const int vec = a.rope.rot % 16 ? 4 : 8;  // as in rope.cu
-  a.turning = a.rope.rot / (2 * vec);
-  a.units = a.turning + (p.D - a.rope.rot) / 8;
-  const int per = kAppendThreads / a.units, blocks = (p.T + per - 1) / per;
+  // vectors as in rope.cu
+  uint64_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(q) |
+                  reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages);
+  for (int64_t s : {n_t, n_h, p.p_p, p.p_h, p.p_n}) bits |= (uint64_t)s * 2;
+  if (q)
+    for (int64_t s : {p.q_t, p.q_h, p.o_t, p.o_h}) bits |= (uint64_t)s * 2;
+  const auto fits = [&](int vec) {
+    return a.rope.rot % (2 * vec) == 0 && (p.D - a.rope.rot) % vec == 0 && bits % (2 * vec) == 0;
+  };
+  const int vec = fits(16) ? 16 : fits(8) ? 8 : 4;
+  a.u = rope_units(p.D, a.rope.rot, vec, true);
+  const int per = kAppendThreads / a.u.units, blocks = (p.T + per - 1) / per;
   const int64_t want = 152 * 8;
   a.run = (int)std::min<int64_t>(a.heads, std::max<int64_t>(4, (int64_t)a.heads * blocks / want));
-  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.run - 1) / a.run));
   const bool inter = rope && rope->layout == PA_ROPE_INTERLEAVED;
-  const auto kfn = vec == 8 ? (inter ? append_kernel<8, true> : append_kernel<8, false>)
-                            : (inter ? append_kernel<4, true> : append_kernel<4, false>);
-  kfn<<<grid, kAppendThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const auto kfn = vec == 16  ? (inter ? append_kernel<16, true> : append_kernel<16, false>)
+                   : vec == 8 ? (inter ? append_kernel<8, true> : append_kernel<8, false>)
+                              : (inter ? append_kernel<4, true> : append_kernel<4, false>);
+  cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)((a.heads + a.run - 1) / a.run));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, a);
 }
 
 }  // namespace pa

@@ -4,7 +4,7 @@
 // Both are bound by memory: the rotation reads and writes each element once.
 // A thread holds the cosines and sines of one unit of pairs at one token
 // (rope.cuh) and takes that unit of many heads, so that they are computed once
-// for a run of heads; four heads' loads are in flight at a time. The backward is
+// for a run of heads; several heads' loads are in flight at a time. The backward is
 // the rotation by minus the angle (a rotation's transpose), times the same
 // amplitude.
 #include <cuda_runtime.h>
@@ -17,31 +17,33 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
   pa_rotary rope;
   RopeTensor t[PA_ROPE_MAX_TENSORS];
-  int count, heads;       // tensors, and their heads in all
-  int run;                // heads per block
-  int64_t tokens;         // B * N
-  int N, units, turning;  // units per row: `turning` ones of pairs, then eight elements each
+  int count, heads;  // tensors, and their heads in all
+  int run;           // heads per block
+  int tokens;        // B * N
+  int N, D;
+  RopeUnits u;
   const int32_t* positions;
   float sign;
 };
 
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
-  const int per = kRopeThreads / p.units;
-  const int at = threadIdx.x / p.units, u = threadIdx.x - at * p.units;
-  const int64_t token = (int64_t)blockIdx.x * per + at;
-  if (at >= per || token >= p.tokens) return;
-  const int64_t b = token / p.N, n = token - b * p.N;
-  const int rot = p.rope.rot, half = rot / 2;
-  const bool turn = u < p.turning;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per = kRopeThreads / p.u.units;
+  const int at = threadIdx.x / p.u.units, u = threadIdx.x - at * p.u.units;
+  const int64_t here = (int64_t)blockIdx.x * per + at;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (at >= per || here >= p.tokens) return;
+  const int token = (int)here, b = token / p.N, n = token - b * p.N;
+  const RopeUnit<T, VEC, INTER> r(p.D, p.rope.rot, p.u.turning, u);
   float c[VEC], s[VEC];
-  if (turn) {
-    const int32_t pos = p.positions ? p.positions[token] : (int32_t)n;
+  if (r.turn) {
+    const int32_t pos = p.positions ? p.positions[token] : n;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       rope_cos_sin(p.rope.turns[u * VEC + i], pos, p.rope.amplitude, c[i], s[i]);
@@ -55,51 +57,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     while (h >= first + p.t[k].H) first += p.t[k++].H;
     const RopeTensor& t = p.t[k];
     const int stop = min(end, first + t.H);
-    const T* x = static_cast<const T*>(t.x) + b * t.x_b + n * t.x_n + (int64_t)(h - first) * t.x_h;
-    T* y = static_cast<T*>(t.y) + b * t.y_b + n * t.y_n + (int64_t)(h - first) * t.y_h;
-    constexpr int U = 4;
-    if (turn) {
-      for (; h < stop; h += U, x += U * t.x_h, y += U * t.y_h) {
-        RopeUnit<T, VEC, INTER> r[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (h + i < stop) r[i].load(x + i * t.x_h, u, half);
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (h + i < stop) {
-            r[i].rotate(c, s);
-            r[i].store(y + i * t.y_h, u, half);
-          }
-      }
-    } else {
-      const int e = rot + 8 * (u - p.turning);
-      for (; h < stop; h += U, x += U * t.x_h, y += U * t.y_h) {
-        PlainUnit<T> r[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (h + i < stop) r[i].load(x + i * t.x_h + e);
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (h + i < stop) r[i].store(y + i * t.y_h + e);
-      }
-    }
+    r.move(static_cast<const T*>(t.x) + b * t.x_b + n * t.x_n + (int64_t)(h - first) * t.x_h, t.x_h,
+           static_cast<T*>(t.y) + b * t.y_b + n * t.y_n + (int64_t)(h - first) * t.y_h, t.y_h, stop - h, r.turn, c, s);
     h = stop;
   }
 }
 
 template <typename T, int VEC>
-cudaError_t launch_vec(RopeArgs& a, cudaStream_t st) {
-  a.turning = a.rope.rot / (2 * VEC);
-  const int64_t blocks = (a.tokens + kRopeThreads / a.units - 1) / (kRopeThreads / a.units);
+cudaError_t launch_vec(RopeArgs& a, bool rest, cudaStream_t st) {
+  a.u = rope_units(a.D, a.rope.rot, VEC, rest);
+  const int per = kRopeThreads / a.u.units;
+  const int64_t blocks = ((int64_t)a.tokens + per - 1) / per;
   // Heads of a block: all of them, or fewer where the tokens alone do not fill the device.
   const int64_t want = 152 * 8;
   a.run = (int)std::min<int64_t>(a.heads, std::max<int64_t>(4, (int64_t)a.heads * blocks / want));
-  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.run - 1) / a.run));
-  if (a.rope.layout == PA_ROPE_INTERLEAVED)
-    rope_kernel<T, VEC, true><<<grid, kRopeThreads, 0, st>>>(a);
-  else
-    rope_kernel<T, VEC, false><<<grid, kRopeThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)((a.heads + a.run - 1) / a.run));
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, a.rope.layout == PA_ROPE_INTERLEAVED ? rope_kernel<T, VEC, true> : rope_kernel<T, VEC, false>, a);
 }
 
 // Position of each token in its run of equal ids. A block takes 1,024 tokens of
@@ -122,6 +101,8 @@ __device__ __forceinline__ int block_max(int v, int* sh) {
 __global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* __restrict__ seg,
                                                                 int32_t* __restrict__ positions, int N, int tiles) {
   __shared__ int sh[kPosThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x / tiles, n0 = (blockIdx.x - b * tiles) * kPosTile;
   const int32_t* row = seg + (int64_t)b * N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -172,27 +153,43 @@ cudaError_t launch_rope(const pa_rotary& rope, const RopeTensor* t, int count, i
   a.rope = rope;
   a.count = count;
   bool in_place = true;
+  uint64_t bits = 0;  // of every address and stride, in bytes
+  const int size = f32 ? 4 : 2;
   for (int i = 0; i < count; ++i) {
     a.t[i] = t[i];
     a.heads += t[i].H;
     in_place = in_place && t[i].x == t[i].y;
+    bits |= reinterpret_cast<uintptr_t>(t[i].x) | reinterpret_cast<uintptr_t>(t[i].y);
+    if (B > 1) bits |= (uint64_t)(t[i].x_b | t[i].y_b) * size;
+    if (t[i].H > 1) bits |= (uint64_t)(t[i].x_h | t[i].y_h) * size;
+    if (N > 1) bits |= (uint64_t)(t[i].x_n | t[i].y_n) * size;
   }
-  a.tokens = (int64_t)B * N;
+  a.tokens = (int)((int64_t)B * N);
   a.N = N;
+  a.D = D;
   a.positions = positions;
   a.sign = backward ? -1.f : 1.f;
-  // Units of eight pairs where the rotated part is a whole number of them; fp32
-  // ones of four are as many bytes.
-  const int vec = f32 || rope.rot % 16 ? 4 : 8;
-  a.units = rope.rot / (2 * vec) + (in_place ? 0 : (D - rope.rot) / 8);
-  if (f32) return launch_vec<float, 4>(a, st);
-  return vec == 8 ? launch_vec<__nv_bfloat16, 8>(a, st) : launch_vec<__nv_bfloat16, 4>(a, st);
+  // Vectors of 32 bytes where every row starts on them and both parts of it are whole numbers
+  // of units, else of 16, else (a rotated part of 8 pairs and 8 more) of 8. In place the rest stays.
+  const auto fits = [&](int vec) {
+    const uint64_t bytes = (uint64_t)vec * size;
+    return rope.rot % (2 * vec) == 0 && (in_place || (D - rope.rot) % vec == 0) && (bits % bytes) == 0 && (uint64_t)D * size % bytes == 0;
+  };
+  if (f32) return fits(8) ? launch_vec<float, 8>(a, !in_place, st) : launch_vec<float, 4>(a, !in_place, st);
+  if (fits(16)) return launch_vec<__nv_bfloat16, 16>(a, !in_place, st);
+  return fits(8) ? launch_vec<__nv_bfloat16, 8>(a, !in_place, st) : launch_vec<__nv_bfloat16, 4>(a, !in_place, st);
 }
 
 cudaError_t launch_positions(int B, int N, const int32_t* seg, int32_t* positions, cudaStream_t st) {
   const int tiles = (N + kPosTile - 1) / kPosTile;
-  positions_kernel<<<(unsigned)((int64_t)B * tiles), kPosThreads, 0, st>>>(seg, positions, N, tiles);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)B * tiles));
+  cfg.blockDim = dim3(kPosThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, positions_kernel, seg, positions, N, tiles);
 }
 
 }  // namespace pa

@@ -18,101 +18,127 @@
 
 namespace pa {
 
+//
+// On an eighth of a turn, |x| <= pi / 4, the series of sine up to x^9 and of cosine up to x^8
+// leave out less than 2e-9 and 3e-8, below fp32's half steps there.
 __device__ __forceinline__ void rope_cos_sin(uint64_t turns, int32_t pos, float amplitude, float& c, float& s) {
-  const uint32_t part = (uint32_t)((turns * (uint64_t)(int64_t)pos) >> 32);  // of a turn, in 2^-32
-  const uint32_t quarter = (part + 0x20000000u) >> 30;                      // nearest, mod 4
-  const int32_t rest = (int32_t)(part - (quarter << 30));                   // -1/8 .. 1/8 of a turn
-  float sn, cs;
-  sincospif((float)rest * 0x1p-31f, &sn, &cs);
+  const uint32_t lo = (uint32_t)turns, hi = (uint32_t)(turns >> 32), p = (uint32_t)pos;
+  const uint32_t part = __umulhi(lo, p) + hi * p - (pos < 0 ? lo : 0u);  // of a turn, in 2^-32
+  const uint32_t quarter = (part + 0x20000000u) >> 30;                    // the nearest one, mod 4
+  const float x = (float)(int32_t)(part - (quarter << 30)) * 1.462918079e-9f;  // 2 pi / 2^32
+  const float x2 = x * x;
+  float sn = fmaf(x2, 1.f / 362880, -1.f / 5040);
+  sn = fmaf(x2, sn, 1.f / 120);
+  sn = fmaf(x2, sn, -1.f / 6);
+  sn = fmaf(x * x2, sn, x);
+  float cs = fmaf(x2, 1.f / 40320, -1.f / 720);
+  cs = fmaf(x2, cs, 1.f / 24);
+  cs = fmaf(x2, cs, -0.5f);
+  cs = fmaf(x2, cs, 1.f);
+  // a quarter turn swaps the two; the sign of the cosine turns at 1/4 and 3/4, the sine's at 1/2
   const float u = (quarter & 1) ? sn : cs, v = (quarter & 1) ? cs : sn;
-  c = (quarter == 1 || quarter == 2) ? -amplitude * u : amplitude * u;
-  s = (quarter & 2) ? -amplitude * v : amplitude * v;
+  c = __uint_as_float(__float_as_uint(amplitude * u) ^ (((quarter + 1) & 2) << 30));
+  s = __uint_as_float(__float_as_uint(amplitude * v) ^ ((quarter & 2) << 30));
 }
 
-// A unit of VEC pairs of one row: pairs VEC u .. VEC u + VEC - 1 of rot / 2.
-// Interleaved pairs are neighbours (2 VEC elements in one run); half pairs lie
-// rot / 2 apart (two runs of VEC elements).
+// The unit of a row that a thread holds: two vectors of VEC elements. Of the rotated part
+// it is VEC pairs (half pairs: elements VEC u .. and rot / 2 + VEC u ..; interleaved ones: 2 VEC
+// neighbours), of the rest 2 VEC neighbours, whose second half may lie past the row's end.
+struct RopeUnits {
+  int units, turning;  // per row, the `turning` ones first
+};
+inline RopeUnits rope_units(int D, int rot, int vec, bool rest) {
+  const int turning = rot / (2 * vec);
+  return {turning + (rest ? (D - rot + 2 * vec - 1) / (2 * vec) : 0), turning};
+}
+
 template <typename T, int VEC, bool INTER>
 struct RopeUnit {
-  static constexpr int W = VEC * 2 * (int)sizeof(T) / 4;  // 32-bit words
-  uint32_t w[W];
-
-  template <int N>
-  static __device__ __forceinline__ void get(uint32_t* to, const T* p) {
-    if constexpr (N == 2) {
+  static constexpr int BYTES = VEC * (int)sizeof(T), W = BYTES / 4;  // of a vector
+  int a, b;   // where in a row the vectors lie
+  bool turn;  // pairs to be rotated
+  bool two;   // the second vector exists
+  __device__ __forceinline__ RopeUnit(int D, int rot, int turning, int u) {
+    turn = u < turning;
+    a = turn ? (INTER ? 2 * u * VEC : u * VEC) : rot + 2 * VEC * (u - turning);
+    b = turn && !INTER ? rot / 2 + u * VEC : a + VEC;
+    two = b < D;
+  }
+  static __device__ __forceinline__ void get(uint32_t (&w)[2 * W], int at, const T* p) {
+    if constexpr (BYTES == 8) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
-      to[0] = v.x, to[1] = v.y;
+      w[at] = v.x, w[at + 1] = v.y;
+    } else if constexpr (BYTES == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[at] = v.x, w[at + 1] = v.y, w[at + 2] = v.z, w[at + 3] = v.w;
     } else {
-#pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
-        to[i] = v.x, to[i + 1] = v.y, to[i + 2] = v.z, to[i + 3] = v.w;
-      }
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[at]), "=r"(w[at + 1]), "=r"(w[at + 2]), "=r"(w[at + 3]), "=r"(w[at + 4]), "=r"(w[at + 5]),
+                     "=r"(w[at + 6]), "=r"(w[at + 7])
+                   : "l"(p)
+                   : "memory");
     }
   }
-  template <int N>
-  static __device__ __forceinline__ void put(T* p, const uint32_t* v) {
-    if constexpr (N == 2) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+  static __device__ __forceinline__ void put(const uint32_t (&w)[2 * W], int at, T* p) {
+    if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[at], w[at + 1]);
+    } else if constexpr (BYTES == 16) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[at], w[at + 1], w[at + 2], w[at + 3]);
     } else {
-#pragma unroll
-      for (int i = 0; i < N; i += 4)
-        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[at]), "r"(w[at + 1]), "r"(w[at + 2]),
+                   "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]), "r"(w[at + 6]), "r"(w[at + 7])
+                   : "memory");
     }
   }
-  __device__ __forceinline__ void load(const T* row, int u, int half) {
-    if constexpr (INTER) {
-      get<W>(w, row + u * (2 * VEC));
-    } else {
-      get<W / 2>(w, row + u * VEC);
-      get<W / 2>(w + W / 2, row + half + u * VEC);
-    }
+  __device__ __forceinline__ void load(uint32_t (&w)[2 * W], const T* row) const {
+    get(w, 0, row + a);
+    if (two) get(w, W, row + b);
   }
-  __device__ __forceinline__ void store(T* row, int u, int half) const {
-    if constexpr (INTER) {
-      put<W>(row + u * (2 * VEC), w);
-    } else {
-      put<W / 2>(row + u * VEC, w);
-      put<W / 2>(row + half + u * VEC, w + W / 2);
-    }
-  }
-  __device__ __forceinline__ void rotate(const float (&c)[VEC], const float (&s)[VEC]) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        uint32_t &wa = INTER ? w[2 * i] : w[i], &wb = INTER ? w[2 * i + 1] : w[W / 2 + i];
-        const float a = __uint_as_float(wa), b = __uint_as_float(wb);
-        wa = __float_as_uint(a * c[i] - b * s[i]);
-        wb = __float_as_uint(b * c[i] + a * s[i]);
-      } else if constexpr (INTER) {
-        const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
-        w[i] = pack(a * c[i] - b * s[i], b * c[i] + a * s[i]);
-      } else if (i % 2 == 0) {
-        uint32_t &wa = w[i / 2], &wb = w[W / 2 + i / 2];
-        const float a0 = __uint_as_float(wa << 16), a1 = __uint_as_float(wa & 0xFFFF0000u);
-        const float b0 = __uint_as_float(wb << 16), b1 = __uint_as_float(wb & 0xFFFF0000u);
-        wa = pack(a0 * c[i] - b0 * s[i], a1 * c[i + 1] - b1 * s[i + 1]);
-        wb = pack(b0 * c[i] + a0 * s[i], b1 * c[i + 1] + a1 * s[i + 1]);
-      }
-    }
+  __device__ __forceinline__ void store(const uint32_t (&w)[2 * W], T* row) const {
+    put(w, 0, row + a);
+    if (two) put(w, W, row + b);
   }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
-};
-
-// Eight elements that are not rotated.
-template <typename T>
-struct PlainUnit {
-  uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
+  static __device__ __forceinline__ void rotate(uint32_t (&w)[2 * W], const float (&c)[VEC], const float (&s)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        uint32_t &wa = INTER ? w[2 * i] : w[i], &wb = INTER ? w[2 * i + 1] : w[W + i];
+        const float x = __uint_as_float(wa), y = __uint_as_float(wb);
+        wa = __float_as_uint(x * c[i] - y * s[i]);
+        wb = __float_as_uint(y * c[i] + x * s[i]);
+      } else if constexpr (INTER) {
+        const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xFFFF0000u);
+        w[i] = pack(x * c[i] - y * s[i], y * c[i] + x * s[i]);
+      } else if (i % 2 == 0) {
+        uint32_t &wa = w[i / 2], &wb = w[W + i / 2];
+        const float x0 = __uint_as_float(wa << 16), x1 = __uint_as_float(wa & 0xFFFF0000u);
+        const float y0 = __uint_as_float(wb << 16), y1 = __uint_as_float(wb & 0xFFFF0000u);
+        wa = pack(x0 * c[i] - y0 * s[i], x1 * c[i + 1] - y1 * s[i + 1]);
+        wb = pack(y0 * c[i] + x0 * s[i], y1 * c[i + 1] + x1 * s[i + 1]);
+      }
+    }
   }
-  __device__ __forceinline__ void store(T* p) const {
+  // n heads of one row, xs and ys elements apart, several loads in flight
+  __device__ __forceinline__ void move(const T* x, int64_t xs, T* y, int64_t ys, int n, bool rotating, const float (&c)[VEC],
+                                       const float (&s)[VEC]) const {
+    constexpr int U = BYTES == 32 ? 2 : 4;
+#pragma unroll 1
+    for (int h = 0; h < n; h += U, x += U * xs, y += U * ys) {
+      uint32_t w[U][2 * W];
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+      for (int i = 0; i < U; ++i)
+        if (h + i < n) load(w[i], x + i * xs);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (h + i < n) {
+          if (rotating) rotate(w[i], c, s);
+          store(w[i], y + i * ys);
+        }
+    }
   }
 };
 
