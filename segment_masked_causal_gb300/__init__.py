@@ -182,12 +182,12 @@ def lib():
             L.pa_positions.restype = ctypes.c_int
             L.pa_rope.argtypes = [P, I32, P, I32, I32, I32, I32, P, I32, P]  # an array of pa_rope_tensor, or its bytes
             L.pa_rope.restype = ctypes.c_int
-            PD, PS = ctypes.POINTER(pa_paged_dims), ctypes.POINTER(pa_paged_strides)
-            L.pa_paged_append.argtypes = [PD, PS, P, P, P, P, P, P, P, P, P, P, P, P]
+            # pa_paged_dims and pa_paged_strides, or their bytes
+            L.pa_paged_append.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, P]
             L.pa_paged_append.restype = ctypes.c_int
             L.pa_paged_workspace_bytes.argtypes = [I32]
             L.pa_paged_workspace_bytes.restype = S
-            L.pa_paged_fwd.argtypes = [PD, PS, P, P, P, P, P, P, P, P, P, S, P]
+            L.pa_paged_fwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, S, P]
             L.pa_paged_fwd.restype = ctypes.c_int
             L.pa_pack_first_fit.argtypes = [P, P, I32, P, I32, I32, I32, U64, U64, P, P, P, P, P, P, P]
             L.pa_pack_first_fit.restype = ctypes.c_int
@@ -985,19 +985,25 @@ class Rotary:
 def pa_positions(seg, positions, stream=None):
     """positions[b, n] = n minus the start of its run of equal ids; both (B, N) int32."""
     import torch
-    if seg.dim() != 2:
+    shape, i32, at = seg.shape, torch.int32, torch.cuda.current_device()
+    if len(shape) != 2:
         raise ValueError("seg must be (B, N)")
-    _want(positions, seg.shape, "positions")
-    _on_current_device(seg, positions)
-    _check(lib().pa_positions(*seg.shape, _ptr(seg, torch.int32, "seg"), _ptr(positions, torch.int32, "positions"),
-                              _stream(stream)))
+    if positions.shape != shape:
+        raise ValueError(f"positions must be {tuple(shape)}, got {tuple(positions.shape)}")
+    if seg.dtype != i32 or positions.dtype != i32:
+        raise ValueError(f"seg and positions must be int32, got {seg.dtype} and {positions.dtype}")
+    if not seg.get_device() == positions.get_device() == at:
+        raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+    if not (seg.is_contiguous() and positions.is_contiguous()):
+        raise ValueError("seg and positions must be contiguous")
+    _check(lib().pa_positions(shape[0], shape[1], seg.data_ptr(), positions.data_ptr(), _stream(stream)))
 
 
 def segment_positions(seg):
     """Positions of packed rows from their segment ids, counting from 0 in each
     segment: (B, N) int32."""
     import torch
-    positions = torch.empty_like(seg, memory_format=torch.contiguous_format)
+    positions = torch.empty(seg.shape, dtype=torch.int32, device=seg.device)
     pa_positions(seg, positions)
     return positions
 
@@ -1007,58 +1013,69 @@ _ROPE_FIELDS = struct.Struct("PPi4xqqqqqq")  # pa_rope_tensor
 
 def pa_rope(tensors, out, rotary, positions=None, backward=False, stream=None):
     """Rotate the (B, H, N, D) tensors into `out` (which may be the tensors
-    themselves), or take their gradients back; see include/pa.h."""
+    themselves; None: new tensors in the same memory order), or take their
+    gradients back; see include/pa.h. Returns the outputs."""
     import torch
-    tensors, out = list(tensors), list(out)
+    tensors = list(tensors)
+    made = out is None
+    out = [torch.empty_like(x) for x in tensors] if made else list(out)
     if len(tensors) != len(out):
         raise ValueError("one output per tensor")
     if not tensors:
-        return
-    x0, parts, at = tensors[0], [], torch.cuda.current_device()
-    if x0.dim() != 4:
-        raise ValueError("tensors must be (B, H, N, D)")
-    B, _, N, D = x0.shape
-    dtype, io = _io_dtype(x0)
+        return out
+    parts, at, pack = [], torch.cuda.current_device(), _ROPE_FIELDS.pack
+    dtype, io = _io_dtype(tensors[0])
+    first = None
     for x, y in zip(tensors, out):
-        if x.dim() != 4 or x.shape[0] != B or x.shape[2:] != x0.shape[2:] or y.shape != x.shape:
-            raise ValueError("the tensors of one call are (B, H, N, D) with one B, N and D, and out has their shapes")
-        if x.dtype != dtype or y.dtype != dtype:
+        shape = x.shape
+        if len(shape) != 4:
+            raise ValueError("tensors must be (B, H, N, D)")
+        B, H, N, D = shape
+        if first is None:
+            first = (B, N, D)
+        elif first != (B, N, D):
+            raise ValueError("the tensors of one call are (B, H, N, D) with one B, N and D")
+        if x.dtype != dtype:
             raise ValueError("the tensors of one call share their type")
-        if not x.get_device() == y.get_device() == at:
+        if x.get_device() != at:
             raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
-        xs, ys = x.stride(), y.stride()
-        if xs[3] != 1 or ys[3] != 1:
+        x_b, x_h, x_n, x_c = x.stride()
+        y_b, y_h, y_n, y_c = y.stride()
+        if not made:
+            if y.shape != shape or y.dtype != dtype:
+                raise ValueError("out must have the tensors' shapes and type")
+            if y.get_device() != at:
+                raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
+        if (x_c != 1 or y_c != 1) and D > 1:
             raise ValueError("the tensors' last dim must be contiguous")
-        parts.append(_ROPE_FIELDS.pack(x.data_ptr(), y.data_ptr(), x.shape[1], *xs[:3], *ys[:3]))
+        parts.append(pack(x.data_ptr(), y.data_ptr(), H, x_b, x_h, x_n, y_b, y_h, y_n))
+    B, N, D = first
     pos = None
     if positions is not None:
-        _want(positions, (B, N), "positions")
-        _on_current_device(positions)
-        pos = _ptr(positions, torch.int32, "positions")
+        if positions.shape != (B, N) or positions.dtype != torch.int32:
+            raise ValueError(f"positions must be {(B, N)} int32, got {tuple(positions.shape)} {positions.dtype}")
+        if positions.get_device() != at:
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at}), got positions on {positions.device}")
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+        pos = positions.data_ptr()
     st, fn = _stream(stream), lib().pa_rope
     for i in range(0, len(parts), PA_ROPE_MAX_TENSORS):
         some = parts[i:i + PA_ROPE_MAX_TENSORS]
-        _check(fn(rotary.ref, len(some), b"".join(some), B, N, D, io, pos, int(backward), st))
+        _check(fn(rotary.ref, len(some), b"".join(some), B, N, D, io, pos, 1 if backward else 0, st))
+    return out
 
 
 def rotary_forward(tensors, rotary, positions=None, out=None):
     """The (B, H, N, D) tensors (q and k, say; bf16 or fp32, any strides with
     the last dim contiguous) rotated to their positions ((B, N) int32, or None
     for 0, 1, ...), as new tensors in the same memory order or into `out`."""
-    import torch
-    tensors = list(tensors)
-    out = [torch.empty_like(x) for x in tensors] if out is None else list(out)
-    pa_rope(tensors, out, rotary, positions)
-    return out
+    return pa_rope(tensors, out, rotary, positions)
 
 
 def rotary_backward(grads, rotary, positions=None, out=None):
     """Gradients of rotary_forward's inputs from those of its outputs."""
-    import torch
-    grads = list(grads)
-    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
-    pa_rope(grads, out, rotary, positions, backward=True)
-    return out
+    return pa_rope(grads, out, rotary, positions, backward=True)
 
 
 # -------------------------------------------------------------- paged cache
@@ -1084,10 +1101,11 @@ class PagedCache:
 
 
 def _rows_of(t, H, D, at, name):
-    """A (T, H, D) bf16 tensor on device `at`, its last dim contiguous: its token and head strides."""
+    """A (T, H, D) bf16 tensor on device `at`, its last dim contiguous (H None: any): its sizes and strides."""
     import torch
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
-        raise ValueError(f"{name} must be (T, {H}, {D}), got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (H is not None and shape[1] != H):
+        raise ValueError(f"{name} must be (T, {'H' if H is None else H}, {D}), got {tuple(shape)}")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
     if t.get_device() != at:
@@ -1095,16 +1113,16 @@ def _rows_of(t, H, D, at, name):
     s_t, s_h, s_c = t.stride()
     if s_c != 1:
         raise ValueError(f"{name}'s last dim must be contiguous")
-    return s_t, s_h
+    return shape[0], shape[1], s_t, s_h
 
 
 def _paged_tables(cache, page_table, q_start, kv_len, at):
     """S and width, the step's three arrays checked."""
     import torch
-    i32 = torch.int32
-    if page_table.dim() != 2:
+    i32, shape = torch.int32, page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be (S, width)")
-    S, width = page_table.shape
+    S, width = shape
     if q_start.shape != (S + 1,) or kv_len.shape != (S,):
         raise ValueError(f"q_start must be {(S + 1,)} and kv_len {(S,)}, got {tuple(q_start.shape)} and {tuple(kv_len.shape)}")
     if not page_table.dtype == q_start.dtype == kv_len.dtype == i32:
@@ -1116,38 +1134,39 @@ def _paged_tables(cache, page_table, q_start, kv_len, at):
     return S, width
 
 
+_PAGED_DIMS, _PAGED_STRIDES = struct.Struct("8if"), struct.Struct("9q")  # pa_paged_dims, pa_paged_strides
+
+
 def pa_paged_append(cache, q, k, v, page_table, q_start, kv_len, rotary=None, positions=None, q_out=None, stream=None):
     """New tokens' keys and values into the cache, their queries rotated into
     q_out (see include/pa.h); q and q_out may both be None."""
     import torch
-    at = torch.cuda.current_device()
+    at, Hkv, D = torch.cuda.current_device(), cache.Hkv, cache.D
     S, width = _paged_tables(cache, page_table, q_start, kv_len, at)
-    n = _rows_of(k, cache.Hkv, cache.D, at, "k")
-    T = k.shape[0]
-    m = _rows_of(v, cache.Hkv, cache.D, at, "v")
-    if v.shape[0] != T or (T > 1 and m[0] != n[0]) or (cache.Hkv > 1 and m[1] != n[1]):
-        raise ValueError("v must have k's shape and strides")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    Hq, qs, os_ = cache.Hkv, (cache.D, cache.D), (cache.D, cache.D)
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs, os_ = _rows_of(q, Hq, cache.D, at, "q"), _rows_of(q_out, Hq, cache.D, at, "q_out")
-        if q.shape[0] != T or q_out.shape[0] != T:
+    T, _, n_t, n_h = _rows_of(k, Hkv, D, at, "k")
+    if _rows_of(v, Hkv, D, at, "v") != (T, Hkv, n_t, n_h):  # strides of dimensions of one are never used
+        Tv, _, m_t, m_h = _rows_of(v, Hkv, D, at, "v")
+        if Tv != T or (T > 1 and m_t != n_t) or (Hkv > 1 and m_h != n_h):
+            raise ValueError("v must have k's shape and strides")
+    Hq, q_t, q_h, o_t, o_h, q_ptr, o_ptr = Hkv, D * Hkv, D, D * Hkv, D, None, None
+    if q is not None and q_out is not None:
+        Tq, Hq, q_t, q_h = _rows_of(q, None, D, at, "q")
+        To, _, o_t, o_h = _rows_of(q_out, Hq, D, at, "q_out")
+        if Tq != T or To != T:
             raise ValueError(f"q and q_out must have k's {T} rows")
-    else:
-        qs = os_ = (cache.D * Hq, cache.D)
+        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out come together")
     pos = None
     if positions is not None:
         _want(positions, (T,), "positions")
         _on_current_device(positions)
         pos = _ptr(positions, torch.int32, "positions")
-    d = pa_paged_dims(S, T, Hq, cache.Hkv, cache.D, cache.pages, cache.page, width, 0.0)
-    _check(lib().pa_paged_append(ctypes.byref(d), ctypes.byref(pa_paged_strides(*qs, *n, *os_, *cache.strides)),
-                                 None if rotary is None else rotary.ref, None if q is None else q.data_ptr(), k.data_ptr(),
-                                 v.data_ptr(), page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), pos,
-                                 None if q_out is None else q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
-                                 _stream(stream)))
+    _check(lib().pa_paged_append(_PAGED_DIMS.pack(S, T, Hq, Hkv, D, cache.pages, cache.page, width, 0.0),
+                                 _PAGED_STRIDES.pack(q_t, q_h, n_t, n_h, o_t, o_h, *cache.strides),
+                                 None if rotary is None else rotary.ref, q_ptr, k.data_ptr(), v.data_ptr(),
+                                 page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), pos, o_ptr,
+                                 cache.k.data_ptr(), cache.v.data_ptr(), _stream(stream)))
 
 
 def paged_append(cache, q, k, v, page_table, q_start, kv_len, rotary=None, positions=None, q_out=None):
@@ -1182,20 +1201,22 @@ def pa_paged_fwd(q, cache, page_table, q_start, kv_len, out, lse, ws, scale=0.0,
     """Attention of a step's queries over the cache (see include/pa.h): out (T, Hq,
     D) bf16 and lse (T, Hq) fp32 are outputs."""
     import torch
-    at = torch.cuda.current_device()
+    at, D = torch.cuda.current_device(), cache.D
     S, width = _paged_tables(cache, page_table, q_start, kv_len, at)
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    qs, os_ = _rows_of(q, Hq, cache.D, at, "q"), _rows_of(out, Hq, cache.D, at, "out")
-    T = q.shape[0]
-    if out.shape[0] != T or lse.shape != (T, Hq):
+    T, Hq, q_t, q_h = _rows_of(q, None, D, at, "q")
+    To, _, o_t, o_h = _rows_of(out, Hq, D, at, "out")
+    if To != T or lse.shape != (T, Hq):
         raise ValueError(f"out must have q's shape and lse be {(T, Hq)}, got {tuple(out.shape)} and {tuple(lse.shape)}")
-    if lse.get_device() != at or ws.get_device() != at:
+    if lse.dtype != torch.float32 or ws.dtype != torch.uint8:
+        raise ValueError(f"lse must be float32 and ws uint8, got {lse.dtype} and {ws.dtype}")
+    if not (lse.is_contiguous() and ws.is_contiguous()):
+        raise ValueError("lse and ws must be contiguous")
+    if not lse.get_device() == ws.get_device() == at:
         raise ValueError(f"every tensor must be on the current CUDA device (cuda:{at})")
-    d = pa_paged_dims(S, T, Hq, cache.Hkv, cache.D, cache.pages, cache.page, width, scale)
-    _check(lib().pa_paged_fwd(ctypes.byref(d), ctypes.byref(pa_paged_strides(*qs, 0, 0, *os_, *cache.strides)), q.data_ptr(),
+    _check(lib().pa_paged_fwd(_PAGED_DIMS.pack(S, T, Hq, cache.Hkv, D, cache.pages, cache.page, width, scale),
+                              _PAGED_STRIDES.pack(q_t, q_h, 0, 0, o_t, o_h, *cache.strides), q.data_ptr(),
                               cache.k.data_ptr(), cache.v.data_ptr(), page_table.data_ptr(), q_start.data_ptr(),
-                              kv_len.data_ptr(), out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(ws, torch.uint8, "ws"),
-                              ws.numel(), _stream(stream)))
+                              kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def paged_forward(q, cache, page_table, q_start, kv_len, scale=0.0, out=None, lse=None, ws=None):

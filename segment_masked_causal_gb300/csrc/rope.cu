@@ -81,38 +81,44 @@ cudaError_t launch_vec(RopeArgs& a, bool rest, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, a.rope.layout == PA_ROPE_INTERLEAVED ? rope_kernel<T, VEC, true> : rope_kernel<T, VEC, false>, a);
 }
 
-// Position of each token in its run of equal ids. A block takes 1,024 tokens of
-// a row; a thread's latest start of a run at or before each of its four tokens
-// comes from a scan of maxima, and the block looks back from its first token,
-// 4,096 ids at a time, for the start that the scan does not see.
+// Position of each token in its run of equal ids. A block takes 1,024 tokens of a row; a
+// thread's latest start of a run at or before each of its four tokens comes from a scan
+// of maxima. The start of the run that the block's first token continues lies before the
+// block: the 4,096 ids there are read along with its own, those further back only if
+// none of them starts one. Bound by the round trips: one, and one more for each 4,096 tokens of
+// a longer run.
 constexpr int kPosThreads = 256, kPosPer = 4, kPosTile = kPosThreads * kPosPer, kPosBack = 16;
-
-__device__ __forceinline__ int block_max(int v, int* sh) {
-  v = __reduce_max_sync(~0u, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int m = sh[0];
-#pragma unroll
-  for (int i = 1; i < kPosThreads / 32; ++i) m = max(m, sh[i]);
-  return m;
-}
 
 __global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* __restrict__ seg,
                                                                 int32_t* __restrict__ positions, int N, int tiles) {
-  __shared__ int sh[kPosThreads / 32];
+  __shared__ int sh[kPosThreads / 32], back[kPosThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x / tiles, n0 = (blockIdx.x - b * tiles) * kPosTile;
   const int32_t* row = seg + (int64_t)b * N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const auto starts = [&](int n) { return n == 0 || row[n] != row[n - 1]; };
+  // whether a run starts at n; false outside the row
+  const auto starts = [&](int n) { return n >= 0 && n < N && (n == 0 || row[n] != row[n - 1]); };
+  // the latest start among the kPosBack * kPosThreads tokens before hi that this thread sees
+  const auto look_back = [&](int hi) {
+    bool at[kPosBack];
+#pragma unroll
+    for (int j = 0; j < kPosBack; ++j) at[j] = starts(hi - 1 - (j * kPosThreads + (int)threadIdx.x));
+    int found = -1;
+#pragma unroll
+    for (int j = kPosBack - 1; j >= 0; --j)
+      if (at[j]) found = hi - 1 - (j * kPosThreads + (int)threadIdx.x);
+    return found;
+  };
+  bool own[kPosPer];
+#pragma unroll
+  for (int i = 0; i < kPosPer; ++i) own[i] = starts(n0 + threadIdx.x * kPosPer + i);
+  int found = look_back(n0);
   int at[kPosPer];  // latest start at or before token n0 + 4 thread + i, as far as this thread sees
   int last = -1;
 #pragma unroll
   for (int i = 0; i < kPosPer; ++i) {
-    const int n = n0 + threadIdx.x * kPosPer + i;
-    if (n < N && starts(n)) last = n;
+    if (own[i]) last = n0 + threadIdx.x * kPosPer + i;
     at[i] = last;
   }
   int before = last;  // inclusive scan over the warp, then over the block
@@ -121,22 +127,27 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* _
     const int v = __shfl_up_sync(~0u, before, o);
     if (lane >= o) before = max(before, v);
   }
-  if (lane == 31) sh[warp] = before;
+  found = __reduce_max_sync(~0u, found);
+  if (lane == 31) {
+    sh[warp] = before;
+    back[warp] = found;
+  }
   int excl = __shfl_up_sync(~0u, before, 1);
   if (lane == 0) excl = -1;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) excl = max(excl, sh[w]);
-  int from = -1;  // start of the run that the block's first token continues
-  if (!starts(n0)) {
-    for (int hi = n0; hi > 0 && from < 0; hi -= kPosThreads * kPosBack) {
-      int found = -1;
+  int from = -1;
 #pragma unroll
-      for (int j = 0; j < kPosBack; ++j) {
-        const int n = hi - 1 - (j * kPosThreads + (int)threadIdx.x);
-        if (n >= 0 && starts(n)) found = max(found, n);
-      }
-      from = block_max(found, sh);
-    }
+  for (int w = 0; w < kPosThreads / 32; ++w) {
+    if (w < warp) excl = max(excl, sh[w]);
+    from = max(from, back[w]);
+  }
+  for (int hi = n0 - kPosThreads * kPosBack; hi > 0 && from < 0; hi -= kPosThreads * kPosBack) {
+    found = __reduce_max_sync(~0u, look_back(hi));
+    __syncthreads();
+    if (lane == 0) back[warp] = found;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPosThreads / 32; ++w) from = max(from, back[w]);
   }
 #pragma unroll
   for (int i = 0; i < kPosPer; ++i) {
