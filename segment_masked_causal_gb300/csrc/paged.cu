@@ -54,7 +54,8 @@ constexpr int kCtas = 160;  // at most; the workspace's layout has room for as m
 constexpr int kThreads = 384;
 // Cost of an item besides its keys, in keys: what Q's load, the pipeline's turn and the
 // epilogue take.
-constexpr int kItemCost = 256;
+constexpr int kItemCost = 256, kPairItemCost = 640;
+constexpr float kPairCost = 1.8f;  // of a key for two tiles
 constexpr int kLeastVisits = 2;   // of a part of an item
 constexpr int kLeastCost = 512;   // of a CTA
 constexpr int kFew = 8;           // rows of an item that the tile holds four times
@@ -111,8 +112,8 @@ struct Partial {
 __host__ __device__ constexpr size_t partial_bytes(int D) { return sizeof(Partial) + (size_t)256 * D * 4; }
 constexpr size_t kOffRecords = 256, kOffPartials = kOffRecords + kCtas * sizeof(int4);
 
-// What a CTA left: the item that it began and did not end, if any (s, i, h, else s = -1),
-// and what its run begins with.
+// What a CTA left: the item that it began and did not end, if any (first row of q, rows of the
+// tile, else 0, kv head), and what its run begins with.
 enum Head : int { kWhole = 0, kGoesOn = 1, kEnds = 2, kEmpty = 3 };
 
 struct FwdArgs {
@@ -140,16 +141,19 @@ __device__ __forceinline__ int visits_of(const FwdArgs& a, const SeqRows& r, int
 // Costs of a sequence's items of one kv head, in keys: item i's and all before it. They are
 // fp32, since they only have to be the same in every CTA, and never to fall as i rises.
 struct Costs {
-  float A, per;
+  float A, per, w;
   int ql, n;
   __device__ __forceinline__ Costs(const FwdArgs& a, const SeqRows& r) {
     ql = r.b - r.a;
     n = items_of(a, ql);
     per = (float)(2 * a.TQ);
-    A = (float)min(max(r.base(), 0), a.p.width * a.p.page) + (float)kItemCost;
+    // a sequence of more than a tile is taken as made of pairs of them
+    w = ql > a.TQ ? kPairCost : 1.f;
+    per *= w;
+    A = w * (float)min(max(r.base(), 0), a.p.width * a.p.page) + (float)(ql > a.TQ ? kPairItemCost : kItemCost);
   }
   __device__ __forceinline__ float before(int i) const { return (A + 0.5f * per * (float)(i + 1)) * (float)i; }
-  __device__ __forceinline__ float of(int i) const { return A + (i == n - 1 ? (float)ql : per * (float)(i + 1)); }
+  __device__ __forceinline__ float of(int i) const { return A + (i == n - 1 ? w * (float)ql : per * (float)(i + 1)); }
   // of the whole sequence and all kv heads, in units of 2^shift keys: the sum over a step fits 32 bits
   __device__ __forceinline__ uint32_t scaled(const FwdArgs& a) const {
     return n ? max(1u, __float2uint_rd((before(n - 1) + of(n - 1)) * (float)a.p.Hkv * a.cost_scale)) : 0u;
@@ -475,9 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {  // what the second kernel has to know
       const Bound &b = m.ends[0], &e = m.ends[1];
       const bool same = b.s == e.s && b.i == e.i && b.h == e.h;
-      int4 rec = make_int4(-1, 0, 0, kWhole);
+      int4 rec = make_int4(0, 0, 0, kWhole);
       if (b.kt > 0 && b.kt < b.nkt) rec.w = !same ? kEnds : e.kt == b.kt ? kEmpty : e.kt == e.nkt ? kEnds : kGoesOn;
-      if (e.kt > 0 && e.kt < e.nkt && !(same && b.kt > 0)) rec = make_int4(e.s, e.i, e.h, rec.w);
+      if (e.kt > 0 && e.kt < e.nkt && !(same && b.kt > 0)) {
+        const int t0 = e.i * 2 * a.TQ;
+        rec = make_int4(e.r.a + t0, min(2 * a.TQ, e.r.b - e.r.a - t0) * a.p.G, e.h, rec.w);
+      }
       reinterpret_cast<int4*>(a.ws + kOffRecords)[blockIdx.x] = rec;
     }
     __syncwarp();
@@ -958,14 +965,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the item that CTA blockIdx.x began and did not end, 32 of its rows a
-// block. What it reads hangs on the records alone, so that all of it is under way after one
-// round trip: a thread takes four columns of a row, of every n-th part where rows are few.
-constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinAhead = 4;
+// Joins the parts of the item that CTA blockIdx.x began and did not end, 16 of its rows at a
+// time. What it reads hangs on the records alone, so that all of it is under way after one
+// round trip: a thread takes four columns of a row (or of two), of every n-th part where rows are
+// few, and has eight loads in flight.
+constexpr int kJoinThreads = 256, kJoinRows = 16, kJoinAhead = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ int slots[kCtas + 1];
-  __shared__ float wt[kCtas][kJoinRows], sum[kJoinRows], top[kJoinRows];
+  __shared__ float2 ml[kCtas][kJoinRows];  // the parts' maxima and sums, then their weights
+  __shared__ float2 sum[kJoinRows];        // the rows' maxima and sums
   __shared__ float4 share[kJoinThreads];
   __shared__ int count;
   constexpr int C4 = D / 4;
@@ -974,106 +983,115 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int4* recs = reinterpret_cast<const int4*>(a.ws + kOffRecords);
   const int P = gridDim.x, tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
   const int4 rec = recs[b];
-  if (rec.x < 0) return;
-  const SeqRows r = seq_rows(a.p, rec.x);
+  int head = b + 1 + lane < P ? recs[b + 1 + lane].w : kWhole;
+  if ((int)blockIdx.y * kJoinRows >= rec.y) return;
   if (tid < 32) {  // the parts: this CTA's, then the following ones' up to the one that ends the item
     int n = 1;
-    bool more = true;
 #pragma unroll 1
-    for (int c0 = b + 1; more && c0 < P; c0 += 32) {
-      const int c = c0 + lane, head = c < P ? recs[c].w : kWhole;
+    for (int c0 = b + 1;; c0 += 32) {
       const uint32_t stop = __ballot_sync(~0u, head != kGoesOn && head != kEmpty);
       const uint32_t upto = stop ? (2u << (__ffs(stop) - 1)) - 1u : ~0u;  // lanes up to the first that ends it
       const uint32_t part = __ballot_sync(~0u, head == kGoesOn || head == kEnds) & upto;
-      if ((part >> lane) & 1) slots[n + __popc(part & ((1u << lane) - 1u))] = c * 2;
+      if ((part >> lane) & 1) slots[n + __popc(part & ((1u << lane) - 1u))] = (c0 + lane) * 2;
       n += __popc(part);
-      more = stop == 0;
+      if (stop) break;
+      head = c0 + 32 + lane < P ? recs[c0 + 32 + lane].w : kWhole;
     }
     if (lane == 0) {
       slots[0] = b * 2 + 1;
       count = n;
     }
   }
-  const int row0 = r.a + rec.y * 2 * a.TQ, all = min(2 * a.TQ, r.b - row0) * a.p.G;
-  const int first = blockIdx.y * kJoinRows, rows = min(kJoinRows, all - first);
-  if (rows <= 0) return;
   __syncthreads();
-  const int n = count, E = rows * C4;
+  const int n = count;
   const uint8_t* parts = a.ws + kOffPartials;
-  const int groups = E >= kJoinThreads ? 1 : kJoinThreads / E;  // threads of an element
-  const int grp = groups == 1 ? 0 : tid / E, e0 = groups == 1 ? tid : tid - grp * E;
-  const auto o_of = [&](int k, int e) {
-    const int c = e / rows, row = e - c * rows;
-    return reinterpret_cast<const float4*>(parts + slots[k] * partial_bytes(D) + sizeof(Partial)) + c * 256 + first + row;
-  };
-  float4 ahead[kJoinAhead];
-#pragma unroll
-  for (int i = 0; i < kJoinAhead; ++i)
-    if (grp < groups && e0 < E && grp + i * groups < n) ahead[i] = *o_of(grp + i * groups, e0);
-  // the parts' weights, a warp a row
 #pragma unroll 1
-  for (int row = tid >> 5; row < rows; row += kJoinThreads / 32) {
-    const auto stat = [&](int k) { return reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D)); };
-    float M = -INFINITY, l = 0.f, m0 = -INFINITY, l0 = 0.f;
-    if (lane < n) {
-      m0 = stat(lane)->m[first + row];
-      l0 = stat(lane)->l[first + row];
-    }
-    M = m0;
-#pragma unroll 1
-    for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, stat(k)->m[first + row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    const float w0 = weight(m0, M);
-    if (lane < n) wt[lane][row] = w0;
-    l = l0 * w0;
-#pragma unroll 1
-    for (int k = lane + 32; k < n; k += 32) {
-      const float x = weight(stat(k)->m[first + row], M);
-      wt[k][row] = x;
-      l = fmaf(stat(k)->l[first + row], x, l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) {
-      sum[row] = l;
-      top[row] = M;
-    }
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int e = e0; e < E; e += kJoinThreads) {  // (one round where threads share an element)
-    const int c = e / rows, row = e - c * rows;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto add = [&](const float4& v, float x) {
-      o.x = fmaf(v.x, x, o.x);
-      o.y = fmaf(v.y, x, o.y);
-      o.z = fmaf(v.z, x, o.z);
-      o.w = fmaf(v.w, x, o.w);
+  for (int first = blockIdx.y * kJoinRows; first < rec.y; first += gridDim.y * kJoinRows) {
+    // rows and columns of this round: 4, 8 or 16 rows, an element a thread, two or a share of one
+    const int rows = min(kJoinRows, rec.y - first), shift = rows <= 4 ? 2 : rows <= 8 ? 3 : 4;
+    const int E = C4 << shift, per = E > kJoinThreads ? 2 : 1, groups = per == 2 ? 1 : kJoinThreads / E;
+    const int grp = per == 2 ? 0 : tid / E, e0 = tid - grp * E, row = e0 & ((1 << shift) - 1);  // E is a multiple of 1 << shift
+    const bool on = row < rows && grp < groups;
+    const auto o_of = [&](int k, int e) {
+      return *(reinterpret_cast<const float4*>(parts + slots[k] * partial_bytes(D) + sizeof(Partial)) + (e >> shift) * 256 + first + row);
     };
-    if (grp < groups) {
-      int k = grp;
-      if (e == e0) {
+    float4 ahead[kJoinAhead];
 #pragma unroll
-        for (int i = 0; i < kJoinAhead; ++i, k += groups)
-          if (k < n) add(ahead[i], wt[k][row]);
+    for (int i = 0; i < kJoinAhead; ++i) {
+      const int e = e0 + (per == 2 && i >= kJoinAhead / 2 ? kJoinThreads : 0), k = per == 2 ? i % (kJoinAhead / 2) : grp + i * groups;
+      if (on && e < E && k < n) ahead[i] = o_of(k, e);
+    }
+#pragma unroll 1
+    for (int e = tid; e < n * kJoinRows; e += kJoinThreads) {
+      const int k = e / kJoinRows, r = e % kJoinRows;
+      const Partial& pt = *reinterpret_cast<const Partial*>(parts + slots[k] * partial_bytes(D));
+      ml[k][r] = make_float2(pt.m[first + r], pt.l[first + r]);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = tid >> 5; r < rows; r += kJoinThreads / 32) {  // a warp a row
+      float M = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[k][r].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+#pragma unroll 1
+      for (int k = lane; k < n; k += 32) {
+        const float2 v = ml[k][r];
+        const float x = weight(v.x, M);
+        ml[k][r].x = x;
+        l = fmaf(v.y, x, l);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+      if (lane == 0) sum[r] = make_float2(M, l);
+    }
+    __syncthreads();
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const auto add = [](float4& to, const float4& v, float x) {
+      to.x = fmaf(v.x, x, to.x);
+      to.y = fmaf(v.y, x, to.y);
+      to.z = fmaf(v.z, x, to.z);
+      to.w = fmaf(v.w, x, to.w);
+    };
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) {
+        const int second = per == 2 && i >= kJoinAhead / 2, k = per == 2 ? i % (kJoinAhead / 2) : grp + i * groups;
+        if (e0 + second * kJoinThreads < E && k < n) {
+          if (second)
+            add(o[1], ahead[i], ml[k][row].x);
+          else
+            add(o[0], ahead[i], ml[k][row].x);
+        }
       }
 #pragma unroll 4
-      for (; k < n; k += groups) add(*o_of(k, e), wt[k][row]);
+      for (int k = per == 2 ? kJoinAhead / 2 : grp + kJoinAhead * groups; k < n; k += groups) {
+        add(o[0], o_of(k, e0), ml[k][row].x);
+        if (e0 + kJoinThreads < E) add(o[1], o_of(k, e0 + kJoinThreads), ml[k][row].x);
+      }
     }
     if (groups > 1) {
-      share[tid] = o;
+      share[tid] = o[0];
       __syncthreads();
-      if (grp > 0) break;
+      if (on && grp == 0)
 #pragma unroll 1
-      for (int i = 1; i < groups; ++i) add(share[i * E + e], 1.f);
+        for (int i = 1; i < groups; ++i) add(o[0], share[i * E + e0], 1.f);
     }
-    const float l = sum[row], inv = l > 0.f ? 1.f / l : 0.f;
-    const int tok = (first + row) / a.p.G, head = rec.z * a.p.G + (first + row - tok * a.p.G);
-    const int64_t at = row0 + tok;
-    *reinterpret_cast<uint2*>(a.out + at * a.p.o_t + (int64_t)head * a.p.o_h + c * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (c == 0) a.lse[at * a.p.Hq + head] = top[row] * 0.6931471805599453f + logf(l);
+    if (on && grp == 0) {
+      const float2 t = sum[row];
+      const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
+      const int tok = (first + row) / a.p.G, h = rec.z * a.p.G + (first + row - tok * a.p.G);
+      const int64_t at = rec.x + tok;
+      __nv_bfloat16* out = a.out + at * a.p.o_t + (int64_t)h * a.p.o_h;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (e0 + i * kJoinThreads < E)
+          *reinterpret_cast<uint2*>(out + ((e0 + i * kJoinThreads) >> shift) * 4) =
+              make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+      if (e0 >> shift == 0) a.lse[at * a.p.Hq + h] = t.x * 0.6931471805599453f + logf(t.y);
+    }
+    __syncthreads();  // the next rows' statistics take the place of these
   }
 }
 
@@ -1113,7 +1131,7 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, tq, tf, tk, tv, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, (std::min(2 * a.TQ, p.T) * p.G + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(ctas, std::min(8, (std::min(2 * a.TQ, p.T) * p.G + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
@@ -1131,7 +1149,7 @@ cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pa
   a.TQf = std::max(1, kFew / p.G);
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
   // All that a step can cost: the units that its sum is counted in, and the CTAs that it can keep busy.
-  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * ((double)p.width * p.page + 2.0 * a.TQ + kItemCost);
+  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * (kPairCost * ((double)p.width * p.page + 2.0 * a.TQ) + kPairItemCost);
   double unit = 1;
   while (most > 2e9 * unit) unit *= 2;
   a.cost_scale = (float)(1 / unit);
