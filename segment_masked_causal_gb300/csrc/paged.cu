@@ -56,7 +56,7 @@ constexpr int kThreads = 384;
 // epilogue take.
 constexpr int kItemCost = 256, kPairItemCost = 640;
 constexpr float kPairCost = 1.8f;  // of a key for two tiles
-constexpr int kLeastVisits = 2;   // of a part of an item
+constexpr int kLeastVisits = 3, kLeastPairVisits = 4;  // of a part of an item
 constexpr int kLeastCost = 512;   // of a CTA
 constexpr int kFew = 8;           // rows of an item that the tile holds four times
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
@@ -71,8 +71,12 @@ struct Layout {
   static constexpr uint32_t OFF_K = 2 * TB, OFF_V = OFF_K + NS * TB, OFF_STAGE = OFF_V + NS * TB;
   static constexpr uint32_t MISC = 4096;
   static constexpr uint32_t SMEM = OFF_STAGE + 8 * kStage + MISC + 1024;
-  // TMEM: a stream's O, and its S with P over the first half of it
-  static constexpr uint32_t TM_O = 0, TM_S = 256, TMEM_COLS = 512;
+  // TMEM: the streams' O, P and S. Heads of 64 leave room for P beside S, so that the next S is
+  // formed during the second product (64 requests of 8,000 keys: 182 -> 174 us); else P lies over
+  // the first half of its S.
+  static constexpr bool OWN_P = D == 64;
+  static constexpr uint32_t TM_O = 0, LD_O = OWN_P ? 64 : 128, TM_S = 256, TM_P = OWN_P ? 128 : TM_S, LD_P = OWN_P ? 64 : 128,
+                            TMEM_COLS = 512;
 };
 
 // A place on the line of work: before visit kt of item (s, i, h), of nkt visits.
@@ -94,7 +98,7 @@ constexpr int kItems = 4;
 
 struct Misc {
   uint64_t q_full[2], q_free[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], sums[2], group[2], fin_s, fin_pv;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2], sums[2], group[2], fin_s, fin_pv;
   uint64_t item_full[kItems], item_free[kItems];
   uint32_t tmem_base;
   int abort_flag;
@@ -161,8 +165,8 @@ struct Costs {
 };
 
 // Where `units` of sequence s's cost lie: a function of them that never falls as they rise,
-// so that the end of one run is the start of the next. A cut that would leave fewer than
-// kLeastVisits on one of its sides moves to the item's end on that side.
+// so that the end of one run is the start of the next. A cut that would leave fewer visits than
+// a join is worth on one of its sides moves to the item's end on that side.
 __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r, uint32_t units) {
   const Costs c(a, r);
   const float H = (float)a.p.Hkv, x = __fdividef((float)units, a.cost_scale * H);  // of one kv head's line
@@ -183,9 +187,10 @@ __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r
   b.r = r;
   b.nkt = visits_of(a, r, i);
   b.kt = min((int)((part - (float)b.h) * (float)b.nkt), b.nkt - 1);
-  if (b.kt < kLeastVisits)
+  const int least = c.ql > a.TQ ? kLeastPairVisits : kLeastVisits;
+  if (b.kt < least)
     b.kt = 0;
-  else if (b.nkt - b.kt < kLeastVisits)
+  else if (b.nkt - b.kt < least)
     b.kt = b.nkt;
   return b;
 }
@@ -422,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.q_full[s], 1);
       mbar_init(&m.q_free[s], 1);
       mbar_init(&m.s_full[s], 2);  // the S issuer itself, and its products
-      mbar_init(&m.p_full[s], 4);  // the four warps of the stream's group
+      mbar_init(&m.s_free[s], 4);  // the four warps of the stream's group
+      mbar_init(&m.p_full[s], 4);
       mbar_init(&m.pv_done[s], 1);
       mbar_init(&m.o_free[s], 8);  // both groups' warps, or those of one group twice
       mbar_init(&m.sums[s], 4);
@@ -603,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
 #pragma unroll 1
         for (int gs = lo; gs <= hi; ++gs) {
-          // the stream's last P, which lies over its S, has been read
-          if ((had >> gs) & 1 && !(ok = g.wait_warp(&m.pv_done[gs], ((odd >> gs) & 1) ^ 1, 5))) break;
+          // the stream's last S has been read, and its P, where that lies over S
+          if ((had >> gs) & 1 && !(ok = g.wait_warp(L::OWN_P ? &m.s_free[gs] : &m.pv_done[gs], ((odd >> gs) & 1) ^ 1, 5))) break;
           had |= 1u << gs;
           odd ^= 1u << gs;
           tc_fence_after();
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             held |= bit;
             held_odd ^= bit;
           }
-          const uint32_t tO = tmem + L::TM_O + gs * 128, tP = tmem + L::TM_S + gs * 128;
+          const uint32_t tO = tmem + L::TM_O + gs * L::LD_O, tP = tmem + L::TM_P + gs * L::LD_P;
           const bool add = !(fresh & bit);
           if (!(ok = g.wait_warp(&m.p_full[gs], (odd >> gs) & 1, 9))) break;
           tc_fence_after();
@@ -717,7 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tO = tmem + lane_base + L::TM_O, tS = tmem + lane_base + L::TM_S + grp * 128;
+    const uint32_t tO = tmem + lane_base + L::TM_O, tS = tmem + lane_base + L::TM_S + grp * 128,
+                   tP = tmem + lane_base + L::TM_P + grp * L::LD_P;
     const float sl2 = a.p.scale_log2;
     const uint64_t sc = f2(sl2, sl2);
     // visits of this stream, phases of its group's barrier, uses of its statistics and of the other's
@@ -741,6 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; kt < it.kt1; kt += step, ++nv) {
         if (!(ok = g.wait_warp(&m.s_full[grp], nv & 1, 10))) break;
         if (!active) {  // in step with the others, nothing to do
+          if (L::OWN_P) {
+            warp_arrive(&m.s_free[grp], lane);
+            if (nv > 0 && !(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+          }
           warp_arrive(&m.p_full[grp], lane);
           continue;
         }
@@ -754,17 +765,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (few) {
           uint32_t x[32];
           tmem_ld32(tS + quarter * 32, x);
+          if (L::OWN_P) {
+            tc_fence_before();
+            warp_arrive(&m.s_free[grp], lane);
+          }
           if (masked) hide32(x, seen32(seen, k0 + quarter * 32, quarter * 32, bad, a.page_shift));
           f = advance(u, max32(x) * sl2, mine_row, rescale);
-          if (rescale && any) scale_o<D>(tO + grp * 128, f);
+          if (L::OWN_P && nv > 0) {  // the last P has been read
+            if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+            tc_fence_after();
+          }
+          if (rescale && any) scale_o<D>(tO + grp * L::LD_O, f);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
-          exp_store32<false>(x, sc, f2(-moff, -moff), tS + quarter * 16, t2, none);
+          exp_store32<false>(x, sc, f2(-moff, -moff), tP + quarter * 16, t2, none);
           const uint32_t zero[16] = {};
 #pragma unroll
-          for (int q = 1; q < 4; ++q) tmem_st16_nowait(tS + ((quarter + q) & 3) * 16, zero);
+          for (int q = 1; q < 4; ++q) tmem_st16_nowait(tP + ((quarter + q) & 3) * 16, zero);
         } else {
           uint32_t x0[32], x1[32], x2[32], x3[32];
           tmem_ld128(tS, x0, x1, x2, x3);
+          if (L::OWN_P) {
+            tc_fence_before();
+            warp_arrive(&m.s_free[grp], lane);
+          }
           if (masked) {
             hide32(x0, seen32(seen, k0, 0, bad, a.page_shift));
             hide32(x1, seen32(seen, k0 + 32, 32, bad, a.page_shift));
@@ -772,14 +795,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
           }
           f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, mine_row, rescale);
-          // the stream's last product has ended (its S was formed after it), so O stands still
-          if (rescale && any) scale_o<D>(tO + grp * 128, f);
+          if (L::OWN_P && nv > 0) {
+            if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+            tc_fence_after();
+          }
+          // the stream's last product has ended (its S was formed after it, or see above), so O stands still
+          if (rescale && any) scale_o<D>(tO + grp * L::LD_O, f);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           const uint64_t off = f2(-moff, -moff);
-          exp_store32<false>(x0, sc, off, tS, t2, none);
-          exp_store32<false>(x1, sc, off, tS + 16, t2, none);
-          exp_store32<false>(x2, sc, off, tS + 32, t2, none);
-          exp_store32<false>(x3, sc, off, tS + 48, t2, none);
+          exp_store32<false>(x0, sc, off, tP, t2, none);
+          exp_store32<false>(x1, sc, off, tP + 16, t2, none);
+          exp_store32<false>(x2, sc, off, tP + 32, t2, none);
+          exp_store32<false>(x3, sc, off, tP + 48, t2, none);
         }
         u.l2 = add2(u.l2, t2);
         any = true;
@@ -844,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fa *= inv;
         fb *= inv;
       }
-      const uint32_t tA = tO + (halves ? 0 : grp * 128), tB = tO + 128;
+      const uint32_t tA = tO + (halves ? 0 : grp * L::LD_O), tB = tO + L::LD_O;
       if (mine_row && c_lo == 0 && (!few || quarter == 0)) {
         if (whole) {
           a.lse[t * a.p.Hq + head] = M * 0.6931471805599453f + logf(lt);
