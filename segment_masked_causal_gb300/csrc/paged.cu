@@ -26,7 +26,8 @@
 // Few rows. A TMEM lane belongs to one warp of four, so where an item has at most eight
 // rows the tile holds them four times and each of a group's warps takes 32 of a visit's
 // 128 keys (its P has zeros for the others); the four parts of a row are joined
-// at the item's end as well. With more rows that join costs more than it saves.
+// at the item's end as well (256 requests of 300 keys: 102 -> 82 us; 64 of up to 16,000: 89 -> 86). With
+// more rows that join costs more than it saves (33 x 5 tokens: 41 us with up to 32 rows, 38 without).
 //
 // The pipeline runs on from item to item: the next item's Q, K and V are loaded while the
 // last one's O is written. Pages arrive by TMA, one box per page and 64 columns, a lane
@@ -53,12 +54,17 @@ namespace {
 constexpr int kCtas = 160;  // at most; the workspace's layout has room for as many
 constexpr int kThreads = 384;
 // Cost of an item besides its keys, in keys: what Q's load, the pipeline's turn and the
-// epilogue take.
+// epilogue take; and of a key for two tiles. With one cost for all, a chunk of 2,001 tokens beside
+// 47 single ones took 148 us; with 1.4 and 448 124, with these 111, with 2.2 and 900 117.
 constexpr int kItemCost = 256, kPairItemCost = 640;
-constexpr float kPairCost = 1.8f;  // of a key for two tiles
-constexpr int kLeastVisits = 3, kLeastPairVisits = 4;  // of a part of an item
-constexpr int kLeastCost = 512;   // of a CTA
-constexpr int kFew = 8;           // rows of an item that the tile holds four times
+constexpr float kPairCost = 1.8f;
+// Visits of a part of an item: fewer are not worth a join (some 3 us, and the part's way through
+// memory). Against two: one token of 700 keys 14.8 -> 13.1 us, chunks of 512 tokens 56 -> 46 us.
+// An item of one tile and more rows than kFew has the longer visits: three of them are
+// worth it (33 x 5 tokens: 29.7 us, with four 31.3).
+constexpr int kLeastVisits = 4, kLeastVisitsOne = 3;
+constexpr int kLeastCost = 512;  // of a CTA; with 1,024 one token of 700 keys took 18.4 us instead of 14.8
+constexpr int kFew = 8;          // rows of an item that the tile holds four times, see above
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
 template <int D>
@@ -187,7 +193,7 @@ __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r
   b.r = r;
   b.nkt = visits_of(a, r, i);
   b.kt = min((int)((part - (float)b.h) * (float)b.nkt), b.nkt - 1);
-  const int least = c.ql > a.TQ ? kLeastPairVisits : kLeastVisits;
+  const int least = c.ql > a.TQ || c.ql * a.p.G <= kFew ? kLeastVisits : kLeastVisitsOne;
   if (b.kt < least)
     b.kt = 0;
   else if (b.nkt - b.kt < least)
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_ends(a, m.ends, reinterpret_cast<uint32_t*>(base + L::OFF_STAGE));
 
   // All roles count alike: ic the items, vc the visits (K and V stages; an item of one tile gives
-  // visit vc to stream vc & 1), n[g] those of stream g, qt the Q buffer of the next item of one tile.
+  // visit vc to stream vc & 1), qt the Q buffer of the next item of one tile.
   int ic = 0, vc = 0;
   bool ok = true;
   const auto next_item = [&](Item& it) {
@@ -701,8 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   umma_bf16_ta(tO, tP + kk * 8, sdesc_add(vd, kk * 2048), idO, (add || (steps & ((1u << kk) - 1u))) ? 1u : 0u);
             }
           }
-          __syncwarp();
-          if (!ok) break;
           odd ^= bit;
           fresh &= ~bit;
           if (leader) umma_commit(&m.pv_done[gs]);

@@ -130,6 +130,32 @@ def test_many_sequences(cuda_dev):
     s.check(*s.forward())
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (3, 1), (8, 1), (10, 2), (64, 1)])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_rows_of_a_tile(cuda_dev, Hq, Hkv, D):
+    """New tokens around the borders at which a tile is held four times, alone, or with
+    the next one: 8 and 128 rows, and what is left behind the last pair."""
+    G = Hq // Hkv
+    few, tile = max(1, 8 // G), 128 // G
+    counts = sorted({1, 2, few, few + 1, tile - 1, tile, tile + 1, 2 * tile - 1, 2 * tile, 2 * tile + 1, 5 * tile + 3} - {0})
+    s = Step([(n, n + 100 * (i % 3)) for i, n in enumerate(counts)], Hq, Hkv, D, 16, cuda_dev, seed=G + D)
+    s.check(*s.forward())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 40, 100])
+def test_items_cut_between_many(cuda_dev, D, new):
+    """Few items over a long context: each is cut into many parts, of one tile and of two."""
+    s = Step([(new, 12000 + new)], 4, 1, D, 128, cuda_dev, seed=D + new)
+    s.check(*s.forward())
+
+
+def test_costs_in_units_of_many_keys(cuda_dev):
+    """Tables so wide that the costs of a step cannot be counted in keys in 32 bits."""
+    s = Step([(1, 700), (90, 300), (2, 5000)], 8, 2, 64, 256, cuda_dev, seed=14, width=1 << 22)
+    s.check(*s.forward())
+
+
 @pytest.mark.parametrize("scale", [0.02, 1.0])
 def test_scale_and_large_scores(cuda_dev, scale):
     s = Step([(4, 500), (1, 77)], 4, 2, 128, 16, cuda_dev, seed=10)
