@@ -740,8 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    tP = tmem + lane_base + L::TM_P + grp * L::LD_P;
     const float sl2 = a.p.scale_log2;
     const uint64_t sc = f2(sl2, sl2);
-    // visits of this stream, phases of its group's barrier, uses of its statistics and of the other's
-    int nv = 0, gp = 0, ex = 0, ex_other = 0;
+    // visits of this stream, phases of its group's barrier and of the two groups'
+    int nv = 0, gp = 0, ex = 0;
     Item it;
     while (ok && next_item(it)) {
       const bool pair = is_pair(it), few = is_few(it);
@@ -829,10 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      if (!part) {  // the other stream's item alone
-        ++ex_other;
-        continue;
-      }
+      if (!part) continue;  // the other stream's item alone
       const bool halves = !pair && visits > 1;  // two streams' O to be joined, half of the columns each
       const bool whole = it.kt1 - it.kt0 == it.nkt;
       const int c_lo = halves ? grp * (L::DL / 2) : 0, c_hi = halves ? min(c_lo + L::DL / 2, D) : D;
@@ -850,12 +847,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.stat[grp][0][r] = M;
         m.stat[grp][1][r] = lt;
         tc_fence_before();
-        warp_arrive(&m.sums[grp], lane);
-        if (!(ok = g.wait_warp(&m.sums[grp], ex & 1, 12))) break;
-        ++ex;
+        // Both groups meet at each item that both have visits of, so neither is ever a phase of
+        // `sums` ahead; an item of one stream meets within its group.
+        warp_arrive(halves ? &m.sums[grp] : &m.group[grp], lane);
         if (halves) {
-          if (!(ok = g.wait_warp(&m.sums[grp ^ 1], ex_other & 1, 13))) break;
-          ++ex_other;
+          if (!(ok = g.wait_warp(&m.sums[grp], ex & 1, 12) && g.wait_warp(&m.sums[grp ^ 1], ex & 1, 13))) break;
+          ++ex;
+        } else {
+          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 12))) break;
+          ++gp;
         }
         tc_fence_after();
         const float *sa = m.stat[halves ? 0 : grp][0], *sb = m.stat[halves ? 1 : grp][0];  // a stream alone counts once

@@ -125,6 +125,21 @@ def test_long_and_many(cuda_dev, lens, Hq, Hkv, D):
     assert all(torch.equal(x, y) for x, y in zip(a, b))  # bit for bit
 
 
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("G,D", [(2, 64), (4, 128)])
+def test_items_of_every_kind_in_turn(cuda_dev, seed, G, D):
+    """Short items that one softmax group takes alone, items that both share and pairs of
+    tiles, one behind the other in every order: the groups meet where they have to."""
+    rng = np.random.default_rng(seed)
+    kinds = [(1, 60), (1, 130), (20, 100), (1, 300), (3, 90), (9, 520), (1, 700), (70, 260), (25, 400), (0, 0)]
+    lens = [kinds[i] for i in rng.choice(len(kinds), 700, p=[.2, .1, .2, .1, .1, .05, .1, .02, .08, .05])]
+    s = Step(lens, 2 * G, 2, D, 64, cuda_dev, seed=seed)
+    a = s.forward()
+    s.check(*a)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(a, s.forward()))
+
+
 def test_many_sequences(cuda_dev):
     s = Step([((i * 7) % 3, (i * 7) % 3 + i % 40) for i in range(3000)], 2, 1, 64, 16, cuda_dev, seed=9, tail=3)
     s.check(*s.forward())
