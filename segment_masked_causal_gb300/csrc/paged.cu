@@ -73,6 +73,11 @@ constexpr float kPairCost = 1.8f;
 // worth it (33 x 5 tokens: 29.7 us, with four 31.3).
 constexpr int kLeastVisits = 4, kLeastVisitsOne = 3;
 constexpr int kLeastCost = 512;  // of a CTA; with 1,024 one token of 700 keys took 18.4 us instead of 14.8
+// Visits of an item of few rows that one stream takes alone, so that its epilogue runs beside the
+// next item's visits (256 requests of 300 keys: 75.6 -> 71.9 us; with 5 instead 64 requests of up to
+// 16,000 keys lose 1%). More rows have longer visits, and take turns from two on (33 x 5 tokens: 30.6
+// us with three alone, 30.0 with one).
+constexpr int kAlone = 3;
 constexpr int kFew = 8;          // rows of an item that the tile holds four times, see above
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
@@ -107,7 +112,8 @@ struct alignas(16) Item {
   int s;              // sequence
   int kt0, kt1, nkt;  // visits of the part, and of the item
   int cap, seen0;     // keys in the cache; keys that the first token sees
-  int unused[3];
+  int turns, stream;  // visit vc goes to stream (vc & turns) | stream (a pair's visits to 0 and 1)
+  int unused;
 };
 constexpr int kItems = 4;
 
@@ -312,7 +318,7 @@ struct Walk {
   __device__ __forceinline__ Item item() const {
     const int t0 = i * 2 * a.TQ;
     return Item{r.a + t0, min(2 * a.TQ, r.b - r.a - t0), h, s, kt0, kt1, nkt, min(r.kv, a.p.width * a.p.page),
-                r.base() + t0 + 1, {0, 0, 0}};
+                r.base() + t0 + 1, 0, 0, 0};
   }
 
  private:
@@ -511,11 +517,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     const PageLanes pl(a, lane, NC);
     Walk w(a, m);
+    int turn = 0;                // the stream of the next item that one takes alone
     uint32_t used = 0, odd = 0;  // bits of the Q buffers: whether they were used, the parity of that
     int qt = 0;
     for (bool more = true; ok && more;) {
       more = w.next();
       Item it = more ? w.item() : Item{};
+      if (!is_pair(it)) {
+        it.turns = it.kt1 - it.kt0 > (is_few(it) ? kAlone : 1);
+        if (!it.turns) it.stream = turn, turn ^= 1;
+      }
       const int slot = ic % kItems;
       if (ic >= kItems && !(ok = g.wait_warp(&m.item_free[slot], (ic / kItems - 1) & 1, 19))) break;
       if (lane == 0) {
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = g.wait_warp(&m.k_full[sk], (vc / NS) & 1, 6))) break;
         const uint32_t bad = m.k_bad[sk];
         const uint64_t kd = sdesc_sw128(smem_u32(bK + sk * L::TB), 16, 1024);
-        const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
+        const int lo = (vc & it.turns) | it.stream, hi = lo + pair;
 #pragma unroll 1
         for (int gs = lo; gs <= hi; ++gs) {
           // the stream's last S has been read, and its P, where that lies over S
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (steps == 0) steps = 1;
         }
         const uint64_t vd = sdesc_sw128(smem_u32(bV + sv * L::TB), L::CHUNK, 1024);
-        const int lo = pair ? 0 : vc & 1, hi = pair ? 1 : lo;
+        const int lo = (vc & it.turns) | it.stream, hi = lo + pair;
 #pragma unroll 1
         for (int gs = lo; gs <= hi; ++gs) {
           const uint32_t bit = 1u << gs;
@@ -740,30 +751,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                    tP = tmem + lane_base + L::TM_P + grp * L::LD_P;
     const float sl2 = a.p.scale_log2;
     const uint64_t sc = f2(sl2, sl2);
-    // visits of this stream, phases of its group's barrier and of the two groups'
-    int nv = 0, gp = 0, ex = 0;
-    Item it;
-    while (ok && next_item(it)) {
-      const bool pair = is_pair(it), few = is_few(it);
-      const int t0 = pair ? grp * a.TQ : 0;  // this stream's first token of the item
-      const int rl = few ? lane : r, tok = t0 + rl / a.p.G;
-      const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
-      const bool mine_row = row < rows && rl < a.TQ * a.p.G;
-      const int first_seen = min(it.seen0 + t0, it.cap);  // keys that the first one sees
-      const int seen = min(it.seen0 + tok, it.cap);
-      const bool active = few || t0 + quarter * 32 / a.p.G < it.nt;  // some row of this warp is a token's
-      const int visits = it.kt1 - it.kt0, step = pair ? 1 : 2;
+    // Parities, in one register since the scores leave few: of this stream's visits (and whether it had
+    // any), of its group's barrier, of the two groups', of all visits; above them the items' number.
+    constexpr uint32_t NV = 1, HAD = 2, GP = 4, EX = 8, VC = 16, IC = 32;
+    uint32_t ph = 0;
+    // The item stays in its place until the epilogue has read it again, for its numbers would take
+    // registers from the scores in between.
+    for (; ok; ph += IC) {
+      const int ring = ph / IC % kItems;
+      if (!(ok = g.wait_warp(&m.item_full[ring], ph / (IC * kItems) & 1, 18))) break;
+      const Item& at = m.items[ring];
+      if (at.nt == 0) break;
+      const bool few = is_few(at);
+      int first_seen, seen, kt, kt1, step;
+      bool mine_row, active;
+      {
+        const Item it = at;
+        const bool pair = is_pair(it);
+        const int t0 = pair ? grp * a.TQ : 0;  // this stream's first token of the item
+        const int rl = few ? lane : r, tok = t0 + rl / a.p.G;
+        mine_row = t0 * a.p.G + rl < it.nt * a.p.G && rl < a.TQ * a.p.G;
+        first_seen = min(it.seen0 + t0, it.cap);  // keys that the first one sees
+        seen = min(it.seen0 + tok, it.cap);
+        active = few || t0 + quarter * 32 / a.p.G < it.nt;  // some row of this warp is a token's
+        step = 1 + it.turns;
+        kt = it.kt0;
+        if (it.turns)
+          kt += (int)(ph / VC & 1) != grp;
+        else if (!pair && it.stream != grp)
+          kt = it.kt1;
+        kt1 = it.kt1;
+        ph ^= (it.kt1 - it.kt0) & 1 ? VC : 0;
+      }
       Running u{-INFINITY, 0ull};
-      int kt = it.kt0 + (pair || (vc & 1) == grp ? 0 : 1);
-      vc += visits;
-      const bool part = kt < it.kt1;  // this stream has visits of the item
+      const bool part = kt < kt1;  // this stream has visits of the item
       bool any = false;
-      for (; kt < it.kt1; kt += step, ++nv) {
-        if (!(ok = g.wait_warp(&m.s_full[grp], nv & 1, 10))) break;
+      for (; kt < kt1; kt += step, ph = (ph ^ NV) | HAD) {
+        if (!(ok = g.wait_warp(&m.s_full[grp], ph & NV, 10))) break;
         if (!active) {  // in step with the others, nothing to do
           if (L::OWN_P) {
             warp_arrive(&m.s_free[grp], lane);
-            if (nv > 0 && !(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+            if ((ph & HAD) && !(ok = g.wait_warp(&m.pv_done[grp], ~ph & NV, 20))) break;
           }
           warp_arrive(&m.p_full[grp], lane);
           continue;
@@ -784,8 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (masked) hide32(x, seen32(seen, k0 + quarter * 32, quarter * 32, bad, a.page_shift));
           f = advance(u, max32(x) * sl2, mine_row, rescale);
-          if (L::OWN_P && nv > 0) {  // the last P has been read
-            if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+          if (L::OWN_P && (ph & HAD)) {  // the last P has been read
+            if (!(ok = g.wait_warp(&m.pv_done[grp], ~ph & NV, 20))) break;
             tc_fence_after();
           }
           if (rescale && any) scale_o<D>(tO + grp * L::LD_O, f);
@@ -797,10 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           uint32_t x0[32], x1[32], x2[32], x3[32];
           tmem_ld128(tS, x0, x1, x2, x3);
-          if (L::OWN_P) {
-            tc_fence_before();
-            warp_arrive(&m.s_free[grp], lane);
-          }
           if (masked) {
             hide32(x0, seen32(seen, k0, 0, bad, a.page_shift));
             hide32(x1, seen32(seen, k0 + 32, 32, bad, a.page_shift));
@@ -808,8 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
           }
           f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, mine_row, rescale);
-          if (L::OWN_P && nv > 0) {
-            if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 20))) break;
+          if (L::OWN_P && (ph & HAD)) {
+            if (!(ok = g.wait_warp(&m.pv_done[grp], ~ph & NV, 20))) break;
             tc_fence_after();
           }
           // the stream's last product has ended (its S was formed after it, or see above), so O stands still
@@ -818,6 +842,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t off = f2(-moff, -moff);
           exp_store32<false>(x0, sc, off, tP, t2, none);
           exp_store32<false>(x1, sc, off, tP + 16, t2, none);
+          // Loaded again, P lies over the first half at most: with all four held until here some registers
+          // go to memory, and other kernels of this loop took 2 to 10% longer.
+          tmem_ld32x2(tS + 64, tS + 96, x2, x3);
+          if (L::OWN_P) {
+            tc_fence_before();
+            warp_arrive(&m.s_free[grp], lane);
+          }
+          if (masked) {
+            hide32(x2, seen32(seen, k0 + 64, 64, bad, a.page_shift));
+            hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
+          }
           exp_store32<false>(x2, sc, off, tP + 32, t2, none);
           exp_store32<false>(x3, sc, off, tP + 48, t2, none);
         }
@@ -829,8 +864,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      if (!part) continue;  // the other stream's item alone
-      const bool halves = !pair && visits > 1;  // two streams' O to be joined, half of the columns each
+      if (!part) {  // the other stream's item alone
+        warp_arrive(&m.item_free[ring], lane);
+        continue;
+      }
+      const Item it = at;
+      const bool pair = is_pair(it);
+      const int t0 = pair ? grp * a.TQ : 0, rl = few ? lane : r, tok = t0 + rl / a.p.G;
+      const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
+      warp_arrive(&m.item_free[ring], lane);
+      const bool halves = it.turns;  // two streams' O to be joined, half of the columns each
       const bool whole = it.kt1 - it.kt0 == it.nkt;
       const int c_lo = halves ? grp * (L::DL / 2) : 0, c_hi = halves ? min(c_lo + L::DL / 2, D) : D;
       const int64_t t = it.row0 + tok;
@@ -840,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned long long dst = reinterpret_cast<unsigned long long>(a.out + t * a.p.o_t + (int64_t)head * a.p.o_h);
       const float2 lp = f2_split(u.l2);
       float M = u.m, lt = lp.x + lp.y, fa = 1.f, fb = 0.f;
-      if (!(ok = g.wait_warp(&m.pv_done[grp], (nv - 1) & 1, 11))) break;
+      if (!(ok = g.wait_warp(&m.pv_done[grp], ~ph & NV, 11))) break;
       tc_fence_after();
       if (!pair) {
         // what the rows' other parts have to know: of the other stream, and of a few rows' warps
@@ -851,11 +894,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // `sums` ahead; an item of one stream meets within its group.
         warp_arrive(halves ? &m.sums[grp] : &m.group[grp], lane);
         if (halves) {
-          if (!(ok = g.wait_warp(&m.sums[grp], ex & 1, 12) && g.wait_warp(&m.sums[grp ^ 1], ex & 1, 13))) break;
-          ++ex;
+          if (!(ok = g.wait_warp(&m.sums[grp], ph / EX & 1, 12) && g.wait_warp(&m.sums[grp ^ 1], ph / EX & 1, 13))) break;
+          ph ^= EX;
         } else {
-          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 12))) break;
-          ++gp;
+          if (!(ok = g.wait_warp(&m.group[grp], ph / GP & 1, 12))) break;
+          ph ^= GP;
         }
         tc_fence_after();
         const float *sa = m.stat[halves ? 0 : grp][0], *sb = m.stat[halves ? 1 : grp][0];  // a stream alone counts once
@@ -924,8 +967,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           warp_arrive(&m.group[grp], lane);
-          if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 14))) break;
-          ++gp;
+          if (!(ok = g.wait_warp(&m.group[grp], ph / GP & 1, 14))) break;
+          ph ^= GP;
           if (rr < rows && c0 + c4 < c_hi) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -940,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (c0 + cs < c_hi) {  // (the last step's sync is the next item's way here)
             warp_arrive(&m.group[grp], lane);
-            if (!(ok = g.wait_warp(&m.group[grp], gp & 1, 15))) break;
-            ++gp;
+            if (!(ok = g.wait_warp(&m.group[grp], ph / GP & 1, 15))) break;
+            ph ^= GP;
           }
         }
         if (!ok) break;
@@ -1171,6 +1214,10 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, tq, tf, tk, tv, a)) != cudaSuccess) return e;
+  // Nothing is cut, and nothing to be joined, where no context holds two parts' visits (one token
+  // of 700 keys: 13.1 -> 12.0 us).
+  const int visits = (p.width * p.page + kTile - 1) / kTile;
+  if (visits < 2 * ((int64_t)p.T * p.G <= kFew ? kLeastVisits : kLeastVisitsOne)) return cudaSuccess;
   cfg.gridDim = dim3(ctas, std::min(8, (std::min(2 * a.TQ, p.T) * p.G + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
