@@ -146,6 +146,7 @@ struct FwdArgs {
   int TQ;   // tokens of a tile; an item has two of them
   int TQf;  // tokens of one that has few rows
   int page_shift;
+  int g_inv;  // ceil(2^16 / G)
   int ctas;
   int least_cost;    // of a CTA, in units
   float cost_scale;  // units a key: a power of two
@@ -154,6 +155,8 @@ struct FwdArgs {
   uint8_t* ws;
 };
 
+// r / G, exact for a row of an item (r < 256, G <= 128) without a division's forty instructions.
+__device__ __forceinline__ int by_group(const FwdArgs& a, int r) { return (r * a.g_inv) >> 16; }
 __device__ __forceinline__ int items_of(const FwdArgs& a, int ql) {
   const int n = 2 * a.TQ;
   return ql <= n ? (ql > 0) : (ql + n - 1) / n;
@@ -248,26 +251,20 @@ __device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], ui
     if (lane >= o) v += u;
   }
   const uint32_t total = __shfl_sync(~0u, v, 31);
-  const uint32_t P = max(1u, min(gridDim.x, total / (uint32_t)a.least_cost));
+  // A run's share of the total, the same numbers in every CTA: as a fraction in 2^-32, which times
+  // c < P stays below one for any rounding of it.
+  const uint32_t P = max(1u, min(gridDim.x, __float2uint_rd(__fdividef((float)total, (float)a.least_cost))));
+  const uint32_t share32 = __float2uint_rd(__fdividef(4294967040.f, (float)P));
   const uint32_t c = blockIdx.x + (lane & 1);
-  uint32_t x = c >= P ? total : __umulhi(total, c * (0xFFFFFFFFu / P + 1));  // of lanes 0 and 1
-  int at = S;
-  uint32_t left = 0;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const uint32_t xe = __shfl_sync(~0u, x, e), hit = __ballot_sync(~0u, xe >= v - mine && xe < v);
-    const int from = hit ? __ffs(hit) - 1 : 0;
-    const uint32_t before = __shfl_sync(~0u, v - mine, from);
-    const SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
-    if (lane == e && hit) {
-      at = from;
-      left = xe - before;
-      if (S <= 32) ends[e].r = t;
-    }
-  }
+  const uint32_t x = c >= P ? total : __umulhi(total, c * share32);  // lane 0's end, and lane 1's
+  const uint32_t x0 = __shfl_sync(~0u, x, 0), x1 = __shfl_sync(~0u, x, 1);
+  const uint32_t hit0 = __ballot_sync(~0u, x0 >= v - mine && x0 < v), hit1 = __ballot_sync(~0u, x1 >= v - mine && x1 < v);
+  const uint32_t hit = lane ? hit1 : hit0;
+  const int from = hit ? __ffs(hit) - 1 : 0;
+  int at = hit ? from : S;
+  uint32_t left = x - __shfl_sync(~0u, v - mine, from);
+  SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
   if (lane < 2) {
-    SeqRows t{0, 0, 0};
-    if (at < S && S <= 32) t = ends[lane].r;
     if (at < S && S > 32) {
       int k = at * per;  // the thread's share, then the sequence in it
       while (left >= sums[k]) left -= sums[k++];
@@ -346,13 +343,15 @@ __device__ __forceinline__ int page_of(const FwdArgs& a, int s, int kt, int cap,
   return id;
 }
 // A producer's lanes: lane l brings chunk l / per of page l % per of a visit.
+static_assert(kTile == 128, "the shifts below");
 struct PageLanes {
   int per, box, page, chunk, lane;
   __device__ __forceinline__ PageLanes(const FwdArgs& a, int lane_, int NC) {
-    per = a.p.page >= kTile ? 1 : kTile / a.p.page;
+    const int shift = max(7 - a.page_shift, 0);
+    per = 1 << shift;
     box = min(a.p.page, kTile);
-    page = lane_ % per;
-    chunk = lane_ / per;
+    page = lane_ & (per - 1);
+    chunk = lane_ >> shift;
     lane = chunk < NC ? page : per;
   }
 };
@@ -769,11 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item it = at;
         const bool pair = is_pair(it);
         const int t0 = pair ? grp * a.TQ : 0;  // this stream's first token of the item
-        const int rl = few ? lane : r, tok = t0 + rl / a.p.G;
+        const int rl = few ? lane : r, tok = t0 + by_group(a, rl);
         mine_row = t0 * a.p.G + rl < it.nt * a.p.G && rl < a.TQ * a.p.G;
         first_seen = min(it.seen0 + t0, it.cap);  // keys that the first one sees
         seen = min(it.seen0 + tok, it.cap);
-        active = few || t0 + quarter * 32 / a.p.G < it.nt;  // some row of this warp is a token's
+        active = few || t0 + by_group(a, quarter * 32) < it.nt;  // some row of this warp is a token's
         step = 1 + it.turns;
         kt = it.kt0;
         if (it.turns)
@@ -823,15 +822,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 1; q < 4; ++q) tmem_st16_nowait(tP + ((quarter + q) & 3) * 16, zero);
         } else {
-          uint32_t x0[32], x1[32], x2[32], x3[32];
-          tmem_ld128(tS, x0, x1, x2, x3);
-          if (masked) {
-            hide32(x0, seen32(seen, k0, 0, bad, a.page_shift));
-            hide32(x1, seen32(seen, k0 + 32, 32, bad, a.page_shift));
-            hide32(x2, seen32(seen, k0 + 64, 64, bad, a.page_shift));
-            hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
+          // Twice through the scores, 64 at a time: maximum, then weights. Held all at once and unrolled
+          // they take every register and half of the loop's code, and its time hangs on how the
+          // compiler lays the rest out (a chunk of 4,096 of 8,192 tokens 320 to 367 us from one build to
+          // the next, now 330 to 333; 33 x 5 tokens 30.2 -> 28.5, a chunk beside 47 tokens 106 -> 102).
+          float ms = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t x0[32], x1[32];
+            tmem_ld32x2(tS + c, tS + c + 32, x0, x1);
+            if (masked) {
+              hide32(x0, seen32(seen, k0 + c, c, bad, a.page_shift));
+              hide32(x1, seen32(seen, k0 + c + 32, c + 32, bad, a.page_shift));
+            }
+            ms = fmax3(ms, max32(x0), max32(x1));
           }
-          f = advance(u, fmax3(fmaxf(max32(x0), max32(x1)), max32(x2), max32(x3)) * sl2, mine_row, rescale);
+          f = advance(u, ms * sl2, mine_row, rescale);
           if (L::OWN_P && (ph & HAD)) {
             if (!(ok = g.wait_warp(&m.pv_done[grp], ~ph & NV, 20))) break;
             tc_fence_after();
@@ -840,21 +846,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rescale && any) scale_o<D>(tO + grp * L::LD_O, f);
           const float moff = (u.m == -INFINITY) ? 0.f : u.m;
           const uint64_t off = f2(-moff, -moff);
-          exp_store32<false>(x0, sc, off, tP, t2, none);
-          exp_store32<false>(x1, sc, off, tP + 16, t2, none);
-          // Loaded again, P lies over the first half at most: with all four held until here some registers
-          // go to memory, and other kernels of this loop took 2 to 10% longer.
-          tmem_ld32x2(tS + 64, tS + 96, x2, x3);
-          if (L::OWN_P) {
-            tc_fence_before();
-            warp_arrive(&m.s_free[grp], lane);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t x0[32], x1[32];
+            tmem_ld32x2(tS + c, tS + c + 32, x0, x1);
+            if (L::OWN_P && c == 64) {
+              tc_fence_before();
+              warp_arrive(&m.s_free[grp], lane);
+            }
+            if (masked) {
+              hide32(x0, seen32(seen, k0 + c, c, bad, a.page_shift));
+              hide32(x1, seen32(seen, k0 + c + 32, c + 32, bad, a.page_shift));
+            }
+            exp_store32<false>(x0, sc, off, tP + c / 2, t2, none);
+            exp_store32<false>(x1, sc, off, tP + c / 2 + 16, t2, none);
           }
-          if (masked) {
-            hide32(x2, seen32(seen, k0 + 64, 64, bad, a.page_shift));
-            hide32(x3, seen32(seen, k0 + 96, 96, bad, a.page_shift));
-          }
-          exp_store32<false>(x2, sc, off, tP + 32, t2, none);
-          exp_store32<false>(x3, sc, off, tP + 48, t2, none);
         }
         u.l2 = add2(u.l2, t2);
         any = true;
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Item it = at;
       const bool pair = is_pair(it);
-      const int t0 = pair ? grp * a.TQ : 0, rl = few ? lane : r, tok = t0 + rl / a.p.G;
+      const int t0 = pair ? grp * a.TQ : 0, rl = few ? lane : r, tok = t0 + by_group(a, rl);
       const int rows = it.nt * a.p.G, row = t0 * a.p.G + rl;  // the item's rows, and this thread's
       warp_arrive(&m.item_free[ring], lane);
       const bool halves = it.turns;  // two streams' O to be joined, half of the columns each
@@ -942,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cs = rows > 4 ? 64 : 128, ld = cs + 4, f4 = cs == 64 ? 4 : 5;
         constexpr int part_ld = kStage / 4;
         float* st = reinterpret_cast<float*>(base + L::OFF_STAGE + grp * 4 * kStage);
-        const int e = threadIdx.x & 127, rr = e >> f4, c4 = (e & ((1 << f4) - 1)) * 4, tk = rr / a.p.G;
+        const int e = threadIdx.x & 127, rr = e >> f4, c4 = (e & ((1 << f4) - 1)) * 4, tk = by_group(a, rr);
         __nv_bfloat16* o = a.out + (it.row0 + tk) * a.p.o_t + (int64_t)(it.h * a.p.G + rr - tk * a.p.G) * a.p.o_h;
 #pragma unroll 1
         for (int c0 = c_lo; ok && c0 < c_hi; c0 += cs) {
@@ -1164,7 +1170,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (on && grp == 0) {
       const float2 t = sum[row];
       const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
-      const int tok = (first + row) / a.p.G, h = rec.z * a.p.G + (first + row - tok * a.p.G);
+      const int tok = by_group(a, first + row), h = rec.z * a.p.G + (first + row - tok * a.p.G);
       const int64_t at = rec.x + tok;
       __nv_bfloat16* out = a.out + at * a.p.o_t + (int64_t)h * a.p.o_h;
 #pragma unroll
@@ -1234,6 +1240,7 @@ cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pa
   a.p = p;
   a.TQ = kTile / p.G;
   a.TQf = std::max(1, kFew / p.G);
+  a.g_inv = (65536 + p.G - 1) / p.G;
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
   // All that a step can cost: the units that its sum is counted in, and the CTAs that it can keep busy.
   const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * (kPairCost * ((double)p.width * p.page + 2.0 * a.TQ) + kPairItemCost);
