@@ -35,14 +35,14 @@
 // that are not there are masked in S, and the second product leaves out the steps of 16
 // keys without any; what is left of the last one's rows of V is set to zero.
 //
-// What bounds it. Tokens of one each: DRAM (64 requests of 4,000 keys, heads 32 on 8 of 128: 169 us,
-// 0.91 of the copy bandwidth), below some 50 MB of keys the start of the pipeline, the last
-// epilogue and the join (one token of 100 keys 10 us). Long chunks: the chain of a stream, S 916
-// cycles, softmax 1,390, PV 790 and their hand-overs, 3,360 a visit of both against 2,048 of
-// tensor work (8,192 tokens of one prompt: 442 to 456 us, 0.62 of the matrix peak). One S buffer for
-// both streams with P beside it takes S out of that chain, but each S then waits for the other
-// stream to load the last one: 4,096 of 8,192 tokens 335 -> 328 us, 64 requests of one token 86 ->
-// 92, a chunk of 2,001 beside 47 single ones 111 -> 123.
+// What bounds it. Tokens of one each: DRAM (64 requests of 4,000 keys, heads 32 on 8 of 128: 163 us,
+// 0.94 of the copy bandwidth), below some 50 MB of keys the start of the pipeline, the last
+// epilogue and the join (one token of 100 keys 8.8 us). Long chunks: the chain of a stream (S, softmax,
+// PV and their hand-overs, 3,200 cycles a visit of both against 2,048 of tensor work), and the
+// code's size: the loops of all roles share the SM's instruction cache (8,192 tokens of one prompt:
+// 442 us, 0.63 of the matrix peak). One S buffer for both streams with P beside it takes PV
+// out of that chain, but each S then waits for the other stream to load the last one (a chunk of 2,001
+// beside 47 single tokens: 10 to 20% longer).
 //
 // Warp roles: 0 Q and K producer, 1 V producer, 2 S issuer and TMEM owner, 3 PV
 // issuer, 4..7 and 8..11 the softmax groups of streams 0 and 1.
@@ -63,22 +63,23 @@ namespace {
 constexpr int kCtas = 160;  // at most; the workspace's layout has room for as many
 constexpr int kThreads = 384;
 // Cost of an item besides its keys, in keys: what Q's load, the pipeline's turn and the
-// epilogue take; and of a key for two tiles. With one cost for all, a chunk of 2,001 tokens beside
-// 47 single ones took 148 us; with 1.4 and 448 124, with these 111, with 2.2 and 900 117.
-constexpr int kItemCost = 256, kPairItemCost = 640;
+// epilogue take; and of a key for two tiles. A chunk of 2,001 tokens beside 47 single ones takes 102 us
+// with these, 111 with 448 and 1.4 for pairs, 103 with 900 and 2.2, 104 with 384 for single
+// tiles; with 192 there 64 requests of up to 16,000 keys take 84.8 us instead of 83.5, and with 256
+// 33 x 5 tokens 29.9 instead of 27.1.
+constexpr int kItemCost = 320, kPairItemCost = 640;
 constexpr float kPairCost = 1.8f;
 // Visits of a part of an item: fewer are not worth a join (some 3 us, and the part's way through
-// memory). Against two: one token of 700 keys 14.8 -> 13.1 us, chunks of 512 tokens 56 -> 46 us.
-// An item of one tile and more rows than kFew has the longer visits: three of them are
-// worth it (33 x 5 tokens: 29.7 us, with four 31.3).
-constexpr int kLeastVisits = 4, kLeastVisitsOne = 3;
-constexpr int kLeastCost = 512;  // of a CTA; with 1,024 one token of 700 keys took 18.4 us instead of 14.8
+// memory), which is not launched at all where no context holds two parts. Against three: one
+// token of 700 keys 14.3 -> 11.7 us, chunks of 1,500 tokens 25.2 -> 19.9, but 8 chunks of 512 42.5 -> 45.1.
+constexpr int kLeastVisits = 4;
+constexpr int kLeastCost = 512;  // of a CTA; with 768 one token of 100 keys takes 10.6 us instead of 8.8
 // Visits of an item of few rows that one stream takes alone, so that its epilogue runs beside the
-// next item's visits (256 requests of 300 keys: 75.6 -> 71.9 us; with 5 instead 64 requests of up to
-// 16,000 keys lose 1%). More rows have longer visits, and take turns from two on (33 x 5 tokens: 30.6
+// next item's visits (256 requests of 300 keys: 75.6 -> 71.9 us; with five visits 64
+// requests of up to 16,000 keys lose 1%). More rows have longer visits, and take turns from two on (33 x 5 tokens: 30.6
 // us with three alone, 30.0 with one).
 constexpr int kAlone = 3;
-constexpr int kFew = 8;          // rows of an item that the tile holds four times, see above
+constexpr int kFew = 8;           // rows of an item that the tile holds four times, see above
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
 
 template <int D>
@@ -211,10 +212,9 @@ __device__ __forceinline__ Bound place(const FwdArgs& a, int s, const SeqRows& r
   b.r = r;
   b.nkt = visits_of(a, r, i);
   b.kt = min((int)((part - (float)b.h) * (float)b.nkt), b.nkt - 1);
-  const int least = c.ql > a.TQ || c.ql * a.p.G <= kFew ? kLeastVisits : kLeastVisitsOne;
-  if (b.kt < least)
+  if (b.kt < kLeastVisits)
     b.kt = 0;
-  else if (b.nkt - b.kt < least)
+  else if (b.nkt - b.kt < kLeastVisits)
     b.kt = b.nkt;
   return b;
 }
@@ -1220,10 +1220,8 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, tq, tf, tk, tv, a)) != cudaSuccess) return e;
-  // Nothing is cut, and nothing to be joined, where no context holds two parts' visits (one token
-  // of 700 keys: 13.1 -> 12.0 us).
-  const int visits = (p.width * p.page + kTile - 1) / kTile;
-  if (visits < 2 * ((int64_t)p.T * p.G <= kFew ? kLeastVisits : kLeastVisitsOne)) return cudaSuccess;
+  // Nothing is cut, and nothing to be joined, where no context holds two parts' visits.
+  if ((p.width * p.page + kTile - 1) / kTile < 2 * kLeastVisits) return cudaSuccess;
   cfg.gridDim = dim3(ctas, std::min(8, (std::min(2 * a.TQ, p.T) * p.G + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
