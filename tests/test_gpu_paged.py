@@ -125,6 +125,20 @@ def test_long_and_many(cuda_dev, lens, Hq, Hkv, D):
     assert all(torch.equal(x, y) for x, y in zip(a, b))  # bit for bit
 
 
+@pytest.mark.parametrize("visits", [6, 7, 8, 9])
+@pytest.mark.parametrize("G,D", [(4, 96), (8, 128), (1, 64)])
+def test_longest_context_without_a_cut(cuda_dev, visits, G, D):
+    """Contexts that fill the page table's width, just below and above what an item needs to be
+    cut: whole items leave no parts to be joined, longer ones do."""
+    n = visits * 128
+    s = Step([(1, n), (9, n), (140, n), (2, n - 1), (33, 70)], 2 * G, 2, D, 64, cuda_dev, seed=visits)
+    s.table = np.ascontiguousarray(s.table[:, :n // 64])
+    s.upload()
+    a, b = s.forward(), s.forward()
+    s.check(*a)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("seed", range(4))
 @pytest.mark.parametrize("G,D", [(2, 64), (4, 128)])
 def test_items_of_every_kind_in_turn(cuda_dev, seed, G, D):
