@@ -20,8 +20,9 @@
 // with P from TMEM. While one stream is in its softmax, the tensor cores work for the
 // other. An item of two tiles gives each stream a tile, and both take every visit (K and
 // V are read from shared memory for 256 rows); an item of one tile has its visits dealt out to
-// the streams in turn, whose sums and O are joined at its end. No stream ever waits for
-// the other's maximum, and O is rescaled, lazily, between a stream's own products.
+// the streams in turn, whose sums and O are joined at its end, or, with few visits, goes whole to
+// one of them. No stream ever waits for the other's maximum, and O is rescaled, lazily, between a
+// stream's own products.
 //
 // Few rows. A TMEM lane belongs to one warp of four, so where an item has at most eight
 // rows the tile holds them four times and each of a group's warps takes 32 of a visit's
@@ -36,11 +37,10 @@
 // keys without any; what is left of the last one's rows of V is set to zero.
 //
 // What bounds it. Tokens of one each: DRAM (64 requests of 4,000 keys, heads 32 on 8 of 128: 163 us,
-// 0.94 of the copy bandwidth), below some 50 MB of keys the start of the pipeline, the last
+// 0.95 of the copy bandwidth), below some 50 MB of keys the start of the pipeline, the last
 // epilogue and the join (one token of 100 keys 8.8 us). Long chunks: the chain of a stream (S, softmax,
-// PV and their hand-overs, 3,200 cycles a visit of both against 2,048 of tensor work), and the
-// code's size: the loops of all roles share the SM's instruction cache (8,192 tokens of one prompt:
-// 442 us, 0.63 of the matrix peak). One S buffer for both streams with P beside it takes PV
+// PV and their hand-overs, 3,200 to 3,700 cycles a visit of both against 2,048 of tensor work; 8,192
+// tokens of one prompt: 444 us, 0.63 of the matrix peak). One S buffer for both streams with P beside it takes PV
 // out of that chain, but each S then waits for the other stream to load the last one (a chunk of 2,001
 // beside 47 single tokens: 10 to 20% longer).
 //
@@ -76,8 +76,8 @@ constexpr int kLeastVisits = 4;
 constexpr int kLeastCost = 512;  // of a CTA; with 768 one token of 100 keys takes 10.6 us instead of 8.8
 // Visits of an item of few rows that one stream takes alone, so that its epilogue runs beside the
 // next item's visits (256 requests of 300 keys: 75.6 -> 71.9 us; with five visits 64
-// requests of up to 16,000 keys lose 1%). More rows have longer visits, and take turns from two on (33 x 5 tokens: 30.6
-// us with three alone, 30.0 with one).
+// requests of up to 16,000 keys lose 1%). More rows have longer visits, and take turns from two on
+// (33 x 5 tokens: 30.6 us with three alone, 30.0 with one).
 constexpr int kAlone = 3;
 constexpr int kFew = 8;           // rows of an item that the tile holds four times, see above
 constexpr int kStage = 2560;      // bytes of a softmax warp's staging buffer
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Twice through the scores, 64 at a time: maximum, then weights. Held all at once and unrolled
           // they take every register and half of the loop's code, and its time hangs on how the
           // compiler lays the rest out (a chunk of 4,096 of 8,192 tokens 320 to 367 us from one build to
-          // the next, now 330 to 333; 33 x 5 tokens 30.2 -> 28.5, a chunk beside 47 tokens 106 -> 102).
+          // the next, now 330 to 337; 33 x 5 tokens 30.2 -> 28.5, a chunk beside 47 tokens 106 -> 102).
           float ms = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 64) {
