@@ -694,6 +694,15 @@ pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* stride
                        const void* v_pages, const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len,
                        void* out, float* lse, void* ws, size_t ws_bytes, pa_stream_t stream);
 
+/*
+ * Self-test of how pa_paged_fwd deals out its work (host only, no device call): `units`
+ * becomes what a step costs, in the units that the kernel would count it in, by the
+ * kernel's own arithmetic. q_start (S + 1) and kv_len (S) are host memory here. The kernel adds
+ * the costs up in 32 bits, so with rising q_start the sum is below 2^32, whatever kv_len holds.
+ * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA, PA_ERR_SHAPE.
+ */
+pa_status pa_selftest_paged_units(const pa_paged_dims* dims, const int32_t* q_start, const int32_t* kv_len, uint64_t* units);
+
 /* Static, human-readable name of a status code. */
 const char* pa_status_string(pa_status s);
 

@@ -43,7 +43,7 @@ EXPORTS = ["pa_workspace_bytes", "pa_fwd", "pa_bwd", "pa_fwd_causal", "pa_bwd_ca
            "pa_bwd_fused_workspace_bytes", "pa_bwd_fused", "pa_logp_workspace_bytes", "pa_logp_plan", "pa_logp_fwd",
            "pa_logp_bwd_workspace_bytes", "pa_logp_bwd", "pa_ckpt_save", "pa_ckpt_load", "pa_bwd_ckpt_workspace_bytes",
            "pa_bwd_ckpt", "pa_rotary_frequencies", "pa_rotary_init", "pa_positions", "pa_rope", "pa_paged_append",
-           "pa_paged_workspace_bytes", "pa_paged_fwd", "pa_status_string"]
+           "pa_paged_workspace_bytes", "pa_paged_fwd", "pa_selftest_paged_units", "pa_status_string"]
 
 
 class LibraryMissing(RuntimeError):
@@ -189,6 +189,8 @@ def lib():
             L.pa_paged_workspace_bytes.restype = S
             L.pa_paged_fwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, S, P]
             L.pa_paged_fwd.restype = ctypes.c_int
+            L.pa_selftest_paged_units.argtypes = [P, P, P, P]
+            L.pa_selftest_paged_units.restype = ctypes.c_int
             L.pa_pack_first_fit.argtypes = [P, P, I32, P, I32, I32, I32, U64, U64, P, P, P, P, P, P, P]
             L.pa_pack_first_fit.restype = ctypes.c_int
             L.pa_status_string.argtypes = [ctypes.c_int]

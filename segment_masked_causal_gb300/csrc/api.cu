@@ -957,6 +957,18 @@ pa_status pa_paged_append(const pa_paged_dims* dims, const pa_paged_strides* str
 
 size_t pa_paged_workspace_bytes(int32_t D) { return D == 64 || D == 96 || D == 128 ? pa::paged_ws_bytes(D) : 0; }
 
+pa_status pa_selftest_paged_units(const pa_paged_dims* dims, const int32_t* q_start, const int32_t* kv_len, uint64_t* units) {
+  if (!dims) return PA_ERR_NULL;
+  const int64_t D = dims->D;
+  const pa_paged_strides s{D, D, D, D, D, D, D, D, D};
+  const pa_status why = paged_checks(dims, &s, false);
+  if (why != PA_OK) return why;
+  if (dims->Hq / dims->Hkv > 128) return PA_ERR_GQA;
+  if (!q_start || !kv_len || !units) return PA_ERR_NULL;
+  *units = pa::paged_units(paged_args(dims, &s, nullptr, q_start, kv_len));
+  return PA_OK;
+}
+
 pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* strides, const void* q, const void* k_pages,
                        const void* v_pages, const int32_t* page_table, const int32_t* q_start, const int32_t* kv_len,
                        void* out, float* lse, void* ws, size_t ws_bytes, pa_stream_t stream) {

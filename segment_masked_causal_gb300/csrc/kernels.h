@@ -215,6 +215,7 @@ struct PagedArgs {
 cudaError_t launch_append(const PagedArgs& p, const pa_rotary* rope, const void* q, const void* k, const void* v, int64_t n_t,
                           int64_t n_h, const int32_t* positions, void* q_out, void* k_pages, void* v_pages, cudaStream_t st);
 size_t paged_ws_bytes(int D);
+uint64_t paged_units(const PagedArgs& p);  // what a step costs; its arrays in host memory
 cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
                              void* ws, cudaStream_t st);
 

@@ -158,7 +158,7 @@ struct FwdArgs {
 
 // r / G, exact for a row of an item (r < 256, G <= 128) without a division's forty instructions.
 __device__ __forceinline__ int by_group(const FwdArgs& a, int r) { return (r * a.g_inv) >> 16; }
-__device__ __forceinline__ int items_of(const FwdArgs& a, int ql) {
+__host__ __device__ __forceinline__ int items_of(const FwdArgs& a, int ql) {
   const int n = 2 * a.TQ;
   return ql <= n ? (ql > 0) : (ql + n - 1) / n;
 }
@@ -168,25 +168,31 @@ __device__ __forceinline__ int visits_of(const FwdArgs& a, const SeqRows& r, int
   return e <= kTile ? 1 : (e + kTile - 1) / kTile;
 }
 // Costs of a sequence's items of one kv head, in keys: item i's and all before it. They are
-// fp32, since they only have to be the same in every CTA, and never to fall as i rises.
+// fp32, since they only have to be the same wherever they are computed (so each product that is added to
+// something is an fmaf, and none is left to the compiler), and never to fall as i rises.
 struct Costs {
   float A, per, w;
   int ql, n;
-  __device__ __forceinline__ Costs(const FwdArgs& a, const SeqRows& r) {
+  __host__ __device__ __forceinline__ Costs(const FwdArgs& a, const SeqRows& r) {
     ql = r.b - r.a;
     n = items_of(a, ql);
     per = (float)(2 * a.TQ);
     // a sequence of more than a tile is taken as made of pairs of them
     w = ql > a.TQ ? kPairCost : 1.f;
     per *= w;
-    A = w * (float)min(max(r.base(), 0), a.p.width * a.p.page) + (float)(ql > a.TQ ? kPairItemCost : kItemCost);
+    A = fmaf(w, (float)min(max(r.base(), 0), a.p.width * a.p.page), (float)(ql > a.TQ ? kPairItemCost : kItemCost));
   }
-  __device__ __forceinline__ float before(int i) const { return (A + 0.5f * per * (float)(i + 1)) * (float)i; }
-  __device__ __forceinline__ float of(int i) const { return A + (i == n - 1 ? w * (float)ql : per * (float)(i + 1)); }
-  // of the whole sequence and all kv heads, in units of 2^shift keys: the sum over a step fits 32 bits
-  __device__ __forceinline__ uint32_t scaled(const FwdArgs& a) const {
-    return n ? max(1u, __float2uint_rd((before(n - 1) + of(n - 1)) * (float)a.p.Hkv * a.cost_scale)) : 0u;
+  __host__ __device__ __forceinline__ float mean(int i) const { return fmaf(0.5f * per, (float)(i + 1), A); }
+  __host__ __device__ __forceinline__ float before(int i) const { return mean(i) * (float)i; }
+  __host__ __device__ __forceinline__ float of(int i) const {
+    return i == n - 1 ? fmaf(w, (float)ql, A) : fmaf(per, (float)(i + 1), A);
   }
+  // of the whole sequence and all kv heads, in units of 2^shift keys
+  __host__ __device__ __forceinline__ float units(const FwdArgs& a) const {
+    return fmaf(mean(n - 1), (float)(n - 1), of(n - 1)) * (float)a.p.Hkv * a.cost_scale;
+  }
+  // the same in whole ones: the sum over a step fits 32 bits (see sized)
+  __device__ __forceinline__ uint32_t scaled(const FwdArgs& a) const { return n ? max(1u, __float2uint_rd(units(a))) : 0u; }
 };
 
 // Where `units` of sequence s's cost lie: a function of them that never falls as they rise,
@@ -1232,20 +1238,40 @@ cudaError_t launch_d(const FwdArgs& a, const void* q, const void* k_pages, const
 
 size_t paged_ws_bytes(int D) { return kOffPartials + 2 * kCtas * partial_bytes(D); }
 
-cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
-                             void* ws, cudaStream_t st) {
+// The step's sizes as the kernel takes them. `most` is the most, in keys, that a step with rising q_start
+// and any kv_len can cost; a unit is so many keys that it stays below half of what 32 bits hold.
+static FwdArgs sized(const PagedArgs& p, double& most) {
   FwdArgs a{};
   a.p = p;
   a.TQ = kTile / p.G;
   a.TQf = std::max(1, kFew / p.G);
   a.g_inv = (65536 + p.G - 1) / p.G;
   while ((1 << a.page_shift) < p.page) ++a.page_shift;
-  // All that a step can cost: the units that its sum is counted in, and the CTAs that it can keep busy.
-  const double most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * (kPairCost * ((double)p.width * p.page + 2.0 * a.TQ) + kPairItemCost);
+  // an item's keys: at most the table's ahead of the new tokens, and its sequence's new tokens up to its end,
+  // which Costs counts whether the table lists them or not
+  most = ((double)p.T / (2 * a.TQ) + p.S) * p.Hkv * (kPairCost * ((double)p.width * p.page + p.T + 2.0 * a.TQ) + kPairItemCost);
   double unit = 1;
   while (most > 2e9 * unit) unit *= 2;
   a.cost_scale = (float)(1 / unit);
   a.least_cost = std::max(1, (int)(kLeastCost / unit));
+  return a;
+}
+
+uint64_t paged_units(const PagedArgs& p) {
+  double most;
+  const FwdArgs a = sized(p, most);
+  uint64_t sum = 0;
+  for (int s = 0; s < p.S; ++s) {
+    const Costs c(a, seq_rows(p, s));
+    if (c.n) sum += std::max<uint64_t>(1, (uint64_t)c.units(a));
+  }
+  return sum;
+}
+
+cudaError_t launch_paged_fwd(const PagedArgs& p, const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                             void* ws, cudaStream_t st) {
+  double most;
+  FwdArgs a = sized(p, most);
   a.ctas = (int)std::min<double>(std::min(sm_count(), kCtas), std::max(1.0, most / kLeastCost));
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;

@@ -10,9 +10,9 @@ namespace pa {
 // What the device-side arrays hold is brought into range here, once for everybody.
 struct SeqRows {
   int a, b, kv;
-  __device__ __forceinline__ int base() const { return kv - (b - a); }  // position of its first new token
+  __host__ __device__ __forceinline__ int base() const { return kv - (b - a); }  // position of its first new token
 };
-__device__ __forceinline__ SeqRows seq_rows(const PagedArgs& p, int s) {
+__host__ __device__ __forceinline__ SeqRows seq_rows(const PagedArgs& p, int s) {
   SeqRows r;
   r.a = min(max(p.q_start[s], 0), p.T);
   r.b = min(max(p.q_start[s + 1], r.a), p.T);

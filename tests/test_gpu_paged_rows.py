@@ -1,0 +1,70 @@
+"""Paged attention where a step is larger than its tables: every row of every
+sequence is written. Tolerances as in test_gpu_paged.py, whose derivation they share."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import segment_masked_causal_gb300 as pa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from segment_masked_causal_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,keys", [
+    ([1_200_000, 5], 1, 1, 16),        # one sequence whose costs alone pass 32 bits
+    ([100_000, 100_000], 64, 8, 16),   # two whose sum does
+    ([3, 200_000, 5], 32, 8, 4096),    # and one beside others, over a longer table
+])
+def test_more_tokens_than_the_table_lists(cuda_dev, lens, Hq, Hkv, keys):
+    """Tokens past the table see the keys that it lists; so do those of a kv_len below the new tokens, from its
+    start on. All rows against the same few keys, in blocks, in fp64."""
+    D, page, S, T = 64, 16, len(lens), sum(lens)
+    g = torch.Generator(device=cuda_dev).manual_seed(S)
+    n = keys // page
+    pool = torch.randn(2, S * n, Hkv, page, D, generator=g, device=cuda_dev).bfloat16()
+    table = torch.arange(S * n, dtype=torch.int32, device=cuda_dev).view(S, n)
+    start = [0] + np.cumsum(lens).tolist()
+    kv = [m - (7 if i == 0 else 0) for i, m in enumerate(lens)]  # the first one's first seven tokens lie before its start
+    kv[0] = max(kv[0], 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)
+    q = torch.randn(T, Hq, D, generator=g, device=cuda_dev, dtype=torch.bfloat16)
+    cache = pa.PagedCache(pool[0], pool[1])
+    out, lse = torch.full_like(q, 7.0), torch.full((T, Hq), 7.0, device=cuda_dev)
+    ws = pa.paged_workspace(q, cache)
+    pa.paged_forward(q, cache, table, i32(start), i32(kv), out=out, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    scale, G = 1 / math.sqrt(D), Hq // Hkv
+    for s in range(S):
+        K, V = (x[s * n:(s + 1) * n].double().transpose(0, 1).reshape(Hkv, keys, D) for x in pool)
+        # no row is left as it was, and blocks of them have the right values: the first, those at the table's
+        # end, some in the middle and the last
+        first, last = start[s], start[s + 1]
+        assert not (lse[first:last] == 7).any() and not (out[first:last] == 7).all(-1).any()
+        block = min(300, last - first)
+        for a in sorted({min(first + x, last - block) for x in (0, max(0, keys - block // 2), (last - first) // 2, last - first)}):
+            rows = torch.arange(a, a + block, device=cuda_dev)
+            seen = (rows - first + kv[s] - lens[s] + 1).clamp(0, min(keys, kv[s]))
+            z = torch.einsum("thgd,hkd->thgk", q[rows].double().view(-1, Hkv, G, D), K) * scale
+            Z = torch.einsum("thgd,hkd->thgk", q[rows].double().abs().view(-1, Hkv, G, D), K.abs()).amax(-1).view(-1, Hq) * scale
+            z = z.masked_fill(torch.arange(keys, device=cuda_dev) >= seen.view(-1, 1, 1, 1), -math.inf)
+            wl = torch.logsumexp(z, -1)
+            w = torch.exp(z - wl.clamp(min=-1e300)[..., None])
+            want = torch.einsum("thgk,hkd->thgd", w, V).reshape(-1, Hq, D)
+            A = torch.einsum("thgk,hkd->thgd", w, V.abs()).reshape(-1, Hq, D)
+            wl = wl.view(-1, Hq)
+            none = torch.isinf(wl)
+            assert (none == (seen == 0).view(-1, 1)).all()
+            assert (lse[rows][none] == -math.inf).all() and (out[rows][none] == 0).all()
+            score = 10 * 2.0 ** -23 * Z
+            tol = (2 * 2.0 ** -8 + 2.0 ** -12 + 2 * score[..., None]) * A + 2.0 ** -8 * want.abs()
+            assert ((out[rows].double() - want).abs() <= tol).all()
+            err = (lse[rows].double() - wl).abs()[~none]
+            assert (err <= (score + 2.0 ** -22 + (64 + keys / 64) * 2.0 ** -24 + 2.0 ** -23 * wl.abs())[~none]).all()
