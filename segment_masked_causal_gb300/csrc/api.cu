@@ -975,8 +975,6 @@ pa_status pa_paged_fwd(const pa_paged_dims* dims, const pa_paged_strides* stride
   pa_status why = paged_checks(dims, strides, false);
   if (why != PA_OK) return why;
   if (dims->Hq / dims->Hkv > 128) return PA_ERR_GQA;
-  // the costs that deal out the work are 64-bit sums of keys over tiles and kv heads
-  if (((double)dims->T + dims->S) * dims->Hkv * ((double)dims->width * dims->page + dims->T + 512) > 4e18) return PA_ERR_SHAPE;
   if (dims->T == 0) return PA_OK;
   for (const void* x : {q, k_pages, v_pages, (const void*)page_table, (const void*)q_start, (const void*)kv_len,
                         (const void*)out, (const void*)lse, (const void*)ws})

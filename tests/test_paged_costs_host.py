@@ -67,3 +67,15 @@ def test_refusals(L):
     d = lambda **kw: ctypes.byref(pa.pa_paged_dims(*{**good, **kw}.values()))
     assert f(d()) == 0 and f(None) == 1 and f(d(), a=None) == 1 and f(d(), b=None) == 1 and f(d(), o=None) == 1
     assert f(d(D=80)) == 2 and f(d(Hq=129)) == 3 and f(d(S=0)) == 4 and f(d(page=8)) == 4
+
+
+def test_no_size_is_refused_for_its_cost(L):
+    """The most tokens over the longest table: what it costs fits (above), so the call goes ahead."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    fake = 0x100000
+    d = pa.pa_paged_dims(1, 1 << 30, 4, 4, 64, 1, 256, (1 << 23) - 2, 0.0)
+    s = pa.pa_paged_strides(256, 64, 0, 0, 256, 64, 65536, 16384, 64)
+    n = L.pa_paged_workspace_bytes(64)
+    assert L.pa_paged_fwd(ctypes.byref(d), ctypes.byref(s), *[fake] * 9, n, None) in (7, 8)
