@@ -684,8 +684,9 @@ pa_status pa_paged_append(const pa_paged_dims* dims, const pa_paged_strides* str
  * holds past a sequence's tokens may be anything (NaN too); the keys and values
  * up to kv_len are finite. P enters the second product in bf16; sums and maxima are
  * fp32. Hq / Hkv is at most 128.
- * ws >= pa_paged_workspace_bytes(D) bytes, its first 4 the status word; a
- * workspace belongs to one stream at a time. The same call gives the same bits.
+ * ws >= pa_paged_workspace_bytes(D) bytes, its first 4 the status word (T 0 launches
+ * nothing and leaves it as it is); a workspace belongs to one stream at a time. The same call
+ * gives the same bits.
  * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA (also Hq / Hkv > 128), PA_ERR_SHAPE, PA_ERR_ALIGN,
  * PA_ERR_WORKSPACE, PA_ERR_ARCH, PA_ERR_CUDA.
  */

@@ -1190,13 +1190,20 @@ def pa_paged_workspace_bytes(D) -> int:
     return int(lib().pa_paged_workspace_bytes(int(D)))
 
 
-def paged_workspace(q, cache):
-    """A device workspace for paged_forward on q and cache (uint8; any lengths)."""
+def _paged_workspace(q, cache):
     import torch
     n = pa_paged_workspace_bytes(cache.D)
     if n == 0:
         raise PAError(2, "head dim must be 64, 96 or 128")
     return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_workspace(q, cache):
+    """A device workspace for paged_forward on q and cache (uint8; any lengths), its
+    status word clear: a step without rows, which launches nothing, leaves it so."""
+    ws = _paged_workspace(q, cache)
+    ws[:4].zero_()
+    return ws
 
 
 def pa_paged_fwd(q, cache, page_table, q_start, kv_len, out, lse, ws, scale=0.0, stream=None):
@@ -1232,7 +1239,7 @@ def paged_forward(q, cache, page_table, q_start, kv_len, scale=0.0, out=None, ls
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = paged_workspace(q, cache)
+        ws = _paged_workspace(q, cache)
     pa_paged_fwd(q, cache, page_table, q_start, kv_len, out, lse, ws, scale)
     return out, lse
 
