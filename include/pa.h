@@ -571,8 +571,9 @@ pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t fo
  * Arguments that a scaling does not name are not looked at.
  * pa_rotary_init (host only) makes the description that the kernels take, from any
  * frequencies (finite) and the amplitude a (1 as a rule). The angle is formed
- * from a 64-bit binary fraction of a turn, so it is as exact at far positions
- * as at near ones (about 5e-8 radians).
+ * from a 64-bit binary fraction of a turn, so that of the given frequencies (of 2^40 radians
+ * at most) is as exact at far positions as at near ones: about 5e-8 radians. What
+ * pa_rotary_frequencies rounds to doubles is off by 2^-53 of itself before that.
  *   rot : a multiple of 8 in [8, 128]
  * Errors: PA_ERR_NULL, PA_ERR_SHAPE (rot; theta, factor, original or frequencies
  * not finite and positive, negative frequencies allowed in pa_rotary_init; low >=

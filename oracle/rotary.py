@@ -38,9 +38,9 @@ def members(rot, interleaved):
 def rotate(x, pos, freq, amplitude=1.0, interleaved=False, backward=False):
     """x (..., D) fp64 with pos (...,) broadcast against its leading dims."""
     a, b = members(2 * len(freq), interleaved)
-    # the angle's whole turns dropped in exact arithmetic: pos times a double in twice its precision
+    # the angle in long double (64 bits or more), without its whole turns before it is a double again
     angle = np.asarray(pos, np.longdouble)[..., None] * np.asarray(freq, np.longdouble)
-    angle = np.asarray(angle, np.float64)
+    angle = np.asarray(np.fmod(angle, 8 * np.arctan(np.longdouble(1))), np.float64)
     z = (x[..., a] + 1j * x[..., b]) * amplitude * np.exp((-1j if backward else 1j) * angle)
     y = x.copy()
     y[..., a], y[..., b] = z.real, z.imag

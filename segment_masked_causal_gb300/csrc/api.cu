@@ -831,6 +831,12 @@ pa_status pa_rotary_frequencies(int32_t rot, int32_t scaling, double theta, doub
   return PA_OK;
 }
 
+// A number of turns without its whole ones, in 2^-64.
+static uint64_t fixed_turns(double t) {
+  const double x = (t - std::nearbyint(t)) * 4294967296.0, h = std::floor(x);
+  return ((uint64_t)(int64_t)h << 32) + (uint64_t)std::llrint((x - h) * 4294967296.0);
+}
+
 pa_status pa_rotary_init(pa_rotary* rotary, int32_t rot, int32_t layout, const double* frequencies, double amplitude) {
   if (!rot_ok(rot) || !std::isfinite(amplitude) || !std::isfinite((float)amplitude)) return PA_ERR_SHAPE;
   if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_DTYPE;
@@ -843,10 +849,9 @@ pa_status pa_rotary_init(pa_rotary* rotary, int32_t rot, int32_t layout, const d
   r.amplitude = (float)amplitude;
   r.ready = kRotaryReady;
   for (int i = 0; i < rot / 2; ++i) {
-    double t = frequencies[i] / 6.283185307179586476925;
-    t -= std::floor(t);
-    // a double below 1 is at most 1 - 2^-53; a tiny negative frequency can come out as 1
-    r.turns[i] = t >= 1.0 ? 0 : (uint64_t)(t * 18446744073709551616.0);
+    // f / 2 pi as a sum of two doubles: a position multiplies what one alone would leave out
+    const double f = frequencies[i], t = f * 0x1.45f306dc9c883p-3;
+    r.turns[i] = fixed_turns(t) + fixed_turns(std::fma(f, 0x1.45f306dc9c883p-3, -t) + f * -0x1.6b01ec5417056p-57);
   }
   *rotary = r;
   return PA_OK;

@@ -4,9 +4,10 @@
 // A pair (x1, x2) at position p with frequency f (radians a position) becomes
 //   y1 = a (x1 cos(p f) - x2 sin(p f)),  y2 = a (x2 cos(p f) + x1 sin(p f)).
 // The angle is formed in turns as a 64-bit binary fraction: with
-// t = round(2^64 frac(f / 2 pi)) the product p t, taken mod 2^64, is the angle's
+// t = 2^64 frac(f / 2 pi) to a unit, the product p t, taken mod 2^64, is the angle's
 // fraction of a turn to 2^-33 for any 32-bit p, whole turns dropping out by
-// themselves. So far positions cost and lose nothing (an fp32 product p f is 0.06
+// themselves; its upper 32 bits, cut off there, are used (2^-32 of a turn, 1.5e-9 radians). So far
+// positions cost and lose nothing (an fp32 product p f is 0.06
 // radians off at a million), no table is read, and the sine and cosine are taken
 // of an eighth of a turn at most, where fp32 holds the angle to 5e-8.
 #pragma once
@@ -18,7 +19,6 @@
 
 namespace pa {
 
-//
 // On an eighth of a turn, |x| <= pi / 4, the series of sine up to x^9 and of cosine up to x^8
 // leave out less than 2e-9 and 3e-8, below fp32's half steps there.
 __device__ __forceinline__ void rope_cos_sin(uint64_t turns, int32_t pos, float amplitude, float& c, float& s) {
