@@ -286,7 +286,9 @@ __device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], ui
   __syncwarp();
 }
 
-// The parts of items in a CTA's run, in order.
+// The parts of items in a CTA's run, in order. A whole warp takes it, and passes sequences without
+// new tokens 128 at a time: one at a time they are 0.1 us each, and a step's slots may be few of very many in
+// use (two tokens in 256 slots: 32 -> 10 us; in 2^24 slots 1.7 s, close to the 2 s after which waits give up).
 struct Walk {
   const FwdArgs& a;
   SeqRows r;
@@ -332,11 +334,29 @@ struct Walk {
     h = 0;
     if (++i < n) return;
     i = 0;
-    for (++s; s < a.p.S; ++s) {
-      r = seq_rows(a.p, s);
-      n = items_of(a, r.b - r.a);
-      if (n > 0) return;
+    if (++s < a.p.S && enter()) return;
+    for (++s; s < a.p.S; s += 128) {
+      uint32_t some[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = s + k * 32 + (int)(threadIdx.x & 31);
+        SeqRows t{0, 0, 0};
+        if (x < a.p.S) t = seq_rows(a.p, x);
+        some[k] = __ballot_sync(~0u, t.b > t.a);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (some[k]) {
+          s += k * 32 + __ffs(some[k]) - 1;
+          enter();
+          return;
+        }
     }
+  }
+  __device__ __forceinline__ bool enter() {  // sequence s; whether it has items
+    r = seq_rows(a.p, s);
+    n = items_of(a, r.b - r.a);
+    return n > 0;
   }
 };
 

@@ -68,3 +68,33 @@ def test_more_tokens_than_the_table_lists(cuda_dev, lens, Hq, Hkv, keys):
             assert ((out[rows].double() - want).abs() <= tol).all()
             err = (lse[rows].double() - wl).abs()[~none]
             assert (err <= (score + 2.0 ** -22 + (64 + keys / 64) * 2.0 ** -24 + 2.0 ** -23 * wl.abs())[~none]).all()
+
+
+@pytest.mark.parametrize("S,used", [(300, [0, 299]), (1000, [1, 33, 34, 162, 163, 900]), ((1 << 24) - 1, [0, 5_000_000, (1 << 24) - 2])])
+def test_few_slots_in_use(cuda_dev, S, used):
+    """A step of a program that keeps a slot for every sequence it may ever run: the slots without new
+    tokens are passed in a fraction of the 2 s after which a kernel's waits give up."""
+    D, page, width, kv_of = 64, 16, 4, [60, 3, 33, 64, 1, 17]
+    n = len(used)
+    g = torch.Generator(device=cuda_dev).manual_seed(S)
+    pool = torch.randn(2, n * width, 2, page, D, generator=g, device=cuda_dev).bfloat16()
+    cache = pa.PagedCache(pool[0], pool[1])
+    at = torch.tensor(used, device=cuda_dev)
+    own = torch.arange(n * width, device=cuda_dev, dtype=torch.int32).view(n, width)
+    table = torch.full((S, width), -1, device=cuda_dev, dtype=torch.int32)
+    kv, new = (torch.zeros(S, device=cuda_dev, dtype=torch.int32) for _ in range(2))
+    lens = torch.tensor(kv_of[:n], device=cuda_dev, dtype=torch.int32)
+    table[at], kv[at], new[at] = own, lens, 1
+    start = torch.zeros(S + 1, device=cuda_dev, dtype=torch.int32)
+    start[1:] = new.cumsum(0)
+    q = torch.randn(n, 4, D, generator=g, device=cuda_dev, dtype=torch.bfloat16)
+    want, wl = pa.paged_forward(q, cache, own, torch.arange(n + 1, device=cuda_dev, dtype=torch.int32), lens)  # the same slots alone
+    out, lse, ws = torch.full_like(q, 7.0), torch.full((n, 4), 7.0, device=cuda_dev), pa.paged_workspace(q, cache)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    pa.paged_forward(q, cache, table, start, kv, out=out, lse=lse, ws=ws)
+    end.record()
+    torch.cuda.synchronize()
+    assert pa.pa_device_status(ws) == 0
+    assert torch.equal(out, want) and torch.equal(lse, wl)  # contexts of one visit are never cut
+    assert begin.elapsed_time(end) < 600
