@@ -978,10 +978,17 @@ class Rotary:
                 raise ValueError(f"frequencies must be rot / 2 = {rot // 2} numbers (at most {PA_ROPE_MAX_PAIRS}), got {len(given)}")
             f = (ctypes.c_double * PA_ROPE_MAX_PAIRS)(*given)
         self.c = pa_rotary()
-        _check(lib().pa_rotary_init(ctypes.byref(self.c), rot, int(bool(interleaved)), f, float(amplitude)))
         self.ref = ctypes.byref(self.c)
+        _check(lib().pa_rotary_init(self.ref, rot, int(bool(interleaved)), f, float(amplitude)))
         self.rot, self.interleaved, self.amplitude = rot, bool(interleaved), float(amplitude)
         self.frequencies = tuple(f[:rot // 2])
+
+    def __reduce__(self):  # copies and pickles are made again from what it was made of: `ref` is an address
+        return _rotary_of, (self.rot, self.interleaved, self.amplitude, self.frequencies)
+
+
+def _rotary_of(rot, interleaved, amplitude, frequencies):
+    return Rotary(rot, interleaved=interleaved, amplitude=amplitude, frequencies=frequencies)
 
 
 def pa_positions(seg, positions, stream=None):
