@@ -197,7 +197,7 @@ cudaError_t launch_rope(const pa_rotary& rope, const RopeTensor* t, int count, i
 }
 
 cudaError_t launch_positions(int B, int N, const int32_t* seg, int32_t* positions, cudaStream_t st) {
-  const int tiles = (N + kPosTile - 1) / kPosTile;
+  const int tiles = (int)(((int64_t)N + kPosTile - 1) / kPosTile);
   cudaLaunchAttribute attr = programmatic_launch();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)B * tiles));
