@@ -598,7 +598,7 @@ pa_status pa_rotary_init(pa_rotary* rotary, int32_t rot, int32_t layout, const d
  * Positions of packed rows: positions[b, n] = n minus the first token of the run of
  * equal ids that token n of row b lies in. So each segment of a packed row counts
  * from 0 (an id that comes back later in the row starts a run of its own there).
- *   seg, positions : (B, N) int32, contiguous, 16-byte aligned; B * N < 2^31
+ *   seg, positions : (B, N) int32, contiguous, 16-byte aligned, apart; B * N < 2^31
  * Errors: PA_ERR_SHAPE, PA_ERR_NULL, PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
  */
 pa_status pa_positions(int32_t B, int32_t N, const int32_t* seg, int32_t* positions, pa_stream_t stream);

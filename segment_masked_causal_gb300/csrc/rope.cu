@@ -91,11 +91,44 @@ cudaError_t launch_vec(RopeArgs& a, bool rest, cudaStream_t st) {
 // of maxima. The start of the run that the block's first token continues lies before the
 // block: the 4,096 ids there are read along with its own, those further back only if
 // none of them starts one. Bound by the round trips: one, and one more for each 4,096 tokens of
-// a longer run.
-constexpr int kPosThreads = 256, kPosPer = 4, kPosTile = kPosThreads * kPosPer, kPosBack = 16;
+// a longer run. Over long rows that would be quadratic, so there a kernel goes ahead that leaves each block's
+// last start in the place of its last token's position, as a negative number, and what lies further back
+// than 4,096 tokens is looked up in those, 1,024 blocks at a time. A place may hold its position
+// by then: that gives the start of its run as well, and with it the end of the search.
+constexpr int kPosThreads = 256, kPosPer = 4, kPosTile = kPosThreads * kPosPer, kPosBack = 16, kPosMarks = 4;
+// The first kernel costs 1.2 us of a row of short runs (32,768 tokens 4.8 -> 6.0 us) and saves 3 us for each 4,096
+// tokens of a long one (one run of 32,768 tokens 25.6 -> 6.4 us, of 2^20 1,054 -> 15, of 2^24 153,500 -> 200).
+constexpr int kPosLong = 32768;
 
-__global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* __restrict__ seg,
-                                                                int32_t* __restrict__ positions, int N, int tiles) {
+// The latest start of a run among a block's tokens, or -1: m in the place of the last one's position.
+__device__ __forceinline__ int32_t pos_mark(int m) { return -2 - m; }
+__device__ __forceinline__ int pos_start(int32_t word, int n) { return word < 0 ? -2 - word : n - word; }
+
+__global__ void __launch_bounds__(kPosThreads) positions_mark_kernel(const int32_t* __restrict__ seg, int32_t* positions, int N,
+                                                                     int tiles) {
+  __shared__ int sh[kPosThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x / tiles, n0 = (blockIdx.x - b * tiles) * kPosTile;
+  const int32_t* row = seg + (int64_t)b * N;
+  int last = -1;
+#pragma unroll
+  for (int i = 0; i < kPosPer; ++i) {
+    const int n = n0 + i * kPosThreads + (int)threadIdx.x;
+    if (n < N && (n == 0 || row[n] != row[n - 1])) last = n;
+  }
+  last = __reduce_max_sync(~0u, last);
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 0; w < kPosThreads / 32; ++w) last = max(last, sh[w]);
+    positions[(int64_t)b * N + min((int64_t)n0 + kPosTile, (int64_t)N) - 1] = pos_mark(last);
+  }
+}
+
+__global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* __restrict__ seg, int32_t* positions, int N,
+                                                                int tiles, bool marked) {
   __shared__ int sh[kPosThreads / 32], back[kPosThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -146,8 +179,18 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const int32_t* _
     if (w < warp) excl = max(excl, sh[w]);
     from = max(from, back[w]);
   }
-  for (int hi = n0 - kPosThreads * kPosBack; hi > 0 && from < 0; hi -= kPosThreads * kPosBack) {
-    found = __reduce_max_sync(~0u, look_back(hi));
+  const auto look_up = [&](int hi) {  // the same among the marks of the kPosMarks * kPosThreads tiles before tile hi
+    int start = -1;
+#pragma unroll
+    for (int j = 0; j < kPosMarks; ++j) {
+      const int t = hi - 1 - (j * kPosThreads + (int)threadIdx.x), n = t * kPosTile + kPosTile - 1;
+      if (t >= 0) start = max(start, pos_start(*(const volatile int32_t*)(positions + (int64_t)b * N + n), n));
+    }
+    return start;
+  };
+  const int unit = marked ? kPosTile : 1, step = marked ? kPosThreads * kPosMarks : kPosThreads * kPosBack;
+  for (int hi = (n0 - kPosThreads * kPosBack) / unit; hi > 0 && from < 0; hi -= step) {
+    found = __reduce_max_sync(~0u, marked ? look_up(hi) : look_back(hi));
     __syncthreads();
     if (lane == 0) back[warp] = found;
     __syncthreads();
@@ -205,7 +248,12 @@ cudaError_t launch_positions(int B, int N, const int32_t* seg, int32_t* position
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, positions_kernel, seg, positions, N, tiles);
+  const bool marked = N > kPosLong;
+  if (marked) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, positions_mark_kernel, seg, positions, N, tiles);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, positions_kernel, seg, positions, N, tiles, marked);
 }
 
 }  // namespace pa
