@@ -272,12 +272,14 @@ __device__ __forceinline__ void find_ends(const FwdArgs& a, Bound (&ends)[2], ui
   SeqRows t{__shfl_sync(~0u, r.a, from), __shfl_sync(~0u, r.b, from), __shfl_sync(~0u, r.kv, from)};
   if (lane < 2) {
     if (at < S && S > 32) {
-      int k = at * per;  // the thread's share, then the sequence in it
-      while (left >= sums[k]) left -= sums[k++];
-      for (at = k * share;; ++at) {
+      // The thread's share, then the sequence in it. Both are there, for the numbers are those that
+      // were added up; the loops end all the same if somebody changes the arrays meanwhile.
+      int k = at * per;
+      while (k < kThreads - 1 && left >= sums[k]) left -= sums[k++];
+      for (at = min(k * share, S - 1);; ++at) {
         t = seq_rows(a.p, at);
         const uint32_t cost = Costs(a, t).scaled(a);
-        if (left < cost) break;
+        if (left < cost || at == S - 1) break;
         left -= cost;
       }
     }

@@ -98,3 +98,35 @@ def test_few_slots_in_use(cuda_dev, S, used):
     assert pa.pa_device_status(ws) == 0
     assert torch.equal(out, want) and torch.equal(lse, wl)  # contexts of one visit are never cut
     assert begin.elapsed_time(end) < 600
+
+
+@pytest.mark.parametrize("S", [40, 8000])
+def test_many_arrays_out_of_range_are_taken_into_it(cuda_dev, S):
+    """q_start that rises and falls over many sequences, so that their rows add up to far more than T and
+    their costs to more than 32 bits: nothing outside the tensors is touched, and the next step is as ever."""
+    D, page, width, T = 64, 16, 2, 20_000
+    rng = np.random.default_rng(S)
+    guard = 64
+    g = torch.Generator(device=cuda_dev).manual_seed(S)
+    pool = torch.randn(2, 8, 1, page, D, generator=g, device=cuda_dev).bfloat16()
+    cache = pa.PagedCache(pool[0], pool[1])
+    i32 = lambda x: torch.from_numpy(np.asarray(x).astype(np.int32)).to(cuda_dev)
+    table = i32(rng.integers(0, 8, (S, width)))
+    q = torch.randn(T, 1, D, generator=g, device=cuda_dev).bfloat16()
+    around = torch.full((T + 2 * guard, 1, D), 7.0, device=cuda_dev, dtype=torch.bfloat16)
+    lse_all = torch.full((T + 2 * guard, 1), 7.0, device=cuda_dev)
+    ws = pa.paged_workspace(q, cache)
+
+    def step(start, kv, tab):
+        pa.paged_forward(q, cache, tab, i32(start), i32(kv), out=around[guard:-guard], lse=lse_all[guard:-guard], ws=ws)
+        torch.cuda.synchronize()
+        assert pa.pa_device_status(ws) == 0
+        assert (around[:guard] == 7).all() and (around[-guard:] == 7).all()
+        assert (lse_all[:guard] == 7).all() and (lse_all[-guard:] == 7).all()
+        return around[guard:-guard].clone(), lse_all[guard:-guard].clone()
+    good = np.linspace(0, T, S + 1), np.full(S, 30)
+    want = step(*good, table)
+    step(np.tile([0, T], S // 2 + 1)[:S + 1], np.full(S, 30), table)
+    bad = rng.integers(-2 ** 31, 2 ** 31, S + 1)
+    step(bad, rng.integers(-2 ** 31, 2 ** 31, S), i32(rng.integers(-2 ** 31, 2 ** 31, (S, width))))
+    assert all(torch.equal(x, y) for x, y in zip(want, step(*good, table)))
