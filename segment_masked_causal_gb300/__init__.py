@@ -1020,6 +1020,20 @@ def segment_positions(seg):
 _ROPE_FIELDS = struct.Struct("PPi4xqqqqqq")  # pa_rope_tensor
 
 
+def _rope_refusals(parts, B, N, D, unit):
+    """What pa_rope refuses of single tensors, for all of them before the first launch
+    (a list of several launches is turned whole or not at all)."""
+    for p in parts:
+        x, y, H, *s = _ROPE_FIELDS.unpack(p)
+        used = [i for i, n in enumerate((B, H, N)) if n > 1]
+        if not 0 < H <= 65535 or any(s[i] < D or s[i + 3] < D for i in used):
+            raise PAError(4, pa_status_string(4))
+        if any(s[i] % unit or s[i + 3] % unit for i in used) or x % 16 or y % 16:
+            raise PAError(5, pa_status_string(5))
+        if x == y and any(s[i] != s[i + 3] for i in used):
+            raise PAError(4, pa_status_string(4))
+
+
 def pa_rope(tensors, out, rotary, positions=None, backward=False, stream=None):
     """Rotate the (B, H, N, D) tensors into `out` (which may be the tensors
     themselves; None: new tensors in the same memory order), or take their
@@ -1069,6 +1083,8 @@ def pa_rope(tensors, out, rotary, positions=None, backward=False, stream=None):
             raise ValueError("positions must be contiguous")
         pos = positions.data_ptr()
     st, fn = _stream(stream), lib().pa_rope
+    if len(parts) > PA_ROPE_MAX_TENSORS:
+        _rope_refusals(parts, B, N, D, 16 // tensors[0].element_size())
     for i in range(0, len(parts), PA_ROPE_MAX_TENSORS):
         some = parts[i:i + PA_ROPE_MAX_TENSORS]
         _check(fn(rotary.ref, len(some), b"".join(some), B, N, D, io, pos, 1 if backward else 0, st))

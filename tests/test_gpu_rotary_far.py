@@ -30,3 +30,23 @@ def test_far_positions_are_as_exact_as_near_ones(cuda_dev, theta, interleaved, b
     X = x.astype(np.float64)
     want = rotary.rotate(X, pos[None, None], r.frequencies, interleaved=interleaved, backward=backward)
     assert (np.abs(y.double().cpu().numpy() - want) <= 2.0 ** -21 * rotary.weight(X, r.frequencies, interleaved)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", ["address", "strides", "gap", "heads"])
+def test_a_list_of_several_launches_is_turned_whole_or_not_at_all(cuda_dev, dtype, bad):
+    r = pa.Rotary(64)
+    xs = [torch.randn(2, 3, 5, 64, device=cuda_dev).to(dtype) for _ in range(6)]
+    keep = [x.clone() for x in xs]
+    wide = torch.randn(2, 3, 5, 80, device=cuda_dev).to(dtype)
+    last = {"address": wide[..., 2:66], "strides": wide.flatten()[:2 * 3 * 5 * 66].view(2, 3, 5, 66)[..., :64],
+            "gap": wide.flatten().as_strided((2, 3, 5, 64), (960, 320, 48, 1)), "heads": wide[:, :0, :, :64]}[bad]
+    kept = wide.clone()
+    with pytest.raises(pa.PAError, match="PA_ERR_ALIGN" if bad in ("address", "strides") else "PA_ERR_SHAPE"):
+        pa.rotary_forward(xs + [last], r, out=xs + [last])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(xs, keep)) and torch.equal(wide, kept)
+    with pytest.raises(pa.PAError):  # alone it is refused as well
+        pa.rotary_forward([last], r, out=[last])
+    turned = pa.rotary_forward(xs, r, out=xs)
+    assert all(torch.equal(a, pa.rotary_forward([b], r)[0]) for a, b in zip(turned, keep))
