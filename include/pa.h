@@ -567,7 +567,9 @@ pa_status pa_bwd_ckpt(const pa_dims* dims, const pa_strides* strides, int32_t fo
  *                   pair comes out factor times slower, the fastest as it was
  *   PA_ROPE_BANDS   by the turns r_i = original f_i / (2 pi) that a pair makes over
  *                   the `original` context: f_i / factor up to r_i = low, f_i from
- *                   r_i = high on, linear in r_i between
+ *                   r_i = high on, linear in r_i between. (Some models' ramp is linear
+ *                   in the pair's index i between two rounded ones instead: theirs are other
+ *                   frequencies, to be given to pa_rotary_init as they are.)
  * Arguments that a scaling does not name are not looked at.
  * pa_rotary_init (host only) makes the description that the kernels take, from any
  * frequencies (finite) and the amplitude a (1 as a rule). The angle is formed
@@ -667,7 +669,7 @@ typedef struct {
  * rotated. q may be NULL, q_out then too; q_out may be q with the same strides.
  * positions (T) int32 replaces the tokens' places as what they are rotated by; NULL:
  * their places. A token that has no place in the cache leaves only its q_out. Two
- * tokens of one place (a page listed for two sequences) leave either's values.
+ * tokens of one place (a page listed for two sequences) leave either's value in each element.
  * Errors: PA_ERR_NULL, PA_ERR_HEAD_DIM, PA_ERR_GQA, PA_ERR_SHAPE (also rot > D),
  * PA_ERR_ALIGN, PA_ERR_ARCH, PA_ERR_CUDA.
  */

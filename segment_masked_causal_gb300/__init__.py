@@ -956,7 +956,8 @@ class Rotary:
     """Rotary positions on the first `rot` elements of a head, in pairs of
     halves or of neighbours (interleaved): frequencies theta^(-2i / rot) with
     `scaling` "plain", "linear", "base" or "bands" by `factor` (see
-    include/pa.h; "bands" takes original, low and high), or the given
+    include/pa.h; "bands" takes original, low and high and is linear in a pair's
+    turns: a model whose ramp is linear in the pair's index gives its `frequencies`), or the given
     `frequencies` (rot / 2 radians a position). `amplitude` multiplies cosine and
     sine. Holds no device memory."""
     __slots__ = ("c", "ref", "rot", "interleaved", "amplitude", "frequencies")
@@ -1255,7 +1256,9 @@ def paged_forward(q, cache, page_table, q_start, kv_len, scale=0.0, out=None, ls
     """Attention of a step's new tokens over the paged cache, their own keys and
     values among it (paged_append). q (T, Hq, D) bf16, rows as in paged_append;
     returns (out, lse), lse (T, Hq) fp32. Rows of no sequence are left as they
-    are (not set, in new outputs)."""
+    are (not set, in new outputs). ws is a paged_workspace, which a program keeps: it
+    spares the allocation, and pa_device_status(ws), which waits for the stream, tells
+    whether the call came through (without one, its status goes with its memory)."""
     import torch
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)

@@ -22,7 +22,9 @@
 // V are read from shared memory for 256 rows); an item of one tile has its visits dealt out to
 // the streams in turn, whose sums and O are joined at its end, or, with few visits, goes whole to
 // one of them. No stream ever waits for the other's maximum, and O is rescaled, lazily, between a
-// stream's own products.
+// stream's own products. P is rounded to bf16 because the matrix instruction takes its second
+// product's two operands in one type and V is bf16; the sums below it are of the weights before that. So out is
+// 2.0e-3 to 2.4e-3 of its norm off, of which its own rounding is 1.7e-3.
 //
 // Few rows. A TMEM lane belongs to one warp of four, so where an item has at most eight
 // rows the tile holds them four times and each of a group's warps takes 32 of a visit's
@@ -40,7 +42,7 @@
 // 0.95 of the copy bandwidth), below some 50 MB of keys the start of the pipeline, the last
 // epilogue and the join (one token of 100 keys 8.8 us). Long chunks: the chain of a stream (S, softmax,
 // PV and their hand-overs, 3,200 to 3,700 cycles a visit of both against 2,048 of tensor work; 8,192
-// tokens of one prompt: 444 us, 0.63 of the matrix peak). One S buffer for both streams with P beside it takes PV
+// tokens of one prompt: 439 us, 0.64 of the matrix peak). One S buffer for both streams with P beside it takes PV
 // out of that chain, but each S then waits for the other stream to load the last one (a chunk of 2,001
 // beside 47 single tokens: 10 to 20% longer).
 //
@@ -63,15 +65,18 @@ namespace {
 constexpr int kCtas = 160;  // at most; the workspace's layout has room for as many
 constexpr int kThreads = 384;
 // Cost of an item besides its keys, in keys: what Q's load, the pipeline's turn and the
-// epilogue take; and of a key for two tiles. A chunk of 2,001 tokens beside 47 single ones takes 102 us
+// epilogue take; and of a key for two tiles. No more than a fit to the times of steps of several
+// kinds: a chunk of 2,001 tokens beside 47 single ones takes 102 us
 // with these, 111 with 448 and 1.4 for pairs, 103 with 900 and 2.2, 104 with 384 for single
 // tiles; with 192 there 64 requests of up to 16,000 keys take 84.8 us instead of 83.5, and with 256
 // 33 x 5 tokens 29.9 instead of 27.1.
 constexpr int kItemCost = 320, kPairItemCost = 640;
 constexpr float kPairCost = 1.8f;
 // Visits of a part of an item: fewer are not worth a join (some 3 us, and the part's way through
-// memory), which is not launched at all where no context holds two parts. Against three: one
-// token of 700 keys 14.3 -> 11.7 us, chunks of 1,500 tokens 25.2 -> 19.9, but 8 chunks of 512 42.5 -> 45.1.
+// memory), which is not launched at all where the table holds less than two parts. Against three,
+// over a table of 32,768 tokens: chunks of 1,500 tokens 25.0 -> 22.1 us, one token of 700 keys 14.5 -> 12.7, but
+// 8 chunks of 512 42.7 -> 45.9 and a chunk of 2,001 beside 47 tokens 99 -> 102; without the join, over tables that
+// just hold them, the first two take 19.9 and 11.8.
 constexpr int kLeastVisits = 4;
 constexpr int kLeastCost = 512;  // of a CTA; with 768 one token of 100 keys takes 10.6 us instead of 8.8
 // Visits of an item of few rows that one stream takes alone, so that its epilogue runs beside the
@@ -114,8 +119,8 @@ struct alignas(16) Item {
   int kt0, kt1, nkt;  // visits of the part, and of the item
   int cap, seen0;     // keys in the cache; keys that the first token sees
   int turns, stream;  // visit vc goes to stream (vc & turns) | stream (a pair's visits to 0 and 1)
-  int unused;
 };
+static_assert(sizeof(Item) == 48, "three vectors, see next_item");
 constexpr int kItems = 4;
 
 struct Misc {
@@ -325,7 +330,7 @@ struct Walk {
   __device__ __forceinline__ Item item() const {
     const int t0 = i * 2 * a.TQ;
     return Item{r.a + t0, min(2 * a.TQ, r.b - r.a - t0), h, s, kt0, kt1, nkt, min(r.kv, a.p.width * a.p.page),
-                r.base() + t0 + 1, 0, 0, 0};
+                r.base() + t0 + 1, 0, 0};
   }
 
  private:
@@ -510,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = m.tmem_base;
   find_ends(a, m.ends, reinterpret_cast<uint32_t*>(base + L::OFF_STAGE));
 
-  // All roles count alike: ic the items, vc the visits (K and V stages; an item of one tile gives
-  // visit vc to stream vc & 1), qt the Q buffer of the next item of one tile.
+  // All roles count alike: ic the items, vc the visits (K and V stages, and the stream of a visit where an item
+  // of one tile takes turns, see Item), qt the Q buffer of the next item of one tile.
   int ic = 0, vc = 0;
   bool ok = true;
   const auto next_item = [&](Item& it) {
